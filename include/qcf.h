@@ -461,6 +461,139 @@ size_t qcf_lm_head_workspace_size(const qcf_dims* dims);
 qcf_status qcf_lm_head(const qcf_model* m, const float* x_last, float* logits, int32_t* token, void* ws,
                        size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ going on from a shared context
+ *
+ * What a program needs after the fused prefill, when several sequences (answers sampled
+ * from one request, or several questions) go on from the same context: positions turned
+ * into rotations for the layouts and scalings models use, a paged cache that grows with
+ * each sequence, and the attention of such a batch, which reads the shared context once
+ * for all sequences.  Tensors here are bf16 or fp16 (rotation also fp32); every tensor of
+ * one call has the same type. */
+#define QCF_BF16 0
+#define QCF_F16 1
+#define QCF_F32 2
+
+/* Frequencies scaled for contexts longer than the model's original length.  Pair k of a
+ * rotated width R has w_k = theta^(-2k/R); with s = factor, L0 = original:
+ *   LINEAR  w_k / s
+ *   BASE    theta replaced by theta * s^(R / (R - 2))                      (R > 2)
+ *   TURNS   r = L0 w_k / (2 pi) turns over the original length, kept where r >= high,
+ *           divided by s where r <= low, blended linearly in r between:
+ *           w_k (g + (1 - g) / s), g = clamp((r - low) / (high - low), 0, 1)
+ *   INDEX   the same blend, linear in the pair index between the indices that make `high`
+ *           and `low` turns: i(t) = R ln(L0 / (2 pi t)) / (2 ln theta),
+ *           a = max(0, floor(i(high))), b = min(R/2 - 1, ceil(i(low))),
+ *           g = 1 - clamp((k - a) / max(b - a, 0.001), 0, 1)
+ * amplitude multiplies cosine and sine (1 for none; a table used to move keys that are
+ * already rotated wants 1). */
+#define QCF_ROPE_SCALE_NONE 0
+#define QCF_ROPE_SCALE_LINEAR 1
+#define QCF_ROPE_SCALE_BASE 2
+#define QCF_ROPE_SCALE_TURNS 3
+#define QCF_ROPE_SCALE_INDEX 4
+typedef struct qcf_rope_scaling {
+  int kind;
+  int original;   /* TURNS, INDEX: original context length, > 0 */
+  double factor;  /* >= 1 */
+  double low, high; /* TURNS: 0 <= low < high; INDEX: 0 < low < high */
+  double amplitude;
+} qcf_rope_scaling;
+
+/* Fills device tables cos, sin [n_pos][R/2] fp32 with the angles of positions first_pos ..
+ * first_pos + n_pos - 1, taken in fp64 and rounded once.  scaling NULL: none.  R even,
+ * 2 <= R <= 512; 0 <= first_pos, first_pos + n_pos <= 2^31 - 1. */
+qcf_status qcf_rope_table_fill(float* cos, float* sin, int first_pos, int n_pos, int R, double theta,
+                               const qcf_rope_scaling* scaling, void* stream);
+
+/* Rotates the first R = t->head_dim entries of every head and copies the others:
+ * row i of x turns by the angles of position pos[i].
+ *   x, y   device, rows of H heads of D contiguous entries; x_stride, y_stride entries
+ *          from row to row (>= H D; multiples of 16 bytes are fastest).  y == x (same stride)
+ *          rotates in place; any other overlap gives wrong rows.
+ *   pos    device [n], each in [0, t->max_pos).  -1 marks a padding row: its row of y is
+ *          left as it was.  Any other position outside the table does the same and sets
+ *          QCF_DEV_BAD_INDEX.
+ *   t      tables of rotated width R = head_dim, even, R <= D; D even, <= 512
+ *   mode   QCF_ROPE_HALF pairs (k, k + R/2) or QCF_ROPE_INTERLEAVED pairs (2k, 2k + 1),
+ *          | QCF_ROPE_INVERSE turns by the negative angle (undoes a rotation of amplitude
+ *          1; also the gradient with respect to x)
+ *   dtype  QCF_BF16, QCF_F16 or QCF_F32; arithmetic in fp32, rounded once.
+ * For bf16 and QCF_ROPE_HALF the bits are those of qcf_rope_reposition. */
+#define QCF_ROPE_HALF 0
+#define QCF_ROPE_INTERLEAVED 1
+#define QCF_ROPE_INVERSE 2
+qcf_status qcf_rope_apply(const void* x, int64_t x_stride, void* y, int64_t y_stride, int n, int H, int D, int dtype,
+                          const int32_t* pos, const qcf_rope_table* t, int mode, void* stream);
+
+/* A paged K/V cache: n_pages pages of page_size rows each, K and V laid out alike.  Row r of
+ * head h of page p starts page_stride p + row_stride r + head_stride h entries from the base,
+ * its D entries contiguous; strides are multiples of 16 bytes, so [page][row][head][D] and
+ * [page][head][row][D] are both covered. */
+typedef struct qcf_paged_kv {
+  void* k;
+  void* v;
+  int dtype;               /* QCF_BF16 or QCF_F16 */
+  int n_pages, page_size;  /* page_size a power of two, 8 .. 256 */
+  int Hkv, D;              /* D 16, 64 or 128 */
+  int64_t page_stride, row_stride, head_stride;
+} qcf_paged_kv;
+
+/* A batch of sequences over one shared prefix.  Rows of q and of new keys belong to sequence
+ * b for row_start[b] <= row < row_start[b + 1]; they are its last tokens: row i of nq new rows
+ * has own position kv_len[b] - nq + i and, for rotation, position prefix_len + that.  Rows in
+ * no sequence (before the first, behind the last) are padding: never read, their outputs left
+ * as they were.  Own token j of sequence b lives in page page_table[b][j / page_size], prefix
+ * token j in page prefix_pages[j / page_size].
+ * Lengths are read on the device, so that a captured graph can be replayed with others; the
+ * host gives upper bounds.  A sequence that breaks one (or has fewer tokens than new rows,
+ * or rows outside [0, n_rows)) is left out and sets QCF_DEV_BAD_INDEX. */
+typedef struct qcf_paged_batch {
+  int n_seq;                    /* <= 65535 */
+  int n_rows;                   /* rows of q, k_new, v_new, o, padding included */
+  int max_q;                    /* bound on a sequence's new rows */
+  int max_len;                  /* bound on kv_len, <= table_stride * page_size */
+  const int32_t* row_start;     /* device [n_seq + 1], ascending */
+  const int32_t* kv_len;        /* device [n_seq], own tokens with the new rows among them */
+  const int32_t* page_table;    /* device [n_seq][table_stride] */
+  int table_stride;
+  int prefix_len;               /* 0: no prefix */
+  const int32_t* prefix_pages;  /* device [ceil(prefix_len / page_size)], or NULL */
+} qcf_paged_batch;
+
+/* Writes the new keys and values of a batch into their pages, the keys rotated on the way,
+ * and rotates the queries of the same rows in the same launch.
+ *   k_new, v_new  device, rows of Hkv heads of D contiguous entries, kv_stride entries apart
+ *   q, q_out      device, rows of Hq heads, q_stride and q_out_stride entries apart, or both
+ *                 NULL; q_out == q (same stride) rotates in place
+ *   t, mode       as in qcf_rope_apply (no QCF_ROPE_INVERSE); t NULL: nothing is rotated, keys
+ *                 (and queries) are copied.  A row whose position is outside the table is left
+ *                 out and sets QCF_DEV_BAD_INDEX, as is the K/V of a row whose page is outside
+ *                 the cache (its q is still rotated).
+ * Two rows of a batch never name the same cache slot (pages of different sequences differ). */
+qcf_status qcf_paged_append(const qcf_paged_kv* cache, const qcf_paged_batch* batch, const void* k_new,
+                            const void* v_new, int64_t kv_stride, const qcf_rope_table* t, int mode, const void* q,
+                            int64_t q_stride, void* q_out, int64_t q_out_stride, int Hq, void* stream);
+
+/* Attention of a batch over its shared prefix and its own tokens: for row i of sequence b at
+ * own position p, o[i,h] = sum_j softmax_j(scale * q[i,h] . K_j) V_j over every prefix token
+ * and own tokens j <= p, g = h / (Hq/Hkv), one softmax over both.  The prefix is read once
+ * for all rows of the batch.
+ *   q    device, rows of Hq heads of D contiguous entries, q_stride entries apart
+ *   o    device [n_rows][Hq][D], the cache's type;  lse device [n_rows][Hq] fp32 natural-log sum of
+ *        exp of the scaled logits, or NULL
+ *   ws   device scratch of qcf_shared_prefix_attn_workspace_size() bytes; it needs no clearing;
+ *        calls that overlap on the GPU (captured graphs replayed side by side among them) need
+ *        separate scratch
+ * scale > 0, Hq / Hkv <= 16.  Cache rows behind a length (the rest of a last page, pages not named) may
+ * hold anything, NaN included; a new token whose value holds NaN or infinity may spoil
+ * every row of its own sequence.  A page outside the cache sets QCF_DEV_BAD_INDEX, and its
+ * keys are left out of the softmax.  Products in the cache's type with fp32 sums, softmax in
+ * fp32.  Results repeat bitwise for the same inputs and bounds. */
+size_t qcf_shared_prefix_attn_workspace_size(const qcf_paged_kv* cache, const qcf_paged_batch* batch, int Hq);
+qcf_status qcf_shared_prefix_attn(const qcf_paged_kv* cache, const qcf_paged_batch* batch, const void* q,
+                                  int64_t q_stride, int Hq, float scale, void* o, float* lse, void* ws, size_t ws_bytes,
+                                  void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,6 +19,10 @@ QCF_DEV_BAD_INDEX = 0x2
 QCF_EPI_STORE_BF16 = 0
 QCF_EPI_ADD_F32 = 1
 QCF_LINEAR_W_KN = 0x10
+QCF_BF16, QCF_F16, QCF_F32 = 0, 1, 2
+QCF_ROPE_INTERLEAVED = 1
+QCF_ROPE_INVERSE = 2
+QCF_ROPE_SCALE = {"none": 0, "linear": 1, "base": 2, "turns": 3, "index": 4}
 
 
 class QcfError(RuntimeError):
@@ -65,6 +69,23 @@ class Outputs(C.Structure):
                 ("scores", C.c_void_p), ("q_crit", C.c_void_p), ("last_logits", C.c_void_p),
                 ("first_token", C.c_void_p), ("first_token_host", C.c_void_p), ("x_rows", C.c_void_p),
                 ("layer_sel", C.c_void_p)]
+
+
+class RopeScaling(C.Structure):
+    _fields_ = [("kind", C.c_int), ("original", C.c_int), ("factor", C.c_double), ("low", C.c_double),
+                ("high", C.c_double), ("amplitude", C.c_double)]
+
+
+class PagedKV(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("dtype", C.c_int), ("n_pages", C.c_int), ("page_size", C.c_int),
+                ("Hkv", C.c_int), ("D", C.c_int), ("page_stride", C.c_int64), ("row_stride", C.c_int64),
+                ("head_stride", C.c_int64)]
+
+
+class PagedBatch(C.Structure):
+    _fields_ = [("n_seq", C.c_int), ("n_rows", C.c_int), ("max_q", C.c_int), ("max_len", C.c_int),
+                ("row_start", C.c_void_p), ("kv_len", C.c_void_p), ("page_table", C.c_void_p),
+                ("table_stride", C.c_int), ("prefix_len", C.c_int), ("prefix_pages", C.c_void_p)]
 
 
 P, I, I64, F, D64, SZ = C.c_void_p, C.c_int, C.c_int64, C.c_float, C.c_double, C.c_size_t
@@ -116,6 +137,12 @@ PROTOTYPES = {
     "qcf_embed_rows": (I, [C.POINTER(Model), P, P, I, P, P]),
     "qcf_lm_head_workspace_size": (SZ, [C.POINTER(Dims)]),
     "qcf_lm_head": (I, [C.POINTER(Model), P, P, P, P, SZ, P]),
+    "qcf_rope_table_fill": (I, [P, P, I, I, I, D64, C.POINTER(RopeScaling), P]),
+    "qcf_rope_apply": (I, [P, I64, P, I64, I, I, I, I, P, C.POINTER(RopeTable), I, P]),
+    "qcf_paged_append": (I, [C.POINTER(PagedKV), C.POINTER(PagedBatch), P, P, I64, C.POINTER(RopeTable), I, P, I64, P,
+                             I64, I, P]),
+    "qcf_shared_prefix_attn_workspace_size": (SZ, [C.POINTER(PagedKV), C.POINTER(PagedBatch), I]),
+    "qcf_shared_prefix_attn": (I, [C.POINTER(PagedKV), C.POINTER(PagedBatch), P, I64, I, F, P, P, P, SZ, P]),
 }
 
 _lock = threading.Lock()

@@ -81,7 +81,8 @@ static const char* kClassNames[KC_COUNT] = {
     "rope_reposition", "anchor_keynorm_topk", "profile_scores", "topn_select", "gather_rows",
     "scatter_kv",      "sparse_causal_attn",  "attn_combine",   "gemm_qkv_rope", "gemm_o_resid",
     "gemm_gate_up_swiglu", "gemm_down_resid", "gemm_other",     "rmsnorm",     "embed_rows",
-    "lm_head_argmax",  "misc",         "probe_gemm",     "probe_attn"};
+    "lm_head_argmax",  "misc",         "probe_gemm",     "probe_attn",  "rope_apply",
+    "rope_table_fill", "paged_append",   "prefix_attn",      "own_attn",       "batch_combine"};
 
 struct TimingState {
   std::mutex mu;

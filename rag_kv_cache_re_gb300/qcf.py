@@ -323,3 +323,202 @@ def qcf_batch_workspace_size(model, reqs) -> int:
     n = len(reqs)
     ra = (_lib.Request * n)(*reqs)
     return int(_lib.lib().qcf_batch_workspace_size(C.byref(model.struct.dims), ra, n))
+
+
+# ------------------------------------------------------------------ going on from a shared context
+
+_DTYPE = {torch.bfloat16: _lib.QCF_BF16, torch.float16: _lib.QCF_F16, torch.float32: _lib.QCF_F32}
+
+
+def _bad(message: str):
+    raise QcfError("binding", 1, message)
+
+
+def _need_here(*ts: Optional[torch.Tensor]):
+    """Every tensor on the current CUDA device: kernels launch there."""
+    dev = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            _bad("tensors must be on the current CUDA device")
+
+
+def _need_i32(t: torch.Tensor, what: str, shape=None):
+    if t.dtype != torch.int32 or not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
+        _bad(f"{what} must be a contiguous int32 tensor" + (f" of shape {shape}" if shape is not None else ""))
+
+
+def _head_rows(t: torch.Tensor, what: str) -> int:
+    """The row stride of a [n][H][D] tensor whose rows hold their heads side by side."""
+    if t.dim() != 3 or t.dtype not in _DTYPE:
+        _bad(f"{what} must be a bf16, fp16 or fp32 tensor [n][H][D]")
+    n, H, D = t.shape
+    s = t.stride()
+    if (D > 1 and s[2] != 1) or (H > 1 and s[1] != D):
+        _bad(f"{what}: the heads of a row must be contiguous")
+    return s[0] if n > 1 else H * D
+
+
+class RopeScaling:
+    """Frequencies scaled for contexts beyond the original length (see qcf_rope_scaling).
+
+    kind: "linear", "base", "turns" or "index"; factor s; original, low and high for the last two."""
+
+    def __init__(self, kind: str, factor: float = 1.0, original: int = 0, low: float = 0.0, high: float = 0.0,
+                 amplitude: float = 1.0):
+        if kind not in _lib.QCF_ROPE_SCALE:
+            _bad(f"unknown scaling {kind!r}")
+        self.struct = _lib.RopeScaling(_lib.QCF_ROPE_SCALE[kind], int(original), float(factor), float(low), float(high),
+                                       float(amplitude))
+
+
+def qcf_rope_table_fill(cos: torch.Tensor, sin: torch.Tensor, theta: float, first_pos: int = 0,
+                        scaling: Optional[RopeScaling] = None, stream=None) -> None:
+    """Fills fp32 device tables [n_pos][R/2] for positions first_pos, first_pos + 1, ..."""
+    _need_cuda(cos, sin)
+    _need_here(cos, sin)
+    if cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.shape != sin.shape or cos.dim() != 2:
+        _bad("cos and sin must be fp32 tensors of one shape [n_pos][R/2]")
+    n, half = cos.shape
+    call("qcf_rope_table_fill", cos.data_ptr(), sin.data_ptr(), int(first_pos), n, 2 * half, float(theta),
+         None if scaling is None else C.byref(scaling.struct), _stream(stream))
+
+
+class ScaledRopeTable:
+    """Device cos/sin tables [max_pos][R/2] fp32, filled on the device; R may be part of the head."""
+
+    def __init__(self, max_pos: int, rotary_dim: int, theta: float, device, scaling: Optional[RopeScaling] = None, stream=None):
+        self.max_pos, self.head_dim = int(max_pos), int(rotary_dim)
+        with torch.cuda.stream(stream):
+            self.cos = torch.empty((self.max_pos, self.head_dim // 2), dtype=torch.float32, device=device)
+            self.sin = torch.empty_like(self.cos)
+        qcf_rope_table_fill(self.cos, self.sin, theta, 0, scaling, stream)
+        self.struct = _lib.RopeTable(self.cos.data_ptr(), self.sin.data_ptr(), self.max_pos, self.head_dim)
+
+
+def qcf_rope_apply(x: torch.Tensor, pos: torch.Tensor, table, interleaved: bool = False, inverse: bool = False,
+                   out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """x [n][H][D] (heads of a row contiguous, any row stride) turned by the angles of pos [n];
+    out=x rotates in place.  Rows at position -1 are left as they were in `out`."""
+    xs = _head_rows(x, "x")
+    n, H, D = x.shape
+    _need_i32(pos, "pos", (n,))
+    if out is None:
+        with torch.cuda.stream(stream):
+            out = torch.empty((n, H, D), dtype=x.dtype, device=x.device)
+        ys = H * D
+    else:
+        if out.shape != x.shape or out.dtype != x.dtype:
+            _bad("out must have the shape and type of x")
+        ys = _head_rows(out, "out")
+    _need_here(x, pos, out, table.cos)
+    if n == 0:   # empty tensors have no address to pass
+        return out
+    call("qcf_rope_apply", x.data_ptr(), xs, out.data_ptr(), ys, n, H, D, _DTYPE[x.dtype], pos.data_ptr(),
+         C.byref(table.struct), (_lib.QCF_ROPE_INTERLEAVED if interleaved else 0) | (_lib.QCF_ROPE_INVERSE if inverse else 0),
+         _stream(stream))
+    return out
+
+
+class PagedKV:
+    """K and V pages of one layer: [n_pages][page_size][Hkv][D] (layout "rows") or
+    [n_pages][Hkv][page_size][D] ("heads"), bf16 or fp16; other strides as given."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, layout: str = "rows"):
+        if layout not in ("rows", "heads"):
+            _bad(f"unknown layout {layout!r}")
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.stride(3) != 1:
+            _bad("k and v must be 4-d tensors of one shape, type and stride, their last dimension contiguous")
+        if k.dtype not in (torch.bfloat16, torch.float16):
+            _bad("the cache holds bf16 or fp16")
+        if not k.is_cuda or k.device != v.device:
+            _bad("k and v must be on one CUDA device")
+        self.k, self.v, self.layout = k, v, layout
+        row, head = (1, 2) if layout == "rows" else (2, 1)
+        n_pages, D = k.shape[0], k.shape[3]
+        self.page_size, self.Hkv, self.D = k.shape[row], k.shape[head], D
+        stride = [s if n > 1 else self.page_size * self.Hkv * D for s, n in zip(k.stride(), k.shape)]
+        self.struct = _lib.PagedKV(k.data_ptr(), v.data_ptr(), _DTYPE[k.dtype], n_pages, self.page_size, self.Hkv, D,
+                                   stride[0], stride[row], stride[head])
+        self.ref = C.byref(self.struct)
+
+
+class PagedBatch:
+    """A batch of sequences over one shared prefix (see qcf_paged_batch).  The tensors are read
+    on the device at each call, so their values may change between calls within the bounds."""
+
+    def __init__(self, row_start: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor, n_rows: int, max_q: int,
+                 max_len: int, prefix_pages: Optional[torch.Tensor] = None, prefix_len: int = 0):
+        n_seq = kv_len.numel()
+        _need_i32(row_start, "row_start", (n_seq + 1,))
+        _need_i32(kv_len, "kv_len", (n_seq,))
+        if page_table.dim() != 2 or page_table.shape[0] != n_seq:
+            _bad("page_table must have one row per sequence")
+        _need_i32(page_table, "page_table")
+        if prefix_pages is not None:
+            _need_i32(prefix_pages, "prefix_pages")
+        self.row_start, self.kv_len, self.page_table, self.prefix_pages = row_start, kv_len, page_table, prefix_pages
+        self.n_rows, self.prefix_len = int(n_rows), int(prefix_len)
+        self.empty = n_seq == 0 or self.n_rows == 0   # nothing to do, and no addresses to pass
+        self.struct = _lib.PagedBatch(n_seq, self.n_rows, int(max_q), int(max_len), row_start.data_ptr(), kv_len.data_ptr(),
+                                      page_table.data_ptr(), page_table.shape[1], self.prefix_len,
+                                      None if prefix_pages is None else prefix_pages.data_ptr())
+        self.ref = C.byref(self.struct)
+
+    def _check(self, cache: PagedKV, *rows: Optional[torch.Tensor]):
+        if self.prefix_len > 0 and (self.prefix_pages is None or self.prefix_pages.numel() * cache.page_size < self.prefix_len):
+            _bad("prefix_pages hold fewer rows than prefix_len")
+        for t in rows:
+            if t is not None and (t.shape[0] != self.n_rows or t.shape[2] != cache.D or t.dtype != cache.k.dtype):
+                _bad(f"rows must be [{self.n_rows}][heads][{cache.D}] of the cache's type")
+        _need_here(cache.k, self.row_start, self.kv_len, self.page_table, self.prefix_pages, *rows)
+
+
+def qcf_paged_append(cache: PagedKV, batch: PagedBatch, k_new: torch.Tensor, v_new: torch.Tensor, table=None,
+                     interleaved: bool = False, q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                     stream=None) -> Optional[torch.Tensor]:
+    """Writes the batch's new keys (rotated when a table is given) and values into their pages;
+    with q, returns the rotated queries (q_out, or a new tensor whose padding rows are unset)."""
+    ks, vs = _head_rows(k_new, "k_new"), _head_rows(v_new, "v_new")
+    if ks != vs or k_new.shape != v_new.shape or k_new.shape[1] != cache.Hkv:
+        _bad("k_new and v_new must have the cache's heads and one row stride")
+    qs = qos = Hq = 0
+    if q is not None:
+        qs, Hq = _head_rows(q, "q"), q.shape[1]
+        if q_out is None:
+            with torch.cuda.stream(stream):
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        qos = _head_rows(q_out, "q_out")
+        if q_out.shape != q.shape:
+            _bad("q_out must have the shape of q")
+    elif q_out is not None:
+        _bad("q_out without q")
+    batch._check(cache, k_new, v_new, q, q_out)
+    if table is not None:
+        _need_here(table.cos)
+    if batch.empty:
+        return q_out
+    call("qcf_paged_append", cache.ref, batch.ref, k_new.data_ptr(), v_new.data_ptr(), ks,
+         None if table is None else C.byref(table.struct), _lib.QCF_ROPE_INTERLEAVED if interleaved else 0,
+         None if q is None else q.data_ptr(), qs, None if q is None else q_out.data_ptr(), qos, Hq, _stream(stream))
+    return q_out
+
+
+def qcf_shared_prefix_attn(cache: PagedKV, batch: PagedBatch, q: torch.Tensor, scale: float, want_lse: bool = False,
+                           out: Optional[torch.Tensor] = None, stream=None):
+    """Attention of the batch's rows q [n_rows][Hq][D] over the shared prefix and their own tokens.
+    Returns out (a new tensor unless given; padding rows are not written), with lse if asked."""
+    qs = _head_rows(q, "q")
+    n, Hq, D = q.shape
+    batch._check(cache, q, out)
+    if out is not None and (out.shape != q.shape or not out.is_contiguous()):
+        _bad("out must be contiguous, of the shape of q")
+    nb = 0 if batch.empty else _lib.lib().qcf_shared_prefix_attn_workspace_size(cache.ref, batch.ref, Hq)
+    with torch.cuda.stream(stream):   # the allocator ties them to the stream that uses them
+        if out is None:
+            out = torch.empty((n, Hq, D), dtype=q.dtype, device=q.device)
+        lse = torch.empty((n, Hq), dtype=torch.float32, device=q.device) if want_lse else None
+        ws = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
+    if not batch.empty:
+        call("qcf_shared_prefix_attn", cache.ref, batch.ref, q.data_ptr(), qs, Hq, float(scale), out.data_ptr(), _ptr(lse),
+             _ptr(ws), nb, _stream(stream))
+    return (out, lse) if want_lse else out
