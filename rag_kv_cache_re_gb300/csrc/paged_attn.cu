@@ -49,7 +49,7 @@ __device__ __forceinline__ uint32_t group_off(int key, int col) {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kOwnWarps * 32, OwnCfg<D>::MIN_CTAS)
-    own_attn_kernel(const PagedView c, const BatchView b, const AttnArgs a, const AttnPlan2 p, const Parts parts,
+    own_attn_kernel(const PagedView c, const BatchView b, const AttnArgs a, const SharedPlan p, const Parts parts,
                     int pre_units, unsigned int* status) {
   using Cfg = OwnCfg<D>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, OwnCfg<D>::MIN_CTAS)
 // its D / 32 output entries of each part.  Parts are added in a fixed order.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) batch_combine_kernel(const PagedView c, const BatchView b, const AttnArgs a,
-                                                            const AttnPlan2 p, const Parts parts) {
+                                                            const SharedPlan p, const Parts parts) {
   constexpr int E = D >= 32 ? D / 32 : 1;
   const int w = static_cast<int>((static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
   const int row = w / a.Hq, h = w - row * a.Hq;
@@ -417,8 +417,8 @@ __global__ void __launch_bounds__(256) batch_combine_kernel(const PagedView c, c
 
 // ------------------------------------------------------------------ host
 
-static AttnPlan2 plan_shared(const PagedView& c, const BatchView& b, int Hq) {
-  AttnPlan2 p = {};
+static SharedPlan plan_shared(const PagedView& c, const BatchView& b, int Hq) {
+  SharedPlan p = {};
   const int G = Hq / c.Hkv, sms = num_sms();
   auto chunks = [&](int64_t units, int len, int* chunk, int* n) {
     // parts of at least 128 keys, enough units to fill every SM four times, and none above 1024
@@ -430,14 +430,25 @@ static AttnPlan2 plan_shared(const PagedView& c, const BatchView& b, int Hq) {
   };
   p.own_row_blocks = std::max(1, (std::min(b.max_q, b.n_rows) * G + kOwnRows - 1) / kOwnRows);
   chunks(static_cast<int64_t>(b.n_seq) * c.Hkv * p.own_row_blocks, std::max(1, b.max_len), &p.own_chunk, &p.own_parts);
-  if (b.prefix_len > 0) {
+  // More than one 16-row MMA tile of score rows per KV head: tcgen05 (one tile has nothing to share,
+  // and the warp-MMA kernel splits its keys over every SM).
+  if (b.prefix_len > 0 && c.D >= 64 && b.n_rows * G > 16) {
+    p.pre_tc = true;
+    p.pre_rows = 2 * (128 / G);
+    p.pre_row_blocks = (b.n_rows + p.pre_rows - 1) / p.pre_rows;
+    p.pre_tiles = (b.prefix_len + 127) / 128;
+    const int64_t total = static_cast<int64_t>(p.pre_row_blocks) * c.Hkv * p.pre_tiles;
+    p.pre_share = static_cast<int>(std::max<int64_t>((total + sms - 1) / sms, std::min(2, p.pre_tiles)));
+    p.pre_ctas = static_cast<int>((total + p.pre_share - 1) / p.pre_share);
+    p.pre_parts = (p.pre_tiles + p.pre_share - 2) / p.pre_share + 1;   // CTAs that one unit can meet
+  } else if (b.prefix_len > 0) {
     p.pre_row_blocks = (b.n_rows * G + kOwnRows - 1) / kOwnRows;
     chunks(static_cast<int64_t>(p.pre_row_blocks) * c.Hkv, b.prefix_len, &p.pre_chunk, &p.pre_parts);
   }
   return p;
 }
 
-size_t parts_bytes(const AttnPlan2& p, const BatchView& b, int Hq, int D) {
+size_t parts_bytes(const SharedPlan& p, const BatchView& b, int Hq, int D) {
   const int n = p.pre_parts + p.own_parts;
   if (n <= 1) return 0;
   const size_t rows = static_cast<size_t>(n) * b.n_rows * Hq;
@@ -445,7 +456,7 @@ size_t parts_bytes(const AttnPlan2& p, const BatchView& b, int Hq, int D) {
 }
 
 template <typename T, int D>
-static qcf_status shared_prefix_attn_launch(const PagedView& c, const BatchView& b, const AttnArgs& a, const AttnPlan2& p,
+static qcf_status shared_prefix_attn_launch(const qcf_paged_kv* cache, const PagedView& c, const BatchView& b, const AttnArgs& a, const SharedPlan& p,
                                             Parts parts, cudaStream_t st) {
   const char* who = "qcf_shared_prefix_attn";
   using Cfg = OwnCfg<D>;
@@ -457,6 +468,10 @@ static qcf_status shared_prefix_attn_launch(const PagedView& c, const BatchView&
   const int64_t pre_units = p.pre_tc ? 0 : static_cast<int64_t>(p.pre_parts) * p.pre_row_blocks * c.Hkv;
   const int64_t units = pre_units + static_cast<int64_t>(b.n_seq) * p.own_row_blocks * p.own_parts * c.Hkv;
   if (units > INT32_MAX) return set_error(QCF_ERR_SHAPE, "%s: %lld units of work are too many for one call", who, (long long)units);
+  if (p.pre_tc) {
+    const qcf_status s = prefix_tc_launch(cache, c, b, a, p, parts, st);
+    if (s != QCF_OK) return s;
+  }
   {
     LaunchScope ls(KC_OWN_ATTN, st);
     own_attn_kernel<T, D><<<static_cast<unsigned>(units), kOwnWarps * 32, Cfg::SMEM, st>>>(
@@ -475,12 +490,12 @@ static qcf_status shared_prefix_attn_launch(const PagedView& c, const BatchView&
 }
 
 template <typename T>
-static qcf_status shared_prefix_attn_type(const PagedView& c, const BatchView& b, const AttnArgs& a, const AttnPlan2& p,
+static qcf_status shared_prefix_attn_type(const qcf_paged_kv* cache, const PagedView& c, const BatchView& b, const AttnArgs& a, const SharedPlan& p,
                                           Parts parts, cudaStream_t st) {
   switch (c.D) {
-    case 16: return shared_prefix_attn_launch<T, 16>(c, b, a, p, parts, st);
-    case 64: return shared_prefix_attn_launch<T, 64>(c, b, a, p, parts, st);
-    default: return shared_prefix_attn_launch<T, 128>(c, b, a, p, parts, st);
+    case 16: return shared_prefix_attn_launch<T, 16>(cache, c, b, a, p, parts, st);
+    case 64: return shared_prefix_attn_launch<T, 64>(cache, c, b, a, p, parts, st);
+    default: return shared_prefix_attn_launch<T, 128>(cache, c, b, a, p, parts, st);
   }
 }
 
@@ -524,7 +539,7 @@ qcf_status qcf_shared_prefix_attn(const qcf_paged_kv* cache, const qcf_paged_bat
   if (take_fault(1)) return set_error(QCF_ERR_INVALID_ARG, "%s: injected invalid index table", who);
   if (take_fault(2)) return set_error(QCF_ERR_WORKSPACE, "%s: injected short workspace", who);
   if (b.n_seq == 0 || b.n_rows == 0) return QCF_OK;
-  const AttnPlan2 p = plan_shared(c, b, Hq);
+  const SharedPlan p = plan_shared(c, b, Hq);
   const size_t need = parts_bytes(p, b, Hq, c.D);
   if (need && (!ws || ws_bytes < need)) return set_error(QCF_ERR_WORKSPACE, "%s: workspace %zu < %zu", who, ws_bytes, need);
   const size_t rows = static_cast<size_t>(p.pre_parts + p.own_parts) * b.n_rows * Hq;
@@ -532,8 +547,8 @@ qcf_status qcf_shared_prefix_attn(const qcf_paged_kv* cache, const qcf_paged_bat
                     reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + align_up(rows * c.D * sizeof(float), 256))};
   const AttnArgs a{q, q_stride, cache->k, cache->v, o, lse, Hq, Hq / c.Hkv, scale * 1.4426950408889634f};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return cache->dtype == QCF_BF16 ? shared_prefix_attn_type<__nv_bfloat16>(c, b, a, p, parts, st)
-                                  : shared_prefix_attn_type<__half>(c, b, a, p, parts, st);
+  return cache->dtype == QCF_BF16 ? shared_prefix_attn_type<__nv_bfloat16>(cache, c, b, a, p, parts, st)
+                                  : shared_prefix_attn_type<__half>(cache, c, b, a, p, parts, st);
 }
 
 }  // extern "C"

@@ -26,7 +26,7 @@ struct Parts {
   float2* ml;
 };
 
-struct AttnPlan2 {
+struct SharedPlan {
   // own tokens: chunks of own_chunk keys (a multiple of the tile), at most own_parts of them
   int own_chunk, own_parts, own_row_blocks;
   // prefix: pre_parts slots per row.  On the warp-MMA kernel a part is a chunk of pre_chunk keys;
@@ -37,11 +37,11 @@ struct AttnPlan2 {
   int pre_rows, pre_tiles, pre_share, pre_ctas;   // tensor-core kernel: rows of q per unit, key tiles
 };
 
-size_t parts_bytes(const AttnPlan2& p, const BatchView& b, int Hq, int D);
+size_t parts_bytes(const SharedPlan& p, const BatchView& b, int Hq, int D);
 
 // The tensor-core kernel of the prefix (prefix_attn.cu): its parts of every row of the batch.
 qcf_status prefix_tc_launch(const qcf_paged_kv* cache, const PagedView& c, const BatchView& b, const AttnArgs& a,
-                            const AttnPlan2& p, Parts parts, cudaStream_t st);
+                            const SharedPlan& p, Parts parts, cudaStream_t st);
 
 // m16n8k16 on warp tensor cores, both 16-bit types, fp32 sums.
 template <typename T>

@@ -1,0 +1,440 @@
+// The shared prefix of a batch on tcgen05 tensor cores (head dims 64 and 128): its K and V are
+// read once for all rows.
+//
+// The score rows of one KV head (rows of the batch x the G query heads that share it) are stacked
+// into units of two 128-row tiles, a and b, which share every K and V tile of 128 keys.  The tiles
+// of all (row block, KV head) units are dealt out evenly: CTA i takes tiles [i share, (i + 1)
+// share) of the whole sequence of units, so the SMs finish together whatever the batch, and a CTA
+// leaves one part for each unit it touched (two or three at most when share is large).
+//
+// Twelve warps:
+//   warp 0      K producer: pages to shared memory by tiled TMA, one box per page and 64 columns,
+//               page ids by lane
+//   warp 2      V producer, the same; rows behind the prefix in its last page are zeroed, since a
+//               free slot may hold NaN and 0 x NaN is NaN
+//   warp 3      Q producer: one unit's two row tiles
+//   warp 1      tensor memory; one thread issues P_x V then S_x = Q_x K^T of the next key tile,
+//               x = a, b in turn, so one tile's products run under the other's softmax
+//   warps 4-7   softmax of a, warps 8-11 of b: thread = score row; maximum, powers of two and sum
+//               in fp32, the weights back to tensor memory over the scores they came from (they
+//               meet V in the cache's 16-bit type, the MMA's), the output rescaled in tensor
+//               memory only when a row's maximum grows by more than 2^8
+// Tensor memory columns: S_a 0, S_b 128 (128 each; the weights take the first 64 of each), O_a
+// 256, O_b 256 + D.  A commit covers every product issued before it, so a full S_x(i + 1) also
+// means that P_x(i) V has been added: no barrier of its own for the output.
+//
+// Bound: HBM below about 285 score rows per KV head, the tensor pipe above.
+#include <algorithm>
+
+#include "paged_attn.cuh"
+
+namespace qcf {
+
+constexpr int kPreKeys = 128;
+constexpr int kPreThreads = 384;
+constexpr int kPreBox = kPreKeys * 128;   // bytes of 64 columns of 128 keys (or score rows)
+
+template <int D>
+struct PreCfg {
+  static constexpr int BOXES = D / 64;
+  static constexpr int TILE = BOXES * kPreBox;               // a K, V or Q tile
+  static constexpr int STAGES = D == 128 ? 2 : 4;            // of K and of V
+  static constexpr int SMEM = 2 * TILE + 2 * STAGES * TILE + 512 + 1024;
+};
+
+__device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+      ::"r"(smem_u32(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+// Instruction descriptor of kind::f16 with both operands of type T (see idesc_bf16_f32).
+template <typename T>
+constexpr uint32_t idesc_16(int M, int N, bool b_mn_major) {
+  return std::is_same<T, __half>::value ? idesc_bf16_f32(M, N, b_mn_major) & ~((1u << 7) | (1u << 10))
+                                        : idesc_bf16_f32(M, N, b_mn_major);
+}
+
+// One CTA's share of one unit.
+struct Segment {
+  int g, row0, nb, t0, nt, part;   // KV head, first row of tile a, row tiles in use, key tiles, part slot
+};
+struct Segments {
+  int cur, end, cta;
+  const SharedPlan& p;
+  int n_rows;
+  __device__ Segments(const SharedPlan& plan, int n_rows_, int total)
+      : cta(static_cast<int>(blockIdx.x)), p(plan), n_rows(n_rows_) {
+    cur = cta * p.pre_share;
+    end = min(total, cur + p.pre_share);
+  }
+  __device__ bool next(Segment& s) {
+    if (cur >= end) return false;
+    const int unit = cur / p.pre_tiles;
+    s.t0 = cur - unit * p.pre_tiles;
+    s.nt = min(p.pre_tiles - s.t0, end - cur);
+    s.g = unit / p.pre_row_blocks;
+    s.row0 = (unit - s.g * p.pre_row_blocks) * p.pre_rows;
+    s.nb = s.row0 + p.pre_rows / 2 < n_rows ? 2 : 1;
+    s.part = cta - unit * p.pre_tiles / p.pre_share;
+    cur += s.nt;
+    return true;
+  }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kPreThreads, 1)
+    prefix_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const __grid_constant__ CUtensorMap tmQ, const PagedView c, const BatchView b, const AttnArgs a,
+                       const SharedPlan p, const Parts parts, int total, unsigned int* status) {
+  using Cfg = PreCfg<D>;
+  constexpr int ST = Cfg::STAGES;
+  constexpr unsigned kAll = 0xffffffffu;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* qbuf = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  uint8_t* kbuf = qbuf + 2 * Cfg::TILE;
+  uint8_t* vbuf = kbuf + ST * Cfg::TILE;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(vbuf + ST * Cfg::TILE);
+  uint64_t* k_empty = k_full + ST;
+  uint64_t* v_full = k_empty + ST;
+  uint64_t* v_empty = v_full + ST;
+  uint64_t* s_full = v_empty + ST;    // [a, b]
+  uint64_t* p_ready = s_full + 2;     // [a, b]
+  uint64_t* o_done = p_ready + 2;     // [a, b]
+  uint64_t* q_full = o_done + 2;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* v_tail = q_empty + 1;
+  uint64_t* mma_end = v_tail + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_end + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_ready[x], 4);
+      mbar_init(&o_done[x], 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(v_tail, 1);
+    mbar_init(mma_end, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Segments segs(p, b.n_rows, total);
+  Segment s;
+
+  if (warp < 4) {
+    // 104 x 128 + 200 x 256 threads: the 168 x 384 registers of the launch
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == 0 || warp == 2) {
+      // ---- K and V producers
+      const bool is_k = warp == 0;
+      const CUtensorMap* map = is_k ? &tmK : &tmV;
+      uint8_t* ring = is_k ? kbuf : vbuf;
+      uint64_t* full = is_k ? k_full : v_full;
+      uint64_t* empty = is_k ? k_empty : v_empty;
+      if (lane == 0) tma_prefetch_desc(map);
+      const int ps = min(1 << c.page_shift, kPreKeys), boxes = kPreKeys / ps;   // rows of a box, pages of a tile
+      // this lane's page of key tile t: its id, n_pages (which reads as zeros) where there is none
+      auto page_of = [&](int t) {
+        const int key = t * kPreKeys + lane * ps;
+        if (lane >= boxes || key >= b.prefix_len) return c.n_pages;
+        const int id = b.prefix_pages[key >> c.page_shift];
+        if (id >= 0 && id < c.n_pages) return id;
+        flag_status(status, QCF_DEV_BAD_INDEX);
+        return c.n_pages;
+      };
+      int n = 0, tails = 0;   // tiles and tail tiles so far
+      bool ok = true;
+      while (ok && segs.next(s)) {
+        int id = page_of(s.t0);
+        for (int i = 0; i < s.nt; ++i, ++n) {
+          const int st = n % ST, t = s.t0 + i;
+          const int next_id = i + 1 < s.nt ? page_of(t + 1) : 0;
+          if (!__all_sync(kAll, mbar_wait(&empty[st], ((n / ST) & 1) ^ 1u))) {
+            ok = false;
+            break;
+          }
+          const int valid = b.prefix_len - t * kPreKeys;   // keys of this tile (at least one)
+          const int stale = valid < kPreKeys ? min(kPreKeys, (valid + ps - 1) / ps * ps) : valid;
+          const bool tail = !is_k && stale > valid;        // a page of the tile ends behind the prefix
+          uint64_t* bar = tail ? v_tail : &full[st];
+          uint8_t* dst = ring + st * Cfg::TILE;
+          if (lane == 0) mbar_arrive_expect_tx(bar, Cfg::TILE);
+          __syncwarp();
+          if (lane < boxes) {
+#pragma unroll
+            for (int h = 0; h < Cfg::BOXES; ++h)
+              tma_load_4d(dst + h * kPreBox + lane * ps * 128, map, bar, h * 64, (t * kPreKeys) & ((1 << c.page_shift) - 1), s.g,
+                          id);
+          }
+          id = next_id;
+          if (tail) {
+            if (!__all_sync(kAll, mbar_wait(v_tail, tails++ & 1))) {
+              ok = false;
+              break;
+            }
+            for (int e = lane; e < (stale - valid) * 8 * Cfg::BOXES; e += 32) {
+              const int h = e / ((stale - valid) * 8), f = e - h * (stale - valid) * 8;
+              *reinterpret_cast<uint4*>(dst + h * kPreBox + valid * 128 + f * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[st]);
+          }
+        }
+      }
+      if (!ok && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
+      // no copy of this warp is in flight when the CTA ends
+      for (int e = max(0, n - ST); e < n; ++e)
+        if (!mbar_wait(&full[e % ST], (e / ST) & 1) && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
+    } else if (warp == 3) {
+      // ---- Q producer: rows (position, head of the group) of both tiles; rows behind the batch are zeros
+      if (lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        const int per = 128 / a.G;
+        int k = 0;
+        bool ok = true;
+        for (; segs.next(s); ++k) {
+          if (!mbar_wait(q_empty, (k & 1) ^ 1u)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(q_full, s.nb * Cfg::BOXES * per * a.G * 128);
+          for (int x = 0; x < s.nb; ++x)
+#pragma unroll
+            for (int h = 0; h < Cfg::BOXES; ++h)
+              tma_load_3d(qbuf + x * Cfg::TILE + h * kPreBox, &tmQ, q_full, h * 64, s.g * a.G, s.row0 + x * per);
+        }
+        if (k > 0 && !mbar_wait(q_full, (k - 1) & 1)) ok = false;
+        if (!ok) flag_status(status, QCF_DEV_TIMEOUT);
+      }
+    } else if (lane == 0) {
+      // ---- MMA issuer
+      constexpr uint32_t idesc_s = idesc_16<T>(128, kPreKeys, false);
+      constexpr uint32_t idesc_o = idesc_16<T>(128, D, true);
+      int n = 0, k = 0;          // key tiles, segments so far
+      uint32_t used[2] = {0, 0}; // weights of a, b taken so far
+      bool ok = true;
+      auto scores = [&](int x, int tile) {   // S_x = Q_x K^T
+        const uint32_t qa = smem_u32(qbuf + x * Cfg::TILE), ka = smem_u32(kbuf + tile % ST * Cfg::TILE);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_f16(tmem + x * 128, sdesc_kmajor_sw128(qa + (kk >> 2) * kPreBox + (kk & 3) * 32),
+                   sdesc_kmajor_sw128(ka + (kk >> 2) * kPreBox + (kk & 3) * 32), idesc_s, kk > 0 ? 1u : 0u);
+        umma_commit(&s_full[x]);
+      };
+      auto wait_k = [&](int tile) { return mbar_wait(&k_full[tile % ST], (tile / ST) & 1); };
+      for (; ok && segs.next(s); ++k) {
+        if (!(ok = mbar_wait(q_full, k & 1) && wait_k(n))) break;
+        tc_fence_after();
+        for (int x = 0; x < s.nb; ++x) scores(x, n);
+        umma_commit(&k_empty[n % ST]);
+        for (int i = 0; i < s.nt && ok; ++i, ++n) {
+          const bool more = i + 1 < s.nt;
+          for (int x = 0; x < s.nb; ++x) {
+            if (!(ok = mbar_wait(&p_ready[x], used[x] & 1))) break;
+            ++used[x];
+            if (x == 0 && !(ok = mbar_wait(&v_full[n % ST], (n / ST) & 1))) break;
+            tc_fence_after();
+            const uint32_t va = smem_u32(vbuf + n % ST * Cfg::TILE);
+#pragma unroll
+            for (int kk = 0; kk < kPreKeys / 16; ++kk)   // O_x += P_x V
+              umma_f16_ts(tmem + 256 + x * D, tmem + x * 128 + kk * 8, sdesc_mnmajor_sw128(va + kk * 2048, kPreBox), idesc_o,
+                          (i > 0 || kk > 0) ? 1u : 0u);
+            if (x == s.nb - 1) umma_commit(&v_empty[n % ST]);
+            if (more) {
+              if (x == 0) {
+                if (!(ok = wait_k(n + 1))) break;
+                tc_fence_after();
+              }
+              scores(x, n + 1);
+              if (x == s.nb - 1) umma_commit(&k_empty[(n + 1) % ST]);
+            } else {
+              umma_commit(&o_done[x]);
+            }
+          }
+        }
+        umma_commit(q_empty);
+      }
+      if (!ok) flag_status(status, QCF_DEV_TIMEOUT);
+      umma_commit(mma_end);   // nothing runs on tensor memory once it is freed
+      if (!mbar_wait(mma_end, 0)) flag_status(status, QCF_DEV_TIMEOUT);
+    }
+  } else {
+    // ---- softmax: thread = score row of tile x
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    const int x = (warp - 4) >> 2, quarter = warp & 3;
+    const int rho = quarter * 32 + lane, per = 128 / a.G, pl = rho / a.G, h = rho - pl * a.G;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_tm = tmem + lane_base + x * 128, o_tm = tmem + lane_base + 256 + x * D;
+    auto page_bad = [&](int t) {   // the page of this lane's 8 keys of tile t lies outside the cache
+      const int key = t * kPreKeys + lane * 8;
+      if (lane >= kPreKeys / 8 || key >= b.prefix_len) return false;
+      const int id = b.prefix_pages[key >> c.page_shift];
+      return id < 0 || id >= c.n_pages;
+    };
+    uint32_t seen = 0, ends = 0;
+    bool ok = true;
+    while (ok && segs.next(s)) {
+      if (x >= s.nb) continue;
+      const int row = s.row0 + x * per + pl;
+      float m = -INFINITY, l = 0.f;
+      bool bad = page_bad(s.t0);
+      for (int i = 0; i < s.nt; ++i) {
+        const int t = s.t0 + i;
+        const unsigned bad8 = __ballot_sync(kAll, bad);
+        bad = i + 1 < s.nt && page_bad(t + 1);
+        if (!__all_sync(kAll, mbar_wait(&s_full[x], seen++ & 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float sv[kPreKeys];
+        tmem_ld64(s_tm, sv);
+        tmem_ld64(s_tm + 64, sv + 64);
+        const int valid = b.prefix_len - t * kPreKeys;
+        if (valid < kPreKeys) {
+#pragma unroll
+          for (int j = 0; j < kPreKeys; ++j)
+            if (j >= valid) sv[j] = -INFINITY;
+        }
+        if (bad8) {
+#pragma unroll
+          for (int j = 0; j < kPreKeys; ++j)
+            if (bad8 >> (j / 8) & 1) sv[j] = -INFINITY;
+        }
+        float mx0 = sv[0], mx1 = sv[1], mx2 = sv[2], mx3 = sv[3];
+#pragma unroll
+        for (int j = 4; j < kPreKeys; j += 4) {
+          mx0 = fmaxf(mx0, sv[j]);
+          mx1 = fmaxf(mx1, sv[j + 1]);
+          mx2 = fmaxf(mx2, sv[j + 2]);
+          mx3 = fmaxf(mx3, sv[j + 3]);
+        }
+        const float top = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * a.scale_log2;
+        const bool grow = top > m + 8.0f;
+        if (__any_sync(kAll, grow)) {
+          const float m_new = grow ? top : m;
+          if (i > 0) {   // the full S of this tile says that every earlier product has been added to O
+            const float f = m == -INFINITY ? 0.f : fast_exp2(m - m_new);
+#pragma unroll 1
+            for (int cc = 0; cc < D / 32; ++cc) {
+              float ov[32];
+              tmem_ld32(o_tm + cc * 32, ov);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] *= f;
+              tmem_st32(o_tm + cc * 32, ov);
+            }
+            l *= f;
+          }
+          m = m_new;
+        }
+        const float nm = m == -INFINITY ? 0.f : -m;
+        float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
+        uint32_t pk[64];
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          const float p0 = fast_exp2(fmaf(sv[2 * e], a.scale_log2, nm));
+          const float p1 = fast_exp2(fmaf(sv[2 * e + 1], a.scale_log2, nm));
+          const float p2 = fast_exp2(fmaf(sv[2 * e + 2], a.scale_log2, nm));
+          const float p3 = fast_exp2(fmaf(sv[2 * e + 3], a.scale_log2, nm));
+          r0 += p0;
+          r1 += p1;
+          r2 += p2;
+          r3 += p3;
+          pk[e] = pack2<T>(p0, p1);
+          pk[e + 1] = pack2<T>(p2, p3);
+        }
+        l += (r0 + r1) + (r2 + r3);
+        tmem_st32u(s_tm, pk);
+        tmem_st32u(s_tm + 32, pk + 32);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[x]);
+      }
+      if (!ok || !__all_sync(kAll, mbar_wait(&o_done[x], ends++ & 1))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const bool mine = pl < per && row < b.n_rows;
+      const int64_t at = (static_cast<int64_t>(s.part) * b.n_rows + (mine ? row : 0)) * a.Hq + s.g * a.G + h;
+#pragma unroll 1
+      for (int cc = 0; cc < D / 32; ++cc) {
+        float ov[32];
+        tmem_ld32(o_tm + cc * 32, ov);
+        if (!mine) continue;
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<float4*>(parts.o + at * D + cc * 32 + e) = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+      }
+      if (mine) parts.ml[at] = make_float2(m, l);
+      tc_fence_before();
+    }
+    if (!ok && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename T, int D>
+static qcf_status prefix_tc_type(const qcf_paged_kv* cache, const PagedView& c, const BatchView& b, const AttnArgs& a,
+                                 const SharedPlan& p, Parts parts, cudaStream_t st) {
+  using Cfg = PreCfg<D>;
+  CUtensorMap tk, tv, tq;
+  const int ps = 1 << c.page_shift;
+  const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(ps), static_cast<uint64_t>(c.Hkv),
+                            static_cast<uint64_t>(c.n_pages)};
+  const uint64_t strides[3] = {static_cast<uint64_t>(c.row_stride) * 2, static_cast<uint64_t>(c.head_stride) * 2,
+                               static_cast<uint64_t>(c.page_stride) * 2};
+  const uint32_t box[4] = {64, static_cast<uint32_t>(std::min(ps, kPreKeys)), 1, 1};
+  const uint64_t qd[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(b.n_rows)};
+  const uint64_t qs[2] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(a.q_stride) * 2};
+  const uint32_t qb[3] = {64, static_cast<uint32_t>(a.G), static_cast<uint32_t>(128 / a.G)};
+  if (!encode_tmap_4d(&tk, cache->k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tmap_4d(&tv, cache->v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tmap_3d(&tq, a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B))
+    return set_error(QCF_ERR_CUDA, "qcf_shared_prefix_attn: tensor map encoding failed");
+  static PerDevice<cudaError_t> smem_attr;
+  const cudaError_t attr = smem_attr.get(current_device(), [] {
+    return cudaFuncSetAttribute(prefix_attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+  });
+  if (attr != cudaSuccess) return cuda_error(attr, "qcf_shared_prefix_attn: smem attribute");
+  LaunchScope ls(KC_PREFIX_ATTN, st);
+  const int total = p.pre_tiles * p.pre_row_blocks * c.Hkv;
+  prefix_attn_kernel<T, D><<<p.pre_ctas, kPreThreads, Cfg::SMEM, st>>>(tk, tv, tq, c, b, a, p, parts, total, device_status_ptr());
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? QCF_OK : cuda_error(e, "qcf_shared_prefix_attn: prefix launch");
+}
+
+qcf_status prefix_tc_launch(const qcf_paged_kv* cache, const PagedView& c, const BatchView& b, const AttnArgs& a,
+                            const SharedPlan& p, Parts parts, cudaStream_t st) {
+  if (cache->dtype == QCF_BF16)
+    return c.D == 128 ? prefix_tc_type<__nv_bfloat16, 128>(cache, c, b, a, p, parts, st)
+                      : prefix_tc_type<__nv_bfloat16, 64>(cache, c, b, a, p, parts, st);
+  return c.D == 128 ? prefix_tc_type<__half, 128>(cache, c, b, a, p, parts, st)
+                    : prefix_tc_type<__half, 64>(cache, c, b, a, p, parts, st);
+}
+
+}  // namespace qcf

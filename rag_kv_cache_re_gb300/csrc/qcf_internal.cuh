@@ -54,6 +54,11 @@ bool encode_tmap_3d(CUtensorMap* map, const void* base, const uint64_t dims[3], 
                     const uint32_t box[3], CUtensorMapSwizzle swizzle,
                     CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 
+// Rank-4 tiled map, dims innermost first, strides of dims 1 to 3 in bytes.
+bool encode_tmap_4d(CUtensorMap* map, const void* base, const uint64_t dims[4], const uint64_t strides_bytes[3],
+                    const uint32_t box[4], CUtensorMapSwizzle swizzle,
+                    CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // Device SM count (cached per device).
