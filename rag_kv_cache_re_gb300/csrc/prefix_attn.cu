@@ -9,12 +9,14 @@
 //
 // Twelve warps:
 //   warp 0      K producer: pages to shared memory by tiled TMA, one box per page and 64 columns,
-//               page ids by lane
+//               page ids by lane; also Q, both row tiles of a unit
 //   warp 2      V producer, the same; rows behind the prefix in its last page are zeroed, since a
 //               free slot may hold NaN and 0 x NaN is NaN
-//   warp 3      Q producer: one unit's two row tiles
-//   warp 1      tensor memory; one thread issues P_x V then S_x = Q_x K^T of the next key tile,
-//               x = a, b in turn, so one tile's products run under the other's softmax
+//   warps 1, 3  one thread each issues the products of row tile x = a, b: P_x V, then S_x = Q_x K^T
+//               of the next key tile, while the other tile is in its softmax.  A thread spends
+//               about 72 cycles on a 64-cycle product and 60 to 160 on each barrier, so one thread
+//               for both tiles was slower than the tensor pipe.  The two take turns: left free,
+//               their products mix, both tiles finish together and then both wait for their softmax
 //   warps 4-7   softmax of a, warps 8-11 of b: thread = score row; maximum, powers of two and sum
 //               in fp32, the weights back to tensor memory over the scores they came from (they
 //               meet V in the cache's 16-bit type, the MMA's), the output rescaled in tensor
@@ -101,31 +103,32 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   uint64_t* v_full = k_empty + ST;
   uint64_t* v_empty = v_full + ST;
   uint64_t* s_full = v_empty + ST;    // [a, b]
-  uint64_t* p_ready = s_full + 2;     // [a, b]
-  uint64_t* o_done = p_ready + 2;     // [a, b]
+  uint64_t* p_ready = s_full + 2;     // [a, b][first, last 64 keys]
+  uint64_t* o_done = p_ready + 4;     // [a, b]
   uint64_t* q_full = o_done + 2;
   uint64_t* q_empty = q_full + 1;
   uint64_t* v_tail = q_empty + 1;
-  uint64_t* mma_end = v_tail + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_end + 1);
+  uint64_t* mma_end = v_tail + 1;     // [a, b]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_end + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
       mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], 1);
+      mbar_init(&k_empty[s], 2);
       mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], 1);
+      mbar_init(&v_empty[s], 2);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
-      mbar_init(&p_ready[x], 4);
+      mbar_init(&p_ready[2 * x], 5);
+      mbar_init(&p_ready[2 * x + 1], 4);
       mbar_init(&o_done[x], 1);
+      mbar_init(&mma_end[x], 1);
     }
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, 2);
     mbar_init(v_tail, 1);
-    mbar_init(mma_end, 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -149,7 +152,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       uint8_t* ring = is_k ? kbuf : vbuf;
       uint64_t* full = is_k ? k_full : v_full;
       uint64_t* empty = is_k ? k_empty : v_empty;
-      if (lane == 0) tma_prefetch_desc(map);
+      if (lane == 0) {
+        tma_prefetch_desc(map);
+        if (is_k) tma_prefetch_desc(&tmQ);
+      }
       const int ps = min(1 << c.page_shift, kPreKeys), boxes = kPreKeys / ps;   // rows of a box, pages of a tile
       // this lane's page of key tile t: its id, n_pages (which reads as zeros) where there is none
       auto page_of = [&](int t) {
@@ -160,7 +166,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         flag_status(status, QCF_DEV_BAD_INDEX);
         return c.n_pages;
       };
-      int n = 0, tails = 0;   // tiles and tail tiles so far
+      int n = 0, tails = 0, k = 0;   // tiles, tail tiles, units of Q so far
       bool ok = true;
       while (ok && segs.next(s)) {
         int id = page_of(s.t0);
@@ -185,6 +191,18 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                           id);
           }
           id = next_id;
+          if (is_k && i == 0) {   // the unit's Q; rows behind the batch are zeros
+            if (!__all_sync(kAll, mbar_wait(q_empty, (k & 1) ^ 1u))) {
+              ok = false;
+              break;
+            }
+            const int per = 128 / a.G;
+            if (lane == 0) mbar_arrive_expect_tx(q_full, s.nb * Cfg::BOXES * per * a.G * 128);
+            __syncwarp();
+            if (lane < s.nb * Cfg::BOXES)
+              tma_load_3d(qbuf + lane * kPreBox, &tmQ, q_full, lane % Cfg::BOXES * 64, s.g * a.G, s.row0 + lane / Cfg::BOXES * per);
+            ++k;
+          }
           if (tail) {
             if (!__all_sync(kAll, mbar_wait(v_tail, tails++ & 1))) {
               ok = false;
@@ -204,78 +222,83 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       // no copy of this warp is in flight when the CTA ends
       for (int e = max(0, n - ST); e < n; ++e)
         if (!mbar_wait(&full[e % ST], (e / ST) & 1) && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
-    } else if (warp == 3) {
-      // ---- Q producer: rows (position, head of the group) of both tiles; rows behind the batch are zeros
-      if (lane == 0) {
-        tma_prefetch_desc(&tmQ);
-        const int per = 128 / a.G;
-        int k = 0;
-        bool ok = true;
-        for (; segs.next(s); ++k) {
-          if (!mbar_wait(q_empty, (k & 1) ^ 1u)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(q_full, s.nb * Cfg::BOXES * per * a.G * 128);
-          for (int x = 0; x < s.nb; ++x)
-#pragma unroll
-            for (int h = 0; h < Cfg::BOXES; ++h)
-              tma_load_3d(qbuf + x * Cfg::TILE + h * kPreBox, &tmQ, q_full, h * 64, s.g * a.G, s.row0 + x * per);
-        }
-        if (k > 0 && !mbar_wait(q_full, (k - 1) & 1)) ok = false;
-        if (!ok) flag_status(status, QCF_DEV_TIMEOUT);
-      }
+      if (k > 0 && !mbar_wait(q_full, (k - 1) & 1) && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
     } else if (lane == 0) {
-      // ---- MMA issuer
+      // ---- MMA issuer of row tile x
+      const int x = warp >> 1;
       constexpr uint32_t idesc_s = idesc_16<T>(128, kPreKeys, false);
       constexpr uint32_t idesc_o = idesc_16<T>(128, D, true);
-      int n = 0, k = 0;          // key tiles, segments so far
-      uint32_t used[2] = {0, 0}; // weights of a, b taken so far
+      int n = 0, k = 0;    // key tiles, segments so far
+      uint32_t used = 0;   // weight tiles taken so far
       bool ok = true;
-      auto scores = [&](int x, int tile) {   // S_x = Q_x K^T
-        const uint32_t qa = smem_u32(qbuf + x * Cfg::TILE), ka = smem_u32(kbuf + tile % ST * Cfg::TILE);
+      // a descriptor's low 14 bits are the address in 16-byte units: steps inside a tile are added to it
+      const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(qbuf + x * Cfg::TILE));
+      const uint64_t k_desc = sdesc_kmajor_sw128(smem_u32(kbuf)), v_desc = sdesc_mnmajor_sw128(smem_u32(vbuf), kPreBox);
+      // The turn: the barrier of a tile's first weights also counts one arrival of the other
+      // issuer, made four products (256 cycles) before the end of its block, which covers what
+      // this thread then takes to see it.
+      auto pass = [&](bool due) {
+        if (due) mbar_arrive(&p_ready[2 * (1 - x)]);
+      };
+      auto scores = [&](int tile, bool due) {   // S_x = Q_x K^T
+        const uint64_t kd = k_desc + tile % ST * (Cfg::TILE >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_f16(tmem + x * 128, sdesc_kmajor_sw128(qa + (kk >> 2) * kPreBox + (kk & 3) * 32),
-                   sdesc_kmajor_sw128(ka + (kk >> 2) * kPreBox + (kk & 3) * 32), idesc_s, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          if (kk == D / 16 - 4) pass(due);
+          const uint64_t at = ((kk >> 2) * kPreBox + (kk & 3) * 32) >> 4;
+          umma_f16(tmem + x * 128, q_desc + at, kd + at, idesc_s, kk > 0 ? 1u : 0u);
+        }
         umma_commit(&s_full[x]);
+        umma_commit(&k_empty[tile % ST]);
       };
       auto wait_k = [&](int tile) { return mbar_wait(&k_full[tile % ST], (tile / ST) & 1); };
       for (; ok && segs.next(s); ++k) {
+        if (x >= s.nb) {   // nothing in tile b: hand on what it would have read (every phase of a barrier is waited for)
+          if (!(ok = mbar_wait(q_full, k & 1))) break;
+          mbar_arrive(q_empty);
+          for (int i = 0; i < s.nt; ++i, ++n) {
+            if (!(ok = wait_k(n))) break;
+            mbar_arrive(&k_empty[n % ST]);
+            if (!(ok = mbar_wait(&v_full[n % ST], (n / ST) & 1))) break;
+            mbar_arrive(&v_empty[n % ST]);
+          }
+          continue;
+        }
         if (!(ok = mbar_wait(q_full, k & 1) && wait_k(n))) break;
         tc_fence_after();
-        for (int x = 0; x < s.nb; ++x) scores(x, n);
-        umma_commit(&k_empty[n % ST]);
-        for (int i = 0; i < s.nt && ok; ++i, ++n) {
+        scores(n, false);
+        for (int i = 0; i < s.nt; ++i, ++n) {
           const bool more = i + 1 < s.nt;
-          for (int x = 0; x < s.nb; ++x) {
-            if (!(ok = mbar_wait(&p_ready[x], used[x] & 1))) break;
-            ++used[x];
-            if (x == 0 && !(ok = mbar_wait(&v_full[n % ST], (n / ST) & 1))) break;
+          if (!(ok = mbar_wait(&v_full[n % ST], (n / ST) & 1) && (!more || wait_k(n + 1)))) break;
+          const uint64_t vd = v_desc + n % ST * (Cfg::TILE >> 4);
+          auto weigh = [&](int half) {   // O_x += P_x V over 64 keys
             tc_fence_after();
-            const uint32_t va = smem_u32(vbuf + n % ST * Cfg::TILE);
 #pragma unroll
-            for (int kk = 0; kk < kPreKeys / 16; ++kk)   // O_x += P_x V
-              umma_f16_ts(tmem + 256 + x * D, tmem + x * 128 + kk * 8, sdesc_mnmajor_sw128(va + kk * 2048, kPreBox), idesc_o,
+            for (int kk = half * (kPreKeys / 32); kk < (half + 1) * (kPreKeys / 32); ++kk)
+              umma_f16_ts(tmem + 256 + x * D, tmem + x * 128 + kk * 8, vd + kk * (2048 >> 4), idesc_o,
                           (i > 0 || kk > 0) ? 1u : 0u);
-            if (x == s.nb - 1) umma_commit(&v_empty[n % ST]);
-            if (more) {
-              if (x == 0) {
-                if (!(ok = wait_k(n + 1))) break;
-                tc_fence_after();
-              }
-              scores(x, n + 1);
-              if (x == s.nb - 1) umma_commit(&k_empty[(n + 1) % ST]);
-            } else {
-              umma_commit(&o_done[x]);
-            }
+          };
+          // a alone, or first of the unit, gives itself the turn; b's last block passes none
+          if (x == 0 && (s.nb == 1 || i == 0)) mbar_arrive(&p_ready[0]);
+          const bool due = s.nb == 2 && (x == 0 || more);
+          if (!(ok = mbar_wait(&p_ready[2 * x], used & 1))) break;
+          weigh(0);
+          if (!(ok = mbar_wait(&p_ready[2 * x + 1], used & 1))) break;
+          weigh(1);
+          ++used;
+          if (more) {
+            scores(n + 1, due);
+          } else {
+            pass(due);
+            umma_commit(&o_done[x]);
           }
+          umma_commit(&v_empty[n % ST]);   // after the scores: a commit costs this thread more than a product
         }
         umma_commit(q_empty);
       }
       if (!ok) flag_status(status, QCF_DEV_TIMEOUT);
-      umma_commit(mma_end);   // nothing runs on tensor memory once it is freed
-      if (!mbar_wait(mma_end, 0)) flag_status(status, QCF_DEV_TIMEOUT);
+      umma_commit(&mma_end[x]);   // nothing runs on tensor memory once it is freed
+      if (!mbar_wait(&mma_end[x], 0)) flag_status(status, QCF_DEV_TIMEOUT);
     }
   } else {
     // ---- softmax: thread = score row of tile x
@@ -307,8 +330,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
         tc_fence_after();
         float sv[kPreKeys];
-        tmem_ld64(s_tm, sv);
-        tmem_ld64(s_tm + 64, sv + 64);
+        tmem_ld128(s_tm, sv);
         const int valid = b.prefix_len - t * kPreKeys;
         if (valid < kPreKeys) {
 #pragma unroll
@@ -320,15 +342,37 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           for (int j = 0; j < kPreKeys; ++j)
             if (bad8 >> (j / 8) & 1) sv[j] = -INFINITY;
         }
-        float mx0 = sv[0], mx1 = sv[1], mx2 = sv[2], mx3 = sv[3];
+        // 64 weights from the logits; they leave in two halves, so that P V of the first 64 keys runs
+        // under the powers of the others
+        const Pair scale2 = make_pair2(a.scale_log2, a.scale_log2);
+        Pair sum[2];
+        uint32_t pk[32];
+        auto weights = [&](int half, float base) {
+          const Pair nm2 = make_pair2(-base, -base);
 #pragma unroll
-        for (int j = 4; j < kPreKeys; j += 4) {
-          mx0 = fmaxf(mx0, sv[j]);
-          mx1 = fmaxf(mx1, sv[j + 1]);
-          mx2 = fmaxf(mx2, sv[j + 2]);
-          mx3 = fmaxf(mx3, sv[j + 3]);
-        }
-        const float top = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * a.scale_log2;
+          for (int e = 0; e < 32; ++e) {
+            const int j = half * 64 + 2 * e;
+            float p0, p1;
+            split(fma2(make_pair2(sv[j], sv[j + 1]), scale2, nm2), p0, p1);
+            p0 = fast_exp2(p0);
+            p1 = fast_exp2(p1);
+            sum[e & 1] = add2(sum[e & 1], make_pair2(p0, p1));
+            pk[e] = pack2<T>(p0, p1);
+          }
+        };
+        // The first half is weighed with the maximum so far, the tile's own found meanwhile (the
+        // special-function unit paces the powers, the comparisons fill its gaps): the maximum
+        // moves only by more than 2^8, so after a unit's first tiles it nearly always stands.
+        sum[0] = sum[1] = make_pair2(0.f, 0.f);
+        weights(0, m == -INFINITY ? 0.f : m);
+        float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+        for (int j = 4; j < kPreKeys - 4; j += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], sv[j + e], sv[j + 4 + e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], sv[kPreKeys - 4 + e]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
         const bool grow = top > m + 8.0f;
         if (__any_sync(kAll, grow)) {
           const float m_new = grow ? top : m;
@@ -345,29 +389,20 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             l *= f;
           }
           m = m_new;
+          sum[0] = sum[1] = make_pair2(0.f, 0.f);
+          weights(0, m == -INFINITY ? 0.f : m);
         }
-        const float nm = m == -INFINITY ? 0.f : -m;
-        float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
-        uint32_t pk[64];
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-          const float p0 = fast_exp2(fmaf(sv[2 * e], a.scale_log2, nm));
-          const float p1 = fast_exp2(fmaf(sv[2 * e + 1], a.scale_log2, nm));
-          const float p2 = fast_exp2(fmaf(sv[2 * e + 2], a.scale_log2, nm));
-          const float p3 = fast_exp2(fmaf(sv[2 * e + 3], a.scale_log2, nm));
-          r0 += p0;
-          r1 += p1;
-          r2 += p2;
-          r3 += p3;
-          pk[e] = pack2<T>(p0, p1);
-          pk[e + 1] = pack2<T>(p2, p3);
+        for (int half = 0; half < 2; ++half) {
+          if (half == 1) weights(1, m == -INFINITY ? 0.f : m);
+          tmem_st32u(s_tm + half * 32, pk);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_ready[2 * x + half]);
         }
-        l += (r0 + r1) + (r2 + r3);
-        tmem_st32u(s_tm, pk);
-        tmem_st32u(s_tm + 32, pk + 32);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_ready[x]);
+        float l0, l1;
+        split(add2(sum[0], sum[1]), l0, l1);
+        l += l0 + l1;
       }
       if (!ok || !__all_sync(kAll, mbar_wait(&o_done[x], ends++ & 1))) {
         ok = false;
