@@ -132,6 +132,7 @@ class RopeTable:
         self.sin = sin_h.to(device, non_blocking=False)
         self.max_pos, self.head_dim = int(max_pos), int(head_dim)
         self.struct = _lib.RopeTable(self.cos.data_ptr(), self.sin.data_ptr(), self.max_pos, self.head_dim)
+        self.ref, self.dev = C.byref(self.struct), self.cos.get_device()
 
 
 # ------------------------------------------------------------------ steps
@@ -326,6 +327,9 @@ def qcf_batch_workspace_size(model, reqs) -> int:
 
 
 # ------------------------------------------------------------------ going on from a shared context
+#
+# These calls run once per layer and decode step, where the host's time counts: everything that
+# does not change from call to call is checked and marshalled when its object is made.
 
 _DTYPE = {torch.bfloat16: _lib.QCF_BF16, torch.float16: _lib.QCF_F16, torch.float32: _lib.QCF_F32}
 
@@ -334,12 +338,24 @@ def _bad(message: str):
     raise QcfError("binding", 1, message)
 
 
-def _need_here(*ts: Optional[torch.Tensor]):
-    """Every tensor on the current CUDA device: kernels launch there."""
-    dev = torch.cuda.current_device()
-    for t in ts:
-        if t is not None and t.get_device() != dev:
-            _bad("tensors must be on the current CUDA device")
+def _here(t: torch.Tensor) -> int:
+    """The device of t, which must be the current one: kernels launch there."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        _bad("tensors must be on the current CUDA device")
+    return dev
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _empty(shape, dtype, dev: int, stream) -> torch.Tensor:
+    """A new tensor, tied by the allocator to the stream that will use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _need_i32(t: torch.Tensor, what: str, shape=None):
@@ -347,15 +363,15 @@ def _need_i32(t: torch.Tensor, what: str, shape=None):
         _bad(f"{what} must be a contiguous int32 tensor" + (f" of shape {shape}" if shape is not None else ""))
 
 
-def _head_rows(t: torch.Tensor, what: str) -> int:
-    """The row stride of a [n][H][D] tensor whose rows hold their heads side by side."""
+def _head_rows(t: torch.Tensor, what: str):
+    """(n, H, D, row stride) of a tensor [n][H][D] whose rows hold their heads side by side."""
     if t.dim() != 3 or t.dtype not in _DTYPE:
         _bad(f"{what} must be a bf16, fp16 or fp32 tensor [n][H][D]")
     n, H, D = t.shape
-    s = t.stride()
-    if (D > 1 and s[2] != 1) or (H > 1 and s[1] != D):
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and D > 1) or (s1 != D and H > 1):
         _bad(f"{what}: the heads of a row must be contiguous")
-    return s[0] if n > 1 else H * D
+    return n, H, D, s0 if n > 1 else H * D
 
 
 class RopeScaling:
@@ -369,18 +385,23 @@ class RopeScaling:
             _bad(f"unknown scaling {kind!r}")
         self.struct = _lib.RopeScaling(_lib.QCF_ROPE_SCALE[kind], int(original), float(factor), float(low), float(high),
                                        float(amplitude))
+        self.ref = C.byref(self.struct)
 
 
 def qcf_rope_table_fill(cos: torch.Tensor, sin: torch.Tensor, theta: float, first_pos: int = 0,
                         scaling: Optional[RopeScaling] = None, stream=None) -> None:
     """Fills fp32 device tables [n_pos][R/2] for positions first_pos, first_pos + 1, ..."""
-    _need_cuda(cos, sin)
-    _need_here(cos, sin)
-    if cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.shape != sin.shape or cos.dim() != 2:
-        _bad("cos and sin must be fp32 tensors of one shape [n_pos][R/2]")
+    if (cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.dim() != 2 or cos.shape != sin.shape
+            or not cos.is_contiguous() or not sin.is_contiguous()):
+        _bad("cos and sin must be contiguous fp32 tensors of one shape [n_pos][R/2]")
+    dev = _here(cos)
+    if sin.get_device() != dev:
+        _bad("tensors must be on the current CUDA device")
     n, half = cos.shape
-    call("qcf_rope_table_fill", cos.data_ptr(), sin.data_ptr(), int(first_pos), n, 2 * half, float(theta),
-         None if scaling is None else C.byref(scaling.struct), _stream(stream))
+    if n == 0:   # empty tensors have no address to pass
+        return
+    call("qcf_rope_table_fill", cos.data_ptr(), sin.data_ptr(), first_pos, n, 2 * half, theta,
+         None if scaling is None else scaling.ref, _raw_stream(stream, dev))
 
 
 class ScaledRopeTable:
@@ -393,29 +414,31 @@ class ScaledRopeTable:
             self.sin = torch.empty_like(self.cos)
         qcf_rope_table_fill(self.cos, self.sin, theta, 0, scaling, stream)
         self.struct = _lib.RopeTable(self.cos.data_ptr(), self.sin.data_ptr(), self.max_pos, self.head_dim)
+        self.ref, self.dev = C.byref(self.struct), self.cos.get_device()
 
 
 def qcf_rope_apply(x: torch.Tensor, pos: torch.Tensor, table, interleaved: bool = False, inverse: bool = False,
                    out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """x [n][H][D] (heads of a row contiguous, any row stride) turned by the angles of pos [n];
     out=x rotates in place.  Rows at position -1 are left as they were in `out`."""
-    xs = _head_rows(x, "x")
-    n, H, D = x.shape
-    _need_i32(pos, "pos", (n,))
+    n, H, D, xs = _head_rows(x, "x")
+    dev = _here(x)
+    if pos.dtype != torch.int32 or pos.dim() != 1 or pos.numel() != n or not pos.is_contiguous():
+        _bad(f"pos must be a contiguous int32 tensor of {n} entries")
+    if pos.get_device() != dev or table.dev != dev:
+        _bad("tensors must be on the current CUDA device")
     if out is None:
-        with torch.cuda.stream(stream):
-            out = torch.empty((n, H, D), dtype=x.dtype, device=x.device)
-        ys = H * D
+        out, ys = _empty((n, H, D), x.dtype, dev, stream), H * D
+    elif out is x:
+        ys = xs
     else:
-        if out.shape != x.shape or out.dtype != x.dtype:
-            _bad("out must have the shape and type of x")
-        ys = _head_rows(out, "out")
-    _need_here(x, pos, out, table.cos)
-    if n == 0:   # empty tensors have no address to pass
-        return out
-    call("qcf_rope_apply", x.data_ptr(), xs, out.data_ptr(), ys, n, H, D, _DTYPE[x.dtype], pos.data_ptr(),
-         C.byref(table.struct), (_lib.QCF_ROPE_INTERLEAVED if interleaved else 0) | (_lib.QCF_ROPE_INVERSE if inverse else 0),
-         _stream(stream))
+        if out.shape != x.shape or out.dtype != x.dtype or out.get_device() != dev:
+            _bad("out must have the shape, type and device of x")
+        ys = _head_rows(out, "out")[3]
+    if n:   # empty tensors have no address to pass
+        call("qcf_rope_apply", x.data_ptr(), xs, out.data_ptr(), ys, n, H, D, _DTYPE[x.dtype], pos.data_ptr(), table.ref,
+             (_lib.QCF_ROPE_INTERLEAVED if interleaved else 0) | (_lib.QCF_ROPE_INVERSE if inverse else 0),
+             _raw_stream(stream, dev))
     return out
 
 
@@ -432,10 +455,11 @@ class PagedKV:
             _bad("the cache holds bf16 or fp16")
         if not k.is_cuda or k.device != v.device:
             _bad("k and v must be on one CUDA device")
-        self.k, self.v, self.layout = k, v, layout
+        self.k, self.v, self.layout, self.dtype, self.dev = k, v, layout, k.dtype, k.get_device()
         row, head = (1, 2) if layout == "rows" else (2, 1)
         n_pages, D = k.shape[0], k.shape[3]
         self.page_size, self.Hkv, self.D = k.shape[row], k.shape[head], D
+        # a dimension of one entry has no stride of its own
         stride = [s if n > 1 else self.page_size * self.Hkv * D for s, n in zip(k.stride(), k.shape)]
         self.struct = _lib.PagedKV(k.data_ptr(), v.data_ptr(), _DTYPE[k.dtype], n_pages, self.page_size, self.Hkv, D,
                                    stride[0], stride[row], stride[head])
@@ -457,20 +481,41 @@ class PagedBatch:
         if prefix_pages is not None:
             _need_i32(prefix_pages, "prefix_pages")
         self.row_start, self.kv_len, self.page_table, self.prefix_pages = row_start, kv_len, page_table, prefix_pages
+        self.dev = row_start.get_device()
+        if any(t is not None and t.get_device() != self.dev for t in (kv_len, page_table, prefix_pages)):
+            _bad("row_start, kv_len, page_table and prefix_pages must be on one device")
         self.n_rows, self.prefix_len = int(n_rows), int(prefix_len)
         self.empty = n_seq == 0 or self.n_rows == 0   # nothing to do, and no addresses to pass
         self.struct = _lib.PagedBatch(n_seq, self.n_rows, int(max_q), int(max_len), row_start.data_ptr(), kv_len.data_ptr(),
                                       page_table.data_ptr(), page_table.shape[1], self.prefix_len,
                                       None if prefix_pages is None else prefix_pages.data_ptr())
         self.ref = C.byref(self.struct)
+        self._prefix_rows = 0 if prefix_pages is None else prefix_pages.numel()
+        self._ws_bytes: Dict[Tuple[int, int, int, int], int] = {}
 
-    def _check(self, cache: PagedKV, *rows: Optional[torch.Tensor]):
-        if self.prefix_len > 0 and (self.prefix_pages is None or self.prefix_pages.numel() * cache.page_size < self.prefix_len):
-            _bad("prefix_pages hold fewer rows than prefix_len")
-        for t in rows:
-            if t is not None and (t.shape[0] != self.n_rows or t.shape[2] != cache.D or t.dtype != cache.k.dtype):
-                _bad(f"rows must be [{self.n_rows}][heads][{cache.D}] of the cache's type")
-        _need_here(cache.k, self.row_start, self.kv_len, self.page_table, self.prefix_pages, *rows)
+    def workspace_size(self, cache: PagedKV, Hq: int) -> int:
+        """qcf_shared_prefix_attn_workspace_size: a function of the layout and the bounds alone."""
+        key = (cache.page_size, cache.Hkv, cache.D, Hq)
+        nb = self._ws_bytes.get(key)
+        if nb is None:
+            nb = 0 if self.empty else _lib.lib().qcf_shared_prefix_attn_workspace_size(cache.ref, self.ref, Hq)
+            self._ws_bytes[key] = nb
+        return nb
+
+
+def _batch_rows(cache: PagedKV, batch: PagedBatch, t: torch.Tensor, what: str):
+    """(H, row stride) of a tensor that holds the batch's rows in the cache's type and head dim."""
+    n, H, D, s = _head_rows(t, what)
+    if n != batch.n_rows or D != cache.D or t.dtype != cache.dtype or t.get_device() != cache.dev:
+        _bad(f"{what} must be [{batch.n_rows}][heads][{cache.D}] of the cache's type and device")
+    return H, s
+
+
+def _cache_and_batch(cache: PagedKV, batch: PagedBatch):
+    if cache.dev != torch.cuda.current_device() or batch.dev != cache.dev:
+        _bad("tensors must be on the current CUDA device")
+    if batch._prefix_rows * cache.page_size < batch.prefix_len:
+        _bad("prefix_pages hold fewer rows than prefix_len")
 
 
 def qcf_paged_append(cache: PagedKV, batch: PagedBatch, k_new: torch.Tensor, v_new: torch.Tensor, table=None,
@@ -478,28 +523,31 @@ def qcf_paged_append(cache: PagedKV, batch: PagedBatch, k_new: torch.Tensor, v_n
                      stream=None) -> Optional[torch.Tensor]:
     """Writes the batch's new keys (rotated when a table is given) and values into their pages;
     with q, returns the rotated queries (q_out, or a new tensor whose padding rows are unset)."""
-    ks, vs = _head_rows(k_new, "k_new"), _head_rows(v_new, "v_new")
-    if ks != vs or k_new.shape != v_new.shape or k_new.shape[1] != cache.Hkv:
+    _cache_and_batch(cache, batch)
+    (Hk, ks), (Hv, vs) = _batch_rows(cache, batch, k_new, "k_new"), _batch_rows(cache, batch, v_new, "v_new")
+    if ks != vs or Hk != Hv or Hk != cache.Hkv:
         _bad("k_new and v_new must have the cache's heads and one row stride")
+    if table is not None and table.dev != cache.dev:
+        _bad("tensors must be on the current CUDA device")
+    qp = qop = None
     qs = qos = Hq = 0
     if q is not None:
-        qs, Hq = _head_rows(q, "q"), q.shape[1]
+        Hq, qs = _batch_rows(cache, batch, q, "q")
         if q_out is None:
-            with torch.cuda.stream(stream):
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        qos = _head_rows(q_out, "q_out")
-        if q_out.shape != q.shape:
-            _bad("q_out must have the shape of q")
+            q_out, qos = _empty(q.shape, q.dtype, cache.dev, stream), Hq * cache.D
+        elif q_out is q:
+            qos = qs
+        else:
+            Ho, qos = _batch_rows(cache, batch, q_out, "q_out")
+            if Ho != Hq:
+                _bad("q_out must have the heads of q")
+        qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         _bad("q_out without q")
-    batch._check(cache, k_new, v_new, q, q_out)
-    if table is not None:
-        _need_here(table.cos)
-    if batch.empty:
-        return q_out
-    call("qcf_paged_append", cache.ref, batch.ref, k_new.data_ptr(), v_new.data_ptr(), ks,
-         None if table is None else C.byref(table.struct), _lib.QCF_ROPE_INTERLEAVED if interleaved else 0,
-         None if q is None else q.data_ptr(), qs, None if q is None else q_out.data_ptr(), qos, Hq, _stream(stream))
+    if not batch.empty:
+        call("qcf_paged_append", cache.ref, batch.ref, k_new.data_ptr(), v_new.data_ptr(), ks,
+             None if table is None else table.ref, _lib.QCF_ROPE_INTERLEAVED if interleaved else 0, qp, qs, qop, qos, Hq,
+             _raw_stream(stream, cache.dev))
     return q_out
 
 
@@ -507,18 +555,16 @@ def qcf_shared_prefix_attn(cache: PagedKV, batch: PagedBatch, q: torch.Tensor, s
                            out: Optional[torch.Tensor] = None, stream=None):
     """Attention of the batch's rows q [n_rows][Hq][D] over the shared prefix and their own tokens.
     Returns out (a new tensor unless given; padding rows are not written), with lse if asked."""
-    qs = _head_rows(q, "q")
-    n, Hq, D = q.shape
-    batch._check(cache, q, out)
-    if out is not None and (out.shape != q.shape or not out.is_contiguous()):
-        _bad("out must be contiguous, of the shape of q")
-    nb = 0 if batch.empty else _lib.lib().qcf_shared_prefix_attn_workspace_size(cache.ref, batch.ref, Hq)
-    with torch.cuda.stream(stream):   # the allocator ties them to the stream that uses them
-        if out is None:
-            out = torch.empty((n, Hq, D), dtype=q.dtype, device=q.device)
-        lse = torch.empty((n, Hq), dtype=torch.float32, device=q.device) if want_lse else None
-        ws = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
+    _cache_and_batch(cache, batch)
+    Hq, qs = _batch_rows(cache, batch, q, "q")
+    if out is None:
+        out = _empty(q.shape, q.dtype, cache.dev, stream)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.get_device() != cache.dev:
+        _bad("out must be contiguous, of the shape, type and device of q")
+    lse = _empty((q.shape[0], Hq), torch.float32, cache.dev, stream) if want_lse else None
     if not batch.empty:
-        call("qcf_shared_prefix_attn", cache.ref, batch.ref, q.data_ptr(), qs, Hq, float(scale), out.data_ptr(), _ptr(lse),
-             _ptr(ws), nb, _stream(stream))
+        nb = batch.workspace_size(cache, Hq)
+        ws = _empty(nb, torch.uint8, cache.dev, stream) if nb else None
+        call("qcf_shared_prefix_attn", cache.ref, batch.ref, q.data_ptr(), qs, Hq, scale, out.data_ptr(),
+             None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), nb, _raw_stream(stream, cache.dev))
     return (out, lse) if want_lse else out
