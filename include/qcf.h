@@ -500,7 +500,7 @@ typedef struct qcf_rope_scaling {
 } qcf_rope_scaling;
 
 /* Fills device tables cos, sin [n_pos][R/2] fp32 with the angles of positions first_pos ..
- * first_pos + n_pos - 1, taken in fp64 and rounded once.  scaling NULL: none.  R even,
+ * first_pos + n_pos - 1: angles in fp64, values to 2^-44 and rounded once.  scaling NULL: none.  R even,
  * 2 <= R <= 512; 0 <= first_pos, first_pos + n_pos <= 2^31 - 1. */
 qcf_status qcf_rope_table_fill(float* cos, float* sin, int first_pos, int n_pos, int R, double theta,
                                const qcf_rope_scaling* scaling, void* stream);

@@ -57,55 +57,54 @@ struct AppendArgs {
   int interleaved;
 };
 
-// A CTA takes `rows` rows (at most one per warp): each warp looks up one row's sequence, page
-// and position, then all threads walk the rows' (item, chunk of 4 heads) units: queries, keys,
-// values.  V: pairs per item of a rotated head (see item_at); values move 16 entries an item.
+// A CTA takes `rows` rows and `chunks` of their chunks of 4 heads (queries, keys, values in turn),
+// one thread per (row, chunk, item): every load is issued before the first warps know where their
+// rows go (one warp per row looks up the sequence, the position and the page).  V: pairs per item
+// (see item_at).
 constexpr int kAppendThreads = 256;
-constexpr int kAppendRows = kAppendThreads / 32;
 constexpr int kAppendHeads = 4;
 
-template <typename T, int V>
-__device__ __forceinline__ void move_heads(const T* src, T* dst, int64_t dst_head, int h0, int H, int D, ItemAt at,
-                                           const Angles<V>* g, bool interleaved) {
-  Vec<T, V> a[kAppendHeads], b[kAppendHeads];
+template <typename T, int V, bool INTER>
+__global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(const PagedView c, const BatchView b, const AppendArgs p,
+                                                                      int rows, int chunks, unsigned int* status) {
+  __shared__ int64_t slot_s[kAppendThreads / 32];   // the row's place in the cache, -1: nowhere
+  __shared__ int pos_s[kAppendThreads / 32];        // the row's position, -1: not a row of the batch
+  const int items = c.D / 2 / V;
+  const int unit = threadIdx.x / items, item = threadIdx.x - unit * items;
+  const int r = unit / chunks;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * rows + r;
+  int chunk = blockIdx.y * chunks + unit - r * chunks;
+  const int cq = (p.Hq + kAppendHeads - 1) / kAppendHeads, ck = (c.Hkv + kAppendHeads - 1) / kAppendHeads;
+  const bool is_q = chunk < cq, is_v = chunk >= cq + ck;
+  const bool real = r < rows && row < b.n_rows && chunk < cq + 2 * ck;
+  const int h0 = (is_q ? chunk : is_v ? chunk - cq - ck : chunk - cq) * kAppendHeads, H = is_q ? p.Hq : c.Hkv;
+  const ItemAt at = item_at<V, INTER>(item, is_v ? 0 : p.R);
+  const T* src = is_q ? static_cast<const T*>(p.q) + row * p.q_stride
+                      : (is_v ? static_cast<const T*>(p.v_new) : static_cast<const T*>(p.k_new)) + row * p.kv_stride;
+  Run<T, V> x[kAppendHeads], y[kAppendHeads];
 #pragma unroll
   for (int i = 0; i < kAppendHeads; ++i)
-    if (h0 + i < H) {
-      a[i] = *reinterpret_cast<const Vec<T, V>*>(src + (h0 + i) * D + at.a);
-      b[i] = *reinterpret_cast<const Vec<T, V>*>(src + (h0 + i) * D + at.b);
+    if (real && h0 + i < H) {
+      x[i].load(src + (h0 + i) * c.D + at.a);
+      y[i].load(src + (h0 + i) * c.D + at.b);
     }
-#pragma unroll
-  for (int i = 0; i < kAppendHeads; ++i)
-    if (h0 + i < H) {
-      if (g) turn_item<T, V>(a[i], b[i], *g, interleaved);
-      *reinterpret_cast<Vec<T, V>*>(dst + (h0 + i) * dst_head + at.a) = a[i];
-      *reinterpret_cast<Vec<T, V>*>(dst + (h0 + i) * dst_head + at.b) = b[i];
-    }
-}
-
-template <typename T, int V>
-__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const PagedView c, const BatchView b, const AppendArgs p,
-                                                                      int rows, unsigned int* status) {
-  __shared__ int64_t slot_s[kAppendRows];   // the row's place in the cache, -1: nowhere
-  __shared__ int pos_s[kAppendRows];        // the row's position, -1: not a row of the batch
-  const int row0 = blockIdx.x * rows;
-  const int n = min(rows, b.n_rows - row0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp < n) {
-    const int row = row0 + warp;
-    const int seq = warp_seq_of_row(b, row);
+  const int row_w = blockIdx.x * rows + warp;
+  if (warp < rows && row_w < b.n_rows) {
+    const int seq = warp_seq_of_row(b, row_w);
     int pos = -1;
     int64_t slot = -1;
     if (seq >= 0) {
       const SeqSpan s = seq_span(b, seq);
+      const bool first = lane == 0 && blockIdx.y == 0;
       if (s.bad) {
-        if (lane == 0) flag_status(status, QCF_DEV_BAD_INDEX);
-      } else if (row < s.row0 + s.nq) {
-        const int own = s.len - s.nq + (row - s.row0);
+        if (first) flag_status(status, QCF_DEV_BAD_INDEX);
+      } else if (row_w < s.row0 + s.nq) {
+        const int own = s.len - s.nq + (row_w - s.row0);
         pos = b.prefix_len + own;
         slot = slot_of(c, b.page_table + static_cast<int64_t>(seq) * b.table_stride, own);
         if (p.R && pos >= p.max_pos) pos = slot = -1;
-        if (slot < 0 && lane == 0) flag_status(status, QCF_DEV_BAD_INDEX);
+        if (slot < 0 && first) flag_status(status, QCF_DEV_BAD_INDEX);
       }
     }
     if (lane == 0) {
@@ -114,49 +113,37 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
     }
   }
   __syncthreads();
-  const int D = c.D, items = D / 2 / V, items_v = D / 16;
-  const int cq = (p.Hq + kAppendHeads - 1) / kAppendHeads, ck = (c.Hkv + kAppendHeads - 1) / kAppendHeads;
-  const int nq = cq * items, nk = ck * items, per_row = nq + nk + ck * items_v;
-  for (int u = threadIdx.x; u < n * per_row; u += kAppendThreads) {
-    const int r = u / per_row;
-    int e = u - r * per_row;
-    const int64_t row = row0 + r;
-    const int pos = pos_s[r];
-    const int64_t slot = slot_s[r];
-    if (pos < 0) continue;
-    if (e < nq + nk) {
-      const bool is_q = e < nq;
-      if (!is_q) {
-        e -= nq;
-        if (slot < 0) continue;
-      }
-      const int chunk = e / items, item = e - chunk * items;
-      const ItemAt at = item_at<V>(item, p.R, p.interleaved);
-      Angles<V> g;
-      const bool turns = p.R && at.turns;
-      if (turns) g = load_angles<V>(p.cos_t, p.sin_t, pos, p.R, item, false);
-      if (is_q)
-        move_heads<T, V>(static_cast<const T*>(p.q) + row * p.q_stride, static_cast<T*>(p.q_out) + row * p.q_out_stride, D,
-                         chunk * kAppendHeads, p.Hq, D, at, turns ? &g : nullptr, p.interleaved);
-      else
-        move_heads<T, V>(static_cast<const T*>(p.k_new) + row * p.kv_stride, static_cast<T*>(p.k) + slot, c.head_stride,
-                         chunk * kAppendHeads, c.Hkv, D, at, turns ? &g : nullptr, p.interleaved);
-    } else if (slot >= 0) {
-      e -= nq + nk;
-      const int chunk = e / items_v, item = e - chunk * items_v;
-      const ItemAt at{16 * item, 16 * item + 8, false};
-      move_heads<T, 8>(static_cast<const T*>(p.v_new) + row * p.kv_stride, static_cast<T*>(p.v) + slot, c.head_stride,
-                       chunk * kAppendHeads, c.Hkv, D, at, nullptr, false);
-    }
+  if (!real) return;
+  const int pos = pos_s[r];
+  const int64_t slot = slot_s[r];
+  if (pos < 0 || (!is_q && slot < 0)) return;
+  if (at.turns) {
+    const Angles<V> g = load_angles<V>(p.cos_t, p.sin_t, pos, p.R, item, false);
+#pragma unroll
+    for (int i = 0; i < kAppendHeads; ++i)
+      if (h0 + i < H) turn_item<T, V, INTER>(x[i], y[i], g);
   }
+  T* dst = is_q ? static_cast<T*>(p.q_out) + row * p.q_out_stride : (is_v ? static_cast<T*>(p.v) : static_cast<T*>(p.k)) + slot;
+  const int64_t step = is_q ? c.D : c.head_stride;
+#pragma unroll
+  for (int i = 0; i < kAppendHeads; ++i)
+    if (h0 + i < H) {
+      x[i].store(dst + (h0 + i) * step + at.a);
+      y[i].store(dst + (h0 + i) * step + at.b);
+    }
 }
 
 template <typename T, int V>
 static cudaError_t append_launch(const PagedView& c, const BatchView& b, const AppendArgs& a, cudaStream_t st) {
-  // enough CTAs to cover every SM twice before rows share one
-  const int rows = std::min(kAppendRows, std::max(1, b.n_rows / (2 * num_sms())));
+  const int items = c.D / 2 / V;
+  const int all = (a.Hq + kAppendHeads - 1) / kAppendHeads + 2 * ((c.Hkv + kAppendHeads - 1) / kAppendHeads);
+  const int chunks = std::min(all, kAppendThreads / items);
+  const int rows = std::min({kAppendThreads / (items * chunks), kAppendThreads / 32, b.n_rows});
+  const int threads = (std::max(rows * 32, rows * chunks * items) + 31) / 32 * 32;
   LaunchScope ls(KC_APPEND, st);
-  paged_append_kernel<T, V><<<(b.n_rows + rows - 1) / rows, kAppendThreads, 0, st>>>(c, b, a, rows, device_status_ptr());
+  const auto kernel = a.interleaved ? paged_append_kernel<T, V, true> : paged_append_kernel<T, V, false>;
+  kernel<<<dim3((b.n_rows + rows - 1) / rows, (all + chunks - 1) / chunks), threads, 0, st>>>(
+      c, b, a, rows, chunks, device_status_ptr());
   return cudaGetLastError();
 }
 

@@ -1,5 +1,6 @@
 // Rotary positions: tables of (scaled) frequencies filled on the device, and the rotation of
 // heads in both pair layouts over all or part of the head.
+#include <algorithm>
 #include <cmath>
 
 #include "rotary.cuh"
@@ -11,60 +12,141 @@ struct FreqTable {
   double w[kMaxRotaryPairs];
 };
 
-// One thread per table entry: the angle p w_k in fp64, its cosine and sine rounded once.
-__global__ void __launch_bounds__(256) rope_table_kernel(float* __restrict__ cos_t, float* __restrict__ sin_t, int first_pos,
-                                                         int64_t n, int half, double amplitude,
-                                                         const __grid_constant__ FreqTable f) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= n) return;
-  const int64_t p = i / half;
-  double s, c;
-  sincos((static_cast<double>(first_pos) + static_cast<double>(p)) * f.w[i - p * half], &s, &c);
-  cos_t[i] = static_cast<float>(c * amplitude);
-  sin_t[i] = static_cast<float>(s * amplitude);
+// Cosine and sine of p w as sums of two floats each (48 bits), and their product: angles add.
+struct TwoSinCos {
+  float c, cl, s, sl;
+};
+// a b - x y (SIGN = -1) or a b + x y (SIGN = +1) of two-float numbers: the leading products exactly
+// (product and its rounding error), the cross terms to 32 bits, the leading sum with its error.
+template <int SIGN>
+__device__ __forceinline__ void two_dot(float ah, float al, float bh, float bl, float xh, float xl, float yh, float yl, float& sum,
+                                        float& rest) {
+  const float xs = SIGN * xh, xls = SIGN * xl;
+  const float p = __fmul_rn(ah, bh), q = __fmul_rn(xs, yh);
+  float lo = __fadd_rn(__fmaf_rn(ah, bh, -p), __fmaf_rn(xs, yh, -q));
+  lo = __fmaf_rn(ah, bl, lo);
+  lo = __fmaf_rn(al, bh, lo);
+  lo = __fmaf_rn(xs, yl, lo);
+  lo = __fmaf_rn(xls, yh, lo);
+  sum = __fadd_rn(p, q);
+  const float t = __fsub_rn(sum, p);
+  rest = __fadd_rn(__fadd_rn(__fsub_rn(p, __fsub_rn(sum, t)), __fsub_rn(q, t)), lo);
+}
+__device__ __forceinline__ TwoSinCos two_add(const TwoSinCos& a, const TwoSinCos& b) {
+  float h, l;
+  TwoSinCos r;
+  two_dot<-1>(a.c, a.cl, b.c, b.cl, a.s, a.sl, b.s, b.sl, h, l);
+  r.c = __fadd_rn(h, l);
+  r.cl = __fsub_rn(l, __fsub_rn(r.c, h));
+  two_dot<1>(a.s, a.sl, b.c, b.cl, a.c, a.cl, b.s, b.sl, h, l);
+  r.s = __fadd_rn(h, l);
+  r.sl = __fsub_rn(l, __fsub_rn(r.s, h));
+  return r;
+}
+
+// Table entries of 16 pairs (blockIdx.y) and na blocks of 256 positions (blockIdx.x).  fp64 runs
+// at 1/64 of the fp32 rate here: a sine and cosine in fp64 of every entry took 511 us for 131072
+// positions of 64 pairs, 50 times the write.  Instead a position is taken apart in base 4,
+// p = 256 a + 64 b1 + 16 b0 + 4 c1 + c0; the fp64 values of the na + 12 parts of a pair become
+// two-float numbers, their angles are added in those (four additions, 2^-47 each), and each entry
+// is rounded once.  The parts are of the position itself, so an entry's bits do not depend on the
+// call that fills it.  Thread = (pair, b and part of c): it forms b + c once and uses it for every a,
+// and a warp writes 64-byte runs.  1024 threads: one CTA per SM has the fewest fp64 values.
+// 131072 positions of 64 pairs: 22.6 us, 3.0 TB/s (with 32 pairs to a CTA, whole 128-byte lines but
+// twice the fp64 values per SM, 28 us).
+constexpr int kTableThreads = 1024, kTablePairs = 16;
+__global__ void __launch_bounds__(kTableThreads) rope_table_kernel(float* __restrict__ cos_t, float* __restrict__ sin_t, int first_pos,
+                                                                   int n_pos, int half, int na, double amplitude,
+                                                                   const __grid_constant__ FreqTable f) {
+  constexpr int PAIRS = kTablePairs, PER = 256 * PAIRS / kTableThreads;   // positions of a thread in each block
+  __shared__ TwoSinCos a_s[16][PAIRS], digit[4][4][PAIRS];
+  const int k0 = blockIdx.y * PAIRS;
+  const int64_t a0 = first_pos / 256 + static_cast<int64_t>(blockIdx.x) * na;
+  for (int e = threadIdx.x; e < (na + 12) * PAIRS; e += kTableThreads) {
+    const int i = e / PAIRS, k = e % PAIRS;
+    if (k0 + k >= half) continue;
+    const int j = i - na;   // digit j % 3 + 1 of place j / 3
+    const double mult = j < 0 ? 256.0 * static_cast<double>(a0 + i) : static_cast<double>((j % 3 + 1) << (2 * (j / 3)));
+    double s, c;
+    sincos(mult * f.w[k0 + k], &s, &c);
+    if (j < 0) {
+      s *= amplitude;
+      c *= amplitude;
+    }
+    TwoSinCos v;
+    v.c = static_cast<float>(c);
+    v.cl = static_cast<float>(c - v.c);
+    v.s = static_cast<float>(s);
+    v.sl = static_cast<float>(s - v.s);
+    (j < 0 ? a_s[i] : digit[j / 3][j % 3 + 1])[k] = v;
+  }
+  if (threadIdx.x < 4 * PAIRS) digit[threadIdx.x / PAIRS][0][threadIdx.x % PAIRS] = TwoSinCos{1.f, 0.f, 0.f, 0.f};
+  __syncthreads();
+  const int k = threadIdx.x % PAIRS;
+  if (k0 + k >= half) return;
+  const int64_t step = static_cast<int64_t>(256) * half;
+  for (int c = 0; c < PER; ++c) {
+    const int p = threadIdx.x / PAIRS * PER + c;
+    const TwoSinCos d = two_add(two_add(digit[3][p >> 6][k], digit[2][p >> 4 & 3][k]),
+                                two_add(digit[1][p >> 2 & 3][k], digit[0][p & 3][k]));
+    const int64_t row = 256 * a0 + p - first_pos;   // of a = 0; the table holds rows 0 .. n_pos - 1
+    const int a_lo = row < 0 ? 1 : 0;               // the first block may begin before first_pos
+    const int64_t left = row < n_pos ? (n_pos - 1 - row) / 256 + 1 : 0;
+    const int a_hi = left < na ? static_cast<int>(left) : na;
+    float* cr = cos_t + (row + 256 * a_lo) * half + k0 + k;
+    float* sr = sin_t + (row + 256 * a_lo) * half + k0 + k;
+#pragma unroll 4
+    for (int a = a_lo; a < a_hi; ++a, cr += step, sr += step) {
+      const TwoSinCos v = a_s[a][k];
+      float h, l;
+      two_dot<-1>(v.c, v.cl, d.c, d.cl, v.s, v.sl, d.s, d.sl, h, l);
+      *cr = __fadd_rn(h, l);
+      two_dot<1>(v.s, v.sl, d.c, d.cl, v.c, v.cl, d.s, d.sl, h, l);
+      *sr = __fadd_rn(h, l);
+    }
+  }
 }
 
 // One thread per (row, item, chunk of kRopeHeads heads): the angles of a row's item are read
-// once and serve every head of the chunk, whose loads are all in flight together.
+// once and serve every head of the chunk, whose loads are all in flight together (and before the
+// position is known).
 constexpr int kRopeHeads = 4;
-template <typename T, int V>
-__global__ void __launch_bounds__(256) rope_apply_kernel(const T* x, int64_t x_stride, T* y, int64_t y_stride, int n, int H,
+template <typename T, int V, bool INTER>
+__global__ void __launch_bounds__(256, 3) rope_apply_kernel(const T* x, int64_t x_stride, T* y, int64_t y_stride, int n, int H,
                                                          int D, int R, const int32_t* __restrict__ pos,
                                                          const float* __restrict__ cos_t, const float* __restrict__ sin_t,
-                                                         int max_pos, bool interleaved, bool inverse, unsigned int* status) {
-  const int items = D / 2 / V, chunks = (H + kRopeHeads - 1) / kRopeHeads;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int64_t unit = t / items;
-  const int item = static_cast<int>(t - unit * items);
-  const int64_t row = unit / chunks;
-  if (row >= n) return;
+                                                         int max_pos, bool inverse, unsigned int* status) {
+  const unsigned items = D / 2 / V, chunks = (H + kRopeHeads - 1) / kRopeHeads;
+  const unsigned t = blockIdx.x * 256u + threadIdx.x;
+  const unsigned unit = t / items, item = t - unit * items, row = unit / chunks;
+  if (row >= static_cast<unsigned>(n)) return;
   const int h0 = static_cast<int>(unit - row * chunks) * kRopeHeads;
+  const ItemAt at = item_at<V, INTER>(item, R);
+  const T* xr = x + row * x_stride;
+  T* yr = y + row * y_stride;
   const int p = pos[row];
+  Run<T, V> a[kRopeHeads], b[kRopeHeads];
+#pragma unroll
+  for (int i = 0; i < kRopeHeads; ++i)
+    if (h0 + i < H) {
+      a[i].load(xr + (h0 + i) * D + at.a);
+      b[i].load(xr + (h0 + i) * D + at.b);
+    }
   if (p < 0 || p >= max_pos) {
     if (p != -1 && h0 == 0 && item == 0) flag_status(status, QCF_DEV_BAD_INDEX);
     return;
   }
-  const ItemAt at = item_at<V>(item, R, interleaved);
-  const T* xr = x + row * x_stride;
-  T* yr = y + row * y_stride;
-  Vec<T, V> a[kRopeHeads], b[kRopeHeads];
-#pragma unroll
-  for (int i = 0; i < kRopeHeads; ++i)
-    if (h0 + i < H) {
-      a[i] = *reinterpret_cast<const Vec<T, V>*>(xr + (h0 + i) * D + at.a);
-      b[i] = *reinterpret_cast<const Vec<T, V>*>(xr + (h0 + i) * D + at.b);
-    }
   if (at.turns) {
     const Angles<V> g = load_angles<V>(cos_t, sin_t, p, R, item, inverse);
 #pragma unroll
     for (int i = 0; i < kRopeHeads; ++i)
-      if (h0 + i < H) turn_item<T, V>(a[i], b[i], g, interleaved);
+      if (h0 + i < H) turn_item<T, V, INTER>(a[i], b[i], g);
   }
 #pragma unroll
   for (int i = 0; i < kRopeHeads; ++i)
     if (h0 + i < H) {
-      *reinterpret_cast<Vec<T, V>*>(yr + (h0 + i) * D + at.a) = a[i];
-      *reinterpret_cast<Vec<T, V>*>(yr + (h0 + i) * D + at.b) = b[i];
+      a[i].store(yr + (h0 + i) * D + at.a);
+      b[i].store(yr + (h0 + i) * D + at.b);
     }
 }
 
@@ -84,9 +166,10 @@ template <typename T, int V>
 static cudaError_t rope_apply_launch(const RopeApply& r) {
   const int64_t threads = static_cast<int64_t>(r.n) * ((r.H + kRopeHeads - 1) / kRopeHeads) * (r.D / 2 / V);
   LaunchScope ls(KC_ROPE_APPLY, r.st);
-  rope_apply_kernel<T, V><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, r.st>>>(
+  const auto kernel = r.mode & QCF_ROPE_INTERLEAVED ? rope_apply_kernel<T, V, true> : rope_apply_kernel<T, V, false>;
+  kernel<<<static_cast<unsigned>((threads + 255) / 256), 256, 0, r.st>>>(
       static_cast<const T*>(r.x), r.x_stride, static_cast<T*>(r.y), r.y_stride, r.n, r.H, r.D, r.R, r.pos, r.t->cos, r.t->sin,
-      r.t->max_pos, (r.mode & QCF_ROPE_INTERLEAVED) != 0, (r.mode & QCF_ROPE_INVERSE) != 0, device_status_ptr());
+      r.t->max_pos, (r.mode & QCF_ROPE_INVERSE) != 0, device_status_ptr());
   return cudaGetLastError();
 }
 
@@ -161,12 +244,14 @@ qcf_status qcf_rope_table_fill(float* cos, float* sin, int first_pos, int n_pos,
   const qcf_status s = rope_frequencies(R, theta, scaling, &f, &amplitude);
   if (s != QCF_OK) return s;
   if (n_pos == 0) return QCF_OK;
-  const int64_t n = static_cast<int64_t>(n_pos) * (R / 2);
-  const int64_t blocks = (n + 255) / 256;
-  if (blocks > INT32_MAX) return set_error(QCF_ERR_SHAPE, "qcf_rope_table_fill: %lld entries", (long long)n);
+  // blocks of 256 positions, up to 16 to a CTA, so that one CTA per SM does
+  const int64_t blocks = (static_cast<int64_t>(first_pos) + n_pos + 255) / 256 - first_pos / 256;
+  const int groups = (R / 2 + kTablePairs - 1) / kTablePairs;
+  const int na = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, (blocks * groups + num_sms() - 1) / num_sms())));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   LaunchScope ls(KC_ROPE_TABLE, st);
-  rope_table_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(cos, sin, first_pos, n, R / 2, amplitude, f);
+  rope_table_kernel<<<dim3(static_cast<unsigned>((blocks + na - 1) / na), groups), kTableThreads, 0, st>>>(cos, sin, first_pos, n_pos, R / 2, na,
+                                                                                           amplitude, f);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? QCF_OK : cuda_error(e, "qcf_rope_table_fill: launch");
 }
@@ -185,7 +270,7 @@ qcf_status qcf_rope_apply(const void* x, int64_t x_stride, void* y, int64_t y_st
   if (take_fault(4) || !aligned16(x) || !aligned16(y) || !aligned16(t->cos) || !aligned16(t->sin))
     return set_error(QCF_ERR_ALIGN, "qcf_rope_apply: pointers must be 16-byte aligned");
   if (take_fault(1)) return set_error(QCF_ERR_INVALID_ARG, "qcf_rope_apply: injected invalid index table");
-  if (static_cast<int64_t>(n) * ((H + kRopeHeads - 1) / kRopeHeads) * (D / 2) / 256 >= INT32_MAX)
+  if (static_cast<int64_t>(n) * ((H + kRopeHeads - 1) / kRopeHeads) * (D / 2) > UINT32_MAX - 256)
     return set_error(QCF_ERR_SHAPE, "qcf_rope_apply: %d rows of %d x %d entries are too many for one call", n, H, D);
   if (n == 0) return QCF_OK;
   const RopeApply r{x, x_stride, y, y_stride, n, H, D, R, pos, t, mode, static_cast<cudaStream_t>(stream)};

@@ -2,6 +2,9 @@
 #pragma once
 
 #include <cuda_fp16.h>
+#include <string.h>
+
+#include <type_traits>
 
 #include "qcf_internal.cuh"
 
@@ -35,12 +38,12 @@ struct ItemAt {
   int a, b;     // first entries of the two runs
   bool turns;
 };
-template <int V>
-__device__ __forceinline__ ItemAt item_at(int item, int R, bool interleaved) {
+template <int V, bool INTER>
+__device__ __forceinline__ ItemAt item_at(int item, int R) {
   const int k = item * V;
   ItemAt it;
   it.turns = k < R / 2;
-  if (it.turns && !interleaved) {
+  if (it.turns && !INTER) {
     it.a = k;
     it.b = R / 2 + k;
   } else {
@@ -76,34 +79,59 @@ __device__ __forceinline__ void turn(float a, float b, float c, float s, float& 
   ob = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
 }
 
+// V entries as they lie in memory: 32-bit words (two 16-bit entries each) kept whole until they are
+// turned, so that a run of 8 waits in four registers.
 template <typename T, int V>
-__device__ __forceinline__ void turn_item(Vec<T, V>& x, Vec<T, V>& y, const Angles<V>& g, bool interleaved) {
-  if (interleaved) {   // pairs (x0, x1), .. then (y0, y1), ..: a V of 1 keeps its one pair in x, y
-    if constexpr (V == 1) {
-      float oa, ob;
-      turn(to_f32(x.v[0]), to_f32(y.v[0]), g.c[0], g.s[0], oa, ob);
-      x.v[0] = from_f32<T>(oa);
-      y.v[0] = from_f32<T>(ob);
-    } else {
+struct Run {
+  static constexpr int BYTES = sizeof(T) * V;
+  using Word = typename std::conditional<BYTES % 4 == 0, uint32_t, uint16_t>::type;
+  static constexpr int N = BYTES / sizeof(Word);
+  Vec<Word, N> w;
+  __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const Vec<Word, N>*>(p); }
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Vec<Word, N>*>(p) = w; }
+};
+__device__ __forceinline__ float2 unpack2(uint32_t w, __nv_bfloat16) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, __half) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+__device__ __forceinline__ uint32_t repack2(float lo, float hi, __nv_bfloat16) { return pack_bf16x2(lo, hi); }
+__device__ __forceinline__ uint32_t repack2(float lo, float hi, __half) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Turns the pairs of one item: x and y are its two runs.
+template <typename T, int V, bool INTER>
+__device__ __forceinline__ void turn_item(Run<T, V>& x, Run<T, V>& y, const Angles<V>& g) {
+  if constexpr (sizeof(T) == 2 && V >= 2) {
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i) {
-        float oa, ob;
-        turn(to_f32(x.v[2 * i]), to_f32(x.v[2 * i + 1]), g.c[i], g.s[i], oa, ob);
-        x.v[2 * i] = from_f32<T>(oa);
-        x.v[2 * i + 1] = from_f32<T>(ob);
-        turn(to_f32(y.v[2 * i]), to_f32(y.v[2 * i + 1]), g.c[V / 2 + i], g.s[V / 2 + i], oa, ob);
-        y.v[2 * i] = from_f32<T>(oa);
-        y.v[2 * i + 1] = from_f32<T>(ob);
+    for (int i = 0; i < V / 2; ++i) {
+      const float2 p = unpack2(x.w.v[i], T()), q = unpack2(y.w.v[i], T());
+      float2 a, b;
+      if constexpr (INTER) {   // a word is a pair; the pairs of x come before those of y
+        turn(p.x, p.y, g.c[i], g.s[i], a.x, a.y);
+        turn(q.x, q.y, g.c[V / 2 + i], g.s[V / 2 + i], b.x, b.y);
+      } else {
+        turn(p.x, q.x, g.c[2 * i], g.s[2 * i], a.x, b.x);
+        turn(p.y, q.y, g.c[2 * i + 1], g.s[2 * i + 1], a.y, b.y);
       }
+      x.w.v[i] = repack2(a.x, a.y, T());
+      y.w.v[i] = repack2(b.x, b.y, T());
     }
   } else {
+    T e[2 * V];
+    memcpy(e, &x, sizeof(T) * V);
+    memcpy(e + V, &y, sizeof(T) * V);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      float oa, ob;
-      turn(to_f32(x.v[i]), to_f32(y.v[i]), g.c[i], g.s[i], oa, ob);
-      x.v[i] = from_f32<T>(oa);
-      y.v[i] = from_f32<T>(ob);
+      const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : V + i;
+      float a, b;
+      turn(to_f32(e[ia]), to_f32(e[ib]), g.c[i], g.s[i], a, b);
+      e[ia] = from_f32<T>(a);
+      e[ib] = from_f32<T>(b);
     }
+    memcpy(&x, e, sizeof(T) * V);
+    memcpy(&y, e + V, sizeof(T) * V);
   }
 }
 
