@@ -12,399 +12,481 @@
 
 namespace qcf {
 
-// ------------------------------------------------------------------ parts on warp tensor cores
+constexpr int kMaxBatchSeqs = 4096;   // each CTA of the stream keeps the first tile of every sequence
+
+// ------------------------------------------------------------------ the stream, on warp tensor cores
 //
-// A unit is up to 64 score rows (new rows x the G query heads of one KV head) of one sequence
-// against a chunk of its own keys, or up to 64 rows of the whole batch against a chunk of the
-// prefix.  Four warps stream tiles of 64 keys through a ring in shared memory, 16 keys of a tile
-// each, with 16-byte asynchronous copies whose addresses come from the page table (keys behind
-// the chunk and keys of bad pages arrive as zeros, so nothing a free slot holds is ever
-// multiplied).  Up to 16 score rows (single tokens): the rows fit one MMA tile, every warp keeps
-// all of them and scores the 16 keys it copied itself, so the warps run free of each other and
-// join at the end.  More rows: 16 to a warp, and every warp scores the whole tile.
-// Single tokens are bound by the K and V bytes: the ring keeps 64 KB (D = 128) in flight per CTA.
-constexpr int kOwnWarps = 4;
-constexpr int kOwnTile = 16 * kOwnWarps;   // keys
-constexpr int kOwnRows = 64;               // score rows of a unit
-
+// A unit is up to 16 score rows (new rows x the G query heads of one KV head; one m16 tile) of one
+// sequence against its own keys, or 16 rows of the whole batch against the prefix.  The 32-key
+// tiles of all units are dealt out evenly to persistent warps, whatever the lengths are, and every
+// warp works alone: it keeps its own ring of K and V tiles full by tiled TMA (one box per page and
+// 64 columns; pages behind a length, or outside the cache, read as zeros), a step ahead of the tile
+// that it scores and across the borders of units, and no warp waits for another.  (Four warps that
+// split a tile and met at two barriers took 1900 cycles per 64 keys of head dim 64, and 90 us for
+// 386 MB of uneven sequences.)
+// The maximum moves only when it grows by more than 2^8: the weights then stay below 2^8 (exact in
+// the fp32 sums, half a step in 16 bits wherever they lie) and most tiles rescale nothing.
+// Bound by the K and V bytes; the rings keep 96 KB or more per SM in flight.
 template <int D>
-struct OwnCfg {
-  static constexpr int STAGES = D == 128 ? 3 : 4;
-  static constexpr int GROUP = 16 * D * 2;                  // bytes of 16 keys (or values)
-  static constexpr int STAGE = 2 * kOwnWarps * GROUP;       // K groups, then V groups
-  static constexpr int MERGE = kOwnWarps * 16 * D * 4 + kOwnWarps * 16 * 8;
-  static constexpr int SMEM = STAGES * STAGE > MERGE ? STAGES * STAGE : MERGE;
-  static constexpr int MIN_CTAS = D == 128 ? 2 : 3;
+struct StreamCfg {
+  static constexpr int COLS = D < 64 ? D : 64, BOXES = D / COLS;
+  static constexpr int BOX = kStreamKeys * COLS * 2;   // 32 keys x COLS entries
+  static constexpr int TILE = BOXES * BOX;             // a K or V tile
+  static constexpr int STAGES = D >= 64 ? 2 : 4;
+  static constexpr int WARPS = D == 128 ? 6 : D == 64 ? 13 : 12;   // 192 and 208 KB of rings (48 KB at head dim 16)
+  static constexpr int RING = STAGES * 2 * TILE;       // of a warp
+  static constexpr int FIXED = WARPS * (RING + STAGES * 8);
 };
-
-// Byte offset of 8 entries at column col of a key in a group; 16-byte pieces are permuted by the
-// key so that eight keys' pieces of one column fall into different banks.
 template <int D>
-__device__ __forceinline__ uint32_t group_off(int key, int col) {
-  if constexpr (D >= 64)
-    return static_cast<uint32_t>(key * (D * 2) + (((col >> 3) ^ (key & 7)) << 4));
-  else
-    return static_cast<uint32_t>(key * (D * 2) + (((col >> 3) ^ ((key >> 2) & 1)) << 4));
+static size_t stream_smem(int n_seq) {
+  return 1024 + StreamCfg<D>::FIXED + (static_cast<size_t>(n_seq) + 2) * sizeof(int);
 }
 
+// Byte offset of 8 entries at column col of a key in a K or V tile, as TMA lays it out.
+template <int D>
+__device__ __forceinline__ uint32_t tile_at(int key, int col) {
+  if constexpr (D >= 64)
+    return static_cast<uint32_t>((col >> 6) * StreamCfg<D>::BOX) + sw128_off(key, (col & 63) >> 3);
+  else
+    return static_cast<uint32_t>(key * (D * 2) + col * 2);
+}
+
+__device__ __forceinline__ int stream_tiles_of(const SeqSpan& s, int G, int Hkv) {
+  return s.nq == 0 ? 0 : (s.len + kStreamKeys - 1) / kStreamKeys * ((s.nq * G + kStreamRows - 1) / kStreamRows) * Hkv;
+}
+
+// One worker's share of one unit.
+struct StreamSeg {
+  bool pre;            // a unit of the prefix
+  int g, rho0;         // KV head, first score row
+  int row0, nq, len;   // of the sequence (the whole batch for the prefix)
+  int t0, nt, tiles;   // key tiles of this share, of the unit
+  int use;             // tiles of the share that any row of the unit sees (own tokens: the last ones none)
+  int part;
+  const int32_t* table;
+};
+struct StreamWalk {
+  int cur, end, seq;
+  __device__ StreamWalk(const BatchView& b, const int* start, int worker) {
+    const int total = start[b.n_seq], share = start[b.n_seq + 1];
+    cur = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(worker) * share));
+    end = min(total, cur + share);
+    int lo = 0, hi = b.n_seq;   // the first sequence whose successor starts behind cur
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (start[mid + 1] > cur) hi = mid; else lo = mid + 1;
+    }
+    seq = lo;
+  }
+  __device__ bool next(StreamSeg& s, const BatchView& b, const SharedPlan& p, const int* start, int worker, int G, int Hkv) {
+    if (cur >= end) return false;
+    s.pre = cur < start[0];
+    int first = 0;
+    if (s.pre) {
+      s.row0 = 0;
+      s.nq = b.n_rows;
+      s.len = b.prefix_len;
+      s.tiles = p.stream_tiles;
+      s.table = b.prefix_pages;
+    } else {
+      while (start[seq + 1] <= cur) ++seq;
+      const SeqSpan q = seq_span(b, seq);
+      s.row0 = q.row0;
+      s.nq = q.nq;
+      s.len = q.len;
+      s.tiles = (q.len + kStreamKeys - 1) / kStreamKeys;
+      s.table = b.page_table + static_cast<int64_t>(seq) * b.table_stride;
+      first = start[seq];
+    }
+    const int u = (cur - first) / s.tiles;
+    first += u * s.tiles;
+    s.t0 = cur - first;
+    s.nt = min(s.tiles - s.t0, end - cur);
+    s.g = u % Hkv;
+    s.rho0 = u / Hkv * kStreamRows;
+    s.part = worker - first / start[b.n_seq + 1];
+    const int reach = s.pre ? s.len : s.len - s.nq + min(s.nq, (s.rho0 + kStreamRows - 1) / G + 1);   // keys any row sees
+    s.use = max(0, min(s.nt, (reach + kStreamKeys - 1) / kStreamKeys - s.t0));
+    cur += s.nt;
+    return true;
+  }
+};
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kOwnWarps * 32, OwnCfg<D>::MIN_CTAS)
-    own_attn_kernel(const PagedView c, const BatchView b, const AttnArgs a, const SharedPlan p, const Parts parts,
-                    int pre_units, unsigned int* status) {
-  using Cfg = OwnCfg<D>;
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
+    stream_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedView c,
+                       const BatchView b, const AttnArgs a, const SharedPlan p, const Workspace ws, unsigned int* status) {
+  using Cfg = StreamCfg<D>;
+  constexpr int ST = Cfg::STAGES, THREADS = Cfg::WARPS * 32;
+  constexpr unsigned kAll = 0xffffffffu;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* rings = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  // Launched while the prefix kernel runs, on whose results nothing here depends; the join, launched
+  // in the same way, waits for this kernel alone, so this one ends after the prefix kernel has.
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, worker = static_cast<int>(blockIdx.x) * Cfg::WARPS + warp;
+  uint8_t* ring = rings + warp * Cfg::RING;                                                     // stage: K tile, V tile
+  uint64_t* full = reinterpret_cast<uint64_t*>(rings + Cfg::WARPS * Cfg::RING) + warp * ST;
+  int* start = reinterpret_cast<int*>(rings + Cfg::WARPS * (Cfg::RING + ST * 8));               // [n_seq + 2]
 
-  // ---- the unit: rows rho0 .. rho0 + rows, keys [k0, k1) of `pages`, part slot `part`
-  int u = static_cast<int>(blockIdx.x);
-  const bool pre = u < pre_units;
-  if (!pre) u -= pre_units;
-  const int g = u % c.Hkv;
-  u /= c.Hkv;
-  int rho0, row0, n_rho, part, k0, k1, last0;   // last0: the last key that score row rho = 0 sees
-  const int32_t* pages;
-  bool only = false;                             // the row's only part: written to o at once
-  if (pre) {
-    const int chunk = u % p.pre_parts;
-    rho0 = u / p.pre_parts * kOwnRows;
-    row0 = 0;
-    n_rho = b.n_rows * a.G;
-    part = chunk;
-    k0 = chunk * p.pre_chunk;
-    k1 = min(b.prefix_len, k0 + p.pre_chunk);
-    last0 = b.prefix_len;                        // no row's limit
-    pages = b.prefix_pages;
-  } else {
-    const int chunk = u % p.own_parts;
-    u /= p.own_parts;
-    rho0 = u % p.own_row_blocks * kOwnRows;
-    const int seq = u / p.own_row_blocks;
-    const SeqSpan s = seq_span(b, seq);
-    if (s.bad && threadIdx.x == 0 && g == 0 && chunk == 0 && rho0 == 0) flag_status(status, QCF_DEV_BAD_INDEX);
-    row0 = s.row0;
-    n_rho = s.nq * a.G;
-    part = p.pre_parts + chunk;
-    k0 = chunk * p.own_chunk;
-    k1 = min(s.len, k0 + p.own_chunk);
-    last0 = s.len - s.nq;
-    pages = b.page_table + static_cast<int64_t>(seq) * b.table_stride;
-    only = p.pre_parts == 0 && s.len <= p.own_chunk;
-    if (k0 >= s.len) return;                     // not a part of this sequence
-  }
-  const int rows = min(kOwnRows, n_rho - rho0);
-  if (rows <= 0) return;
-  const int reach = pre ? k1 : last0 + (rho0 + rows - 1) / a.G + 1;   // keys behind it are seen by no row
-  k1 = min(k1, reach);
-  const bool by_keys = rows <= 16;               // warps split the keys, not the rows
-  const int n_tiles = k1 > k0 ? (k1 - k0 + kOwnTile - 1) / kOwnTile : 0;
-
-  // ---- this thread's score rows: r_lo = (lane / 4), r_hi = r_lo + 8 of the warp's 16
-  const int w_rho = rho0 + (by_keys ? 0 : warp * 16);
-  const int lo = w_rho + (lane >> 2), hi = lo + 8, end = rho0 + rows;
-  const int qc = (lane & 3) * 2;
-  auto q_row = [&](int rho) {
-    return static_cast<const T*>(a.q) + static_cast<int64_t>(row0 + rho / a.G) * a.q_stride +
-           static_cast<int64_t>(g * a.G + rho % a.G) * D;
-  };
-  uint32_t qf[D / 16][4];
+  // ---- the deal: first tile of every sequence
   {
-    const T* ql = lo < end ? q_row(lo) : nullptr;
-    const T* qh = hi < end ? q_row(hi) : nullptr;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      qf[ks][0] = ql ? *reinterpret_cast<const uint32_t*>(ql + ks * 16 + qc) : 0u;
-      qf[ks][1] = qh ? *reinterpret_cast<const uint32_t*>(qh + ks * 16 + qc) : 0u;
-      qf[ks][2] = ql ? *reinterpret_cast<const uint32_t*>(ql + ks * 16 + qc + 8) : 0u;
-      qf[ks][3] = qh ? *reinterpret_cast<const uint32_t*>(qh + ks * 16 + qc + 8) : 0u;
+    __shared__ int sums[Cfg::WARPS];
+    if (lane == 0) {
+      for (int s = 0; s < ST; ++s) mbar_init(&full[s], 1);
+      fence_mbar_init();
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
     }
+    const int per = (b.n_seq + THREADS - 1) / THREADS, s0 = threadIdx.x * per, s1 = min(b.n_seq, s0 + per);
+    int mine = 0;
+    for (int s = s0; s < s1; ++s) {
+      const SeqSpan q = seq_span(b, s);
+      if (q.bad && blockIdx.x == 0) flag_status(status, QCF_DEV_BAD_INDEX);
+      const int n = stream_tiles_of(q, a.G, c.Hkv);
+      start[s] = n;
+      mine += n;
+    }
+    int run = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kAll, run, o);
+      if (lane >= o) run += v;
+    }
+    if (lane == 31) sums[warp] = run;
+    __syncthreads();
+    int at = (p.pre_stream ? p.stream_blocks * p.stream_tiles * c.Hkv : 0) + run - mine;
+    for (int w = 0; w < warp; ++w) at += sums[w];
+    for (int s = s0; s < s1; ++s) {
+      const int n = start[s];
+      start[s] = at;
+      at += n;
+    }
+    if (threadIdx.x == THREADS - 1) {   // the last thread's end is the total
+      start[b.n_seq] = at;
+      start[b.n_seq + 1] = max((at + p.workers - 1) / p.workers, kMinShare);
+    }
+    __syncthreads();
+    if (blockIdx.x == 0)
+      for (int s = threadIdx.x; s < b.n_seq + 2; s += THREADS) ws.deal[s] = start[s];
   }
-  const int lim_lo = pre ? last0 : last0 + lo / a.G, lim_hi = pre ? last0 : last0 + hi / a.G;
-  const int lim_min = pre ? last0 : last0 + w_rho / a.G;   // every row of the warp sees the keys up to here
 
-  // ---- copies: tile t, this warp's 16 keys.  The page ids of the warp's next 32 tiles sit in the
-  // lanes (two ids where a page holds 8 keys).
-  const uint32_t ring = smem_u32(smem);
-  const int ps = 1 << c.page_shift;
-  const T* Kg = static_cast<const T*>(a.k) + static_cast<int64_t>(g) * c.head_stride;
-  const T* Vg = static_cast<const T*>(a.v) + static_cast<int64_t>(g) * c.head_stride;
-  auto ids_of = [&](int t, int which) {          // the lane's tile t + lane; -1 for a page outside the cache
-    const int key = k0 + (t + lane) * kOwnTile + warp * 16 + which * 8;
-    if (key >= k1) return -2;                    // behind the chunk: nothing to read
-    const int id = pages[key >> c.page_shift];
-    if (id >= 0 && id < c.n_pages) return id;
-    flag_status(status, QCF_DEV_BAD_INDEX);
-    return -1;
-  };
-  int id0 = -2, id1 = -2;
-  auto copy_tile = [&](int t) {
-    if ((t & 31) == 0) {
-      id0 = ids_of(t, 0);
-      if (ps == 8) id1 = ids_of(t, 1);
+  // ---- copies: a walk of its own, up to ST - 1 tiles ahead.  The lanes hold the page ids of the next
+  // 32 groups of 8 keys (8 tiles) of the unit; n_pages, which reads as zeros, behind its length or
+  // outside the cache.
+  StreamWalk ahead(b, start, worker);
+  StreamSeg cs;
+  int ci = 0, cn = 0, ids = 0;   // tile of the segment, tiles issued, page id of this lane's group
+  unsigned out = 0, bad = 0;     // groups outside the cache: of the next 8 tiles, of the tiles issued (4 bits each, tile % 8)
+  cs.use = 0;
+  bool copies = true;
+  const int ps = min(1 << c.page_shift, kStreamKeys), pages = kStreamKeys / ps;   // rows of a box, pages of a tile
+  auto copy_next = [&]() {
+    while (copies && ci == cs.use) {   // segments without a tile to read are passed over
+      copies = ahead.next(cs, b, p, start, worker, a.G, c.Hkv);
+      ci = 0;
     }
-    const int i0 = __shfl_sync(0xffffffffu, id0, t & 31);
-    const int i1 = ps == 8 ? __shfl_sync(0xffffffffu, id1, t & 31) : i0;
-    const int kb = k0 + t * kOwnTile + warp * 16;
-    const uint32_t dst = ring + (t % Cfg::STAGES) * Cfg::STAGE + warp * Cfg::GROUP;
-    constexpr int PIECES = D / 8, STEP = 32 / PIECES > 0 ? 32 / PIECES : 1;   // keys per warp-wide copy
-    const int pc = lane % PIECES;
-#pragma unroll
-    for (int i = 0; i < 16 / STEP; ++i) {
-      const int key = i * STEP + lane / PIECES;
-      const int id = key < 8 ? i0 : i1;
-      const bool take = kb + key < k1 && id >= 0;
-      const int64_t off = take ? id * c.page_stride + ((kb + key) & (ps - 1)) * c.row_stride + pc * 8 : 0;
-      const uint32_t at = dst + group_off<D>(key, pc * 8);
-      cp_async16(at, Kg + off, take);
-      cp_async16(at + kOwnWarps * Cfg::GROUP, Vg + off, take);
-    }
-  };
-  // bad pages inside the group of 16 keys at kb: bit 0 the first 8 keys, bit 1 the others
-  auto bad_of = [&](int kb) {
-    unsigned bad = 0;
-#pragma unroll
-    for (int half = 0; half < 2; ++half)
-      if (kb + half * 8 < k1) {
-        const int id = pages[(kb + half * 8) >> c.page_shift];
-        if (id < 0 || id >= c.n_pages) bad |= 1u << half;
+    if (!copies) return;
+    if ((ci & 7) == 0) {
+      const int key = (cs.t0 + ci) * kStreamKeys + lane * 8;
+      ids = key < cs.len ? cs.table[key >> c.page_shift] : c.n_pages;
+      const bool wrong = key < cs.len && (ids < 0 || ids >= c.n_pages);
+      if (wrong) {
+        flag_status(status, QCF_DEV_BAD_INDEX);
+        ids = c.n_pages;
       }
-    return bad;
-  };
-
-  float m_lo = -INFINITY, m_hi = -INFINITY, l_lo = 0.f, l_hi = 0.f;
-  float acc[D / 8][4];
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-  const int mi = lane >> 3, mr = lane & 7;
-
-  // 16 keys at kb, in shared memory at kaddr and vaddr
-  auto score_group = [&](uint32_t kaddr, uint32_t vaddr, int kb) {
-    float sc[2][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      uint32_t b0, b1, b2, b3;
-      ldsm_x4(kaddr + group_off<D>((mi >> 1) * 8 + mr, ks * 16 + (mi & 1) * 8), b0, b1, b2, b3);
-      mma_16816<T>(sc[0], qf[ks], b0, b1);
-      mma_16816<T>(sc[1], qf[ks], b2, b3);
+      out = __ballot_sync(kAll, wrong);
     }
-    const unsigned bad = bad_of(kb);
-    const bool whole = kb + 15 < k1 && kb + 15 <= lim_min && bad == 0;
-    float top_lo = -INFINITY, top_hi = -INFINITY;
+    const int at = (cn & 7) * 4;
+    bad = (bad & ~(15u << at)) | (out >> ((ci & 7) * 4) & 15u) << at;
+    const int st = cn % ST, page = lane & 3, key0 = (cs.t0 + ci) * kStreamKeys;
+    const int id = __shfl_sync(kAll, ids, (ci & 7) * 4 + page * (ps >> 3));
+    if (lane == 0) mbar_arrive_expect_tx(&full[st], 2 * Cfg::TILE);
+    __syncwarp();
+    if (lane < 8 && page < pages) {   // lanes 0 .. 3: K, 4 .. 7: V
+      uint8_t* dst = ring + (2 * st + (lane >> 2)) * Cfg::TILE + page * ps * Cfg::COLS * 2;
+      const CUtensorMap* map = lane < 4 ? &tmK : &tmV;
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+      for (int h = 0; h < Cfg::BOXES; ++h)
+        tma_load_4d(dst + h * Cfg::BOX, map, &full[st], h * Cfg::COLS, key0 & ((1 << c.page_shift) - 1), cs.g, id);
+    }
+    ++ci;
+    ++cn;
+  };
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float x = sc[nt][e] * a.scale_log2;
-        if (!whole) {
-          const int key = kb + nt * 8 + qc + (e & 1);
-          if (key >= k1 || key > (e < 2 ? lim_lo : lim_hi) || (bad >> nt & 1)) x = -INFINITY;
+  for (int i = 0; i < ST - 1; ++i) copy_next();
+
+  // ---- scores
+  const int mi = lane >> 3, mr = lane & 7, qc = (lane & 3) * 2, r_lo = lane >> 2;
+  StreamWalk walk(b, start, worker);
+  StreamSeg s;
+  int n = 0;
+  bool ok = true;
+  while (ok && walk.next(s, b, p, start, worker, a.G, c.Hkv)) {
+    const int end = min(s.rho0 + kStreamRows, s.nq * a.G), lo = s.rho0 + r_lo, hi = lo + 8;   // this thread's score rows
+    uint32_t qf[D / 16][4];
+    {
+      auto q_row = [&](int rho) {
+        return static_cast<const T*>(a.q) + static_cast<int64_t>(s.row0 + rho / a.G) * a.q_stride +
+               static_cast<int64_t>(s.g * a.G + rho % a.G) * D;
+      };
+      const T* ql = lo < end ? q_row(lo) : nullptr;
+      const T* qh = hi < end ? q_row(hi) : nullptr;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        qf[ks][0] = ql ? *reinterpret_cast<const uint32_t*>(ql + ks * 16 + qc) : 0u;
+        qf[ks][1] = qh ? *reinterpret_cast<const uint32_t*>(qh + ks * 16 + qc) : 0u;
+        qf[ks][2] = ql ? *reinterpret_cast<const uint32_t*>(ql + ks * 16 + qc + 8) : 0u;
+        qf[ks][3] = qh ? *reinterpret_cast<const uint32_t*>(qh + ks * 16 + qc + 8) : 0u;
+      }
+    }
+    // the last key a row sees: all of the prefix, or the own token of its position
+    const int lim_lo = s.pre ? s.len : s.len - s.nq + lo / a.G, lim_hi = s.pre ? s.len : s.len - s.nq + hi / a.G;
+    const int lim_min = s.pre ? s.len : s.len - s.nq + s.rho0 / a.G;
+    float m_lo = -INFINITY, m_hi = -INFINITY, l_lo = 0.f, l_hi = 0.f;
+    float acc[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+
+    for (int i = 0; i < s.use; ++i, ++n) {
+      const int st = n % ST, kb = (s.t0 + i) * kStreamKeys;
+      copy_next();   // into the stage of tile n - 1, which every lane has left
+      const unsigned gone = bad >> ((n & 7) * 4) & 15u;   // its groups of 8 keys outside the cache
+      if (!__all_sync(kAll, mbar_wait(&full[st], (n / ST) & 1))) {
+        ok = false;
+        break;
+      }
+      uint8_t* k_tile = ring + 2 * st * Cfg::TILE;
+      uint8_t* v_tile = k_tile + Cfg::TILE;
+      const uint32_t ka = smem_u32(k_tile), va = smem_u32(v_tile);
+      if (kb + kStreamKeys > s.len) {   // values behind the length: a free slot may hold NaN, and 0 x NaN is NaN
+        for (int e = lane; e < kStreamKeys * (D / 8); e += 32) {
+          const int key = e / (D / 8);
+          if (kb + key >= s.len) *reinterpret_cast<uint4*>(v_tile + tile_at<D>(key, e % (D / 8) * 8)) = make_uint4(0u, 0u, 0u, 0u);
         }
-        sc[nt][e] = x;
-        if (e < 2) top_lo = fmaxf(top_lo, x); else top_hi = fmaxf(top_hi, x);
+        fence_proxy_async_smem();   // before the stage's next copy
+        __syncwarp();
       }
+      float sc[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4(ka + tile_at<D>(h * 16 + (mi >> 1) * 8 + mr, ks * 16 + (mi & 1) * 8), b0, b1, b2, b3);
+          mma_16816<T>(sc[2 * h], qf[ks], b0, b1);
+          mma_16816<T>(sc[2 * h + 1], qf[ks], b2, b3);
+        }
+      if (kb + kStreamKeys > s.len || kb + kStreamKeys - 1 > lim_min || gone) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = kb + j * 8 + qc + (e & 1);
+            if (key >= s.len || key > (e < 2 ? lim_lo : lim_hi) || (gone >> j & 1)) sc[j][e] = -INFINITY;
+          }
+      }
+      float top_lo = fmaxf(max3(sc[0][0], sc[0][1], sc[1][0]), max3(sc[1][1], sc[2][0], sc[2][1]));
+      float top_hi = fmaxf(max3(sc[0][2], sc[0][3], sc[1][2]), max3(sc[1][3], sc[2][2], sc[2][3]));
+      top_lo = max3(top_lo, sc[3][0], sc[3][1]) * a.scale_log2;
+      top_hi = max3(top_hi, sc[3][2], sc[3][3]) * a.scale_log2;
+      // rows of a quad share their maximum only when one of them asks for it
+      if (__any_sync(kAll, top_lo > m_lo + 8.f || top_hi > m_hi + 8.f)) {
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) {
+          top_lo = fmaxf(top_lo, __shfl_xor_sync(kAll, top_lo, o));
+          top_hi = fmaxf(top_hi, __shfl_xor_sync(kAll, top_hi, o));
+        }
+        const float n_lo = fmaxf(m_lo, top_lo), n_hi = fmaxf(m_hi, top_hi);
+        const float f_lo = m_lo == -INFINITY ? 0.f : fast_exp2(m_lo - n_lo), f_hi = m_hi == -INFINITY ? 0.f : fast_exp2(m_hi - n_hi);
+        m_lo = n_lo;
+        m_hi = n_hi;
+        l_lo *= f_lo;
+        l_hi *= f_hi;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          acc[j][0] *= f_lo;
+          acc[j][1] *= f_lo;
+          acc[j][2] *= f_hi;
+          acc[j][3] *= f_hi;
+        }
+      }
+      const float b_lo = m_lo == -INFINITY ? 0.f : -m_lo, b_hi = m_hi == -INFINITY ? 0.f : -m_hi;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sc[j][0] = fast_exp2(fmaf(sc[j][0], a.scale_log2, b_lo));
+        sc[j][1] = fast_exp2(fmaf(sc[j][1], a.scale_log2, b_lo));
+        sc[j][2] = fast_exp2(fmaf(sc[j][2], a.scale_log2, b_hi));
+        sc[j][3] = fast_exp2(fmaf(sc[j][3], a.scale_log2, b_hi));
+        l_lo += sc[j][0] + sc[j][1];
+        l_hi += sc[j][2] + sc[j][3];
+      }
+      // the weights meet the values in the cache's 16-bit type (the MMA's); their sum stays fp32
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t pa[4] = {pack2<T>(sc[2 * h][0], sc[2 * h][1]), pack2<T>(sc[2 * h][2], sc[2 * h][3]),
+                                pack2<T>(sc[2 * h + 1][0], sc[2 * h + 1][1]), pack2<T>(sc[2 * h + 1][2], sc[2 * h + 1][3])};
+#pragma unroll
+        for (int dp = 0; dp < D / 16; ++dp) {
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4_t(va + tile_at<D>(h * 16 + (mi & 1) * 8 + mr, dp * 16 + (mi >> 1) * 8), b0, b1, b2, b3);
+          mma_16816<T>(acc[2 * dp], pa, b0, b1);
+          mma_16816<T>(acc[2 * dp + 1], pa, b2, b3);
+        }
+      }
+      __syncwarp();
+    }
+    if (!ok) break;
 #pragma unroll
     for (int o = 1; o <= 2; o <<= 1) {
-      top_lo = fmaxf(top_lo, __shfl_xor_sync(0xffffffffu, top_lo, o));
-      top_hi = fmaxf(top_hi, __shfl_xor_sync(0xffffffffu, top_hi, o));
+      l_lo += __shfl_xor_sync(kAll, l_lo, o);
+      l_hi += __shfl_xor_sync(kAll, l_hi, o);
     }
-    // the maximum moves only when it grows by more than 2^8: the weights then stay below 2^8
-    // (exact in fp32 sums, half a step in 16 bits wherever they lie) and most groups rescale nothing
-    if (__any_sync(0xffffffffu, top_lo > m_lo + 8.f || top_hi > m_hi + 8.f)) {
-      const float n_lo = fmaxf(m_lo, top_lo), n_hi = fmaxf(m_hi, top_hi);
-      const float f_lo = m_lo == -INFINITY ? 0.f : exp2f(m_lo - n_lo), f_hi = m_hi == -INFINITY ? 0.f : exp2f(m_hi - n_hi);
-      m_lo = n_lo;
-      m_hi = n_hi;
-      l_lo *= f_lo;
-      l_hi *= f_hi;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        acc[i][0] *= f_lo;
-        acc[i][1] *= f_lo;
-        acc[i][2] *= f_hi;
-        acc[i][3] *= f_hi;
-      }
-    }
-    const float b_lo = m_lo == -INFINITY ? 0.f : m_lo, b_hi = m_hi == -INFINITY ? 0.f : m_hi;
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      sc[nt][0] = exp2f(sc[nt][0] - b_lo);
-      sc[nt][1] = exp2f(sc[nt][1] - b_lo);
-      sc[nt][2] = exp2f(sc[nt][2] - b_hi);
-      sc[nt][3] = exp2f(sc[nt][3] - b_hi);
-      l_lo += sc[nt][0] + sc[nt][1];
-      l_hi += sc[nt][2] + sc[nt][3];
-    }
-    // the weights meet the values in the cache's 16-bit type (the MMA's); their sum stays fp32
-    const uint32_t pa[4] = {pack2<T>(sc[0][0], sc[0][1]), pack2<T>(sc[0][2], sc[0][3]), pack2<T>(sc[1][0], sc[1][1]),
-                            pack2<T>(sc[1][2], sc[1][3])};
-#pragma unroll
-    for (int dp = 0; dp < D / 16; ++dp) {
-      uint32_t b0, b1, b2, b3;
-      ldsm_x4_t(vaddr + group_off<D>((mi & 1) * 8 + mr, dp * 16 + (mi >> 1) * 8), b0, b1, b2, b3);
-      mma_16816<T>(acc[2 * dp], pa, b0, b1);
-      mma_16816<T>(acc[2 * dp + 1], pa, b2, b3);
-    }
-  };
 
-#pragma unroll
-  for (int t = 0; t < Cfg::STAGES - 1; ++t) {
-    if (t < n_tiles) copy_tile(t);
-    cp_async_commit();
-  }
-  for (int t = 0; t < n_tiles; ++t) {
-    cp_async_wait<Cfg::STAGES - 2>();
-    if (by_keys) __syncwarp(); else __syncthreads();
-    // the slot of tile t - 1 takes tile t + STAGES - 1: every reader of it is past the barrier
-    if (t + Cfg::STAGES - 1 < n_tiles) copy_tile(t + Cfg::STAGES - 1);
-    cp_async_commit();
-    const uint32_t st = ring + (t % Cfg::STAGES) * Cfg::STAGE;
-    const int kb = k0 + t * kOwnTile;
-    if (by_keys) {
-      if (kb + warp * 16 < k1)
-        score_group(st + warp * Cfg::GROUP, st + (kOwnWarps + warp) * Cfg::GROUP, kb + warp * 16);
-    } else if (w_rho < end) {
-#pragma unroll 1
-      for (int w = 0; w < kOwnWarps; ++w)
-        if (kb + w * 16 < k1) score_group(st + w * Cfg::GROUP, st + (kOwnWarps + w) * Cfg::GROUP, kb + w * 16);
-    }
-  }
-#pragma unroll
-  for (int o = 1; o <= 2; o <<= 1) {
-    l_lo += __shfl_xor_sync(0xffffffffu, l_lo, o);
-    l_hi += __shfl_xor_sync(0xffffffffu, l_hi, o);
-  }
-
-  // ---- the unit's rows leave: as a part, or finished
-  const int64_t slot = static_cast<int64_t>(part) * b.n_rows;
-  auto place = [&](int rho) { return static_cast<int64_t>(row0 + rho / a.G) * a.Hq + g * a.G + rho % a.G; };
-  auto put_ml = [&](int rho, float m, float l) {
-    if (only) {
-      if (a.lse) a.lse[place(rho)] = (m + log2f(l)) * 0.69314718055994531f;
-    } else {
-      parts.ml[slot * a.Hq + place(rho)] = make_float2(m, l);
-    }
-  };
-  if (!by_keys) {
+    // ---- the rows' sums leave: as a part, or finished
+    const bool only = b.prefix_len == 0 && s.nt == s.tiles;
+    float* part_o = s.part > 0 ? ws.spill_o + static_cast<int64_t>(worker) * kStreamRows * D : s.pre ? ws.pre_o : ws.own_o;
+    float2* part_ml = s.part > 0 ? ws.spill_ml + static_cast<int64_t>(worker) * kStreamRows : s.pre ? ws.pre_ml : ws.own_ml;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int rho = half ? hi : lo;
       if (rho >= end) continue;
-      const float m = half ? m_hi : m_lo, l = half ? l_hi : l_lo, inv = l > 0.f ? 1.f / l : 0.f;
-      if ((lane & 3) == 0) put_ml(rho, m, l);
+      const float m = half ? m_hi : m_lo, l = half ? l_hi : l_lo;
+      const int64_t place = static_cast<int64_t>(s.row0 + rho / a.G) * a.Hq + s.g * a.G + rho % a.G;
+      const int64_t slot = s.part > 0 ? static_cast<int64_t>(rho - s.rho0) : place;
       if (only) {
-        T* o = static_cast<T*>(a.o) + place(rho) * D;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        T* o = static_cast<T*>(a.o) + place * D;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          *reinterpret_cast<uint32_t*>(o + i * 8 + qc) = pack2<T>(acc[i][2 * half] * inv, acc[i][2 * half + 1] * inv);
+        for (int j = 0; j < D / 8; ++j)
+          *reinterpret_cast<uint32_t*>(o + j * 8 + qc) = pack2<T>(acc[j][2 * half] * inv, acc[j][2 * half + 1] * inv);
+        if (a.lse && qc == 0) a.lse[place] = (m + log2f(l)) * 0.69314718055994531f;
       } else {
-        float* o = parts.o + (slot * a.Hq + place(rho)) * D;
+        float* o = part_o + slot * D;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          *reinterpret_cast<float2*>(o + i * 8 + qc) = make_float2(acc[i][2 * half], acc[i][2 * half + 1]);
+        for (int j = 0; j < D / 8; ++j)
+          *reinterpret_cast<float2*>(o + j * 8 + qc) = make_float2(acc[j][2 * half], acc[j][2 * half + 1]);
+        if (qc == 0) part_ml[slot] = make_float2(m, l);
       }
     }
-    return;
   }
-  // the warps' sums of the same rows meet in the ring, now free
-  cp_async_wait<0>();
-  __syncthreads();
-  float* so = reinterpret_cast<float*>(smem);
-  float2* sml = reinterpret_cast<float2*>(smem + kOwnWarps * 16 * D * 4);
-  {
-    const int r = lane >> 2;
-    if ((lane & 3) == 0) {
-      sml[warp * 16 + r] = make_float2(m_lo, l_lo);
-      sml[warp * 16 + r + 8] = make_float2(m_hi, l_hi);
-    }
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      *reinterpret_cast<float2*>(so + (warp * 16 + r) * D + i * 8 + qc) = make_float2(acc[i][0], acc[i][1]);
-      *reinterpret_cast<float2*>(so + (warp * 16 + r + 8) * D + i * 8 + qc) = make_float2(acc[i][2], acc[i][3]);
-    }
+  if (!ok) {
+    flag_status(status, QCF_DEV_TIMEOUT);
+    for (int e = n; e < cn; ++e) mbar_wait(&full[e % ST], (e / ST) & 1);   // no copy is in flight when the warp ends
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < rows * (D / 4); i += kOwnWarps * 32) {
-    const int r = i / (D / 4), d = i % (D / 4) * 4;
-    float M = -INFINITY, L = 0.f;
-#pragma unroll
-    for (int w = 0; w < kOwnWarps; ++w) M = fmaxf(M, sml[w * 16 + r].x);
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kOwnWarps; ++w) {
-      const float2 ml = sml[w * 16 + r];
-      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-      const float4 v = *reinterpret_cast<const float4*>(so + (w * 16 + r) * D + d);
-      L += ml.y * f;
-      s.x += v.x * f;
-      s.y += v.y * f;
-      s.z += v.z * f;
-      s.w += v.w * f;
-    }
-    const int rho = rho0 + r;
-    if (d == 0) put_ml(rho, M, L);
-    if (only) {
-      const float inv = L > 0.f ? 1.f / L : 0.f;
-      *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + place(rho) * D + d) =
-          make_uint2(pack2<T>(s.x * inv, s.y * inv), pack2<T>(s.z * inv, s.w * inv));
-    } else {
-      *reinterpret_cast<float4*>(parts.o + (slot * a.Hq + place(rho)) * D + d) = s;
-    }
-  }
+  pdl_wait();
 }
 
 // ------------------------------------------------------------------ joining the parts
 //
-// One warp per (row, head): the parts' maxima and sums are read by lanes, then every lane adds
-// its D / 32 output entries of each part.  Parts are added in a fixed order.
+// `per` warps (1, 2, 4 or 8) for each (row, head), more where a row may have many parts: lanes read
+// the parts' maxima and sums, every warp adds its share of the parts (lane: D / 32 output entries),
+// and the warps' sums meet in shared memory, always in the same order.  Launched while the kernels
+// before it run; what does not depend on them (the row's sequence) is found meanwhile.
+constexpr int kCombineWarps = 8;
 template <typename T, int D>
-__global__ void __launch_bounds__(256) batch_combine_kernel(const PagedView c, const BatchView b, const AttnArgs a,
-                                                            const SharedPlan p, const Parts parts) {
+__global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const PagedView c, const BatchView b, const AttnArgs a,
+                                                                           const SharedPlan p, const Workspace ws, int per) {
   constexpr int E = D >= 32 ? D / 32 : 1;
-  const int w = static_cast<int>((static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
-  const int row = w / a.Hq, h = w - row * a.Hq;
-  if (row >= b.n_rows) return;
-  const int seq = warp_seq_of_row(b, row);
-  if (seq < 0) return;
-  const SeqSpan s = seq_span(b, seq);
-  if (row >= s.row0 + s.nq) return;
-  const int n_own = (s.len + p.own_chunk - 1) / p.own_chunk;
-  int n_pre = p.pre_parts;
-  if (p.pre_tc) {   // the CTAs that share this row's unit
-    const int unit = h / a.G * p.pre_row_blocks + row / p.pre_rows;
-    n_pre = ((unit + 1) * p.pre_tiles - 1) / p.pre_share - unit * p.pre_tiles / p.pre_share + 1;
+  __shared__ float met[kCombineWarps][D + 1];   // a warp's sums, its normaliser
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % per;
+  const int64_t pair = static_cast<int64_t>(blockIdx.x) * (kCombineWarps / per) + warp / per;
+  const int row = static_cast<int>(pair / a.Hq), h = static_cast<int>(pair - static_cast<int64_t>(row) * a.Hq);
+  int seq = -1;
+  SeqSpan s = {};
+  if (row < b.n_rows) {
+    seq = warp_seq_of_row(b, row);
+    if (seq >= 0) s = seq_span(b, seq);
   }
-  if (p.pre_parts == 0 && n_own == 1) return;   // already written
-  const int n = n_pre + n_own;
-  const int64_t stride = static_cast<int64_t>(b.n_rows) * a.Hq, at = static_cast<int64_t>(row) * a.Hq + h;
-  auto slot = [&](int i) { return (i < n_pre ? i : p.pre_parts + i - n_pre) * stride + at; };
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, parts.ml[slot(i)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.f;
+  pdl_wait();
+  bool live = seq >= 0 && row < s.row0 + s.nq;
+  int n = 0, n_pre = 0, pre_cta = 0, pre_local = 0, own_cta = 0, rho = 0;
+  const int64_t at = pair;
+  if (live) {
+    const int g = h / a.G, hh = h - g * a.G, share = ws.deal[b.n_seq + 1];
+    // parts: the prefix's (on tcgen05, or of the stream), then the own tokens'
+    if (p.pre_tc) {   // the CTAs that share this row's unit
+      const int unit = g * p.pre_row_blocks + row / p.pre_rows;
+      n_pre = ((unit + 1) * p.pre_tiles - 1) / p.pre_share - unit * p.pre_tiles / p.pre_share + 1;
+    } else if (p.pre_stream) {
+      const int r = row * a.G + hh, first = (r / kStreamRows * c.Hkv + g) * p.stream_tiles;
+      pre_cta = first / share;
+      pre_local = r % kStreamRows;
+      n_pre = (first + p.stream_tiles - 1) / share - pre_cta + 1;
+    }
+    rho = (row - s.row0) * a.G + hh;
+    const int tiles = (s.len + kStreamKeys - 1) / kStreamKeys;
+    const int first = ws.deal[seq] + (rho / kStreamRows * c.Hkv + g) * tiles;
+    own_cta = first / share;
+    n = n_pre + (first + tiles - 1) / share - own_cta + 1;
+    live = n_pre > 0 || n > 1;   // else already written
+  }
+  // the place of part i's sums: row of tc_o, of own_o or pre_o, or of spill_o
+  auto part = [&](int i, const float*& o) {
+    if (i < n_pre && p.pre_tc) {
+      const int64_t r = static_cast<int64_t>(i) * b.n_rows * a.Hq + at;
+      o = ws.tc_o + r * D;
+      return ws.tc_ml + r;
+    }
+    const bool pre = i < n_pre;
+    if (!pre) i -= n_pre;
+    if (i == 0) {
+      o = (pre ? ws.pre_o : ws.own_o) + at * D;
+      return (pre ? ws.pre_ml : ws.own_ml) + at;
+    }
+    const int64_t r = static_cast<int64_t>((pre ? pre_cta : own_cta) + i) * kStreamRows + (pre ? pre_local : rho % kStreamRows);
+    o = ws.spill_o + r * D;
+    return ws.spill_ml + r;
+  };
+  float M = -INFINITY, L = 0.f;
   Vec<float, E> sum;
 #pragma unroll
   for (int e = 0; e < E; ++e) sum.v[e] = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    float f = 0.f;
-    if (i0 + lane < n) {
-      const float2 ml = parts.ml[slot(i0 + lane)];
-      f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-      L += ml.y * f;
-    }
-    const int m = min(32, n - i0);
-#pragma unroll 4
-    for (int i = 0; i < m; ++i) {
-      const float fi = __shfl_sync(0xffffffffu, f, i);
-      if (fi == 0.f || lane * E >= D) continue;   // a part without keys for this row holds no sums
-      const Vec<float, E> v = *reinterpret_cast<const Vec<float, E>*>(parts.o + slot(i0 + i) * D + lane * E);
+  if (live) {
+    const float* po = nullptr;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, part(i, po)->x);
 #pragma unroll
-      for (int e = 0; e < E; ++e) sum.v[e] = fmaf(v.v[e], fi, sum.v[e]);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const int share = (n + per - 1) / per, i_end = min(n, (sub + 1) * share);
+    for (int i0 = sub * share; i0 < i_end; i0 += 32) {
+      float f = 0.f;
+      if (i0 + lane < i_end) {
+        const float2 ml = *part(i0 + lane, po);
+        f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+        L += ml.y * f;
+      }
+      const int m = min(32, i_end - i0);
+#pragma unroll 4
+      for (int i = 0; i < m; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        const float* o = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(po), i));
+        if (fi == 0.f || lane * E >= D) continue;   // a part without keys for this row
+        const Vec<float, E> v = *reinterpret_cast<const Vec<float, E>*>(o + lane * E);
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum.v[e] = fmaf(v.v[e], fi, sum.v[e]);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  }
+  if (per > 1) {
+    if (lane * E < D)
+#pragma unroll
+      for (int e = 0; e < E; ++e) met[warp][lane * E + e] = sum.v[e];
+    if (lane == 0) met[warp][D] = L;
+    __syncthreads();
+    if (sub > 0) return;
+    for (int w = 1; w < per; ++w) {
+      if (lane * E < D)
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum.v[e] += met[warp + w][lane * E + e];
+      L += met[warp + w][D];
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if (!live) return;
   const float inv = L > 0.f ? 1.f / L : 0.f;
   if (lane * E < D) {
     Vec<T, E> r;
@@ -420,19 +502,9 @@ __global__ void __launch_bounds__(256) batch_combine_kernel(const PagedView c, c
 static SharedPlan plan_shared(const PagedView& c, const BatchView& b, int Hq) {
   SharedPlan p = {};
   const int G = Hq / c.Hkv, sms = num_sms();
-  auto chunks = [&](int64_t units, int len, int* chunk, int* n) {
-    // parts of at least 128 keys, enough units to fill every SM four times, and none above 1024
-    // keys, so that one long sequence does not outlast the others
-    const int64_t fill = std::min<int64_t>((4 * sms + units - 1) / std::max<int64_t>(units, 1), (len + 127) / 128);
-    const int want = static_cast<int>(std::max<int64_t>({1, fill, (len + 1023) / 1024}));
-    *chunk = std::max(kOwnTile, ((len + want - 1) / want + kOwnTile - 1) / kOwnTile * kOwnTile);
-    *n = (len + *chunk - 1) / *chunk;
-  };
-  p.own_row_blocks = std::max(1, (std::min(b.max_q, b.n_rows) * G + kOwnRows - 1) / kOwnRows);
-  chunks(static_cast<int64_t>(b.n_seq) * c.Hkv * p.own_row_blocks, std::max(1, b.max_len), &p.own_chunk, &p.own_parts);
   // More than one 16-row MMA tile of score rows per KV head: tcgen05 (one tile has nothing to share,
-  // and the warp-MMA kernel splits its keys over every SM).
-  if (b.prefix_len > 0 && c.D >= 64 && b.n_rows * G > 16) {
+  // and the stream splits its keys over every SM).
+  if (b.prefix_len > 0 && c.D >= 64 && static_cast<int64_t>(b.n_rows) * G > 16) {
     p.pre_tc = true;
     p.pre_rows = 2 * (128 / G);
     p.pre_row_blocks = (b.n_rows + p.pre_rows - 1) / p.pre_rows;
@@ -442,60 +514,93 @@ static SharedPlan plan_shared(const PagedView& c, const BatchView& b, int Hq) {
     p.pre_ctas = static_cast<int>((total + p.pre_share - 1) / p.pre_share);
     p.pre_parts = (p.pre_tiles + p.pre_share - 2) / p.pre_share + 1;   // CTAs that one unit can meet
   } else if (b.prefix_len > 0) {
-    p.pre_row_blocks = (b.n_rows * G + kOwnRows - 1) / kOwnRows;
-    chunks(static_cast<int64_t>(p.pre_row_blocks) * c.Hkv, b.prefix_len, &p.pre_chunk, &p.pre_parts);
+    p.pre_stream = true;
+    p.stream_blocks = static_cast<int>((static_cast<int64_t>(b.n_rows) * G + kStreamRows - 1) / kStreamRows);
+    p.stream_tiles = (b.prefix_len + kStreamKeys - 1) / kStreamKeys;
   }
+  p.ctas = sms;
+  p.workers = sms * (c.D == 128 ? StreamCfg<128>::WARPS : c.D == 64 ? StreamCfg<64>::WARPS : StreamCfg<16>::WARPS);
   return p;
 }
 
-size_t parts_bytes(const SharedPlan& p, const BatchView& b, int Hq, int D) {
-  const int n = p.pre_parts + p.own_parts;
-  if (n <= 1) return 0;
-  const size_t rows = static_cast<size_t>(n) * b.n_rows * Hq;
-  return align_up(rows * D * sizeof(float), 256) + align_up(rows * sizeof(float2), 256);
+// Tiles of the stream at most: every sequence as long and as wide as its bounds.
+static int64_t most_tiles(const SharedPlan& p, const BatchView& b, int G, int Hkv) {
+  const int64_t rows = std::min(b.max_q, b.n_rows);
+  return (static_cast<int64_t>(p.stream_blocks) * p.stream_tiles +
+          b.n_seq * ((rows * G + kStreamRows - 1) / kStreamRows) * ((b.max_len + kStreamKeys - 1) / kStreamKeys)) *
+         Hkv;
+}
+
+size_t workspace_layout(const SharedPlan& p, const BatchView& b, int Hq, int D, void* base, Workspace* w) {
+  uint8_t* at = static_cast<uint8_t*>(base);
+  size_t used = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* r = at + used;
+    used += align_up(bytes, 256);
+    return r;
+  };
+  const size_t rows = static_cast<size_t>(b.n_rows) * Hq, o = rows * D * sizeof(float), ml = rows * sizeof(float2);
+  w->deal = reinterpret_cast<int*>(take((static_cast<size_t>(b.n_seq) + 2) * sizeof(int)));
+  w->tc_o = reinterpret_cast<float*>(take(p.pre_parts * o));
+  w->tc_ml = reinterpret_cast<float2*>(take(p.pre_parts * ml));
+  w->own_o = reinterpret_cast<float*>(take(o));
+  w->own_ml = reinterpret_cast<float2*>(take(ml));
+  w->pre_o = reinterpret_cast<float*>(take(p.pre_stream ? o : 0));
+  w->pre_ml = reinterpret_cast<float2*>(take(p.pre_stream ? ml : 0));
+  w->spill_o = reinterpret_cast<float*>(take(static_cast<size_t>(p.workers) * kStreamRows * D * sizeof(float)));
+  w->spill_ml = reinterpret_cast<float2*>(take(static_cast<size_t>(p.workers) * kStreamRows * sizeof(float2)));
+  return used;
 }
 
 template <typename T, int D>
-static qcf_status shared_prefix_attn_launch(const qcf_paged_kv* cache, const PagedView& c, const BatchView& b, const AttnArgs& a, const SharedPlan& p,
-                                            Parts parts, cudaStream_t st) {
-  const char* who = "qcf_shared_prefix_attn";
-  using Cfg = OwnCfg<D>;
+static cudaError_t stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedView& c, const BatchView& b,
+                                 const AttnArgs& a, const SharedPlan& p, const Workspace& w, cudaStream_t st) {
   static PerDevice<cudaError_t> smem_attr;
   const cudaError_t attr = smem_attr.get(current_device(), [] {
-    return cudaFuncSetAttribute(own_attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+    return cudaFuncSetAttribute(stream_attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(stream_smem<D>(kMaxBatchSeqs)));
   });
-  if (attr != cudaSuccess) return cuda_error(attr, "qcf_shared_prefix_attn: smem attribute");
-  const int64_t pre_units = p.pre_tc ? 0 : static_cast<int64_t>(p.pre_parts) * p.pre_row_blocks * c.Hkv;
-  const int64_t units = pre_units + static_cast<int64_t>(b.n_seq) * p.own_row_blocks * p.own_parts * c.Hkv;
-  if (units > INT32_MAX) return set_error(QCF_ERR_SHAPE, "%s: %lld units of work are too many for one call", who, (long long)units);
+  if (attr != cudaSuccess) return attr;
+  LaunchScope ls(KC_OWN_ATTN, st);
+  const dim3 grid(p.ctas), block(StreamCfg<D>::WARPS * 32);
+  if (p.pre_tc)
+    return launch_pdl(stream_attn_kernel<T, D>, grid, block, stream_smem<D>(b.n_seq), st, tk, tv, c, b, a, p, w, device_status_ptr());
+  stream_attn_kernel<T, D><<<grid, block, stream_smem<D>(b.n_seq), st>>>(tk, tv, c, b, a, p, w, device_status_ptr());
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+static qcf_status shared_prefix_attn_launch(const qcf_paged_kv* cache, const PagedView& c, const BatchView& b, const AttnArgs& a,
+                                            const SharedPlan& p, const Workspace& w, cudaStream_t st) {
   if (p.pre_tc) {
-    const qcf_status s = prefix_tc_launch(cache, c, b, a, p, parts, st);
+    const qcf_status s = prefix_tc_launch(cache, c, b, a, p, w, st);
     if (s != QCF_OK) return s;
   }
-  {
-    LaunchScope ls(KC_OWN_ATTN, st);
-    own_attn_kernel<T, D><<<static_cast<unsigned>(units), kOwnWarps * 32, Cfg::SMEM, st>>>(
-        c, b, a, p, parts, static_cast<int>(pre_units), device_status_ptr());
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_error(e, "qcf_shared_prefix_attn: launch");
-  }
-  if (p.pre_parts + p.own_parts > 1) {
-    LaunchScope ls(KC_BATCH_COMBINE, st);
-    const int64_t warps = static_cast<int64_t>(b.n_rows) * a.Hq;
-    batch_combine_kernel<T, D><<<static_cast<unsigned>((warps + 7) / 8), 256, 0, st>>>(c, b, a, p, parts);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_error(e, "qcf_shared_prefix_attn: combine launch");
-  }
-  return QCF_OK;
+  CUtensorMap tk, tv;
+  const int rows = std::min(1 << c.page_shift, kStreamKeys);
+  const CUtensorMapSwizzle sw = D >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
+  if (!encode_pages(&tk, cache->k, c, rows, StreamCfg<D>::COLS, sw) || !encode_pages(&tv, cache->v, c, rows, StreamCfg<D>::COLS, sw))
+    return set_error(QCF_ERR_CUDA, "qcf_shared_prefix_attn: tensor map encoding failed");
+  cudaError_t e = stream_launch<T, D>(tk, tv, c, b, a, p, w, st);
+  if (e != cudaSuccess) return cuda_error(e, "qcf_shared_prefix_attn: launch");
+  LaunchScope ls(KC_BATCH_COMBINE, st);
+  // parts of a row, about (lengths are known on the device): a warp for every few of them
+  const int64_t share = std::max<int64_t>(kMinShare, most_tiles(p, b, a.G, c.Hkv) / p.workers);
+  const int64_t many = p.pre_parts + (p.stream_tiles + (b.max_len + kStreamKeys - 1) / kStreamKeys) / share + 1;
+  const int per = many <= 4 ? 1 : many <= 8 ? 2 : many <= 16 ? 4 : 8;
+  const int64_t pairs = static_cast<int64_t>(b.n_rows) * a.Hq, at_once = kCombineWarps / per;
+  e = launch_pdl(batch_combine_kernel<T, D>, dim3(static_cast<unsigned>((pairs + at_once - 1) / at_once)), dim3(kCombineWarps * 32), 0,
+                 st, c, b, a, p, w, per);
+  return e == cudaSuccess ? QCF_OK : cuda_error(e, "qcf_shared_prefix_attn: combine launch");
 }
 
 template <typename T>
-static qcf_status shared_prefix_attn_type(const qcf_paged_kv* cache, const PagedView& c, const BatchView& b, const AttnArgs& a, const SharedPlan& p,
-                                          Parts parts, cudaStream_t st) {
+static qcf_status shared_prefix_attn_type(const qcf_paged_kv* cache, const PagedView& c, const BatchView& b, const AttnArgs& a,
+                                          const SharedPlan& p, const Workspace& w, cudaStream_t st) {
   switch (c.D) {
-    case 16: return shared_prefix_attn_launch<T, 16>(cache, c, b, a, p, parts, st);
-    case 64: return shared_prefix_attn_launch<T, 64>(cache, c, b, a, p, parts, st);
-    default: return shared_prefix_attn_launch<T, 128>(cache, c, b, a, p, parts, st);
+    case 16: return shared_prefix_attn_launch<T, 16>(cache, c, b, a, p, w, st);
+    case 64: return shared_prefix_attn_launch<T, 64>(cache, c, b, a, p, w, st);
+    default: return shared_prefix_attn_launch<T, 128>(cache, c, b, a, p, w, st);
   }
 }
 
@@ -503,9 +608,14 @@ static qcf_status check_attn(const char* who, const qcf_paged_kv* cache, const q
                              BatchView* b) {
   const qcf_status s = check_paged(who, cache, batch, c, b);
   if (s != QCF_OK) return s;
+  if (b->n_seq > kMaxBatchSeqs) return set_error(QCF_ERR_SHAPE, "%s: n_seq=%d (at most %d)", who, b->n_seq, kMaxBatchSeqs);
   if (Hq <= 0 || Hq % c->Hkv || Hq / c->Hkv > 16) return set_error(QCF_ERR_SHAPE, "%s: Hq=%d Hkv=%d", who, Hq, c->Hkv);
   if (static_cast<int64_t>(b->n_rows) * Hq > INT32_MAX / 128)
     return set_error(QCF_ERR_SHAPE, "%s: %d rows of %d heads are too many for one call", who, b->n_rows, Hq);
+  const SharedPlan p = plan_shared(*c, *b, Hq);
+  if (most_tiles(p, *b, Hq / c->Hkv, c->Hkv) > INT32_MAX - (1 << 20) ||
+      static_cast<int64_t>(p.pre_row_blocks) * c->Hkv * p.pre_tiles > INT32_MAX - (1 << 20))
+    return set_error(QCF_ERR_SHAPE, "%s: the bounds allow more work than one call takes", who);
   return QCF_OK;
 }
 
@@ -520,7 +630,8 @@ size_t qcf_shared_prefix_attn_workspace_size(const qcf_paged_kv* cache, const qc
   BatchView b;
   if (check_attn("qcf_shared_prefix_attn_workspace_size", cache, batch, Hq, &c, &b) != QCF_OK) return 0;
   if (b.n_seq == 0 || b.n_rows == 0) return 0;
-  return parts_bytes(plan_shared(c, b, Hq), b, Hq, c.D);
+  Workspace w;
+  return workspace_layout(plan_shared(c, b, Hq), b, Hq, c.D, nullptr, &w);
 }
 
 qcf_status qcf_shared_prefix_attn(const qcf_paged_kv* cache, const qcf_paged_batch* batch, const void* q, int64_t q_stride,
@@ -540,15 +651,13 @@ qcf_status qcf_shared_prefix_attn(const qcf_paged_kv* cache, const qcf_paged_bat
   if (take_fault(2)) return set_error(QCF_ERR_WORKSPACE, "%s: injected short workspace", who);
   if (b.n_seq == 0 || b.n_rows == 0) return QCF_OK;
   const SharedPlan p = plan_shared(c, b, Hq);
-  const size_t need = parts_bytes(p, b, Hq, c.D);
-  if (need && (!ws || ws_bytes < need)) return set_error(QCF_ERR_WORKSPACE, "%s: workspace %zu < %zu", who, ws_bytes, need);
-  const size_t rows = static_cast<size_t>(p.pre_parts + p.own_parts) * b.n_rows * Hq;
-  const Parts parts{static_cast<float*>(ws),
-                    reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + align_up(rows * c.D * sizeof(float), 256))};
+  Workspace w;
+  const size_t need = workspace_layout(p, b, Hq, c.D, ws, &w);
+  if (!ws || ws_bytes < need) return set_error(QCF_ERR_WORKSPACE, "%s: workspace %zu < %zu", who, ws_bytes, need);
   const AttnArgs a{q, q_stride, cache->k, cache->v, o, lse, Hq, Hq / c.Hkv, scale * 1.4426950408889634f};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return cache->dtype == QCF_BF16 ? shared_prefix_attn_type<__nv_bfloat16>(cache, c, b, a, p, parts, st)
-                                  : shared_prefix_attn_type<__half>(cache, c, b, a, p, parts, st);
+  return cache->dtype == QCF_BF16 ? shared_prefix_attn_type<__nv_bfloat16>(cache, c, b, a, p, w, st)
+                                  : shared_prefix_attn_type<__half>(cache, c, b, a, p, w, st);
 }
 
 }  // extern "C"

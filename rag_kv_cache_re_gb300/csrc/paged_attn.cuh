@@ -18,30 +18,60 @@ struct AttnArgs {
 };
 
 // Every part (a range of keys of the prefix, or of a sequence's own tokens) of a row and head
-// leaves its unnormalised output, maximum and sum of powers of two; the combine kernel joins
-// them.  A row whose only part is its sequence's single own one is written at once.
-//   o   [part][n_rows][Hq][D] fp32      ml  [part][n_rows][Hq] (maximum, sum)
-struct Parts {
-  float* o;
-  float2* ml;
-};
-
+// leaves its unnormalised output (fp32 [D]), maximum and sum of powers of two; the combine kernel
+// joins them.  A row whose only part is the whole of its sequence is written to o at once.
+//
+// The prefix on tcgen05 (pre_tc): the key tiles of all (row block, KV head) units are dealt out
+// evenly, pre_share to a CTA; a part is the CTA's place among those that share the unit.
+// The stream (own tokens, and the prefix where tcgen05 does not take it): the 32-key tiles of all
+// (sequence, block of 16 score rows, KV head) units, dealt out in the same way over `workers`
+// warps, by lengths that are read on the device.  Part 0 of a unit has a slot per row; a later part
+// begins where a worker's share begins, so each worker has one slot for it.
 struct SharedPlan {
-  // own tokens: chunks of own_chunk keys (a multiple of the tile), at most own_parts of them
-  int own_chunk, own_parts, own_row_blocks;
-  // prefix: pre_parts slots per row.  On the warp-MMA kernel a part is a chunk of pre_chunk keys;
-  // on the tensor-core kernel the tiles of all (row block, KV head) units are dealt out evenly,
-  // pre_share to a CTA, and the part is the CTA's place among those that share the unit.
-  int pre_parts, pre_chunk, pre_row_blocks;
   bool pre_tc;
-  int pre_rows, pre_tiles, pre_share, pre_ctas;   // tensor-core kernel: rows of q per unit, key tiles
+  int pre_row_blocks, pre_rows, pre_tiles, pre_share, pre_ctas, pre_parts;
+  bool pre_stream;                   // the prefix is part of the stream
+  int stream_blocks, stream_tiles;   // its blocks of 16 score rows and key tiles
+  int ctas, workers;
 };
+constexpr int kStreamRows = 16;      // score rows of a stream unit
+constexpr int kStreamKeys = 32;      // keys of a tile
+constexpr int kMinShare = 2;         // tiles dealt to a worker at least
 
-size_t parts_bytes(const SharedPlan& p, const BatchView& b, int Hq, int D);
+struct Workspace {
+  float* tc_o;        // [pre_parts][n_rows][Hq][D]
+  float2* tc_ml;      // [pre_parts][n_rows][Hq]: maximum, sum
+  float* own_o;       // [n_rows][Hq][D]: part 0 of the own tokens
+  float2* own_ml;
+  float* pre_o;       // part 0 of a streamed prefix
+  float2* pre_ml;
+  float* spill_o;     // [workers][16][D]: the part a worker's share begins in the middle of
+  float2* spill_ml;
+  int* deal;          // [n_seq + 2]: first tile of each sequence, the total, tiles to a worker
+};
+size_t workspace_layout(const SharedPlan& p, const BatchView& b, int Hq, int D, void* base, Workspace* w);
 
 // The tensor-core kernel of the prefix (prefix_attn.cu): its parts of every row of the batch.
 qcf_status prefix_tc_launch(const qcf_paged_kv* cache, const PagedView& c, const BatchView& b, const AttnArgs& a,
-                            const SharedPlan& p, Parts parts, cudaStream_t st);
+                            const SharedPlan& p, const Workspace& w, cudaStream_t st);
+
+__device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+      ::"r"(smem_u32(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+// Tensor map of the pages: entries of a head, rows of a page, heads, pages; boxes of `rows` rows
+// and `cols` entries of one head and page.
+inline bool encode_pages(CUtensorMap* map, const void* base, const PagedView& c, int rows, int cols, CUtensorMapSwizzle sw) {
+  const uint64_t dims[4] = {static_cast<uint64_t>(c.D), static_cast<uint64_t>(1) << c.page_shift, static_cast<uint64_t>(c.Hkv),
+                            static_cast<uint64_t>(c.n_pages)};
+  const uint64_t strides[3] = {static_cast<uint64_t>(c.row_stride) * 2, static_cast<uint64_t>(c.head_stride) * 2,
+                               static_cast<uint64_t>(c.page_stride) * 2};
+  const uint32_t box[4] = {static_cast<uint32_t>(cols), static_cast<uint32_t>(rows), 1, 1};
+  return encode_tmap_4d(map, base, dims, strides, box, sw);
+}
 
 // m16n8k16 on warp tensor cores, both 16-bit types, fp32 sums.
 template <typename T>
@@ -69,15 +99,6 @@ template <>
 __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t smem, const void* src, bool take) {   // zeros when not taken
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(src), "r"(take ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // 32 lanes x 128 consecutive 32-bit columns in one load; the wait sits in the same statement so no

@@ -44,13 +44,6 @@ struct PreCfg {
   static constexpr int SMEM = 2 * TILE + 2 * STAGES * TILE + 512 + 1024;
 };
 
-__device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
-      ::"r"(smem_u32(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
-      : "memory");
-}
-
 // Instruction descriptor of kind::f16 with both operands of type T (see idesc_bf16_f32).
 template <typename T>
 constexpr uint32_t idesc_16(int M, int N, bool b_mn_major) {
@@ -89,10 +82,11 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kPreThreads, 1)
     prefix_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const __grid_constant__ CUtensorMap tmQ, const PagedView c, const BatchView b, const AttnArgs a,
-                       const SharedPlan p, const Parts parts, int total, unsigned int* status) {
+                       const SharedPlan p, const Workspace ws, int total, unsigned int* status) {
   using Cfg = PreCfg<D>;
   constexpr int ST = Cfg::STAGES;
   constexpr unsigned kAll = 0xffffffffu;
+  pdl_launch_dependents();   // the stream's CTAs take over SMs as this kernel leaves them
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* qbuf = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -418,9 +412,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (!mine) continue;
 #pragma unroll
         for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<float4*>(parts.o + at * D + cc * 32 + e) = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+          *reinterpret_cast<float4*>(ws.tc_o + at * D + cc * 32 + e) = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
       }
-      if (mine) parts.ml[at] = make_float2(m, l);
+      if (mine) ws.tc_ml[at] = make_float2(m, l);
       tc_fence_before();
     }
     if (!ok && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
@@ -435,20 +429,15 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 
 template <typename T, int D>
 static qcf_status prefix_tc_type(const qcf_paged_kv* cache, const PagedView& c, const BatchView& b, const AttnArgs& a,
-                                 const SharedPlan& p, Parts parts, cudaStream_t st) {
+                                 const SharedPlan& p, const Workspace& w, cudaStream_t st) {
   using Cfg = PreCfg<D>;
   CUtensorMap tk, tv, tq;
-  const int ps = 1 << c.page_shift;
-  const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(ps), static_cast<uint64_t>(c.Hkv),
-                            static_cast<uint64_t>(c.n_pages)};
-  const uint64_t strides[3] = {static_cast<uint64_t>(c.row_stride) * 2, static_cast<uint64_t>(c.head_stride) * 2,
-                               static_cast<uint64_t>(c.page_stride) * 2};
-  const uint32_t box[4] = {64, static_cast<uint32_t>(std::min(ps, kPreKeys)), 1, 1};
+  const int rows = std::min(1 << c.page_shift, kPreKeys);
   const uint64_t qd[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(b.n_rows)};
   const uint64_t qs[2] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(a.q_stride) * 2};
   const uint32_t qb[3] = {64, static_cast<uint32_t>(a.G), static_cast<uint32_t>(128 / a.G)};
-  if (!encode_tmap_4d(&tk, cache->k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_tmap_4d(&tv, cache->v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  if (!encode_pages(&tk, cache->k, c, rows, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_pages(&tv, cache->v, c, rows, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_tmap_3d(&tq, a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B))
     return set_error(QCF_ERR_CUDA, "qcf_shared_prefix_attn: tensor map encoding failed");
   static PerDevice<cudaError_t> smem_attr;
@@ -458,18 +447,18 @@ static qcf_status prefix_tc_type(const qcf_paged_kv* cache, const PagedView& c, 
   if (attr != cudaSuccess) return cuda_error(attr, "qcf_shared_prefix_attn: smem attribute");
   LaunchScope ls(KC_PREFIX_ATTN, st);
   const int total = p.pre_tiles * p.pre_row_blocks * c.Hkv;
-  prefix_attn_kernel<T, D><<<p.pre_ctas, kPreThreads, Cfg::SMEM, st>>>(tk, tv, tq, c, b, a, p, parts, total, device_status_ptr());
+  prefix_attn_kernel<T, D><<<p.pre_ctas, kPreThreads, Cfg::SMEM, st>>>(tk, tv, tq, c, b, a, p, w, total, device_status_ptr());
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? QCF_OK : cuda_error(e, "qcf_shared_prefix_attn: prefix launch");
 }
 
 qcf_status prefix_tc_launch(const qcf_paged_kv* cache, const PagedView& c, const BatchView& b, const AttnArgs& a,
-                            const SharedPlan& p, Parts parts, cudaStream_t st) {
+                            const SharedPlan& p, const Workspace& w, cudaStream_t st) {
   if (cache->dtype == QCF_BF16)
-    return c.D == 128 ? prefix_tc_type<__nv_bfloat16, 128>(cache, c, b, a, p, parts, st)
-                      : prefix_tc_type<__nv_bfloat16, 64>(cache, c, b, a, p, parts, st);
-  return c.D == 128 ? prefix_tc_type<__half, 128>(cache, c, b, a, p, parts, st)
-                    : prefix_tc_type<__half, 64>(cache, c, b, a, p, parts, st);
+    return c.D == 128 ? prefix_tc_type<__nv_bfloat16, 128>(cache, c, b, a, p, w, st)
+                      : prefix_tc_type<__nv_bfloat16, 64>(cache, c, b, a, p, w, st);
+  return c.D == 128 ? prefix_tc_type<__half, 128>(cache, c, b, a, p, w, st)
+                    : prefix_tc_type<__half, 64>(cache, c, b, a, p, w, st);
 }
 
 }  // namespace qcf
