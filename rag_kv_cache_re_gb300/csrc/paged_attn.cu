@@ -33,7 +33,7 @@ struct StreamCfg {
   static constexpr int BOX = kStreamKeys * COLS * 2;   // 32 keys x COLS entries
   static constexpr int TILE = BOXES * BOX;             // a K or V tile
   static constexpr int STAGES = D >= 64 ? 2 : 4;
-  static constexpr int WARPS = D == 128 ? 6 : D == 64 ? 13 : 12;   // 192 and 208 KB of rings (48 KB at head dim 16)
+  static constexpr int WARPS = D == 128 ? 6 : 12;      // 192 KB of rings (48 KB at head dim 16)
   static constexpr int RING = STAGES * 2 * TILE;       // of a warp
   static constexpr int FIXED = WARPS * (RING + STAGES * 8);
 };
@@ -382,33 +382,36 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
 
 // ------------------------------------------------------------------ joining the parts
 //
-// `per` warps (1, 2, 4 or 8) for each (row, head), more where a row may have many parts: lanes read
-// the parts' maxima and sums, every warp adds its share of the parts (lane: D / 32 output entries),
-// and the warps' sums meet in shared memory, always in the same order.  Launched while the kernels
-// before it run; what does not depend on them (the row's sequence) is found meanwhile.
-constexpr int kCombineWarps = 8;
+// `per` warps (1, 2, 4 or 8) for each (row, head), more where a row may have many parts.  A lane has
+// D / 32 output entries; four parts at a time are loaded, sums and statistics together, and added
+// with a running maximum; several warps' results meet in shared memory, always in the same order.
+// Launched while the kernels before it run; what does not depend on them (the row's sequence) is
+// found meanwhile.  Bound by latencies: position, deal, parts.
+constexpr int kCombineWarps = 8, kCombineBatch = 4;
 template <typename T, int D>
 __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const PagedView c, const BatchView b, const AttnArgs a,
                                                                            const SharedPlan p, const Workspace ws, int per) {
   constexpr int E = D >= 32 ? D / 32 : 1;
-  __shared__ float met[kCombineWarps][D + 1];   // a warp's sums, its normaliser
+  __shared__ float met[kCombineWarps][D + 2];   // a warp's sums, normaliser, maximum
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % per;
-  const int64_t pair = static_cast<int64_t>(blockIdx.x) * (kCombineWarps / per) + warp / per;
-  const int row = static_cast<int>(pair / a.Hq), h = static_cast<int>(pair - static_cast<int64_t>(row) * a.Hq);
+  const unsigned pair = blockIdx.x * static_cast<unsigned>(kCombineWarps / per) + warp / per;   // (row, head)
+  const int row = static_cast<int>(pair / a.Hq), h = static_cast<int>(pair - static_cast<unsigned>(row) * a.Hq);
   int seq = -1;
   SeqSpan s = {};
   if (row < b.n_rows) {
     seq = warp_seq_of_row(b, row);
     if (seq >= 0) s = seq_span(b, seq);
   }
+  const bool real = seq >= 0 && row < s.row0 + s.nq;
+  const int g = h / a.G, hh = h - g * a.G;
   pdl_wait();
-  bool live = seq >= 0 && row < s.row0 + s.nq;
   int n = 0, n_pre = 0, pre_cta = 0, pre_local = 0, own_cta = 0, rho = 0;
-  const int64_t at = pair;
-  if (live) {
-    const int g = h / a.G, hh = h - g * a.G, share = ws.deal[b.n_seq + 1];
+  if (real) {
+    const int share = ws.deal[b.n_seq + 1], mine = ws.deal[seq];
     // parts: the prefix's (on tcgen05, or of the stream), then the own tokens'
-    if (p.pre_tc) {   // the CTAs that share this row's unit
+    if (p.pre_even) {
+      n_pre = p.pre_parts;
+    } else if (p.pre_tc) {   // the CTAs that share this row's unit
       const int unit = g * p.pre_row_blocks + row / p.pre_rows;
       n_pre = ((unit + 1) * p.pre_tiles - 1) / p.pre_share - unit * p.pre_tiles / p.pre_share + 1;
     } else if (p.pre_stream) {
@@ -419,11 +422,12 @@ __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const
     }
     rho = (row - s.row0) * a.G + hh;
     const int tiles = (s.len + kStreamKeys - 1) / kStreamKeys;
-    const int first = ws.deal[seq] + (rho / kStreamRows * c.Hkv + g) * tiles;
+    const int first = mine + (rho / kStreamRows * c.Hkv + g) * tiles;
     own_cta = first / share;
     n = n_pre + (first + tiles - 1) / share - own_cta + 1;
-    live = n_pre > 0 || n > 1;   // else already written
+    if (n_pre == 0 && n == 1) n = 0;   // already written
   }
+  const int64_t at = pair;
   // the place of part i's sums: row of tc_o, of own_o or pre_o, or of spill_o
   auto part = [&](int i, const float*& o) {
     if (i < n_pre && p.pre_tc) {
@@ -445,48 +449,55 @@ __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const
   Vec<float, E> sum;
 #pragma unroll
   for (int e = 0; e < E; ++e) sum.v[e] = 0.f;
-  if (live) {
-    const float* po = nullptr;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, part(i, po)->x);
+  const int share = (n + per - 1) / per, i_end = min(n, (sub + 1) * share);
+  const int d0 = D >= 32 ? lane * E : lane % D;
+  for (int i0 = sub * share; i0 < i_end; i0 += kCombineBatch) {
+    float2 ml[kCombineBatch];
+    Vec<float, E> v[kCombineBatch];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const int share = (n + per - 1) / per, i_end = min(n, (sub + 1) * share);
-    for (int i0 = sub * share; i0 < i_end; i0 += 32) {
-      float f = 0.f;
-      if (i0 + lane < i_end) {
-        const float2 ml = *part(i0 + lane, po);
-        f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-        L += ml.y * f;
+    for (int j = 0; j < kCombineBatch; ++j)
+      if (i0 + j < i_end) {
+        const float* o;
+        ml[j] = *part(i0 + j, o);
+        v[j] = *reinterpret_cast<const Vec<float, E>*>(o + d0);
       }
-      const int m = min(32, i_end - i0);
-#pragma unroll 4
-      for (int i = 0; i < m; ++i) {
-        const float fi = __shfl_sync(0xffffffffu, f, i);
-        const float* o = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(po), i));
-        if (fi == 0.f || lane * E >= D) continue;   // a part without keys for this row
-        const Vec<float, E> v = *reinterpret_cast<const Vec<float, E>*>(o + lane * E);
 #pragma unroll
-        for (int e = 0; e < E; ++e) sum.v[e] = fmaf(v.v[e], fi, sum.v[e]);
+    for (int j = 0; j < kCombineBatch; ++j)
+      if (i0 + j < i_end && ml[j].x != -INFINITY) {   // a part without keys for this row has no sums
+        const float top = fmaxf(M, ml[j].x);
+        const float f = exp2f(ml[j].x - top), k = M == -INFINITY ? 0.f : exp2f(M - top);
+        M = top;
+        L = fmaf(ml[j].y, f, L * k);
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum.v[e] = fmaf(v[j].v[e], f, sum.v[e] * k);
       }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
   }
   if (per > 1) {
     if (lane * E < D)
 #pragma unroll
       for (int e = 0; e < E; ++e) met[warp][lane * E + e] = sum.v[e];
-    if (lane == 0) met[warp][D] = L;
+    if (lane == 0) {
+      met[warp][D] = L;
+      met[warp][D + 1] = M;
+    }
     __syncthreads();
     if (sub > 0) return;
+    float top = M;
+    for (int w = 1; w < per; ++w) top = fmaxf(top, met[warp + w][D + 1]);
+    const float k = M == -INFINITY ? 0.f : exp2f(M - top);
+    L *= k;
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum.v[e] *= k;
     for (int w = 1; w < per; ++w) {
+      const float mw = met[warp + w][D + 1], f = mw == -INFINITY ? 0.f : exp2f(mw - top);
+      L = fmaf(met[warp + w][D], f, L);
       if (lane * E < D)
 #pragma unroll
-        for (int e = 0; e < E; ++e) sum.v[e] += met[warp + w][lane * E + e];
-      L += met[warp + w][D];
+        for (int e = 0; e < E; ++e) sum.v[e] = fmaf(met[warp + w][lane * E + e], f, sum.v[e]);
     }
+    M = top;
   }
-  if (!live) return;
+  if (n == 0) return;
   const float inv = L > 0.f ? 1.f / L : 0.f;
   if (lane * E < D) {
     Vec<T, E> r;
@@ -509,10 +520,20 @@ static SharedPlan plan_shared(const PagedView& c, const BatchView& b, int Hq) {
     p.pre_rows = 2 * (128 / G);
     p.pre_row_blocks = (b.n_rows + p.pre_rows - 1) / p.pre_rows;
     p.pre_tiles = (b.prefix_len + 127) / 128;
-    const int64_t total = static_cast<int64_t>(p.pre_row_blocks) * c.Hkv * p.pre_tiles;
+    const int64_t units = static_cast<int64_t>(p.pre_row_blocks) * c.Hkv, total = units * p.pre_tiles;
     p.pre_share = static_cast<int>(std::max<int64_t>((total + sms - 1) / sms, std::min(2, p.pre_tiles)));
-    p.pre_ctas = static_cast<int>((total + p.pre_share - 1) / p.pre_share);
-    p.pre_parts = (p.pre_tiles + p.pre_share - 2) / p.pre_share + 1;   // CTAs that one unit can meet
+    // Each unit in equal parts where that takes no CTA more than a tile longer (a second unit costs a
+    // CTA about three): the KV heads then read the same rows at the same time, which share DRAM pages
+    // (32 rows, 64 heads, 131072 keys: see prefix_attn.cu).
+    const int each = units <= sms ? (p.pre_tiles + static_cast<int>(sms / units) - 1) / static_cast<int>(sms / units) : INT32_MAX;
+    if (each <= p.pre_share + 1) {
+      p.pre_even = true;
+      p.pre_parts = (p.pre_tiles + std::max(each, p.pre_share) - 1) / std::max(each, p.pre_share);
+      p.pre_ctas = static_cast<int>(units * p.pre_parts);
+    } else {
+      p.pre_ctas = static_cast<int>((total + p.pre_share - 1) / p.pre_share);
+      p.pre_parts = (p.pre_tiles + p.pre_share - 2) / p.pre_share + 1;   // CTAs that one unit can meet
+    }
   } else if (b.prefix_len > 0) {
     p.pre_stream = true;
     p.stream_blocks = static_cast<int>((static_cast<int64_t>(b.n_rows) * G + kStreamRows - 1) / kStreamRows);
@@ -587,7 +608,7 @@ static qcf_status shared_prefix_attn_launch(const qcf_paged_kv* cache, const Pag
   // parts of a row, about (lengths are known on the device): a warp for every few of them
   const int64_t share = std::max<int64_t>(kMinShare, most_tiles(p, b, a.G, c.Hkv) / p.workers);
   const int64_t many = p.pre_parts + (p.stream_tiles + (b.max_len + kStreamKeys - 1) / kStreamKeys) / share + 1;
-  const int per = many <= 4 ? 1 : many <= 8 ? 2 : many <= 16 ? 4 : 8;
+  const int per = many <= 16 ? 1 : many <= 32 ? 2 : many <= 64 ? 4 : 8;
   const int64_t pairs = static_cast<int64_t>(b.n_rows) * a.Hq, at_once = kCombineWarps / per;
   e = launch_pdl(batch_combine_kernel<T, D>, dim3(static_cast<unsigned>((pairs + at_once - 1) / at_once)), dim3(kCombineWarps * 32), 0,
                  st, c, b, a, p, w, per);

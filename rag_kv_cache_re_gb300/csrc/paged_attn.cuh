@@ -21,14 +21,15 @@ struct AttnArgs {
 // leaves its unnormalised output (fp32 [D]), maximum and sum of powers of two; the combine kernel
 // joins them.  A row whose only part is the whole of its sequence is written to o at once.
 //
-// The prefix on tcgen05 (pre_tc): the key tiles of all (row block, KV head) units are dealt out
-// evenly, pre_share to a CTA; a part is the CTA's place among those that share the unit.
+// The prefix on tcgen05 (pre_tc): either every (row block, KV head) unit in pre_parts equal parts, a
+// CTA each (pre_even), or the key tiles of all units dealt out evenly, pre_share to a CTA, a part
+// being the CTA's place among those that share the unit.
 // The stream (own tokens, and the prefix where tcgen05 does not take it): the 32-key tiles of all
 // (sequence, block of 16 score rows, KV head) units, dealt out in the same way over `workers`
 // warps, by lengths that are read on the device.  Part 0 of a unit has a slot per row; a later part
 // begins where a worker's share begins, so each worker has one slot for it.
 struct SharedPlan {
-  bool pre_tc;
+  bool pre_tc, pre_even;
   int pre_row_blocks, pre_rows, pre_tiles, pre_share, pre_ctas, pre_parts;
   bool pre_stream;                   // the prefix is part of the stream
   int stream_blocks, stream_tiles;   // its blocks of 16 score rows and key tiles
@@ -99,6 +100,11 @@ template <>
 __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// Named barrier over the `count` threads that meet at `id`.
+__device__ __forceinline__ void bar_sync(int id, int count) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
 // 32 lanes x 128 consecutive 32-bit columns in one load; the wait sits in the same statement so no

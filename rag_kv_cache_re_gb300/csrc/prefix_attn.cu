@@ -40,8 +40,9 @@ template <int D>
 struct PreCfg {
   static constexpr int BOXES = D / 64;
   static constexpr int TILE = BOXES * kPreBox;               // a K, V or Q tile
-  static constexpr int STAGES = D == 128 ? 2 : 4;            // of K and of V
-  static constexpr int SMEM = 2 * TILE + 2 * STAGES * TILE + 512 + 1024;
+  static constexpr int K_STAGES = D == 128 ? 3 : 5;          // K runs a tile ahead of V
+  static constexpr int V_STAGES = D == 128 ? 2 : 5;
+  static constexpr int SMEM = (2 + K_STAGES + V_STAGES) * TILE + 512 + 1024;
 };
 
 // Instruction descriptor of kind::f16 with both operands of type T (see idesc_bf16_f32).
@@ -61,8 +62,15 @@ struct Segments {
   int n_rows;
   __device__ Segments(const SharedPlan& plan, int n_rows_, int total)
       : cta(static_cast<int>(blockIdx.x)), p(plan), n_rows(n_rows_) {
-    cur = cta * p.pre_share;
-    end = min(total, cur + p.pre_share);
+    if (p.pre_even) {   // CTA = (part, unit): the units' same parts start together
+      const int units = total / p.pre_tiles, unit = cta % units, part = cta / units;
+      cur = unit * p.pre_tiles + static_cast<int>(static_cast<int64_t>(part) * p.pre_tiles / p.pre_parts);
+      end = unit * p.pre_tiles + static_cast<int>(static_cast<int64_t>(part + 1) * p.pre_tiles / p.pre_parts);
+      cta = part;
+    } else {
+      cur = cta * p.pre_share;
+      end = min(total, cur + p.pre_share);
+    }
   }
   __device__ bool next(Segment& s) {
     if (cur >= end) return false;
@@ -72,31 +80,39 @@ struct Segments {
     s.g = unit / p.pre_row_blocks;
     s.row0 = (unit - s.g * p.pre_row_blocks) * p.pre_rows;
     s.nb = s.row0 + p.pre_rows / 2 < n_rows ? 2 : 1;
-    s.part = cta - unit * p.pre_tiles / p.pre_share;
+    s.part = p.pre_even ? cta : cta - unit * p.pre_tiles / p.pre_share;
     cur += s.nt;
     return true;
   }
 };
 
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* smem_src, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];"
+               ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(smem_src)), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+// The shared memory of this thread's bulk stores has been read.
+__device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kPreThreads, 1)
     prefix_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                       const __grid_constant__ CUtensorMap tmQ, const PagedView c, const BatchView b, const AttnArgs a,
+                       const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO, const PagedView c, const BatchView b, const AttnArgs a,
                        const SharedPlan p, const Workspace ws, int total, unsigned int* status) {
   using Cfg = PreCfg<D>;
-  constexpr int ST = Cfg::STAGES;
+  constexpr int KST = Cfg::K_STAGES, VST = Cfg::V_STAGES;
   constexpr unsigned kAll = 0xffffffffu;
   pdl_launch_dependents();   // the stream's CTAs take over SMs as this kernel leaves them
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* qbuf = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   uint8_t* kbuf = qbuf + 2 * Cfg::TILE;
-  uint8_t* vbuf = kbuf + ST * Cfg::TILE;
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(vbuf + ST * Cfg::TILE);
-  uint64_t* k_empty = k_full + ST;
-  uint64_t* v_full = k_empty + ST;
-  uint64_t* v_empty = v_full + ST;
-  uint64_t* s_full = v_empty + ST;    // [a, b]
+  uint8_t* vbuf = kbuf + KST * Cfg::TILE;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(vbuf + VST * Cfg::TILE);
+  uint64_t* k_empty = k_full + KST;
+  uint64_t* v_full = k_empty + KST;
+  uint64_t* v_empty = v_full + VST;
+  uint64_t* s_full = v_empty + VST;    // [a, b]
   uint64_t* p_ready = s_full + 2;     // [a, b][first, last 64 keys]
   uint64_t* o_done = p_ready + 4;     // [a, b]
   uint64_t* q_full = o_done + 2;
@@ -107,9 +123,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < ST; ++s) {
+    for (int s = 0; s < KST; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 2);
+    }
+    for (int s = 0; s < VST; ++s) {
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 2);
     }
@@ -121,7 +139,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       mbar_init(&mma_end[x], 1);
     }
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 2);
+    mbar_init(q_empty, 4);   // both issuers' products have read Q, both tiles' sums have left through its memory
     mbar_init(v_tail, 1);
     fence_mbar_init();
   }
@@ -146,6 +164,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       uint8_t* ring = is_k ? kbuf : vbuf;
       uint64_t* full = is_k ? k_full : v_full;
       uint64_t* empty = is_k ? k_empty : v_empty;
+      const int ST = is_k ? KST : VST;
       if (lane == 0) {
         tma_prefetch_desc(map);
         if (is_k) tma_prefetch_desc(&tmQ);
@@ -235,7 +254,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (due) mbar_arrive(&p_ready[2 * (1 - x)]);
       };
       auto scores = [&](int tile, bool due) {   // S_x = Q_x K^T
-        const uint64_t kd = k_desc + tile % ST * (Cfg::TILE >> 4);
+        const uint64_t kd = k_desc + tile % KST * (Cfg::TILE >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           if (kk == D / 16 - 4) pass(due);
@@ -243,18 +262,19 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           umma_f16(tmem + x * 128, q_desc + at, kd + at, idesc_s, kk > 0 ? 1u : 0u);
         }
         umma_commit(&s_full[x]);
-        umma_commit(&k_empty[tile % ST]);
+        umma_commit(&k_empty[tile % KST]);
       };
-      auto wait_k = [&](int tile) { return mbar_wait(&k_full[tile % ST], (tile / ST) & 1); };
+      auto wait_k = [&](int tile) { return mbar_wait(&k_full[tile % KST], (tile / KST) & 1); };
       for (; ok && segs.next(s); ++k) {
         if (x >= s.nb) {   // nothing in tile b: hand on what it would have read (every phase of a barrier is waited for)
           if (!(ok = mbar_wait(q_full, k & 1))) break;
           mbar_arrive(q_empty);
+          mbar_arrive(q_empty);   // for the softmax of b too
           for (int i = 0; i < s.nt; ++i, ++n) {
             if (!(ok = wait_k(n))) break;
-            mbar_arrive(&k_empty[n % ST]);
-            if (!(ok = mbar_wait(&v_full[n % ST], (n / ST) & 1))) break;
-            mbar_arrive(&v_empty[n % ST]);
+            mbar_arrive(&k_empty[n % KST]);
+            if (!(ok = mbar_wait(&v_full[n % VST], (n / VST) & 1))) break;
+            mbar_arrive(&v_empty[n % VST]);
           }
           continue;
         }
@@ -263,8 +283,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         scores(n, false);
         for (int i = 0; i < s.nt; ++i, ++n) {
           const bool more = i + 1 < s.nt;
-          if (!(ok = mbar_wait(&v_full[n % ST], (n / ST) & 1) && (!more || wait_k(n + 1)))) break;
-          const uint64_t vd = v_desc + n % ST * (Cfg::TILE >> 4);
+          if (!(ok = mbar_wait(&v_full[n % VST], (n / VST) & 1) && (!more || wait_k(n + 1)))) break;
+          const uint64_t vd = v_desc + n % VST * (Cfg::TILE >> 4);
           auto weigh = [&](int half) {   // O_x += P_x V over 64 keys
             tc_fence_after();
 #pragma unroll
@@ -286,7 +306,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             pass(due);
             umma_commit(&o_done[x]);
           }
-          umma_commit(&v_empty[n % ST]);   // after the scores: a commit costs this thread more than a product
+          umma_commit(&v_empty[n % VST]);   // after the scores: a commit costs this thread more than a product
         }
         umma_commit(q_empty);
       }
@@ -403,20 +423,42 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         break;
       }
       tc_fence_after();
-      const bool mine = pl < per && row < b.n_rows;
-      const int64_t at = (static_cast<int64_t>(s.part) * b.n_rows + (mine ? row : 0)) * a.Hq + s.g * a.G + h;
+      // The sums leave through the tile's Q memory (its products are done: O is), 32 columns a box, by
+      // tiled TMA stores of whole lines, rows behind the batch cut off; written row by row from the
+      // threads that hold them they took 7 us.
+      if (pl < per && row < b.n_rows)
+        ws.tc_ml[(static_cast<int64_t>(s.part) * b.n_rows + row) * a.Hq + s.g * a.G + h] = make_float2(m, l);
+      uint8_t* stage = qbuf + x * Cfg::TILE;
 #pragma unroll 1
-      for (int cc = 0; cc < D / 32; ++cc) {
-        float ov[32];
-        tmem_ld32(o_tm + cc * 32, ov);
-        if (!mine) continue;
+      for (int c0 = 0; c0 < D / 32; c0 += Cfg::BOXES) {
+        if (c0 > 0) {
+          if (rho == 0) bulk_wait_read0();
+          bar_sync(1 + x, 128);
+        }
 #pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<float4*>(ws.tc_o + at * D + cc * 32 + e) = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+        for (int cc = 0; cc < Cfg::BOXES; ++cc) {
+          float ov[32];
+          tmem_ld32(o_tm + (c0 + cc) * 32, ov);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(stage + cc * kPreBox + sw128_off(rho, e / 4)) = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+        }
+        fence_proxy_async_smem();
+        bar_sync(1 + x, 128);
+        if (rho == 0) {
+#pragma unroll
+          for (int cc = 0; cc < Cfg::BOXES; ++cc)
+            tma_store_4d(&tmO, stage + cc * kPreBox, (c0 + cc) * 32, s.g * a.G, s.row0 + x * per, s.part);
+          bulk_commit_group();
+        }
       }
-      if (mine) ws.tc_ml[at] = make_float2(m, l);
       tc_fence_before();
+      if (rho == 0) {
+        bulk_wait_read0();
+        mbar_arrive(q_empty);
+      }
     }
+    if (rho == 0) bulk_wait_group0();
     if (!ok && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
   }
   tc_fence_before();
@@ -431,14 +473,20 @@ template <typename T, int D>
 static qcf_status prefix_tc_type(const qcf_paged_kv* cache, const PagedView& c, const BatchView& b, const AttnArgs& a,
                                  const SharedPlan& p, const Workspace& w, cudaStream_t st) {
   using Cfg = PreCfg<D>;
-  CUtensorMap tk, tv, tq;
+  CUtensorMap tk, tv, tq, to;
   const int rows = std::min(1 << c.page_shift, kPreKeys);
   const uint64_t qd[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(b.n_rows)};
   const uint64_t qs[2] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(a.q_stride) * 2};
+  const uint64_t od[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(b.n_rows),
+                          static_cast<uint64_t>(p.pre_parts)};
+  const uint64_t os[3] = {static_cast<uint64_t>(D) * 4, static_cast<uint64_t>(a.Hq) * D * 4,
+                          static_cast<uint64_t>(b.n_rows) * a.Hq * D * 4};
+  const uint32_t ob[4] = {32, static_cast<uint32_t>(a.G), static_cast<uint32_t>(128 / a.G), 1};
   const uint32_t qb[3] = {64, static_cast<uint32_t>(a.G), static_cast<uint32_t>(128 / a.G)};
   if (!encode_pages(&tk, cache->k, c, rows, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_pages(&tv, cache->v, c, rows, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_tmap_3d(&tq, a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B))
+      !encode_tmap_3d(&tq, a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tmap_4d(&to, w.tc_o, od, os, ob, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_FLOAT32))
     return set_error(QCF_ERR_CUDA, "qcf_shared_prefix_attn: tensor map encoding failed");
   static PerDevice<cudaError_t> smem_attr;
   const cudaError_t attr = smem_attr.get(current_device(), [] {
@@ -447,7 +495,7 @@ static qcf_status prefix_tc_type(const qcf_paged_kv* cache, const PagedView& c, 
   if (attr != cudaSuccess) return cuda_error(attr, "qcf_shared_prefix_attn: smem attribute");
   LaunchScope ls(KC_PREFIX_ATTN, st);
   const int total = p.pre_tiles * p.pre_row_blocks * c.Hkv;
-  prefix_attn_kernel<T, D><<<p.pre_ctas, kPreThreads, Cfg::SMEM, st>>>(tk, tv, tq, c, b, a, p, w, total, device_status_ptr());
+  prefix_attn_kernel<T, D><<<p.pre_ctas, kPreThreads, Cfg::SMEM, st>>>(tk, tv, tq, to, c, b, a, p, w, total, device_status_ptr());
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? QCF_OK : cuda_error(e, "qcf_shared_prefix_attn: prefix launch");
 }
