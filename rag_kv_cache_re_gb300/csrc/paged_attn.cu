@@ -122,9 +122,7 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* rings = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-  // Launched while the prefix kernel runs, on whose results nothing here depends; the join, launched
-  // in the same way, waits for this kernel alone, so this one ends after the prefix kernel has.
-  pdl_launch_dependents();
+  pdl_launch_dependents();   // the prefix kernel takes over SMs as this one leaves them
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, worker = static_cast<int>(blockIdx.x) * Cfg::WARPS + warp;
   uint8_t* ring = rings + warp * Cfg::RING;                                                     // stage: K tile, V tile
   uint64_t* full = reinterpret_cast<uint64_t*>(rings + Cfg::WARPS * Cfg::RING) + warp * ST;
@@ -377,25 +375,25 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
     flag_status(status, QCF_DEV_TIMEOUT);
     for (int e = n; e < cn; ++e) mbar_wait(&full[e % ST], (e / ST) & 1);   // no copy is in flight when the warp ends
   }
-  pdl_wait();
 }
 
 // ------------------------------------------------------------------ joining the parts
 //
-// `per` warps (1, 2, 4 or 8) for each (row, head), more where a row may have many parts.  A lane has
-// D / 32 output entries; four parts at a time are loaded, sums and statistics together, and added
-// with a running maximum; several warps' results meet in shared memory, always in the same order.
-// Launched while the kernels before it run; what does not depend on them (the row's sequence) is
-// found meanwhile.  Bound by latencies: position, deal, parts.
-constexpr int kCombineWarps = 8, kCombineBatch = 4;
-template <typename T, int D>
+// A warp joins HB neighbouring heads of a row (they share their KV head, so their parts): a lane has
+// 16-byte pieces of them, and a batch of parts is loaded, sums and statistics together, before it is
+// added with a running maximum.  `per` warps (1, 2, 4 or 8; more than one only with HB = 1) share the
+// parts of one head where there may be many; their results meet in shared memory, always in the
+// same order.  Launched while the kernels before it run; what does not depend on them (the row's
+// sequence) is found meanwhile.  Bound by latencies: row, deal, one for each batch of parts.
+constexpr int kCombineWarps = 8;
+template <typename T, int D, int HB>
 __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const PagedView c, const BatchView b, const AttnArgs a,
                                                                            const SharedPlan p, const Workspace ws, int per) {
-  constexpr int E = D >= 32 ? D / 32 : 1;
-  __shared__ float met[kCombineWarps][D + 2];   // a warp's sums, normaliser, maximum
+  constexpr int NV = HB * D > 128 ? HB * D / 128 : 1, BATCH = HB > 1 ? 2 : 4;
+  __shared__ float met[HB > 1 ? 1 : kCombineWarps][D + 2];   // a warp's sums, normaliser, maximum
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % per;
-  const unsigned pair = blockIdx.x * static_cast<unsigned>(kCombineWarps / per) + warp / per;   // (row, head)
-  const int row = static_cast<int>(pair / a.Hq), h = static_cast<int>(pair - static_cast<unsigned>(row) * a.Hq);
+  const unsigned unit = blockIdx.x * static_cast<unsigned>(kCombineWarps / per) + warp / per, groups = a.Hq / HB;
+  const int row = static_cast<int>(unit / groups), h = static_cast<int>(unit - row * groups) * HB;
   int seq = -1;
   SeqSpan s = {};
   if (row < b.n_rows) {
@@ -412,8 +410,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const
     if (p.pre_even) {
       n_pre = p.pre_parts;
     } else if (p.pre_tc) {   // the CTAs that share this row's unit
-      const int unit = g * p.pre_row_blocks + row / p.pre_rows;
-      n_pre = ((unit + 1) * p.pre_tiles - 1) / p.pre_share - unit * p.pre_tiles / p.pre_share + 1;
+      const int u = g * p.pre_row_blocks + row / p.pre_rows;
+      n_pre = ((u + 1) * p.pre_tiles - 1) / p.pre_share - u * p.pre_tiles / p.pre_share + 1;
     } else if (p.pre_stream) {
       const int r = row * a.G + hh, first = (r / kStreamRows * c.Hkv + g) * p.stream_tiles;
       pre_cta = first / share;
@@ -427,8 +425,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const
     n = n_pre + (first + tiles - 1) / share - own_cta + 1;
     if (n_pre == 0 && n == 1) n = 0;   // already written
   }
-  const int64_t at = pair;
-  // the place of part i's sums: row of tc_o, of own_o or pre_o, or of spill_o
+  const int64_t at = static_cast<int64_t>(row) * a.Hq + h;
+  // the place of part i's sums of head h (the other heads' follow): row of tc_o, of own_o or pre_o, or of spill_o
   auto part = [&](int i, const float*& o) {
     if (i < n_pre && p.pre_tc) {
       const int64_t r = static_cast<int64_t>(i) * b.n_rows * a.Hq + at;
@@ -445,67 +443,75 @@ __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const
     o = ws.spill_o + r * D;
     return ws.spill_ml + r;
   };
-  float M = -INFINITY, L = 0.f;
-  Vec<float, E> sum;
+  const bool has = lane * 4 < HB * D;   // this lane's pieces: entries 128 k + 4 lane of the HB heads
+  float M[NV], L[NV], sum[NV][4];
 #pragma unroll
-  for (int e = 0; e < E; ++e) sum.v[e] = 0.f;
-  const int share = (n + per - 1) / per, i_end = min(n, (sub + 1) * share);
-  const int d0 = D >= 32 ? lane * E : lane % D;
-  for (int i0 = sub * share; i0 < i_end; i0 += kCombineBatch) {
-    float2 ml[kCombineBatch];
-    Vec<float, E> v[kCombineBatch];
+  for (int k = 0; k < NV; ++k) {
+    M[k] = -INFINITY;
+    L[k] = sum[k][0] = sum[k][1] = sum[k][2] = sum[k][3] = 0.f;
+  }
+  const int each = (n + per - 1) / per, i_end = min(n, (sub + 1) * each);
+  for (int i0 = sub * each; i0 < i_end; i0 += BATCH) {
+    float2 ml[BATCH][NV];
+    float4 v[BATCH][NV];
 #pragma unroll
-    for (int j = 0; j < kCombineBatch; ++j)
-      if (i0 + j < i_end) {
+    for (int j = 0; j < BATCH; ++j)
+      if (i0 + j < i_end && has) {
         const float* o;
-        ml[j] = *part(i0 + j, o);
-        v[j] = *reinterpret_cast<const Vec<float, E>*>(o + d0);
+        const float2* m = part(i0 + j, o);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          ml[j][k] = m[(k * 128 + lane * 4) / D];
+          v[j][k] = *reinterpret_cast<const float4*>(o + k * 128 + lane * 4);
+        }
       }
 #pragma unroll
-    for (int j = 0; j < kCombineBatch; ++j)
-      if (i0 + j < i_end && ml[j].x != -INFINITY) {   // a part without keys for this row has no sums
-        const float top = fmaxf(M, ml[j].x);
-        const float f = exp2f(ml[j].x - top), k = M == -INFINITY ? 0.f : exp2f(M - top);
-        M = top;
-        L = fmaf(ml[j].y, f, L * k);
+    for (int j = 0; j < BATCH; ++j)
 #pragma unroll
-        for (int e = 0; e < E; ++e) sum.v[e] = fmaf(v[j].v[e], f, sum.v[e] * k);
+      for (int k = 0; k < NV; ++k)
+        if (i0 + j < i_end && has && ml[j][k].x != -INFINITY) {   // a part without keys for this row has no sums
+          const float top = fmaxf(M[k], ml[j][k].x);
+          const float f = exp2f(ml[j][k].x - top), e = M[k] == -INFINITY ? 0.f : exp2f(M[k] - top);
+          M[k] = top;
+          L[k] = fmaf(ml[j][k].y, f, L[k] * e);
+          sum[k][0] = fmaf(v[j][k].x, f, sum[k][0] * e);
+          sum[k][1] = fmaf(v[j][k].y, f, sum[k][1] * e);
+          sum[k][2] = fmaf(v[j][k].z, f, sum[k][2] * e);
+          sum[k][3] = fmaf(v[j][k].w, f, sum[k][3] * e);
+        }
+  }
+  if constexpr (HB == 1) {
+    if (per > 1) {
+      if (has)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) met[warp][lane * 4 + e] = sum[0][e];
+      if (lane == 0) {
+        met[warp][D] = L[0];
+        met[warp][D + 1] = M[0];
       }
-  }
-  if (per > 1) {
-    if (lane * E < D)
+      __syncthreads();
+      if (sub > 0) return;
+      float top = -INFINITY;
+      for (int w = 0; w < per; ++w) top = fmaxf(top, met[warp + w][D + 1]);
+      M[0] = top;
+      L[0] = sum[0][0] = sum[0][1] = sum[0][2] = sum[0][3] = 0.f;
+      for (int w = 0; w < per; ++w) {
+        const float mw = met[warp + w][D + 1], f = mw == -INFINITY ? 0.f : exp2f(mw - top);
+        L[0] = fmaf(met[warp + w][D], f, L[0]);
+        if (has)
 #pragma unroll
-      for (int e = 0; e < E; ++e) met[warp][lane * E + e] = sum.v[e];
-    if (lane == 0) {
-      met[warp][D] = L;
-      met[warp][D + 1] = M;
+          for (int e = 0; e < 4; ++e) sum[0][e] = fmaf(met[warp + w][lane * 4 + e], f, sum[0][e]);
+      }
     }
-    __syncthreads();
-    if (sub > 0) return;
-    float top = M;
-    for (int w = 1; w < per; ++w) top = fmaxf(top, met[warp + w][D + 1]);
-    const float k = M == -INFINITY ? 0.f : exp2f(M - top);
-    L *= k;
-#pragma unroll
-    for (int e = 0; e < E; ++e) sum.v[e] *= k;
-    for (int w = 1; w < per; ++w) {
-      const float mw = met[warp + w][D + 1], f = mw == -INFINITY ? 0.f : exp2f(mw - top);
-      L = fmaf(met[warp + w][D], f, L);
-      if (lane * E < D)
-#pragma unroll
-        for (int e = 0; e < E; ++e) sum.v[e] = fmaf(met[warp + w][lane * E + e], f, sum.v[e]);
-    }
-    M = top;
   }
-  if (n == 0) return;
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  if (lane * E < D) {
-    Vec<T, E> r;
+  if (n == 0 || !has) return;
 #pragma unroll
-    for (int e = 0; e < E; ++e) r.v[e] = from_f32<T>(sum.v[e] * inv);
-    *reinterpret_cast<Vec<T, E>*>(static_cast<T*>(a.o) + at * D + lane * E) = r;
+  for (int k = 0; k < NV; ++k) {
+    const float inv = L[k] > 0.f ? 1.f / L[k] : 0.f;
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + at * D + k * 128 + lane * 4) =
+        make_uint2(pack2<T>(sum[k][0] * inv, sum[k][1] * inv), pack2<T>(sum[k][2] * inv, sum[k][3] * inv));
+    if (a.lse && (k * 128 + lane * 4) % D == 0) a.lse[at + (k * 128 + lane * 4) / D] = (M[k] + log2f(L[k])) * 0.69314718055994531f;
   }
-  if (a.lse && lane == 0) a.lse[at] = (M + log2f(L)) * 0.69314718055994531f;
 }
 
 // ------------------------------------------------------------------ host
@@ -584,8 +590,6 @@ static cudaError_t stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, c
   if (attr != cudaSuccess) return attr;
   LaunchScope ls(KC_OWN_ATTN, st);
   const dim3 grid(p.ctas), block(StreamCfg<D>::WARPS * 32);
-  if (p.pre_tc)
-    return launch_pdl(stream_attn_kernel<T, D>, grid, block, stream_smem<D>(b.n_seq), st, tk, tv, c, b, a, p, w, device_status_ptr());
   stream_attn_kernel<T, D><<<grid, block, stream_smem<D>(b.n_seq), st>>>(tk, tv, c, b, a, p, w, device_status_ptr());
   return cudaGetLastError();
 }
@@ -593,10 +597,6 @@ static cudaError_t stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, c
 template <typename T, int D>
 static qcf_status shared_prefix_attn_launch(const qcf_paged_kv* cache, const PagedView& c, const BatchView& b, const AttnArgs& a,
                                             const SharedPlan& p, const Workspace& w, cudaStream_t st) {
-  if (p.pre_tc) {
-    const qcf_status s = prefix_tc_launch(cache, c, b, a, p, w, st);
-    if (s != QCF_OK) return s;
-  }
   CUtensorMap tk, tv;
   const int rows = std::min(1 << c.page_shift, kStreamKeys);
   const CUtensorMapSwizzle sw = D >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
@@ -604,14 +604,22 @@ static qcf_status shared_prefix_attn_launch(const qcf_paged_kv* cache, const Pag
     return set_error(QCF_ERR_CUDA, "qcf_shared_prefix_attn: tensor map encoding failed");
   cudaError_t e = stream_launch<T, D>(tk, tv, c, b, a, p, w, st);
   if (e != cudaSuccess) return cuda_error(e, "qcf_shared_prefix_attn: launch");
+  if (p.pre_tc) {
+    const qcf_status s = prefix_tc_launch(cache, c, b, a, p, w, st);
+    if (s != QCF_OK) return s;
+  }
   LaunchScope ls(KC_BATCH_COMBINE, st);
   // parts of a row, about (lengths are known on the device): a warp for every few of them
   const int64_t share = std::max<int64_t>(kMinShare, most_tiles(p, b, a.G, c.Hkv) / p.workers);
   const int64_t many = p.pre_parts + (p.stream_tiles + (b.max_len + kStreamKeys - 1) / kStreamKeys) / share + 1;
   const int per = many <= 16 ? 1 : many <= 32 ? 2 : many <= 64 ? 4 : 8;
-  const int64_t pairs = static_cast<int64_t>(b.n_rows) * a.Hq, at_once = kCombineWarps / per;
-  e = launch_pdl(batch_combine_kernel<T, D>, dim3(static_cast<unsigned>((pairs + at_once - 1) / at_once)), dim3(kCombineWarps * 32), 0,
-                 st, c, b, a, p, w, per);
+  // many rows: a warp takes four heads of a KV head and looks their row up once (12512 pairs: 17 us with
+  // one head a warp)
+  const int64_t pairs = static_cast<int64_t>(b.n_rows) * a.Hq;
+  const bool four = per == 1 && a.G % 4 == 0 && pairs >= 32 * num_sms();
+  const int64_t units = four ? pairs / 4 : pairs, at_once = kCombineWarps / per;
+  e = launch_pdl(four ? batch_combine_kernel<T, D, 4> : batch_combine_kernel<T, D, 1>,
+                 dim3(static_cast<unsigned>((units + at_once - 1) / at_once)), dim3(kCombineWarps * 32), 0, st, c, b, a, p, w, per);
   return e == cudaSuccess ? QCF_OK : cuda_error(e, "qcf_shared_prefix_attn: combine launch");
 }
 

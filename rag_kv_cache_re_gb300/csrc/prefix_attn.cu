@@ -102,7 +102,15 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   using Cfg = PreCfg<D>;
   constexpr int KST = Cfg::K_STAGES, VST = Cfg::V_STAGES;
   constexpr unsigned kAll = 0xffffffffu;
-  pdl_launch_dependents();   // the stream's CTAs take over SMs as this kernel leaves them
+  // Launched while the stream kernel runs, on whose results nothing here depends; the join, launched
+  // in the same way, waits for this kernel alone, so this one ends after the stream has.
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmO);
+  }
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* qbuf = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -165,10 +173,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       uint64_t* full = is_k ? k_full : v_full;
       uint64_t* empty = is_k ? k_empty : v_empty;
       const int ST = is_k ? KST : VST;
-      if (lane == 0) {
-        tma_prefetch_desc(map);
-        if (is_k) tma_prefetch_desc(&tmQ);
-      }
       const int ps = min(1 << c.page_shift, kPreKeys), boxes = kPreKeys / ps;   // rows of a box, pages of a tile
       // this lane's page of key tile t: its id, n_pages (which reads as zeros) where there is none
       auto page_of = [&](int t) {
@@ -467,6 +471,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  pdl_wait();
 }
 
 template <typename T, int D>
@@ -495,8 +500,8 @@ static qcf_status prefix_tc_type(const qcf_paged_kv* cache, const PagedView& c, 
   if (attr != cudaSuccess) return cuda_error(attr, "qcf_shared_prefix_attn: smem attribute");
   LaunchScope ls(KC_PREFIX_ATTN, st);
   const int total = p.pre_tiles * p.pre_row_blocks * c.Hkv;
-  prefix_attn_kernel<T, D><<<p.pre_ctas, kPreThreads, Cfg::SMEM, st>>>(tk, tv, tq, to, c, b, a, p, w, total, device_status_ptr());
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(prefix_attn_kernel<T, D>, dim3(p.pre_ctas), dim3(kPreThreads), Cfg::SMEM, st, tk, tv, tq, to, c, b, a,
+                                   p, w, total, device_status_ptr());
   return e == cudaSuccess ? QCF_OK : cuda_error(e, "qcf_shared_prefix_attn: prefix launch");
 }
 
