@@ -548,7 +548,7 @@ typedef struct qcf_paged_kv {
  * host gives upper bounds.  A sequence that breaks one (or has fewer tokens than new rows,
  * or rows outside [0, n_rows)) is left out and sets QCF_DEV_BAD_INDEX. */
 typedef struct qcf_paged_batch {
-  int n_seq;                    /* <= 65535; attention: <= 4096 */
+  int n_seq;                    /* <= 65535; attention: <= 2048 */
   int n_rows;                   /* rows of q, k_new, v_new, o, padding included */
   int max_q;                    /* bound on a sequence's new rows */
   int max_len;                  /* bound on kv_len, <= table_stride * page_size */

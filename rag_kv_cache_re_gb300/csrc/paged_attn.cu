@@ -12,7 +12,7 @@
 
 namespace qcf {
 
-constexpr int kMaxBatchSeqs = 4096;   // each CTA of the stream keeps the first tile of every sequence
+constexpr int kMaxBatchSeqs = 2048;   // each CTA of the stream keeps 12 bytes of every sequence
 
 // ------------------------------------------------------------------ the stream, on warp tensor cores
 //
@@ -20,8 +20,8 @@ constexpr int kMaxBatchSeqs = 4096;   // each CTA of the stream keeps the first 
 // sequence against its own keys, or 16 rows of the whole batch against the prefix.  The 32-key
 // tiles of all units are dealt out evenly to persistent warps, whatever the lengths are, and every
 // warp works alone: it keeps its own ring of K and V tiles full by tiled TMA (one box per page and
-// 64 columns; pages behind a length, or outside the cache, read as zeros), a step ahead of the tile
-// that it scores and across the borders of units, and no warp waits for another.  (Four warps that
+// 64 columns; pages behind a length, or outside the cache, read as zeros), ahead of the tile that it
+// scores and across the borders of units, and no warp waits for another.  (Four warps that
 // split a tile and met at two barriers took 1900 cycles per 64 keys of head dim 64, and 90 us for
 // 386 MB of uneven sequences.)
 // The maximum moves only when it grows by more than 2^8: the weights then stay below 2^8 (exact in
@@ -39,7 +39,7 @@ struct StreamCfg {
 };
 template <int D>
 static size_t stream_smem(int n_seq) {
-  return 1024 + StreamCfg<D>::FIXED + (static_cast<size_t>(n_seq) + 2) * sizeof(int);
+  return 1024 + StreamCfg<D>::FIXED + (3 * static_cast<size_t>(n_seq) + 3) * sizeof(int);
 }
 
 // Byte offset of 8 entries at column col of a key in a K or V tile, as TMA lays it out.
@@ -55,6 +55,14 @@ __device__ __forceinline__ int stream_tiles_of(const SeqSpan& s, int G, int Hkv)
   return s.nq == 0 ? 0 : (s.len + kStreamKeys - 1) / kStreamKeys * ((s.nq * G + kStreamRows - 1) / kStreamRows) * Hkv;
 }
 
+// What every CTA keeps of the batch in shared memory: small loads from global memory take 2 us once
+// the rings are streaming, so nothing between two units may wait for one.
+struct StreamDeal {
+  const int* start;   // [n_seq + 2]: first tile of each sequence, the total, tiles to a worker
+  const int* row0;    // [n_seq + 1]
+  const int* len;     // [n_seq]
+};
+
 // One worker's share of one unit.
 struct StreamSeg {
   bool pre;            // a unit of the prefix
@@ -67,7 +75,8 @@ struct StreamSeg {
 };
 struct StreamWalk {
   int cur, end, seq;
-  __device__ StreamWalk(const BatchView& b, const int* start, int worker) {
+  __device__ StreamWalk(const BatchView& b, const StreamDeal& deal, int worker) {
+    const int* start = deal.start;
     const int total = start[b.n_seq], share = start[b.n_seq + 1];
     cur = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(worker) * share));
     end = min(total, cur + share);
@@ -78,8 +87,9 @@ struct StreamWalk {
     }
     seq = lo;
   }
-  __device__ bool next(StreamSeg& s, const BatchView& b, const SharedPlan& p, const int* start, int worker, int G, int Hkv) {
+  __device__ bool next(StreamSeg& s, const BatchView& b, const SharedPlan& p, const StreamDeal& deal, int worker, int G, int Hkv) {
     if (cur >= end) return false;
+    const int* start = deal.start;
     s.pre = cur < start[0];
     int first = 0;
     if (s.pre) {
@@ -90,11 +100,10 @@ struct StreamWalk {
       s.table = b.prefix_pages;
     } else {
       while (start[seq + 1] <= cur) ++seq;
-      const SeqSpan q = seq_span(b, seq);
-      s.row0 = q.row0;
-      s.nq = q.nq;
-      s.len = q.len;
-      s.tiles = (q.len + kStreamKeys - 1) / kStreamKeys;
+      s.row0 = deal.row0[seq];
+      s.nq = deal.row0[seq + 1] - s.row0;
+      s.len = deal.len[seq];
+      s.tiles = (s.len + kStreamKeys - 1) / kStreamKeys;
       s.table = b.page_table + static_cast<int64_t>(seq) * b.table_stride;
       first = start[seq];
     }
@@ -123,11 +132,21 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* rings = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   pdl_launch_dependents();   // the prefix kernel takes over SMs as this one leaves them
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, worker = static_cast<int>(blockIdx.x) * Cfg::WARPS + warp;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int worker = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);   // few workers: one to an SM first
   uint8_t* ring = rings + warp * Cfg::RING;                                                     // stage: K tile, V tile
   uint64_t* full = reinterpret_cast<uint64_t*>(rings + Cfg::WARPS * Cfg::RING) + warp * ST;
-  int* start = reinterpret_cast<int*>(rings + Cfg::WARPS * (Cfg::RING + ST * 8));               // [n_seq + 2]
+  int* start = reinterpret_cast<int*>(rings + Cfg::WARPS * (Cfg::RING + ST * 8));
+  int* row0 = start + b.n_seq + 2;
+  int* len = row0 + b.n_seq + 1;
+  const StreamDeal deal{start, row0, len};
 
+  {   // the page table and the queries on their way to L2 while the deal is found
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x, tables = static_cast<int64_t>(b.n_seq) * b.table_stride / 32;
+    const int lines = a.Hq * D / 64;   // 128-byte lines of a row of q
+    if (i < tables) prefetch_l2(b.page_table + i * 32);
+    if (i < static_cast<int64_t>(b.n_rows) * lines) prefetch_l2(static_cast<const T*>(a.q) + i / lines * a.q_stride + i % lines * 64);
+  }
   // ---- the deal: first tile of every sequence
   {
     __shared__ int sums[Cfg::WARPS];
@@ -144,6 +163,9 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
       if (q.bad && blockIdx.x == 0) flag_status(status, QCF_DEV_BAD_INDEX);
       const int n = stream_tiles_of(q, a.G, c.Hkv);
       start[s] = n;
+      row0[s] = q.row0;
+      if (s == b.n_seq - 1) row0[s + 1] = b.row_start[s + 1];
+      len[s] = q.len;
       mine += n;
     }
     int run = mine;
@@ -170,32 +192,41 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
       for (int s = threadIdx.x; s < b.n_seq + 2; s += THREADS) ws.deal[s] = start[s];
   }
 
-  // ---- copies: a walk of its own, up to ST - 1 tiles ahead.  The lanes hold the page ids of the next
-  // 32 groups of 8 keys (8 tiles) of the unit; n_pages, which reads as zeros, behind its length or
-  // outside the cache.
-  StreamWalk ahead(b, start, worker);
-  StreamSeg cs;
-  int ci = 0, cn = 0, ids = 0;   // tile of the segment, tiles issued, page id of this lane's group
-  unsigned out = 0, bad = 0;     // groups outside the cache: of the next 8 tiles, of the tiles issued (4 bits each, tile % 8)
-  cs.use = 0;
-  bool copies = true;
+  // ---- copies: a walk of its own, up to ST tiles ahead of the scores.  The lanes hold the page ids of
+  // a window of 32 groups of 8 keys (8 tiles) of a unit, and those of the next window, asked for when
+  // the window before began.
+  StreamWalk ahead(b, deal, worker);
+  StreamSeg cs, ns;              // units of this window and the next
+  int ci = 0, ni = 0, ids = 0, nids = 0, cn = 0;   // tile of the unit, page id of this lane's group; tiles issued
+  unsigned out = 0, bad = 0;     // groups outside the cache: of the window, of the tiles issued (4 bits each, tile % 8)
+  bool copies = ahead.next(cs, b, p, deal, worker, a.G, c.Hkv), more = copies;
+  StreamWalk walk = ahead;       // of the scores
+  StreamSeg s = cs;
+  bool live = copies;
+  auto ask = [&](const StreamSeg& u, int i) {   // page ids of the window at tile i of u
+    const int key = (u.t0 + i) * kStreamKeys + lane * 8;
+    return key < u.len ? u.table[key >> c.page_shift] : c.n_pages;
+  };
+  auto next_window = [&]() {     // ns, ni: the window behind cs, ci
+    ns = cs;
+    ni = ci + 8;
+    while (more && ni >= ns.use) {   // units without a tile to read are passed over
+      more = ahead.next(ns, b, p, deal, worker, a.G, c.Hkv);
+      ni = 0;
+    }
+    if (more) nids = ask(ns, ni);
+  };
+  auto enter_window = [&]() {    // the ids of cs at tile ci: n_pages, which reads as zeros, behind the length or outside the cache
+    const bool wrong = ids < 0 || ids > c.n_pages || (ids == c.n_pages && (cs.t0 + ci) * kStreamKeys + lane * 8 < cs.len);
+    if (wrong) {
+      flag_status(status, QCF_DEV_BAD_INDEX);
+      ids = c.n_pages;
+    }
+    out = __ballot_sync(kAll, wrong);
+  };
   const int ps = min(1 << c.page_shift, kStreamKeys), pages = kStreamKeys / ps;   // rows of a box, pages of a tile
   auto copy_next = [&]() {
-    while (copies && ci == cs.use) {   // segments without a tile to read are passed over
-      copies = ahead.next(cs, b, p, start, worker, a.G, c.Hkv);
-      ci = 0;
-    }
     if (!copies) return;
-    if ((ci & 7) == 0) {
-      const int key = (cs.t0 + ci) * kStreamKeys + lane * 8;
-      ids = key < cs.len ? cs.table[key >> c.page_shift] : c.n_pages;
-      const bool wrong = key < cs.len && (ids < 0 || ids >= c.n_pages);
-      if (wrong) {
-        flag_status(status, QCF_DEV_BAD_INDEX);
-        ids = c.n_pages;
-      }
-      out = __ballot_sync(kAll, wrong);
-    }
     const int at = (cn & 7) * 4;
     bad = (bad & ~(15u << at)) | (out >> ((ci & 7) * 4) & 15u) << at;
     const int st = cn % ST, page = lane & 3, key0 = (cs.t0 + ci) * kStreamKeys;
@@ -209,36 +240,54 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
       for (int h = 0; h < Cfg::BOXES; ++h)
         tma_load_4d(dst + h * Cfg::BOX, map, &full[st], h * Cfg::COLS, key0 & ((1 << c.page_shift) - 1), cs.g, id);
     }
-    ++ci;
     ++cn;
+    ++ci;
+    if ((ci & 7) == 0 || ci == cs.use) {
+      copies = more;
+      if (!copies) return;
+      cs = ns;
+      ci = ni;
+      ids = nids;
+      enter_window();
+      next_window();
+    }
   };
+  const int mi = lane >> 3, mr = lane & 7, qc = (lane & 3) * 2, r_lo = lane >> 2;
+  uint32_t qf[D / 16][4];
+  auto load_q = [&](const StreamSeg& u) {
+    const int end = min(u.rho0 + kStreamRows, u.nq * a.G), lo = u.rho0 + r_lo, hi = lo + 8;
+    auto q_row = [&](int rho) {
+      return static_cast<const T*>(a.q) + static_cast<int64_t>(u.row0 + rho / a.G) * a.q_stride +
+             static_cast<int64_t>(u.g * a.G + rho % a.G) * D;
+    };
+    const T* ql = lo < end ? q_row(lo) : nullptr;
+    const T* qh = hi < end ? q_row(hi) : nullptr;
 #pragma unroll
-  for (int i = 0; i < ST - 1; ++i) copy_next();
+    for (int ks = 0; ks < D / 16; ++ks) {
+      qf[ks][0] = ql ? *reinterpret_cast<const uint32_t*>(ql + ks * 16 + qc) : 0u;
+      qf[ks][1] = qh ? *reinterpret_cast<const uint32_t*>(qh + ks * 16 + qc) : 0u;
+      qf[ks][2] = ql ? *reinterpret_cast<const uint32_t*>(ql + ks * 16 + qc + 8) : 0u;
+      qf[ks][3] = qh ? *reinterpret_cast<const uint32_t*>(qh + ks * 16 + qc + 8) : 0u;
+    }
+  };
+  if (live) {
+    while (more && ci >= cs.use) more = ahead.next(cs, b, p, deal, worker, a.G, c.Hkv);   // the first unit with a tile to read
+    copies = more;
+    if (copies) ids = ask(cs, 0);
+    load_q(s);
+    if (copies) {
+      enter_window();
+      next_window();
+    }
+#pragma unroll
+    for (int i = 0; i < ST; ++i) copy_next();
+  }
 
   // ---- scores
-  const int mi = lane >> 3, mr = lane & 7, qc = (lane & 3) * 2, r_lo = lane >> 2;
-  StreamWalk walk(b, start, worker);
-  StreamSeg s;
   int n = 0;
   bool ok = true;
-  while (ok && walk.next(s, b, p, start, worker, a.G, c.Hkv)) {
+  while (live) {
     const int end = min(s.rho0 + kStreamRows, s.nq * a.G), lo = s.rho0 + r_lo, hi = lo + 8;   // this thread's score rows
-    uint32_t qf[D / 16][4];
-    {
-      auto q_row = [&](int rho) {
-        return static_cast<const T*>(a.q) + static_cast<int64_t>(s.row0 + rho / a.G) * a.q_stride +
-               static_cast<int64_t>(s.g * a.G + rho % a.G) * D;
-      };
-      const T* ql = lo < end ? q_row(lo) : nullptr;
-      const T* qh = hi < end ? q_row(hi) : nullptr;
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        qf[ks][0] = ql ? *reinterpret_cast<const uint32_t*>(ql + ks * 16 + qc) : 0u;
-        qf[ks][1] = qh ? *reinterpret_cast<const uint32_t*>(qh + ks * 16 + qc) : 0u;
-        qf[ks][2] = ql ? *reinterpret_cast<const uint32_t*>(ql + ks * 16 + qc + 8) : 0u;
-        qf[ks][3] = qh ? *reinterpret_cast<const uint32_t*>(qh + ks * 16 + qc + 8) : 0u;
-      }
-    }
     // the last key a row sees: all of the prefix, or the own token of its position
     const int lim_lo = s.pre ? s.len : s.len - s.nq + lo / a.G, lim_hi = s.pre ? s.len : s.len - s.nq + hi / a.G;
     const int lim_min = s.pre ? s.len : s.len - s.nq + s.rho0 / a.G;
@@ -249,7 +298,6 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
 
     for (int i = 0; i < s.use; ++i, ++n) {
       const int st = n % ST, kb = (s.t0 + i) * kStreamKeys;
-      copy_next();   // into the stage of tile n - 1, which every lane has left
       const unsigned gone = bad >> ((n & 7) * 4) & 15u;   // its groups of 8 keys outside the cache
       if (!__all_sync(kAll, mbar_wait(&full[st], (n / ST) & 1))) {
         ok = false;
@@ -336,6 +384,7 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
         }
       }
       __syncwarp();
+      copy_next();   // into the stage that every lane has left
     }
     if (!ok) break;
 #pragma unroll
@@ -344,7 +393,10 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
       l_hi += __shfl_xor_sync(kAll, l_hi, o);
     }
 
-    // ---- the rows' sums leave: as a part, or finished
+    // ---- the rows' sums leave, as a part or finished, while the next unit's queries come
+    StreamSeg next;
+    live = walk.next(next, b, p, deal, worker, a.G, c.Hkv);
+    if (live) load_q(next);
     const bool only = b.prefix_len == 0 && s.nt == s.tiles;
     float* part_o = s.part > 0 ? ws.spill_o + static_cast<int64_t>(worker) * kStreamRows * D : s.pre ? ws.pre_o : ws.own_o;
     float2* part_ml = s.part > 0 ? ws.spill_ml + static_cast<int64_t>(worker) * kStreamRows : s.pre ? ws.pre_ml : ws.own_ml;
@@ -370,6 +422,7 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
         if (qc == 0) part_ml[slot] = make_float2(m, l);
       }
     }
+    s = next;
   }
   if (!ok) {
     flag_status(status, QCF_DEV_TIMEOUT);

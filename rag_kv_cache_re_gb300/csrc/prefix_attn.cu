@@ -462,7 +462,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         mbar_arrive(q_empty);
       }
     }
-    if (rho == 0) bulk_wait_group0();
     if (!ok && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
   }
   tc_fence_before();
