@@ -73,50 +73,71 @@ struct StreamSeg {
   int part;
   const int32_t* table;
 };
+// Walks a worker's share.  Only the first unit is found by division; every other begins at its first
+// tile, behind the one before.
 struct StreamWalk {
-  int cur, end, seq;
-  __device__ StreamWalk(const BatchView& b, const StreamDeal& deal, int worker) {
+  int cur, end, seq, seq_end;   // tiles; the sequence and where it ends (the prefix: seq -1)
+  StreamSeg at;
+  __device__ void enter(const BatchView& b, const SharedPlan& p, const StreamDeal& deal) {   // the sequence that holds tile cur
+    at.pre = seq < 0;
+    if (at.pre) {
+      at.row0 = 0;
+      at.nq = b.n_rows;
+      at.len = b.prefix_len;
+      at.tiles = p.stream_tiles;
+      at.table = b.prefix_pages;
+      seq_end = deal.start[0];
+    } else {
+      at.row0 = deal.row0[seq];
+      at.nq = deal.row0[seq + 1] - at.row0;
+      at.len = deal.len[seq];
+      at.tiles = (at.len + kStreamKeys - 1) / kStreamKeys;
+      at.table = b.page_table + static_cast<int64_t>(seq) * b.table_stride;
+      seq_end = deal.start[seq + 1];
+    }
+    at.g = at.rho0 = 0;
+  }
+  __device__ StreamWalk(const BatchView& b, const SharedPlan& p, const StreamDeal& deal, int worker, int Hkv) {
     const int* start = deal.start;
     const int total = start[b.n_seq], share = start[b.n_seq + 1];
     cur = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(worker) * share));
     end = min(total, cur + share);
-    int lo = 0, hi = b.n_seq;   // the first sequence whose successor starts behind cur
-    while (lo < hi) {
+    at.t0 = at.part = 0;
+    if (cur >= end) return;
+    int lo = -1, hi = b.n_seq;   // the last sequence that begins at or before cur (-1: the prefix), of those with tiles
+    while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (start[mid + 1] > cur) hi = mid; else lo = mid + 1;
+      if (start[mid] <= cur) lo = mid; else hi = mid;
     }
     seq = lo;
+    enter(b, p, deal);
+    const int first = seq < 0 ? 0 : start[seq], u = (cur - first) / at.tiles;
+    at.t0 = cur - first - u * at.tiles;
+    at.g = u % Hkv;
+    at.rho0 = u / Hkv * kStreamRows;
+    if (at.t0 > 0) at.part = worker - (cur - at.t0) / share;
   }
-  __device__ bool next(StreamSeg& s, const BatchView& b, const SharedPlan& p, const StreamDeal& deal, int worker, int G, int Hkv) {
+  __device__ bool next(StreamSeg& s, const BatchView& b, const SharedPlan& p, const AttnArgs& a, const StreamDeal& deal, int Hkv) {
     if (cur >= end) return false;
-    const int* start = deal.start;
-    s.pre = cur < start[0];
-    int first = 0;
-    if (s.pre) {
-      s.row0 = 0;
-      s.nq = b.n_rows;
-      s.len = b.prefix_len;
-      s.tiles = p.stream_tiles;
-      s.table = b.prefix_pages;
-    } else {
-      while (start[seq + 1] <= cur) ++seq;
-      s.row0 = deal.row0[seq];
-      s.nq = deal.row0[seq + 1] - s.row0;
-      s.len = deal.len[seq];
-      s.tiles = (s.len + kStreamKeys - 1) / kStreamKeys;
-      s.table = b.page_table + static_cast<int64_t>(seq) * b.table_stride;
-      first = start[seq];
+    at.nt = min(at.tiles - at.t0, end - cur);
+    const int reach =
+        at.pre ? at.len : at.len - at.nq + min(at.nq, div_g(a, at.rho0 + kStreamRows - 1) + 1);   // keys any row sees
+    at.use = max(0, min(at.nt, (reach + kStreamKeys - 1) / kStreamKeys - at.t0));
+    s = at;
+    cur += at.nt;
+    at.t0 = at.part = 0;
+    if (cur < end) {
+      if (cur < seq_end) {
+        if (++at.g == Hkv) {
+          at.g = 0;
+          at.rho0 += kStreamRows;
+        }
+      } else {
+        do ++seq;
+        while (deal.start[seq + 1] <= cur);
+        enter(b, p, deal);
+      }
     }
-    const int u = (cur - first) / s.tiles;
-    first += u * s.tiles;
-    s.t0 = cur - first;
-    s.nt = min(s.tiles - s.t0, end - cur);
-    s.g = u % Hkv;
-    s.rho0 = u / Hkv * kStreamRows;
-    s.part = worker - first / start[b.n_seq + 1];
-    const int reach = s.pre ? s.len : s.len - s.nq + min(s.nq, (s.rho0 + kStreamRows - 1) / G + 1);   // keys any row sees
-    s.use = max(0, min(s.nt, (reach + kStreamKeys - 1) / kStreamKeys - s.t0));
-    cur += s.nt;
     return true;
   }
 };
@@ -195,11 +216,11 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
   // ---- copies: a walk of its own, up to ST tiles ahead of the scores.  The lanes hold the page ids of
   // a window of 32 groups of 8 keys (8 tiles) of a unit, and those of the next window, asked for when
   // the window before began.
-  StreamWalk ahead(b, deal, worker);
+  StreamWalk ahead(b, p, deal, worker, c.Hkv);
   StreamSeg cs, ns;              // units of this window and the next
   int ci = 0, ni = 0, ids = 0, nids = 0, cn = 0;   // tile of the unit, page id of this lane's group; tiles issued
   unsigned out = 0, bad = 0;     // groups outside the cache: of the window, of the tiles issued (4 bits each, tile % 8)
-  bool copies = ahead.next(cs, b, p, deal, worker, a.G, c.Hkv), more = copies;
+  bool copies = ahead.next(cs, b, p, a, deal, c.Hkv), more = copies;
   StreamWalk walk = ahead;       // of the scores
   StreamSeg s = cs;
   bool live = copies;
@@ -211,7 +232,7 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
     ns = cs;
     ni = ci + 8;
     while (more && ni >= ns.use) {   // units without a tile to read are passed over
-      more = ahead.next(ns, b, p, deal, worker, a.G, c.Hkv);
+      more = ahead.next(ns, b, p, a, deal, c.Hkv);
       ni = 0;
     }
     if (more) nids = ask(ns, ni);
@@ -257,8 +278,9 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
   auto load_q = [&](const StreamSeg& u) {
     const int end = min(u.rho0 + kStreamRows, u.nq * a.G), lo = u.rho0 + r_lo, hi = lo + 8;
     auto q_row = [&](int rho) {
-      return static_cast<const T*>(a.q) + static_cast<int64_t>(u.row0 + rho / a.G) * a.q_stride +
-             static_cast<int64_t>(u.g * a.G + rho % a.G) * D;
+      const int r = div_g(a, rho);
+      return static_cast<const T*>(a.q) + static_cast<int64_t>(u.row0 + r) * a.q_stride +
+             static_cast<int64_t>(u.g * a.G + rho - r * a.G) * D;
     };
     const T* ql = lo < end ? q_row(lo) : nullptr;
     const T* qh = hi < end ? q_row(hi) : nullptr;
@@ -271,7 +293,7 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
     }
   };
   if (live) {
-    while (more && ci >= cs.use) more = ahead.next(cs, b, p, deal, worker, a.G, c.Hkv);   // the first unit with a tile to read
+    while (more && ci >= cs.use) more = ahead.next(cs, b, p, a, deal, c.Hkv);   // the first unit with a tile to read
     copies = more;
     if (copies) ids = ask(cs, 0);
     load_q(s);
@@ -289,8 +311,8 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
   while (live) {
     const int end = min(s.rho0 + kStreamRows, s.nq * a.G), lo = s.rho0 + r_lo, hi = lo + 8;   // this thread's score rows
     // the last key a row sees: all of the prefix, or the own token of its position
-    const int lim_lo = s.pre ? s.len : s.len - s.nq + lo / a.G, lim_hi = s.pre ? s.len : s.len - s.nq + hi / a.G;
-    const int lim_min = s.pre ? s.len : s.len - s.nq + s.rho0 / a.G;
+    const int lim_lo = s.pre ? s.len : s.len - s.nq + div_g(a, lo), lim_hi = s.pre ? s.len : s.len - s.nq + div_g(a, hi);
+    const int lim_min = s.pre ? s.len : s.len - s.nq + div_g(a, s.rho0);
     float m_lo = -INFINITY, m_hi = -INFINITY, l_lo = 0.f, l_hi = 0.f;
     float acc[D / 8][4];
 #pragma unroll
@@ -395,7 +417,7 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
 
     // ---- the rows' sums leave, as a part or finished, while the next unit's queries come
     StreamSeg next;
-    live = walk.next(next, b, p, deal, worker, a.G, c.Hkv);
+    live = walk.next(next, b, p, a, deal, c.Hkv);
     if (live) load_q(next);
     const bool only = b.prefix_len == 0 && s.nt == s.tiles;
     float* part_o = s.part > 0 ? ws.spill_o + static_cast<int64_t>(worker) * kStreamRows * D : s.pre ? ws.pre_o : ws.own_o;
@@ -405,7 +427,8 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
       const int rho = half ? hi : lo;
       if (rho >= end) continue;
       const float m = half ? m_hi : m_lo, l = half ? l_hi : l_lo;
-      const int64_t place = static_cast<int64_t>(s.row0 + rho / a.G) * a.Hq + s.g * a.G + rho % a.G;
+      const int r = div_g(a, rho);
+      const int64_t place = static_cast<int64_t>(s.row0 + r) * a.Hq + s.g * a.G + rho - r * a.G;
       const int64_t slot = s.part > 0 ? static_cast<int64_t>(rho - s.rho0) : place;
       if (only) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -736,7 +759,8 @@ qcf_status qcf_shared_prefix_attn(const qcf_paged_kv* cache, const qcf_paged_bat
   Workspace w;
   const size_t need = workspace_layout(p, b, Hq, c.D, ws, &w);
   if (!ws || ws_bytes < need) return set_error(QCF_ERR_WORKSPACE, "%s: workspace %zu < %zu", who, ws_bytes, need);
-  const AttnArgs a{q, q_stride, cache->k, cache->v, o, lse, Hq, Hq / c.Hkv, scale * 1.4426950408889634f};
+  const AttnArgs a{q, q_stride, cache->k, cache->v, o, lse, Hq, Hq / c.Hkv,
+                   static_cast<uint32_t>(((1ull << 32) + Hq / c.Hkv - 1) / (Hq / c.Hkv)), scale * 1.4426950408889634f};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return cache->dtype == QCF_BF16 ? shared_prefix_attn_type<__nv_bfloat16>(cache, c, b, a, p, w, st)
                                   : shared_prefix_attn_type<__half>(cache, c, b, a, p, w, st);

@@ -14,8 +14,13 @@ struct AttnArgs {
   void* o;
   float* lse;
   int Hq, G;          // G = Hq / Hkv
+  uint32_t g_mul;     // ceil(2^32 / G): n / G as a product, for n < 2^28 (an integer division takes a warp over 100 cycles)
   float scale_log2;   // scale * log2(e): logits are kept in powers of two
 };
+
+__device__ __forceinline__ int div_g(const AttnArgs& a, int n) {
+  return a.G == 1 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), a.g_mul));
+}
 
 // Every part (a range of keys of the prefix, or of a sequence's own tokens) of a row and head
 // leaves its unnormalised output (fp32 [D]), maximum and sum of powers of two; the combine kernel
