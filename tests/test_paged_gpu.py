@@ -293,6 +293,12 @@ ATTN_CASES = [  # new, lens, prefix, Hq, Hkv, D, page
     ([1, 40], [260, 100], 515, 7, 1, 64, 16),
     ([20, 1, 1], [20, 3000, 1], 260, 32, 16, 64, 64),
     ([1] * 200, [1 + i % 5 for i in range(200)], 6000, 8, 2, 64, 16),
+    ([97] * 8, [100 + 29 * i for i in range(8)], 1000, 32, 8, 128, 16),     # units of the prefix dealt out, the last row block half empty
+    ([61, 3, 70], [61, 900, 70], 2000, 48, 3, 64, 32),                      # 16 heads a KV head
+    ([5] * 9, [5 + 40 * i for i in range(9)], 400, 15, 5, 128, 8),          # 3 heads a KV head: rows left over in every tile
+    ([1] * 700, [1 + (37 * i) % 90 for i in range(700)], 131, 2, 1, 128, 8),
+    ([300], [300], 64, 4, 1, 128, 64),                                      # a long question: early rows see few of its keys
+    ([1] * 40, [1 + 11 * i for i in range(40)], 90, 8, 8, 16, 16),          # head dim 16 with more rows than a tile
 ]
 
 
@@ -319,6 +325,57 @@ def test_shared_prefix_attn_growing_logits(Q):
         ramp = torch.linspace(0.05, 6.0, 2000, device=DEV)[:, None, None]
         bt.rows(bt.k)[bt.prefix_at()] = (ramp * torch.ones(2000, 2, D, device=DEV)).to(torch.bfloat16)
         check_attention(Q, bt, 8)
+
+
+def test_shared_prefix_attn_many_sequences(Q):
+    """As many sequences as a call takes; most of one token, some empty."""
+    n = 2048
+    new = [0 if i % 7 == 3 else 1 for i in range(n)]
+    lens = [q + (i * 13) % 5 for i, q in enumerate(new)]
+    bt = R.Batch(new, lens, 40, 1, 64, 8, "rows", torch.bfloat16, seed=21).fill()
+    q = bt.randn(bt.n_rows, 2, 64)
+    cache, batch = bt.bind(Q)
+    got = Q.qcf_shared_prefix_attn(cache, batch, q, 0.125)
+    # every sequence alone is too many calls of the reference: gather all keys and mask
+    at = bt.prefix_at()
+    K, V = bt.rows(bt.k)[at][:, 0].double(), bt.rows(bt.v)[at][:, 0].double()
+    seq = torch.tensor([i for i, x in enumerate(new) if x], device=DEV)
+    pos = torch.arange(8, device=DEV)
+    page = bt.table.long()[seq][:, pos // 8]
+    live = pos < bt.kv_len[seq][:, None]
+    Ko = torch.where(live[..., None], bt.rows(bt.k)[page, pos % 8][:, :, 0].double(), 0.0)
+    Vo = torch.where(live[..., None], bt.rows(bt.v)[page, pos % 8][:, :, 0].double(), 0.0)
+    x = torch.cat([torch.einsum("nhd,jd->nhj", q.double(), K), torch.einsum("nhd,njd->nhj", q.double(), Ko).masked_fill(~live[:, None], -math.inf)], -1) * 0.125
+    p = torch.softmax(x, -1)
+    ref = torch.einsum("nhj,jd->nhd", p[..., :40], V) + torch.einsum("nhj,njd->nhd", p[..., 40:], Vo)
+    A = torch.einsum("nhj,jd->nhd", p[..., :40], V.abs()) + torch.einsum("nhj,njd->nhd", p[..., 40:], Vo.abs())
+    # half a step of the weights and of the output; the 32-bit errors of _paged_reference.attention stay below 2^-13 here
+    # (magnitudes of a logit's sum below 64 * 4 * 4 * 0.125)
+    within(got, ref, (2.0 ** -8 + 2.0 ** -12) * A + 2.0 ** -8 * ref.abs(), "many sequences")
+
+
+def test_shared_prefix_attn_refuses_what_it_cannot_take(Q):
+    from rag_kv_cache_re_gb300 import QcfError
+    bt = R.Batch([1] * 3, [4] * 3, 10, 2, 64, 16, "rows", torch.bfloat16, seed=1).fill()
+    cache, batch = bt.bind(Q)
+    q = bt.randn(3, 8, 64)
+    for bad in (lambda: Q.qcf_shared_prefix_attn(cache, batch, q.cpu(), 0.1), lambda: Q.qcf_shared_prefix_attn(cache, batch, q[:2], 0.1),
+                lambda: Q.qcf_shared_prefix_attn(cache, batch, q.half(), 0.1), lambda: Q.qcf_shared_prefix_attn(cache, batch, q[:, :3].contiguous(), 0.1),
+                lambda: Q.qcf_shared_prefix_attn(cache, batch, q, 0.0), lambda: Q.qcf_shared_prefix_attn(cache, batch, q, 0.1, out=q[:, :4]),
+                lambda: Q.qcf_shared_prefix_attn(cache, batch, q.transpose(1, 2).contiguous().transpose(1, 2), 0.1),
+                lambda: Q.qcf_shared_prefix_attn(cache, bt.bind(Q, prefix_len=33)[1], q, 0.1),
+                lambda: Q.qcf_shared_prefix_attn(cache, bt.bind(Q, max_len=17)[1], q, 0.1),
+                lambda: Q.qcf_paged_append(cache, batch, q[:, :2], q[:, 2:5]), lambda: Q.qcf_paged_append(cache, batch, q[:, :2], q[:, 2:4], q_out=q),
+                lambda: Q.qcf_paged_append(cache, batch, q[:, :1], q[:, 1:2]),
+                lambda: Q.qcf_rope_apply(q, torch.zeros(2, dtype=torch.int32, device=DEV), Q.ScaledRopeTable(8, 64, 1e4, DEV)),
+                lambda: Q.qcf_rope_apply(q, torch.zeros(3, dtype=torch.int64, device=DEV), Q.ScaledRopeTable(8, 64, 1e4, DEV)),
+                lambda: Q.qcf_rope_apply(q, torch.zeros(3, dtype=torch.int32, device=DEV), Q.ScaledRopeTable(8, 128, 1e4, DEV))):
+        with pytest.raises(QcfError):
+            bad()
+    many = torch.zeros(2050, dtype=torch.int32, device=DEV)
+    batch = Q.PagedBatch(many, many[1:].clone(), torch.zeros((2049, 1), dtype=torch.int32, device=DEV), 3, 1, 16)
+    with pytest.raises(QcfError):
+        Q.qcf_shared_prefix_attn(cache, batch, q, 0.1)
 
 
 def test_shared_prefix_attn_loose_bounds(Q):
