@@ -44,21 +44,23 @@ __device__ __forceinline__ TwoSinCos two_add(const TwoSinCos& a, const TwoSinCos
   return r;
 }
 
-// Table entries of 16 pairs (blockIdx.y) and na blocks of 256 positions (blockIdx.x).  fp64 runs
+// Table entries of PAIRS pairs (blockIdx.y) and na blocks of 256 positions (blockIdx.x).  fp64 runs
 // at 1/64 of the fp32 rate here: a sine and cosine in fp64 of every entry took 511 us for 131072
 // positions of 64 pairs, 50 times the write.  Instead a position is taken apart in base 4,
 // p = 256 a + 64 b1 + 16 b0 + 4 c1 + c0; the fp64 values of the na + 12 parts of a pair become
 // two-float numbers, their angles are added in those (four additions, 2^-47 each), and each entry
 // is rounded once.  The parts are of the position itself, so an entry's bits do not depend on the
 // call that fills it.  Thread = (pair, b and part of c): it forms b + c once and uses it for every a,
-// and a warp writes 64-byte runs.  1024 threads: one CTA per SM has the fewest fp64 values.
-// 131072 positions of 64 pairs: 22.6 us, 3.0 TB/s (with 32 pairs to a CTA, whole 128-byte lines but
-// twice the fp64 values per SM, 28 us).
-constexpr int kTableThreads = 1024, kTablePairs = 16;
+// and a warp writes runs of 4 PAIRS bytes.  1024 threads: one CTA per SM has the fewest fp64 values.
+// 131072 positions of 64 pairs, 16 to a CTA: 22.6 us, 3.0 TB/s (32, whole 128-byte lines but twice
+// the fp64 values per SM: 28 us).  8192 positions of 32 pairs: 5.7 us with 8 to a CTA, 8.5 with 16,
+// which fills 64 SMs only.
+constexpr int kTableThreads = 1024;
+template <int PAIRS>
 __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(float* __restrict__ cos_t, float* __restrict__ sin_t, int first_pos,
                                                                    int n_pos, int half, int na, double amplitude,
                                                                    const __grid_constant__ FreqTable f) {
-  constexpr int PAIRS = kTablePairs, PER = 256 * PAIRS / kTableThreads;   // positions of a thread in each block
+  constexpr int PER = 256 * PAIRS / kTableThreads;   // positions of a thread in each block
   __shared__ TwoSinCos a_s[16][PAIRS], digit[4][4][PAIRS];
   const int k0 = blockIdx.y * PAIRS;
   const int64_t a0 = first_pos / 256 + static_cast<int64_t>(blockIdx.x) * na;
@@ -244,13 +246,16 @@ qcf_status qcf_rope_table_fill(float* cos, float* sin, int first_pos, int n_pos,
   const qcf_status s = rope_frequencies(R, theta, scaling, &f, &amplitude);
   if (s != QCF_OK) return s;
   if (n_pos == 0) return QCF_OK;
-  // blocks of 256 positions, up to 16 to a CTA, so that one CTA per SM does
+  // blocks of 256 positions, up to 16 to a CTA, so that one CTA per SM does; 16 pairs to a CTA, or 8
+  // where that leaves SMs idle (its fp64 values are then most of the time)
   const int64_t blocks = (static_cast<int64_t>(first_pos) + n_pos + 255) / 256 - first_pos / 256;
-  const int groups = (R / 2 + kTablePairs - 1) / kTablePairs;
+  const bool few = blocks * ((R / 2 + 15) / 16) < num_sms();
+  const int groups = few ? (R / 2 + 7) / 8 : (R / 2 + 15) / 16;
   const int na = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, (blocks * groups + num_sms() - 1) / num_sms())));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   LaunchScope ls(KC_ROPE_TABLE, st);
-  rope_table_kernel<<<dim3(static_cast<unsigned>((blocks + na - 1) / na), groups), kTableThreads, 0, st>>>(cos, sin, first_pos, n_pos, R / 2, na,
+  const auto kernel = few ? rope_table_kernel<8> : rope_table_kernel<16>;
+  kernel<<<dim3(static_cast<unsigned>((blocks + na - 1) / na), groups), kTableThreads, 0, st>>>(cos, sin, first_pos, n_pos, R / 2, na,
                                                                                            amplitude, f);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? QCF_OK : cuda_error(e, "qcf_rope_table_fill: launch");
