@@ -747,7 +747,7 @@ qcf_status qcf_shared_prefix_attn(const qcf_paged_kv* cache, const qcf_paged_bat
   const qcf_status s = check_attn(who, cache, batch, Hq, &c, &b);
   if (s != QCF_OK) return s;
   if (!q || !o) return set_error(QCF_ERR_INVALID_ARG, "%s: NULL pointer", who);
-  if (!(scale > 0.f) || !std::isfinite(scale)) return set_error(QCF_ERR_INVALID_ARG, "%s: scale=%g", who, scale);
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f)) return set_error(QCF_ERR_INVALID_ARG, "%s: scale=%g", who, scale);
   if (q_stride < static_cast<int64_t>(Hq) * c.D)
     return set_error(QCF_ERR_SHAPE, "%s: q_stride %lld for %d x %d entries", who, (long long)q_stride, Hq, c.D);
   if (take_fault(4) || !aligned16(q) || !aligned16(o) || q_stride % 8 || (reinterpret_cast<uintptr_t>(ws) & 255u))

@@ -462,6 +462,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         mbar_arrive(q_empty);
       }
     }
+    if (rho == 0) bulk_wait_group0();   // the stores are done, not only read, before this kernel counts as complete
     if (!ok && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
   }
   tc_fence_before();

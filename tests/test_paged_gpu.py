@@ -297,6 +297,7 @@ ATTN_CASES = [  # new, lens, prefix, Hq, Hkv, D, page
     ([61, 3, 70], [61, 900, 70], 2000, 48, 3, 64, 32),                      # 16 heads a KV head
     ([5] * 9, [5 + 40 * i for i in range(9)], 400, 15, 5, 128, 8),          # 3 heads a KV head: rows left over in every tile
     ([1] * 700, [1 + (37 * i) % 90 for i in range(700)], 131, 2, 1, 128, 8),
+    ([1, 6, 9], [300, 6, 40], 1500, 32, 4, 128, 256),
     ([300], [300], 64, 4, 1, 128, 64),                                      # a long question: early rows see few of its keys
     ([1] * 40, [1 + 11 * i for i in range(40)], 90, 8, 8, 16, 16),          # head dim 16 with more rows than a tile
 ]
@@ -468,12 +469,13 @@ def test_cache_beyond_32_bit_offsets(Q):
 
 # ----------------------------------------------------------------- streams, graphs, the way they are used
 
-def test_captured_steps_replay_with_other_lengths(Q):
+@pytest.mark.parametrize("Hkv", [8, 4])   # 12 and 24 score rows a KV head: the prefix in the stream, and on its own kernel
+def test_captured_steps_replay_with_other_lengths(Q, Hkv):
     """Append and attention captured once; replayed after tokens and lengths changed, two graphs and
     an eager call side by side on different streams."""
     made = []
     for seed in (1, 2):
-        bt = R.Batch([1, 1, 1], [5, 60, 200], 700, 8, 128, 16, "rows", torch.bfloat16, seed=seed, table_cols=40, spare=30).fill()
+        bt = R.Batch([1, 1, 1], [5, 60, 200], 700, Hkv, 128, 16, "rows", torch.bfloat16, seed=seed, table_cols=40, spare=30).fill()
         bt.table[:, 13:] = 0
         order = torch.randperm(bt.k.shape[0], device=DEV)
         used = set(bt.prefix_pages.tolist()) | {int(p) for b in range(3) for p in bt.table[b, : -(-bt.lens[b] // 16)]}
@@ -482,12 +484,12 @@ def test_captured_steps_replay_with_other_lengths(Q):
             n = -(-bt.lens[b] // 16)
             bt.table[b, n: n + 3] = torch.tensor([spare.pop() for _ in range(3)], dtype=torch.int32)
         table = Q.ScaledRopeTable(2000, 128, 1e4, DEV)
-        rows = bt.randn(3, 32 + 16, 128)
+        rows = bt.randn(3, 32 + 2 * Hkv, 128)
         cache, batch = bt.bind(Q, max_len=640)
         qo, out = torch.empty(3, 32, 128, dtype=torch.bfloat16, device=DEV), torch.empty(3, 32, 128, dtype=torch.bfloat16, device=DEV)
 
         def step(rows=rows, cache=cache, batch=batch, table=table, qo=qo, out=out):
-            q, k, v = rows.split([32, 8, 8], 1)
+            q, k, v = rows.split([32, Hkv, Hkv], 1)
             Q.qcf_paged_append(cache, batch, k, v, table, q=q, q_out=qo)
             Q.qcf_shared_prefix_attn(cache, batch, qo, 0.09, out=out)
 
@@ -505,7 +507,7 @@ def test_captured_steps_replay_with_other_lengths(Q):
         for bt, rows, *_ in made:
             bt.kv_len += 1
             bt.lens = [n + 1 for n in bt.lens]
-            rows.copy_(bt.randn(3, 48, 128))
+            rows.copy_(bt.randn(3, 32 + 2 * Hkv, 128))
         torch.cuda.synchronize()
         for bt, rows, graph, step, qo, out, stream in made:
             with torch.cuda.stream(stream):
