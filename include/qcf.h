@@ -541,8 +541,8 @@ typedef struct qcf_paged_kv {
 /* A batch of sequences over one shared prefix.  Rows of q and of new keys belong to sequence
  * b for row_start[b] <= row < row_start[b + 1]; they are its last tokens: row i of nq new rows
  * has own position kv_len[b] - nq + i and, for rotation, position prefix_len + that.  Rows in
- * no sequence (before the first, behind the last) are padding: never read, their outputs left
- * as they were.  Own token j of sequence b lives in page page_table[b][j / page_size], prefix
+ * no sequence (before the first, behind the last) are padding: without effect, whatever they
+ * hold, their outputs left as they were.  Own token j of sequence b lives in page page_table[b][j / page_size], prefix
  * token j in page prefix_pages[j / page_size].
  * Lengths are read on the device, so that a captured graph can be replayed with others; the
  * host gives upper bounds.  A sequence that breaks one (or has fewer tokens than new rows,
@@ -579,8 +579,9 @@ qcf_status qcf_paged_append(const qcf_paged_kv* cache, const qcf_paged_batch* ba
  * and own tokens j <= p, g = h / (Hq/Hkv), one softmax over both.  The prefix is read once
  * for all rows of the batch.
  *   q    device, rows of Hq heads of D contiguous entries, q_stride entries apart
- *   o    device [n_rows][Hq][D], the cache's type;  lse device [n_rows][Hq] fp32 natural-log sum of
- *        exp of the scaled logits, or NULL
+ *   o    device [n_rows][Hq][D], the cache's type; may be q itself (q_stride = Hq D), and
+ *        overlaps nothing else
+ *   lse  device [n_rows][Hq] fp32 natural-log sum of exp of the scaled logits, or NULL
  *   ws   device scratch of qcf_shared_prefix_attn_workspace_size() bytes; it needs no clearing;
  *        calls that overlap on the GPU (captured graphs replayed side by side among them) need
  *        separate scratch

@@ -13,6 +13,7 @@
 namespace qcf {
 
 constexpr int kMaxBatchSeqs = 2048;   // each CTA of the stream keeps 12 bytes of every sequence
+constexpr int kMostTiles = INT32_MAX - (1 << 20);   // tiles of one call, with room for the shares' rounding
 
 // ------------------------------------------------------------------ the stream, on warp tensor cores
 //
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
   }
   // ---- the deal: first tile of every sequence
   {
-    __shared__ int sums[Cfg::WARPS];
+    __shared__ int64_t sums[Cfg::WARPS];
     if (lane == 0) {
       for (int s = 0; s < ST; ++s) mbar_init(&full[s], 1);
       fence_mbar_init();
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
       tma_prefetch_desc(&tmV);
     }
     const int per = (b.n_seq + THREADS - 1) / THREADS, s0 = threadIdx.x * per, s1 = min(b.n_seq, s0 + per);
-    int mine = 0;
+    int64_t mine = 0;
     for (int s = s0; s < s1; ++s) {
       const SeqSpan q = seq_span(b, s);
       if (q.bad && blockIdx.x == 0) flag_status(status, QCF_DEV_BAD_INDEX);
@@ -189,18 +190,26 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
       len[s] = q.len;
       mine += n;
     }
-    int run = mine;
+    int64_t run = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(kAll, run, o);
+      const int64_t v = __shfl_up_sync(kAll, run, o);
       if (lane >= o) run += v;
     }
     if (lane == 31) sums[warp] = run;
     __syncthreads();
-    int at = (p.pre_stream ? p.stream_blocks * p.stream_tiles * c.Hkv : 0) + run - mine;
-    for (int w = 0; w < warp; ++w) at += sums[w];
+    const int pre = p.pre_stream ? p.stream_blocks * p.stream_tiles * c.Hkv : 0;
+    int64_t all = pre, before = pre + run - mine;
+    for (int w = 0; w < Cfg::WARPS; ++w) {
+      all += sums[w];
+      if (w < warp) before += sums[w];
+    }
+    // more tiles than the bounds allow come only of sequences that overlap: nothing is done for them
+    const bool over = all > kMostTiles;
+    if (over && blockIdx.x == 0 && threadIdx.x == 0) flag_status(status, QCF_DEV_BAD_INDEX);
+    int at = over ? 0 : static_cast<int>(before);
     for (int s = s0; s < s1; ++s) {
-      const int n = start[s];
+      const int n = over ? 0 : start[s];
       start[s] = at;
       at += n;
     }
@@ -480,7 +489,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const
   const int g = h / a.G, hh = h - g * a.G;
   pdl_wait();
   int n = 0, n_pre = 0, pre_cta = 0, pre_local = 0, own_cta = 0, rho = 0;
-  if (real) {
+  if (real && ws.deal[b.n_seq] > 0) {   // a batch that was dealt
     const int share = ws.deal[b.n_seq + 1], mine = ws.deal[seq];
     // parts: the prefix's (on tcgen05, or of the stream), then the own tokens'
     if (p.pre_even) {
@@ -545,7 +554,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const
     for (int j = 0; j < BATCH; ++j)
 #pragma unroll
       for (int k = 0; k < NV; ++k)
-        if (i0 + j < i_end && has && ml[j][k].x != -INFINITY) {   // a part without keys for this row has no sums
+        if (i0 + j < i_end && has && ml[j][k].y != 0.f) {   // a part without keys for this row has no sums
           const float top = fmaxf(M[k], ml[j][k].x);
           const float f = exp2f(ml[j][k].x - top), e = M[k] == -INFINITY ? 0.f : exp2f(M[k] - top);
           M[k] = top;
@@ -626,11 +635,12 @@ static SharedPlan plan_shared(const PagedView& c, const BatchView& b, int Hq) {
   return p;
 }
 
-// Tiles of the stream at most: every sequence as long and as wide as its bounds.
+// Tiles of the stream at most: every sequence as long as its bound, and as wide as its bound or as all rows allow.
 static int64_t most_tiles(const SharedPlan& p, const BatchView& b, int G, int Hkv) {
-  const int64_t rows = std::min(b.max_q, b.n_rows);
+  const int64_t rows = std::min(b.max_q, b.n_rows), blocks = b.n_seq * ((rows * G + kStreamRows - 1) / kStreamRows);
+  const int64_t together = (static_cast<int64_t>(b.n_rows) * G + static_cast<int64_t>(b.n_seq) * (kStreamRows - 1)) / kStreamRows;
   return (static_cast<int64_t>(p.stream_blocks) * p.stream_tiles +
-          b.n_seq * ((rows * G + kStreamRows - 1) / kStreamRows) * ((b.max_len + kStreamKeys - 1) / kStreamKeys)) *
+          std::min(blocks, together) * ((b.max_len + kStreamKeys - 1) / kStreamKeys)) *
          Hkv;
 }
 
@@ -718,8 +728,7 @@ static qcf_status check_attn(const char* who, const qcf_paged_kv* cache, const q
   if (static_cast<int64_t>(b->n_rows) * Hq > INT32_MAX / 128)
     return set_error(QCF_ERR_SHAPE, "%s: %d rows of %d heads are too many for one call", who, b->n_rows, Hq);
   const SharedPlan p = plan_shared(*c, *b, Hq);
-  if (most_tiles(p, *b, Hq / c->Hkv, c->Hkv) > INT32_MAX - (1 << 20) ||
-      static_cast<int64_t>(p.pre_row_blocks) * c->Hkv * p.pre_tiles > INT32_MAX - (1 << 20))
+  if (most_tiles(p, *b, Hq / c->Hkv, c->Hkv) > kMostTiles || static_cast<int64_t>(p.pre_row_blocks) * c->Hkv * p.pre_tiles > kMostTiles)
     return set_error(QCF_ERR_SHAPE, "%s: the bounds allow more work than one call takes", who);
   return QCF_OK;
 }

@@ -332,13 +332,13 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       return id < 0 || id >= c.n_pages;
     };
     uint32_t seen = 0, ends = 0;
-    bool ok = true;
-    while (ok && segs.next(s)) {
+    bool ok = true;   // a warp whose wait ran out still meets the others at the tile's barriers
+    while (segs.next(s)) {
       if (x >= s.nb) continue;
       const int row = s.row0 + x * per + pl;
       float m = -INFINITY, l = 0.f;
       bool bad = page_bad(s.t0);
-      for (int i = 0; i < s.nt; ++i) {
+      for (int i = 0; ok && i < s.nt; ++i) {
         const int t = s.t0 + i;
         const unsigned bad8 = __ballot_sync(kAll, bad);
         bad = i + 1 < s.nt && page_bad(t + 1);
@@ -422,10 +422,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         split(add2(sum[0], sum[1]), l0, l1);
         l += l0 + l1;
       }
-      if (!ok || !__all_sync(kAll, mbar_wait(&o_done[x], ends++ & 1))) {
-        ok = false;
-        break;
-      }
+      ok = ok && __all_sync(kAll, mbar_wait(&o_done[x], ends++ & 1));
       tc_fence_after();
       // The sums leave through the tile's Q memory (its products are done: O is), 32 columns a box, by
       // tiled TMA stores of whole lines, rows behind the batch cut off; written row by row from the

@@ -398,6 +398,8 @@ def qcf_rope_table_fill(cos: torch.Tensor, sin: torch.Tensor, theta: float, firs
     if sin.get_device() != dev:
         _bad("tensors must be on the current CUDA device")
     n, half = cos.shape
+    if not 0 <= first_pos <= 2**31 - 1 - n:
+        _bad(f"positions {first_pos} .. {first_pos} + {n} exceed 31 bits")
     if n == 0:   # empty tensors have no address to pass
         return
     call("qcf_rope_table_fill", cos.data_ptr(), sin.data_ptr(), first_pos, n, 2 * half, theta,
@@ -485,6 +487,8 @@ class PagedBatch:
         if any(t is not None and t.get_device() != self.dev for t in (kv_len, page_table, prefix_pages)):
             _bad("row_start, kv_len, page_table and prefix_pages must be on one device")
         self.n_rows, self.prefix_len = int(n_rows), int(prefix_len)
+        if not all(0 <= int(v) < 2**31 for v in (n_rows, max_q, max_len, prefix_len)):
+            _bad("n_rows, max_q, max_len and prefix_len must be 32-bit counts")
         self.empty = n_seq == 0 or self.n_rows == 0   # nothing to do, and no addresses to pass
         self.struct = _lib.PagedBatch(n_seq, self.n_rows, int(max_q), int(max_len), row_start.data_ptr(), kv_len.data_ptr(),
                                       page_table.data_ptr(), page_table.shape[1], self.prefix_len,

@@ -366,6 +366,7 @@ def test_shared_prefix_attn_refuses_what_it_cannot_take(Q):
                 lambda: Q.qcf_shared_prefix_attn(cache, batch, q.transpose(1, 2).contiguous().transpose(1, 2), 0.1),
                 lambda: Q.qcf_shared_prefix_attn(cache, bt.bind(Q, prefix_len=33)[1], q, 0.1),
                 lambda: Q.qcf_shared_prefix_attn(cache, bt.bind(Q, max_len=17)[1], q, 0.1),
+                lambda: bt.bind(Q, max_len=1 << 32), lambda: bt.bind(Q, max_q=-1),
                 lambda: Q.qcf_paged_append(cache, batch, q[:, :2], q[:, 2:5]), lambda: Q.qcf_paged_append(cache, batch, q[:, :2], q[:, 2:4], q_out=q),
                 lambda: Q.qcf_paged_append(cache, batch, q[:, :1], q[:, 1:2]),
                 lambda: Q.qcf_rope_apply(q, torch.zeros(2, dtype=torch.int32, device=DEV), Q.ScaledRopeTable(8, 64, 1e4, DEV)),
@@ -433,6 +434,46 @@ def test_shared_prefix_attn_leaves_bad_sequences_out(Q):
             assert torch.all(out[bad] == 7.0)
             keep = [r for r in range(6) if not bad.start <= r < bad.stop]
             within(out[keep], o[keep], tol[keep], change)
+
+
+def test_shared_prefix_attn_nan_queries_and_output_over_q(Q):
+    """A NaN in one head's query makes that head's row NaN, joined or not, and nothing else; the output may be q."""
+    for new, lens, prefix, Hq, D in (([1, 1, 9], [300, 2, 60], 0, 8, 128), ([1, 1, 1], [300, 2, 60], 900, 8, 64), ([3, 1, 30], [300, 2, 60], 900, 8, 128),
+                                     ([1, 1, 9], [300, 2, 60], 50, 8, 16)):
+        bt = R.Batch(new, lens, prefix, 2, D, 16, "rows", torch.bfloat16, seed=12).fill()
+        q = bt.randn(bt.n_rows, Hq, D)
+        o, _, tol, _ = R.attention(bt, q, 0.1)
+        cache, batch = bt.bind(Q)
+        q[1, 3, 5] = math.nan
+        got, lse = Q.qcf_shared_prefix_attn(cache, batch, q, 0.1, want_lse=True)
+        gone = torch.zeros(bt.n_rows, Hq, dtype=torch.bool, device=DEV)
+        gone[1, 3] = True
+        assert torch.equal(lse.isnan(), gone) and torch.equal(got.isnan(), gone[..., None].expand_as(got))
+        within(got[~gone], o[~gone], tol[~gone], "other rows")
+        assert Q.qcf_shared_prefix_attn(cache, batch, q, 0.1, out=q) is q
+        assert torch.equal(q.view(torch.int16), got.view(torch.int16))
+
+
+def test_shared_prefix_attn_wide_bounds_of_many_sequences(Q):
+    """Each of 256 sequences may be long and may bring many rows, but all rows together are few."""
+    bt = R.Batch([1] * 255 + [40], [1 + i % 30 for i in range(255)] + [70], 90, 8, 128, 16, "rows", torch.bfloat16, seed=14, table_cols=8192).fill()
+    check_attention(Q, bt, 64, max_q=512, max_len=131072)
+
+
+def test_shared_prefix_attn_overlapping_sequences_are_not_run(Q):
+    """Row ranges that go back make more work than the bounds allow: flagged, nothing written, nothing hangs."""
+    n, rows = 2048, 512
+    for prefix in (0, 100):
+        cache = Q.PagedKV(*(torch.zeros(4, 256, 8, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2)))
+        start = torch.tensor([0, rows] * (n // 2) + [0], dtype=torch.int32, device=DEV)   # every second range runs backwards
+        lens = torch.full((n,), 131072, dtype=torch.int32, device=DEV)
+        table = torch.zeros(n, 512, dtype=torch.int32, device=DEV)
+        pages = torch.zeros(1, dtype=torch.int32, device=DEV) if prefix else None
+        batch = Q.PagedBatch(start, lens, table, rows, rows, 131072, pages, prefix)
+        out = torch.full((rows, 64, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+        Q.qcf_shared_prefix_attn(cache, batch, torch.ones_like(out), 0.1, out=out)
+        assert Q.qcf_query_status() == 2
+        assert torch.all(out == 7.0)
 
 
 def test_empty_batches_write_nothing(Q):
