@@ -153,7 +153,6 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* rings = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-  pdl_launch_dependents();   // the prefix kernel takes over SMs as this one leaves them
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int worker = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);   // few workers: one to an SM first
   uint8_t* ring = rings + warp * Cfg::RING;                                                     // stage: K tile, V tile
@@ -163,6 +162,13 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
   int* len = row0 + b.n_seq + 1;
   const StreamDeal deal{start, row0, len};
 
+  if (lane == 0) {
+    for (int s = 0; s < ST; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  pdl_launch_dependents();   // the prefix kernel takes over SMs as this one leaves them
   {   // the page table and the queries on their way to L2 while the deal is found
     const int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x, tables = static_cast<int64_t>(b.n_seq) * b.table_stride / 32;
     const int lines = a.Hq * D / 64;   // 128-byte lines of a row of q
@@ -172,12 +178,6 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
   // ---- the deal: first tile of every sequence
   {
     __shared__ int64_t sums[Cfg::WARPS];
-    if (lane == 0) {
-      for (int s = 0; s < ST; ++s) mbar_init(&full[s], 1);
-      fence_mbar_init();
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-    }
     const int per = (b.n_seq + THREADS - 1) / THREADS, s0 = threadIdx.x * per, s1 = min(b.n_seq, s0 + per);
     int64_t mine = 0;
     for (int s = s0; s < s1; ++s) {
@@ -218,8 +218,7 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
       start[b.n_seq + 1] = max((at + p.workers - 1) / p.workers, kMinShare);
     }
     __syncthreads();
-    if (blockIdx.x == 0)
-      for (int s = threadIdx.x; s < b.n_seq + 2; s += THREADS) ws.deal[s] = start[s];
+    if (blockIdx.x == 0 && threadIdx.x == 0) *ws.share = start[b.n_seq + 1];
   }
 
   // ---- copies: a walk of its own, up to ST tiles ahead of the scores.  The lanes hold the page ids of
@@ -312,6 +311,17 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
     }
 #pragma unroll
     for (int i = 0; i < ST; ++i) copy_next();
+  }
+
+  // what the join needs to know of each row, found while the first tiles come
+  for (int64_t row = blockIdx.x + static_cast<int64_t>(gridDim.x) * threadIdx.x; row < b.n_rows; row += static_cast<int64_t>(gridDim.x) * THREADS) {
+    int lo = -1, hi = b.n_seq;   // the last sequence that begins at or before the row
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (row0[mid] <= row) lo = mid; else hi = mid;
+    }
+    const bool real = lo >= 0 && row < row0[lo + 1] && start[lo + 1] > start[lo];
+    ws.rows[row] = real ? make_int4(static_cast<int>(row) - row0[lo], start[lo], (len[lo] + kStreamKeys - 1) / kStreamKeys, 0) : make_int4(-1, 0, 0, 0);
   }
 
   // ---- scores
@@ -464,62 +474,92 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
 
 // ------------------------------------------------------------------ joining the parts
 //
-// A warp joins HB neighbouring heads of a row (they share their KV head, so their parts): a lane has
-// 16-byte pieces of them, and a batch of parts is loaded, sums and statistics together, before it is
-// added with a running maximum.  `per` warps (1, 2, 4 or 8; more than one only with HB = 1) share the
-// parts of one head where there may be many; their results meet in shared memory, always in the
-// same order.  Launched while the kernels before it run; what does not depend on them (the row's
-// sequence) is found meanwhile.  Bound by latencies: row, deal, one for each batch of parts.
+// A warp joins the parts of one head of a row: a lane has 16 bytes of each, and a batch of parts is
+// loaded, sums and statistics together, before it is added with a running maximum.  `per` warps
+// (1, 2, 4 or 8) share the parts where there may be many; their results meet in shared memory,
+// always in the same order.  The parts of the tcgen05 prefix and the first of the own tokens have
+// places that depend on the row alone, and are on their way while the row's deal is read.
+// Bound by latencies: the end of the kernel before it, the row, a batch of parts, the next.  5 us
+// for 2048 pairs of 15 parts and for 128 of 80, against a join that returns at once; batches of 8
+// took 0.6 us less of the latter and 3 more of the former, two warps a pair 1.5 more of it.
 constexpr int kCombineWarps = 8;
-template <typename T, int D, int HB>
+template <typename T, int D>
 __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const PagedView c, const BatchView b, const AttnArgs a,
                                                                            const SharedPlan p, const Workspace ws, int per) {
-  constexpr int NV = HB * D > 128 ? HB * D / 128 : 1, BATCH = HB > 1 ? 2 : 4;
-  __shared__ float met[HB > 1 ? 1 : kCombineWarps][D + 2];   // a warp's sums, normaliser, maximum
+  constexpr int BATCH = 4;
+  __shared__ float met[kCombineWarps][D + 2];   // a warp's sums, normaliser, maximum
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % per;
-  const unsigned unit = blockIdx.x * static_cast<unsigned>(kCombineWarps / per) + warp / per, groups = a.Hq / HB;
-  const int row = static_cast<int>(unit / groups), h = static_cast<int>(unit - row * groups) * HB;
-  int seq = -1;
-  SeqSpan s = {};
-  if (row < b.n_rows) {
-    seq = warp_seq_of_row(b, row);
-    if (seq >= 0) s = seq_span(b, seq);
-  }
-  const bool real = seq >= 0 && row < s.row0 + s.nq;
+  const unsigned unit = blockIdx.x * static_cast<unsigned>(kCombineWarps / per) + warp / per;
+  const int row = static_cast<int>(unit / a.Hq), h = static_cast<int>(unit - row * a.Hq);
   const int g = h / a.G, hh = h - g * a.G;
+  const int64_t at = static_cast<int64_t>(row) * a.Hq + h;
+  const bool has = row < b.n_rows && lane * 4 < D;   // this lane's entries: 4 lane ..
+  int known = 0;   // parts: the first of the own tokens, the prefix's, the others of the own tokens
+  if (p.pre_even) {
+    known = 1 + p.pre_parts;
+  } else if (p.pre_tc) {   // the CTAs that share this row's unit
+    const int u = g * p.pre_row_blocks + row / p.pre_rows;
+    known = 2 + ((u + 1) * p.pre_tiles - 1) / p.pre_share - u * p.pre_tiles / p.pre_share;
+  }
   pdl_wait();
-  int n = 0, n_pre = 0, pre_cta = 0, pre_local = 0, own_cta = 0, rho = 0;
-  if (real && ws.deal[b.n_seq] > 0) {   // a batch that was dealt
-    const int share = ws.deal[b.n_seq + 1], mine = ws.deal[seq];
-    // parts: the prefix's (on tcgen05, or of the stream), then the own tokens'
-    if (p.pre_even) {
-      n_pre = p.pre_parts;
-    } else if (p.pre_tc) {   // the CTAs that share this row's unit
-      const int u = g * p.pre_row_blocks + row / p.pre_rows;
-      n_pre = ((u + 1) * p.pre_tiles - 1) / p.pre_share - u * p.pre_tiles / p.pre_share + 1;
-    } else if (p.pre_stream) {
+  int4 at_row = make_int4(-1, 0, 0, 0);   // row of its sequence (-1: of none), the sequence's first tile, tiles of its length
+  int share = 1;
+  if (row < b.n_rows) {
+    at_row = ws.rows[row];
+    share = *ws.share;
+  }
+  float M = -INFINITY, L = 0.f, sum[4] = {0.f, 0.f, 0.f, 0.f};
+  // parts first, first + per, ... below end; place(i, o): its statistics, and its sums in o
+  auto join = [&](int first, int end, auto place) {
+    for (int i0 = first; i0 < end; i0 += per * BATCH) {
+      float2 ml[BATCH];
+      float4 v[BATCH];
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j)
+        if (i0 + per * j < end && has) {
+          const float* o;
+          ml[j] = *place(i0 + per * j, o);
+          v[j] = *reinterpret_cast<const float4*>(o + lane * 4);
+        }
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j)
+        if (i0 + per * j < end && has && ml[j].y != 0.f) {   // a part without keys for this row has no sums
+          const float top = fmaxf(M, ml[j].x);
+          const float f = fast_exp2(ml[j].x - top), e = M == -INFINITY ? 0.f : fast_exp2(M - top);
+          M = top;
+          L = fmaf(ml[j].y, f, L * e);
+          sum[0] = fmaf(v[j].x, f, sum[0] * e);
+          sum[1] = fmaf(v[j].y, f, sum[1] * e);
+          sum[2] = fmaf(v[j].z, f, sum[2] * e);
+          sum[3] = fmaf(v[j].w, f, sum[3] * e);
+        }
+    }
+  };
+  join(sub, known, [&](int i, const float*& o) {
+    const int64_t r = i == 0 ? at : static_cast<int64_t>(i - 1) * b.n_rows * a.Hq + at;
+    o = (i == 0 ? ws.own_o : ws.tc_o) + r * D;
+    return (i == 0 ? ws.own_ml : ws.tc_ml) + r;
+  });
+  // by the deal: a streamed prefix, the other parts of the own tokens
+  int n_pre = 0, n_own = 0, pre_cta = 0, pre_local = 0, own_cta = 0, rho = 0;
+  if (at_row.x >= 0) {
+    if (p.pre_stream) {
       const int r = row * a.G + hh, first = (r / kStreamRows * c.Hkv + g) * p.stream_tiles;
       pre_cta = first / share;
       pre_local = r % kStreamRows;
       n_pre = (first + p.stream_tiles - 1) / share - pre_cta + 1;
     }
-    rho = (row - s.row0) * a.G + hh;
-    const int tiles = (s.len + kStreamKeys - 1) / kStreamKeys;
-    const int first = mine + (rho / kStreamRows * c.Hkv + g) * tiles;
+    rho = at_row.x * a.G + hh;
+    const int first = at_row.y + (rho / kStreamRows * c.Hkv + g) * at_row.z;
     own_cta = first / share;
-    n = n_pre + (first + tiles - 1) / share - own_cta + 1;
-    if (n_pre == 0 && n == 1) n = 0;   // already written
+    n_own = (first + at_row.z - 1) / share - own_cta + 1;
   }
-  const int64_t at = static_cast<int64_t>(row) * a.Hq + h;
-  // the place of part i's sums of head h (the other heads' follow): row of tc_o, of own_o or pre_o, or of spill_o
-  auto part = [&](int i, const float*& o) {
-    if (i < n_pre && p.pre_tc) {
-      const int64_t r = static_cast<int64_t>(i) * b.n_rows * a.Hq + at;
-      o = ws.tc_o + r * D;
-      return ws.tc_ml + r;
-    }
+  const int skip = known > 0 ? 1 : 0;   // the first of the own tokens' parts
+  const bool done = known + n_pre + n_own <= 1 || at_row.x < 0;   // written already, or not a row of a sequence
+  const int left = done ? 0 : n_pre + n_own - skip;
+  join(sub, left, [&](int i, const float*& o) {
     const bool pre = i < n_pre;
-    if (!pre) i -= n_pre;
+    if (!pre) i += skip - n_pre;
     if (i == 0) {
       o = (pre ? ws.pre_o : ws.own_o) + at * D;
       return (pre ? ws.pre_ml : ws.own_ml) + at;
@@ -527,76 +567,33 @@ __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const
     const int64_t r = static_cast<int64_t>((pre ? pre_cta : own_cta) + i) * kStreamRows + (pre ? pre_local : rho % kStreamRows);
     o = ws.spill_o + r * D;
     return ws.spill_ml + r;
-  };
-  const bool has = lane * 4 < HB * D;   // this lane's pieces: entries 128 k + 4 lane of the HB heads
-  float M[NV], L[NV], sum[NV][4];
+  });
+  if (per > 1) {
+    if (lane * 4 < D)
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    M[k] = -INFINITY;
-    L[k] = sum[k][0] = sum[k][1] = sum[k][2] = sum[k][3] = 0.f;
-  }
-  const int each = (n + per - 1) / per, i_end = min(n, (sub + 1) * each);
-  for (int i0 = sub * each; i0 < i_end; i0 += BATCH) {
-    float2 ml[BATCH][NV];
-    float4 v[BATCH][NV];
+      for (int e = 0; e < 4; ++e) met[warp][lane * 4 + e] = sum[e];
+    if (lane == 0) {
+      met[warp][D] = L;
+      met[warp][D + 1] = M;
+    }
+    __syncthreads();
+    if (sub > 0) return;
+    float top = -INFINITY;
+    for (int w = 0; w < per; ++w) top = fmaxf(top, met[warp + w][D + 1]);
+    M = top;
+    L = sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
+    for (int w = 0; w < per; ++w) {
+      const float mw = met[warp + w][D + 1], f = mw == -INFINITY ? 0.f : fast_exp2(mw - top);
+      L = fmaf(met[warp + w][D], f, L);
+      if (lane * 4 < D)
 #pragma unroll
-    for (int j = 0; j < BATCH; ++j)
-      if (i0 + j < i_end && has) {
-        const float* o;
-        const float2* m = part(i0 + j, o);
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-          ml[j][k] = m[(k * 128 + lane * 4) / D];
-          v[j][k] = *reinterpret_cast<const float4*>(o + k * 128 + lane * 4);
-        }
-      }
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j)
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (i0 + j < i_end && has && ml[j][k].y != 0.f) {   // a part without keys for this row has no sums
-          const float top = fmaxf(M[k], ml[j][k].x);
-          const float f = exp2f(ml[j][k].x - top), e = M[k] == -INFINITY ? 0.f : exp2f(M[k] - top);
-          M[k] = top;
-          L[k] = fmaf(ml[j][k].y, f, L[k] * e);
-          sum[k][0] = fmaf(v[j][k].x, f, sum[k][0] * e);
-          sum[k][1] = fmaf(v[j][k].y, f, sum[k][1] * e);
-          sum[k][2] = fmaf(v[j][k].z, f, sum[k][2] * e);
-          sum[k][3] = fmaf(v[j][k].w, f, sum[k][3] * e);
-        }
-  }
-  if constexpr (HB == 1) {
-    if (per > 1) {
-      if (has)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) met[warp][lane * 4 + e] = sum[0][e];
-      if (lane == 0) {
-        met[warp][D] = L[0];
-        met[warp][D + 1] = M[0];
-      }
-      __syncthreads();
-      if (sub > 0) return;
-      float top = -INFINITY;
-      for (int w = 0; w < per; ++w) top = fmaxf(top, met[warp + w][D + 1]);
-      M[0] = top;
-      L[0] = sum[0][0] = sum[0][1] = sum[0][2] = sum[0][3] = 0.f;
-      for (int w = 0; w < per; ++w) {
-        const float mw = met[warp + w][D + 1], f = mw == -INFINITY ? 0.f : exp2f(mw - top);
-        L[0] = fmaf(met[warp + w][D], f, L[0]);
-        if (has)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sum[0][e] = fmaf(met[warp + w][lane * 4 + e], f, sum[0][e]);
-      }
+        for (int e = 0; e < 4; ++e) sum[e] = fmaf(met[warp + w][lane * 4 + e], f, sum[e]);
     }
   }
-  if (n == 0 || !has) return;
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const float inv = L[k] > 0.f ? 1.f / L[k] : 0.f;
-    *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + at * D + k * 128 + lane * 4) =
-        make_uint2(pack2<T>(sum[k][0] * inv, sum[k][1] * inv), pack2<T>(sum[k][2] * inv, sum[k][3] * inv));
-    if (a.lse && (k * 128 + lane * 4) % D == 0) a.lse[at + (k * 128 + lane * 4) / D] = (M[k] + log2f(L[k])) * 0.69314718055994531f;
-  }
+  if (done || !has) return;
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + at * D + lane * 4) = make_uint2(pack2<T>(sum[0] * inv, sum[1] * inv), pack2<T>(sum[2] * inv, sum[3] * inv));
+  if (a.lse && lane == 0) a.lse[at] = (M + log2f(L)) * 0.69314718055994531f;
 }
 
 // ------------------------------------------------------------------ host
@@ -653,7 +650,8 @@ size_t workspace_layout(const SharedPlan& p, const BatchView& b, int Hq, int D, 
     return r;
   };
   const size_t rows = static_cast<size_t>(b.n_rows) * Hq, o = rows * D * sizeof(float), ml = rows * sizeof(float2);
-  w->deal = reinterpret_cast<int*>(take((static_cast<size_t>(b.n_seq) + 2) * sizeof(int)));
+  w->rows = reinterpret_cast<int4*>(take(static_cast<size_t>(b.n_rows) * sizeof(int4)));
+  w->share = reinterpret_cast<int*>(take(sizeof(int)));
   w->tc_o = reinterpret_cast<float*>(take(p.pre_parts * o));
   w->tc_ml = reinterpret_cast<float2*>(take(p.pre_parts * ml));
   w->own_o = reinterpret_cast<float*>(take(o));
@@ -699,13 +697,9 @@ static qcf_status shared_prefix_attn_launch(const qcf_paged_kv* cache, const Pag
   const int64_t share = std::max<int64_t>(kMinShare, most_tiles(p, b, a.G, c.Hkv) / p.workers);
   const int64_t many = p.pre_parts + (p.stream_tiles + (b.max_len + kStreamKeys - 1) / kStreamKeys) / share + 1;
   const int per = many <= 16 ? 1 : many <= 32 ? 2 : many <= 64 ? 4 : 8;
-  // many rows: a warp takes four heads of a KV head and looks their row up once (12512 pairs: 17 us with
-  // one head a warp)
-  const int64_t pairs = static_cast<int64_t>(b.n_rows) * a.Hq;
-  const bool four = per == 1 && a.G % 4 == 0 && pairs >= 32 * num_sms();
-  const int64_t units = four ? pairs / 4 : pairs, at_once = kCombineWarps / per;
-  e = launch_pdl(four ? batch_combine_kernel<T, D, 4> : batch_combine_kernel<T, D, 1>,
-                 dim3(static_cast<unsigned>((units + at_once - 1) / at_once)), dim3(kCombineWarps * 32), 0, st, c, b, a, p, w, per);
+  const int64_t pairs = static_cast<int64_t>(b.n_rows) * a.Hq, at_once = kCombineWarps / per;
+  e = launch_pdl(batch_combine_kernel<T, D>, dim3(static_cast<unsigned>((pairs + at_once - 1) / at_once)), dim3(kCombineWarps * 32), 0,
+                 st, c, b, a, p, w, per);
   return e == cudaSuccess ? QCF_OK : cuda_error(e, "qcf_shared_prefix_attn: combine launch");
 }
 

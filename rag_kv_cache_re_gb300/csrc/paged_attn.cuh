@@ -53,7 +53,8 @@ struct Workspace {
   float2* pre_ml;
   float* spill_o;     // [workers][16][D]: the part a worker's share begins in the middle of
   float2* spill_ml;
-  int* deal;          // [n_seq + 2]: first tile of each sequence, the total, tiles to a worker
+  int4* rows;         // [n_rows]: row of its sequence (-1: of none), the sequence's first tile, tiles of its length
+  int* share;         // tiles dealt to a worker
 };
 size_t workspace_layout(const SharedPlan& p, const BatchView& b, int Hq, int D, void* base, Workspace* w);
 
