@@ -577,7 +577,7 @@ qcf_status qcf_paged_append(const qcf_paged_kv* cache, const qcf_paged_batch* ba
 /* Attention of a batch over its shared prefix and its own tokens: for row i of sequence b at
  * own position p, o[i,h] = sum_j softmax_j(scale * q[i,h] . K_j) V_j over every prefix token
  * and own tokens j <= p, g = h / (Hq/Hkv), one softmax over both.  The prefix is read once
- * for all rows of the batch.
+ * for all rows of the batch (a short one once for every 16 of a KV head's score rows).
  *   q    device, rows of Hq heads of D contiguous entries, q_stride entries apart
  *   o    device [n_rows][Hq][D], the cache's type; may be q itself (q_stride = Hq D), and
  *        overlaps nothing else

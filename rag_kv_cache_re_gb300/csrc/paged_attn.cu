@@ -601,9 +601,16 @@ __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const
 static SharedPlan plan_shared(const PagedView& c, const BatchView& b, int Hq) {
   SharedPlan p = {};
   const int G = Hq / c.Hkv, sms = num_sms();
-  // More than one 16-row MMA tile of score rows per KV head: tcgen05 (one tile has nothing to share,
-  // and the stream splits its keys over every SM).
-  if (b.prefix_len > 0 && c.D >= 64 && static_cast<int64_t>(b.n_rows) * G > 16) {
+  p.ctas = sms;
+  p.workers = sms * (c.D == 128 ? StreamCfg<128>::WARPS : c.D == 64 ? StreamCfg<64>::WARPS : StreamCfg<16>::WARPS);
+  // The prefix goes to tcgen05 where more than one 16-row block of score rows shares it and its tiles
+  // would be more than three to each warp of the stream; below that a kernel of its own costs more
+  // than it saves.  32 query heads over 8 KV heads, head dim 128, in us (stream / tcgen05): 8 rows
+  // and 1000 keys (0.6 tiles a warp) 14.3 / 19.3, 24 and 1000 (1.7) 19.0 / 20.8, 8 and 5120 (2.8)
+  // 19.8 / 21.7, 24 and 3000 keys (4.9) 30.3 / 23.4, 64 and 3000 (13) 44.3 / 36.6.
+  const int64_t blocks = (static_cast<int64_t>(b.n_rows) * G + kStreamRows - 1) / kStreamRows;
+  const int64_t tiles = (static_cast<int64_t>(b.prefix_len) + kStreamKeys - 1) / kStreamKeys;
+  if (c.D >= 64 && blocks > 1 && blocks * tiles * c.Hkv > 3 * static_cast<int64_t>(p.workers)) {
     p.pre_tc = true;
     p.pre_rows = 2 * (128 / G);
     p.pre_row_blocks = (b.n_rows + p.pre_rows - 1) / p.pre_rows;
@@ -612,7 +619,8 @@ static SharedPlan plan_shared(const PagedView& c, const BatchView& b, int Hq) {
     p.pre_share = static_cast<int>(std::max<int64_t>((total + sms - 1) / sms, std::min(2, p.pre_tiles)));
     // Each unit in equal parts where that takes no CTA more than a tile longer (a second unit costs a
     // CTA about three): the KV heads then read the same rows at the same time, which share DRAM pages
-    // (32 rows, 64 heads, 131072 keys: see prefix_attn.cu).
+    // (the call with 32 rows, 64 heads and 131072 keys 117.0 us, dealt out 120.4; with 64 rows, 32
+    // heads and 5120 keys 36.7 and 40.3).
     const int each = units <= sms ? (p.pre_tiles + static_cast<int>(sms / units) - 1) / static_cast<int>(sms / units) : INT32_MAX;
     if (each <= p.pre_share + 1) {
       p.pre_even = true;
@@ -624,11 +632,9 @@ static SharedPlan plan_shared(const PagedView& c, const BatchView& b, int Hq) {
     }
   } else if (b.prefix_len > 0) {
     p.pre_stream = true;
-    p.stream_blocks = static_cast<int>((static_cast<int64_t>(b.n_rows) * G + kStreamRows - 1) / kStreamRows);
-    p.stream_tiles = (b.prefix_len + kStreamKeys - 1) / kStreamKeys;
+    p.stream_blocks = static_cast<int>(blocks);
+    p.stream_tiles = static_cast<int>(tiles);
   }
-  p.ctas = sms;
-  p.workers = sms * (c.D == 128 ? StreamCfg<128>::WARPS : c.D == 64 ? StreamCfg<64>::WARPS : StreamCfg<16>::WARPS);
   return p;
 }
 

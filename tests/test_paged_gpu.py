@@ -300,12 +300,23 @@ ATTN_CASES = [  # new, lens, prefix, Hq, Hkv, D, page
     ([1, 6, 9], [300, 6, 40], 1500, 32, 4, 128, 256),
     ([300], [300], 64, 4, 1, 128, 64),                                      # a long question: early rows see few of its keys
     ([1] * 40, [1 + 11 * i for i in range(40)], 90, 8, 8, 16, 16),          # head dim 16 with more rows than a tile
+    # prefixes long enough for their own kernel, with 7, 3, 8, 2 and 4 heads a KV head and last pages cut short
+    ([1, 2, 3, 4], [30, 2, 300, 16], 9000, 28, 4, 128, 8),
+    ([5] * 9, [5 + 40 * i for i in range(9)], 3003, 15, 5, 128, 8),
+    ([1, 6, 9], [300, 6, 40], 9000, 32, 4, 128, 256),
+    ([20, 1, 1], [20, 3000, 1], 4000, 32, 16, 64, 64),
+    ([1, 40], [260, 100], 12000, 7, 1, 64, 16),
+    ([7, 0, 1, 64, 0], [7, 5, 200, 80, 0], 3001, 16, 4, 128, 32),
+]
+LONG_CASES = [   # either side of the border between the two kernels: 3 tiles of 32 keys to each of 152 x 6 (D = 64: x 12) warps
+    ([1] * 8, [3] * 8, 2736 * 32 // 16, 32, 8, 128, 16), ([1] * 8, [3] * 8, 2736 * 32 // 16 + 1, 32, 8, 128, 16),
+    ([1] * 8, [3] * 8, 5472 * 32 // 16, 32, 8, 64, 16), ([1] * 8, [3] * 8, 5472 * 32 // 16 + 1, 32, 8, 64, 16),
 ]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("layout", ["rows", "heads"])
-@pytest.mark.parametrize("new,lens,prefix,Hq,Hkv,D,page", ATTN_CASES)
+@pytest.mark.parametrize("new,lens,prefix,Hq,Hkv,D,page", ATTN_CASES + LONG_CASES)
 def test_shared_prefix_attn(Q, dtype, layout, new, lens, prefix, Hq, Hkv, D, page):
     other = layout == "heads"
     bt = R.Batch(new, lens, prefix, Hkv, D, page, layout, TYPES[dtype], seed=len(new) + prefix, pad=5 * other, lead=3 * other).fill()
@@ -314,17 +325,18 @@ def test_shared_prefix_attn(Q, dtype, layout, new, lens, prefix, Hq, Hkv, D, pag
 
 @pytest.mark.parametrize("std,scale", [(8.0, None), (1.0, 4.0), (0.01, None)])
 @pytest.mark.parametrize("D", [64, 128])
-def test_shared_prefix_attn_sharp_and_flat(Q, D, std, scale):
-    bt = R.Batch([1, 2, 1, 30], [40, 9, 700, 64], 1500, 2, D, 16, "rows", torch.bfloat16, seed=3).fill()
+@pytest.mark.parametrize("prefix", [1500, 10000])
+def test_shared_prefix_attn_sharp_and_flat(Q, prefix, D, std, scale):
+    bt = R.Batch([1, 2, 1, 30], [40, 9, 700, 64], prefix, 2, D, 16, "rows", torch.bfloat16, seed=3).fill()
     check_attention(Q, bt, 8, std=std, scale=scale)
 
 
 def test_shared_prefix_attn_growing_logits(Q):
     """Keys whose logits grow along the prefix: the running maximum moves in every tile."""
-    for D in (64, 128):
-        bt = R.Batch([1, 1, 16], [300, 2, 60], 2000, 2, D, 32, "rows", torch.bfloat16, seed=6).fill()
-        ramp = torch.linspace(0.05, 6.0, 2000, device=DEV)[:, None, None]
-        bt.rows(bt.k)[bt.prefix_at()] = (ramp * torch.ones(2000, 2, D, device=DEV)).to(torch.bfloat16)
+    for D, prefix in ((64, 2000), (128, 2000), (64, 18000), (128, 18000)):
+        bt = R.Batch([1, 1, 16], [300, 2, 60], prefix, 2, D, 32, "rows", torch.bfloat16, seed=6).fill()
+        ramp = torch.linspace(0.05, 6.0, prefix, device=DEV)[:, None, None]
+        bt.rows(bt.k)[bt.prefix_at()] = (ramp * torch.ones(prefix, 2, D, device=DEV)).to(torch.bfloat16)
         check_attention(Q, bt, 8)
 
 
@@ -388,11 +400,11 @@ def test_shared_prefix_attn_loose_bounds(Q):
 
 
 def test_shared_prefix_attn_leaves_bad_pages_out(Q):
-    for D, prefix in ((64, 300), (128, 300), (128, 2000)):
-        bt = R.Batch([1] * 6, [5, 40, 9, 1, 17, 300], prefix, 2, D, 16, "rows", torch.bfloat16, seed=5, spare=0).fill()
+    for D, prefix, Hq, Hkv in ((64, 300, 8, 2), (128, 300, 8, 2), (128, 2000, 8, 2), (64, 8000, 64, 8), (128, 8000, 64, 8)):
+        bt = R.Batch([1] * 6, [5, 40, 9, 1, 17, 300], prefix, Hkv, D, 16, "rows", torch.bfloat16, seed=5, spare=0).fill()
         bt.prefix_pages[3] = bt.k.shape[0] + 4
         bt.prefix_pages[7] = -1
-        q = bt.randn(6, 8, D)
+        q = bt.randn(6, Hq, D)
         good = bt.prefix_pages.clone()
         good[3], good[7] = 0, 0
         cache, batch = bt.bind(Q)
@@ -401,8 +413,8 @@ def test_shared_prefix_attn_leaves_bad_pages_out(Q):
         bt.prefix_pages.copy_(good)
         o, _, tol, _ = R.attention(bt, q, 0.1, skip_prefix=[*range(48, 64), *range(112, 128)])
         within(got, o, tol, "prefix pages")
-        # own pages: the second sequence loses rows 16 .. 31, the fifth all of its two pages and has no prefix
-        bt = R.Batch([1] * 6, [5, 40, 9, 1, 17, 300], 0, 2, D, 16, "rows", torch.bfloat16, seed=5).fill()
+        # own pages: the fifth sequence loses all of its two pages and has no prefix
+        bt = R.Batch([1] * 6, [5, 40, 9, 1, 17, 300], 0, Hkv, D, 16, "rows", torch.bfloat16, seed=5).fill()
         bt.table[4, :2] = torch.tensor([1 << 30, -7], dtype=torch.int32)
         cache, batch = bt.bind(Q)
         got, lse = Q.qcf_shared_prefix_attn(cache, batch, q, 0.1, want_lse=True)
@@ -415,9 +427,9 @@ def test_shared_prefix_attn_leaves_bad_pages_out(Q):
 
 
 def test_shared_prefix_attn_leaves_bad_sequences_out(Q):
-    for D in (64, 128):
+    for D, prefix in ((64, 150), (128, 150), (128, 24000)):
         for change in ("short", "long", "rows"):
-            bt = R.Batch([2, 3, 1], [40, 20, 7], 150, 2, D, 16, "rows", torch.bfloat16, seed=9).fill()
+            bt = R.Batch([2, 3, 1], [40, 20, 7], prefix, 2, D, 16, "rows", torch.bfloat16, seed=9).fill()
             q = bt.randn(6, 8, D)
             o, _, tol, _ = R.attention(bt, q, 0.1)
             cache, batch = bt.bind(Q)
@@ -439,7 +451,7 @@ def test_shared_prefix_attn_leaves_bad_sequences_out(Q):
 def test_shared_prefix_attn_nan_queries_and_output_over_q(Q):
     """A NaN in one head's query makes that head's row NaN, joined or not, and nothing else; the output may be q."""
     for new, lens, prefix, Hq, D in (([1, 1, 9], [300, 2, 60], 0, 8, 128), ([1, 1, 1], [300, 2, 60], 900, 8, 64), ([3, 1, 30], [300, 2, 60], 900, 8, 128),
-                                     ([1, 1, 9], [300, 2, 60], 50, 8, 16)):
+                                     ([3, 1, 30], [300, 2, 60], 6000, 8, 128), ([1, 1, 9], [300, 2, 60], 50, 8, 16)):
         bt = R.Batch(new, lens, prefix, 2, D, 16, "rows", torch.bfloat16, seed=12).fill()
         q = bt.randn(bt.n_rows, Hq, D)
         o, _, tol, _ = R.attention(bt, q, 0.1)
@@ -510,13 +522,13 @@ def test_cache_beyond_32_bit_offsets(Q):
 
 # ----------------------------------------------------------------- streams, graphs, the way they are used
 
-@pytest.mark.parametrize("Hkv", [8, 4])   # 12 and 24 score rows a KV head: the prefix in the stream, and on its own kernel
-def test_captured_steps_replay_with_other_lengths(Q, Hkv):
+@pytest.mark.parametrize("Hkv,prefix", [(8, 700), (4, 700), (4, 12000)])   # the prefix in the stream (one block of rows, two), and on its own kernel
+def test_captured_steps_replay_with_other_lengths(Q, Hkv, prefix):
     """Append and attention captured once; replayed after tokens and lengths changed, two graphs and
     an eager call side by side on different streams."""
     made = []
     for seed in (1, 2):
-        bt = R.Batch([1, 1, 1], [5, 60, 200], 700, Hkv, 128, 16, "rows", torch.bfloat16, seed=seed, table_cols=40, spare=30).fill()
+        bt = R.Batch([1, 1, 1], [5, 60, 200], prefix, Hkv, 128, 16, "rows", torch.bfloat16, seed=seed, table_cols=40, spare=30).fill()
         bt.table[:, 13:] = 0
         order = torch.randperm(bt.k.shape[0], device=DEV)
         used = set(bt.prefix_pages.tolist()) | {int(p) for b in range(3) for p in bt.table[b, : -(-bt.lens[b] // 16)]}
@@ -524,7 +536,7 @@ def test_captured_steps_replay_with_other_lengths(Q, Hkv):
         for b in range(3):
             n = -(-bt.lens[b] // 16)
             bt.table[b, n: n + 3] = torch.tensor([spare.pop() for _ in range(3)], dtype=torch.int32)
-        table = Q.ScaledRopeTable(2000, 128, 1e4, DEV)
+        table = Q.ScaledRopeTable(prefix + 1300, 128, 1e4, DEV)
         rows = bt.randn(3, 32 + 2 * Hkv, 128)
         cache, batch = bt.bind(Q, max_len=640)
         qo, out = torch.empty(3, 32, 128, dtype=torch.bfloat16, device=DEV), torch.empty(3, 32, 128, dtype=torch.bfloat16, device=DEV)
