@@ -589,7 +589,8 @@ qcf_status qcf_paged_append(const qcf_paged_kv* cache, const qcf_paged_batch* ba
  * hold anything, NaN included; a new token whose value holds NaN or infinity may spoil
  * every row of its own sequence.  A page outside the cache sets QCF_DEV_BAD_INDEX, and its
  * keys are left out of the softmax.  Products in the cache's type with fp32 sums, softmax in
- * fp32.  Results repeat bitwise for the same inputs and bounds. */
+ * fp32.  Results repeat bitwise for the same inputs and bounds.  Own tokens are scored 16 rows at a
+ * time, for steps and questions; the prefill of a long text is qcf_sparse_causal_attn's work. */
 size_t qcf_shared_prefix_attn_workspace_size(const qcf_paged_kv* cache, const qcf_paged_batch* batch, int Hq);
 qcf_status qcf_shared_prefix_attn(const qcf_paged_kv* cache, const qcf_paged_batch* batch, const void* q,
                                   int64_t q_stride, int Hq, float scale, void* o, float* lse, void* ws, size_t ws_bytes,

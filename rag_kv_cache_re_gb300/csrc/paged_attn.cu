@@ -27,7 +27,10 @@ constexpr int kMostTiles = INT32_MAX - (1 << 20);   // tiles of one call, with r
 // 386 MB of uneven sequences.)
 // The maximum moves only when it grows by more than 2^8: the weights then stay below 2^8 (exact in
 // the fp32 sums, half a step in 16 bits wherever they lie) and most tiles rescale nothing.
-// Bound by the K and V bytes; the rings keep 96 KB or more per SM in flight.
+// Bound by the K and V bytes; the rings keep 96 KB or more per SM in flight.  386 MB of uneven
+// sequences of head dim 64 in 66 to 71 us (5.4 to 5.8 TB/s), 67 MB of short ones in 20, of which
+// about 5 pass before the first tile is scored.  It serves any number of new rows, but a question of
+// thousands of tokens is work for 128-row tiles.
 template <int D>
 struct StreamCfg {
   static constexpr int COLS = D < 64 ? D : 64, BOXES = D / COLS;

@@ -25,7 +25,10 @@
 // 256, O_b 256 + D.  A commit covers every product issued before it, so a full S_x(i + 1) also
 // means that P_x(i) V has been added: no barrier of its own for the output.
 //
-// Bound: HBM below about 285 score rows per KV head, the tensor pipe above.
+// Bound: HBM below about 285 score rows per KV head, the tensor pipe above.  131072 keys of 8 KV heads
+// against 256 score rows each: 99 us, 5.4 TB/s and 1.39 PFLOP/s at once; 16384 keys against 1564: 80 us,
+// 1.2 PFLOP/s.  A pair of 128 x 128 tiles takes 2860 to 3030 cycles, 2048 of them products: the S
+// products read both operands from shared memory at its full rate.
 #include <algorithm>
 
 #include "paged_attn.cuh"

@@ -111,7 +111,9 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(float* __rest
 
 // One thread per (row, item, chunk of kRopeHeads heads): the angles of a row's item are read
 // once and serve every head of the chunk, whose loads are all in flight together (and before the
-// position is known).
+// position is known).  HBM-bound: 17984 rows of 72 heads of 128 in bf16 take 97.7 us, 6.8 TB/s, the
+// rate of a copy; with the entries unpacked as they come (twice the registers) 152 us, with 8 heads
+// to a thread 224.
 constexpr int kRopeHeads = 4;
 template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(256, 3) rope_apply_kernel(const T* x, int64_t x_stride, T* y, int64_t y_stride, int n, int H,
