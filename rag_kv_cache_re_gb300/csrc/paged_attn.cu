@@ -25,8 +25,7 @@ constexpr int kMostTiles = INT32_MAX - (1 << 20);   // tiles of one call, with r
 // scores and across the borders of units, and no warp waits for another.  (Four warps that
 // split a tile and met at two barriers took 1900 cycles per 64 keys of head dim 64, and 90 us for
 // 386 MB of uneven sequences.)
-// The maximum moves only when it grows by more than 2^8: the weights then stay below 2^8 (exact in
-// the fp32 sums, half a step in 16 bits wherever they lie) and most tiles rescale nothing.
+// The maximum moves only when it grows by more than 2^8 (see kWeightLift), so most tiles rescale nothing.
 // Bound by the K and V bytes; the rings keep 96 KB or more per SM in flight.  386 MB of uneven
 // sequences of head dim 64 in 66 to 71 us (5.4 to 5.8 TB/s), 67 MB of short ones in 20, of which
 // about 5 pass before the first tile is scored.  It serves any number of new rows, but a question of
@@ -152,6 +151,7 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
                        const BatchView b, const AttnArgs a, const SharedPlan p, const Workspace ws, unsigned int* status) {
   using Cfg = StreamCfg<D>;
   constexpr int ST = Cfg::STAGES, THREADS = Cfg::WARPS * 32;
+  constexpr float kLift = kWeightLift<T>;
   constexpr unsigned kAll = 0xffffffffu;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -384,13 +384,13 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
       top_lo = max3(top_lo, sc[3][0], sc[3][1]) * a.scale_log2;
       top_hi = max3(top_hi, sc[3][2], sc[3][3]) * a.scale_log2;
       // rows of a quad share their maximum only when one of them asks for it
-      if (__any_sync(kAll, top_lo > m_lo + 8.f || top_hi > m_hi + 8.f)) {
+      if (__any_sync(kAll, top_lo > m_lo + (8.f + kLift) || top_hi > m_hi + (8.f + kLift))) {
 #pragma unroll
         for (int o = 1; o <= 2; o <<= 1) {
           top_lo = fmaxf(top_lo, __shfl_xor_sync(kAll, top_lo, o));
           top_hi = fmaxf(top_hi, __shfl_xor_sync(kAll, top_hi, o));
         }
-        const float n_lo = fmaxf(m_lo, top_lo), n_hi = fmaxf(m_hi, top_hi);
+        const float n_lo = fmaxf(m_lo, top_lo - kLift), n_hi = fmaxf(m_hi, top_hi - kLift);
         const float f_lo = m_lo == -INFINITY ? 0.f : fast_exp2(m_lo - n_lo), f_hi = m_hi == -INFINITY ? 0.f : fast_exp2(m_hi - n_hi);
         m_lo = n_lo;
         m_hi = n_hi;

@@ -18,6 +18,13 @@ struct AttnArgs {
   float scale_log2;   // scale * log2(e): logits are kept in powers of two
 };
 
+// Weights are powers 2^(x - m).  m follows the maximum of the logits x by steps of more than 2^8, so
+// they stay below 2^8 above their first maximum; in fp16 m lies 7 below that maximum, so that weights
+// down to 2^-21 of the largest are normal numbers (the top ones below 2^15), and many small
+// weights next to a large one keep their bits.  bf16 has the exponents of fp32.
+template <typename T>
+constexpr float kWeightLift = std::is_same<T, __half>::value ? 7.f : 0.f;
+
 __device__ __forceinline__ int div_g(const AttnArgs& a, int n) {
   return a.G == 1 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), a.g_mul));
 }

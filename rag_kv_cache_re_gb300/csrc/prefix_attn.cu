@@ -394,9 +394,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], sv[kPreKeys - 4 + e]);
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-        const bool grow = top > m + 8.0f;
+        const bool grow = top > m + (8.0f + kWeightLift<T>);
         if (__any_sync(kAll, grow)) {
-          const float m_new = grow ? top : m;
+          const float m_new = grow ? top - kWeightLift<T> : m;
           if (i > 0) {   // the full S of this tile says that every earlier product has been added to O
             const float f = m == -INFINITY ? 0.f : fast_exp2(m - m_new);
 #pragma unroll 1

@@ -125,7 +125,8 @@ def attention(bt, q, scale, skip_prefix=()):
       logits: fp32 sums of D exact products, (D + 8) 2^-24 of the sum of their magnitudes, and
         the exponent's argument and result rounded (2^-21): a relative error d of each weight,
         twice (weight and normaliser): 2 d A
-      weights rounded to the cache's type before they meet the values: half a step of A
+      weights rounded to the cache's type before they meet the values: half a step of A, and in fp16
+        2^-25 for each weight below 2^-14 of its unit, which is 2^-7 of the largest or less: 2^-32 sum_j |V_j|
       fp32 sums of the weighted values and the merging of partial sums: 2^-18 A
       the output rounded once: half a step of |o|.
     lse: the largest error of a logit, and a logarithm and a sum of it in 32 bits (2^-20 of 1 + |lse|)."""
@@ -155,9 +156,10 @@ def attention(bt, q, scale, skip_prefix=()):
             p = torch.exp(x - torch.where(e.isinf(), 0.0, e)[..., None])
             oh = torch.einsum("gnj,jd->ngd", p, V[:, h])
             A = torch.einsum("gnj,jd->ngd", p, V[:, h].abs())
+            small = 2.0 ** -32 * V[:, h].abs().sum(0) if bt.dtype == torch.float16 else 0.0
             d = ((D + 8) * 2.0 ** -24 * top + 2.0 ** -21).transpose(0, 1)[..., None]
             o[r: r + nq, h * G: (h + 1) * G] = oh
             lse[r: r + nq, h * G: (h + 1) * G] = e.transpose(0, 1)
             ltol[r: r + nq, h * G: (h + 1) * G] = d[..., 0] + 2.0 ** -20 * (1 + e.transpose(0, 1).abs())
-            tol[r: r + nq, h * G: (h + 1) * G] = (2 * d + step + 2.0 ** -18) * A + step * oh.abs() + 2.0 ** -25
+            tol[r: r + nq, h * G: (h + 1) * G] = (2 * d + step + 2.0 ** -18) * A + step * oh.abs() + 2.0 ** -25 + small
     return o, lse, tol, ltol

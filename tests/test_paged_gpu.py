@@ -340,6 +340,26 @@ def test_shared_prefix_attn_growing_logits(Q):
         check_attention(Q, bt, 8)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES)[:2])
+@pytest.mark.parametrize("D", [16, 64, 128])
+@pytest.mark.parametrize("prefix", [0, 2000, 18000])
+def test_shared_prefix_attn_small_weights_count(Q, prefix, D, dtype):
+    """One key far above thousands whose weights are 2^-20.4 of its own: below fp16's normal range beside a
+    largest weight of 1, and more than a hundredth of the sum."""
+    bt = R.Batch([1, 1, 16], [18000 if prefix == 0 else 300, 2, 60], prefix, 2, D, 32, "rows", TYPES[dtype], seed=16).fill()
+    q = torch.zeros(bt.n_rows, 8, D, dtype=TYPES[dtype], device=DEV)
+    q[..., 0] = 8.0
+    bt.k.zero_()
+    for at in [bt.prefix_at()] + [bt.own_at(b) for b in range(3)]:
+        bt.rows(bt.v)[at] = (1.0 + 0.25 * torch.rand(at[0].numel(), 2, D, generator=bt.g, device=DEV)).to(TYPES[dtype])
+    for at in [bt.prefix_at()] if prefix else [bt.own_at(b) for b in range(3)]:
+        bt.rows(bt.k)[at[0][1], at[1][1], :, 0] = 1.7675
+        bt.rows(bt.v)[at[0][1], at[1][1]] = 0.0
+    o, _, tol, _ = R.attention(bt, q, 1.0)
+    cache, batch = bt.bind(Q)
+    within(Q.qcf_shared_prefix_attn(cache, batch, q, 1.0), o, tol, "small weights")
+
+
 def test_shared_prefix_attn_many_sequences(Q):
     """As many sequences as a call takes; most of one token, some empty."""
     n = 2048
