@@ -171,7 +171,9 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  pdl_launch_dependents();   // the prefix kernel takes over SMs as this one leaves them
+  // the prefix kernel takes over SMs as this one leaves them; a join that came early would only wait
+  // beside the scores (4 rows over 5120 keys: 14.7 us for 13.4)
+  if (p.pre_tc) pdl_launch_dependents();
   {   // the page table and the queries on their way to L2 while the deal is found
     const int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x, tables = static_cast<int64_t>(b.n_seq) * b.table_stride / 32;
     const int lines = a.Hq * D / 64;   // 128-byte lines of a row of q
@@ -493,10 +495,11 @@ __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const
   __shared__ float met[kCombineWarps][D + 2];   // a warp's sums, normaliser, maximum
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % per;
   const unsigned unit = blockIdx.x * static_cast<unsigned>(kCombineWarps / per) + warp / per;
-  const int row = static_cast<int>(unit / a.Hq), h = static_cast<int>(unit - row * a.Hq);
+  const bool out = unit >= static_cast<unsigned>(b.n_rows) * a.Hq;   // behind the last pair: nothing to do, but for the barrier
+  const int row = out ? 0 : static_cast<int>(unit / a.Hq), h = out ? 0 : static_cast<int>(unit - row * a.Hq);
   const int g = h / a.G, hh = h - g * a.G;
   const int64_t at = static_cast<int64_t>(row) * a.Hq + h;
-  const bool has = row < b.n_rows && lane * 4 < D;   // this lane's entries: 4 lane ..
+  const bool has = lane * 4 < D;   // this lane's entries: 4 lane ..
   int known = 0;   // parts: the first of the own tokens, the prefix's, the others of the own tokens
   if (p.pre_even) {
     known = 1 + p.pre_parts;
@@ -505,12 +508,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const
     known = 2 + ((u + 1) * p.pre_tiles - 1) / p.pre_share - u * p.pre_tiles / p.pre_share;
   }
   pdl_wait();
-  int4 at_row = make_int4(-1, 0, 0, 0);   // row of its sequence (-1: of none), the sequence's first tile, tiles of its length
-  int share = 1;
-  if (row < b.n_rows) {
-    at_row = ws.rows[row];
-    share = *ws.share;
-  }
+  const int4 at_row = ws.rows[row];   // row of its sequence (-1: of none), the sequence's first tile, tiles of its length
+  const int share = *ws.share;
   float M = -INFINITY, L = 0.f, sum[4] = {0.f, 0.f, 0.f, 0.f};
   // parts first, first + per, ... below end; place(i, o): its statistics, and its sums in o
   auto join = [&](int first, int end, auto place) {
@@ -518,15 +517,14 @@ __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const
       float2 ml[BATCH];
       float4 v[BATCH];
 #pragma unroll
-      for (int j = 0; j < BATCH; ++j)
-        if (i0 + per * j < end && has) {
-          const float* o;
-          ml[j] = *place(i0 + per * j, o);
-          v[j] = *reinterpret_cast<const float4*>(o + lane * 4);
-        }
+      for (int j = 0; j < BATCH; ++j) {   // behind the end the last part again: loads without branches stay together
+        const float* o;
+        ml[j] = *place(min(i0 + per * j, end - 1), o);
+        v[j] = *reinterpret_cast<const float4*>(o + (has ? lane * 4 : 0));
+      }
 #pragma unroll
       for (int j = 0; j < BATCH; ++j)
-        if (i0 + per * j < end && has && ml[j].y != 0.f) {   // a part without keys for this row has no sums
+        if (i0 + per * j < end && ml[j].y != 0.f) {   // a part without keys for this row has no sums
           const float top = fmaxf(M, ml[j].x);
           const float f = fast_exp2(ml[j].x - top), e = M == -INFINITY ? 0.f : fast_exp2(M - top);
           M = top;
@@ -558,7 +556,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const
     n_own = (first + at_row.z - 1) / share - own_cta + 1;
   }
   const int skip = known > 0 ? 1 : 0;   // the first of the own tokens' parts
-  const bool done = known + n_pre + n_own <= 1 || at_row.x < 0;   // written already, or not a row of a sequence
+  const bool done = out || known + n_pre + n_own <= 1 || at_row.x < 0;   // written already, or not a row of a sequence
   const int left = done ? 0 : n_pre + n_own - skip;
   join(sub, left, [&](int i, const float*& o) {
     const bool pre = i < n_pre;
@@ -572,7 +570,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const
     return ws.spill_ml + r;
   });
   if (per > 1) {
-    if (lane * 4 < D)
+    if (has)
 #pragma unroll
       for (int e = 0; e < 4; ++e) met[warp][lane * 4 + e] = sum[e];
     if (lane == 0) {
@@ -588,7 +586,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const
     for (int w = 0; w < per; ++w) {
       const float mw = met[warp + w][D + 1], f = mw == -INFINITY ? 0.f : fast_exp2(mw - top);
       L = fmaf(met[warp + w][D], f, L);
-      if (lane * 4 < D)
+      if (has)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[e] = fmaf(met[warp + w][lane * 4 + e], f, sum[e]);
     }
