@@ -485,8 +485,8 @@ __global__ void __launch_bounds__(StreamCfg<D>::WARPS * 32, 1)
 // always in the same order.  The parts of the tcgen05 prefix and the first of the own tokens have
 // places that depend on the row alone, and are on their way while the row's deal is read.
 // Bound by latencies: the end of the kernel before it, the row, a batch of parts, the next.  5 us
-// for 2048 pairs of 15 parts and for 128 of 80, against a join that returns at once; batches of 8
-// took 0.6 us less of the latter and 3 more of the former, two warps a pair 1.5 more of it.
+// for 2048 pairs of 15 parts and 4 for 128 of 80, against a join that returns at once; batches of 8,
+// or more than 64 registers, took 2 to 4 us more of the former, two warps a pair 1.5.
 constexpr int kCombineWarps = 8;
 template <typename T, int D>
 __global__ void __launch_bounds__(kCombineWarps * 32) batch_combine_kernel(const PagedView c, const BatchView b, const AttnArgs a,

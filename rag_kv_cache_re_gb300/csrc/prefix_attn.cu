@@ -105,9 +105,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   using Cfg = PreCfg<D>;
   constexpr int KST = Cfg::K_STAGES, VST = Cfg::V_STAGES;
   constexpr unsigned kAll = 0xffffffffu;
-  // Launched while the stream kernel runs, on whose results nothing here depends; the join, launched
-  // in the same way, waits for this kernel alone, so this one ends after the stream has.
-  pdl_launch_dependents();
+  // Launched while the stream kernel runs, on whose results nothing here depends; the join waits for
+  // this kernel alone, so this one ends after the stream has (its pdl_wait).
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
