@@ -498,12 +498,17 @@ class PagedBatch:
         self._ws_bytes: Dict[Tuple[int, int, int, int], int] = {}
 
     def workspace_size(self, cache: PagedKV, Hq: int) -> int:
-        """qcf_shared_prefix_attn_workspace_size: a function of the layout and the bounds alone."""
+        """qcf_shared_prefix_attn_workspace_size: a function of the layout and the bounds alone.  0 for an
+        empty batch, and for a layout the library refuses: that is not kept, for it may be refused for
+        what the key does not hold (an address, a stride)."""
+        if self.empty:
+            return 0
         key = (cache.page_size, cache.Hkv, cache.D, Hq)
         nb = self._ws_bytes.get(key)
         if nb is None:
-            nb = 0 if self.empty else _lib.lib().qcf_shared_prefix_attn_workspace_size(cache.ref, self.ref, Hq)
-            self._ws_bytes[key] = nb
+            nb = _lib.lib().qcf_shared_prefix_attn_workspace_size(cache.ref, self.ref, Hq)
+            if nb:
+                self._ws_bytes[key] = nb
         return nb
 
 

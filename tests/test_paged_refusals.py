@@ -147,3 +147,20 @@ def test_binding_refuses_host_tensors(L):
         Q.PagedBatch(torch.zeros(4, dtype=torch.int64), i, torch.zeros((3, 2), dtype=torch.int32), 3, 1, 32)
     with pytest.raises(L.QcfError):
         Q.PagedBatch(torch.zeros(4, dtype=torch.int32), i, torch.zeros((2, 2), dtype=torch.int32), 3, 1, 32)
+
+
+def test_a_refused_layout_leaves_no_workspace_size_behind(L):
+    """The size that one batch keeps for a layout is asked for again after a cache of that layout was refused."""
+    torch = pytest.importorskip("torch")
+    from types import SimpleNamespace
+    from rag_kv_cache_re_gb300 import qcf as Q
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+    bt = Q.PagedBatch(i32(0, 1, 2), i32(5, 9), torch.zeros((2, 4), dtype=torch.int32), 2, 1, 64)
+
+    def layout(**kw):
+        struct = cache(L, **kw)
+        return SimpleNamespace(struct=struct, ref=C.byref(struct), page_size=16, Hkv=8, D=128)
+    for wrong in (dict(row_stride=1028), dict(k=P + 2), dict(n_pages=0)):
+        assert bt.workspace_size(layout(**wrong), 32) == 0
+    good = bt.workspace_size(layout(), 32)
+    assert good > 0 and bt.workspace_size(layout(), 32) == good
