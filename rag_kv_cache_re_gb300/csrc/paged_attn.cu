@@ -762,6 +762,9 @@ qcf_status qcf_shared_prefix_attn(const qcf_paged_kv* cache, const qcf_paged_bat
     return set_error(QCF_ERR_SHAPE, "%s: q_stride %lld for %d x %d entries", who, (long long)q_stride, Hq, c.D);
   if (take_fault(4) || !aligned16(q) || !aligned16(o) || q_stride % 8 || (reinterpret_cast<uintptr_t>(ws) & 255u))
     return set_error(QCF_ERR_ALIGN, "%s: pointers and strides must be multiples of 16 bytes, ws of 256", who);
+  // warps write finished rows of o while others still load the queries of other rows
+  if (o == q && q_stride != static_cast<int64_t>(Hq) * c.D)
+    return set_error(QCF_ERR_SHAPE, "%s: o is q, whose rows lie %lld entries apart instead of %d x %d", who, (long long)q_stride, Hq, c.D);
   if (take_fault(1)) return set_error(QCF_ERR_INVALID_ARG, "%s: injected invalid index table", who);
   if (take_fault(2)) return set_error(QCF_ERR_WORKSPACE, "%s: injected short workspace", who);
   if (b.n_seq == 0 || b.n_rows == 0) return QCF_OK;

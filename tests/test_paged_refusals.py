@@ -164,3 +164,12 @@ def test_a_refused_layout_leaves_no_workspace_size_behind(L):
         assert bt.workspace_size(layout(**wrong), 32) == 0
     good = bt.workspace_size(layout(), 32)
     assert good > 0 and bt.workspace_size(layout(), 32) == good
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(q=P, o=P, qs=4096), OK), (dict(q=P, o=P, qs=4104), SHAPE), (dict(q=P, o=P, qs=6144), SHAPE), (dict(q=P, o=2 * P, qs=6144), OK),
+    (dict(q=P, o=P, qs=6144, Hq=48), OK)])
+def test_attention_writes_over_its_queries_only_row_for_row(L, kw, expect):
+    """o may be q only where the rows of both lie Hq D entries apart."""
+    assert attend(L, cache(L), batch(L), **kw) == expect
+    assert attend(L, cache(L), batch(L, prefix_len=0, prefix_pages=None), **kw) == expect
