@@ -518,6 +518,8 @@ qcf_status qcf_rope_table_fill(float* cos, float* sin, int first_pos, int n_pos,
  *          | QCF_ROPE_INVERSE turns by the negative angle (undoes a rotation of amplitude
  *          1; also the gradient with respect to x)
  *   dtype  QCF_BF16, QCF_F16 or QCF_F32; arithmetic in fp32, rounded once.
+ * One call takes n ceil(H / 4) (D / 2) / V < 2^32 - 256, V the largest of 8, 4, 2, 1 that divides
+ * R / 2, (D - R) / 2 and both strides; more rows are refused (QCF_ERR_SHAPE) and go in several calls.
  * For bf16 and QCF_ROPE_HALF the bits are those of qcf_rope_reposition. */
 #define QCF_ROPE_HALF 0
 #define QCF_ROPE_INTERLEAVED 1

@@ -277,7 +277,8 @@ qcf_status qcf_rope_apply(const void* x, int64_t x_stride, void* y, int64_t y_st
   if (take_fault(4) || !aligned16(x) || !aligned16(y) || !aligned16(t->cos) || !aligned16(t->sin))
     return set_error(QCF_ERR_ALIGN, "qcf_rope_apply: pointers must be 16-byte aligned");
   if (take_fault(1)) return set_error(QCF_ERR_INVALID_ARG, "qcf_rope_apply: injected invalid index table");
-  if (static_cast<int64_t>(n) * ((H + kRopeHeads - 1) / kRopeHeads) * (D / 2) > UINT32_MAX - 256)
+  // threads are counted in 32 bits
+  if (static_cast<int64_t>(n) * ((H + kRopeHeads - 1) / kRopeHeads) * (D / 2 / item_width(R, D, x_stride, y_stride)) > UINT32_MAX - 256)
     return set_error(QCF_ERR_SHAPE, "qcf_rope_apply: %d rows of %d x %d entries are too many for one call", n, H, D);
   if (n == 0) return QCF_OK;
   const RopeApply r{x, x_stride, y, y_stride, n, H, D, R, pos, t, mode, static_cast<cudaStream_t>(stream)};
