@@ -680,6 +680,8 @@ static cudaError_t stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, c
   });
   if (attr != cudaSuccess) return attr;
   LaunchScope ls(KC_OWN_ATTN, st);
+  // Not launch_pdl: that this kernel starts behind all earlier work is what lets it, and the prefix kernel
+  // launched beside it, read queries and pages and write the scratch without a wait of their own.
   const dim3 grid(p.ctas), block(StreamCfg<D>::WARPS * 32);
   stream_attn_kernel<T, D><<<grid, block, stream_smem<D>(b.n_seq), st>>>(tk, tv, c, b, a, p, w, device_status_ptr());
   return cudaGetLastError();

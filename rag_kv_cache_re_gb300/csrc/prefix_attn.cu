@@ -105,8 +105,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   using Cfg = PreCfg<D>;
   constexpr int KST = Cfg::K_STAGES, VST = Cfg::V_STAGES;
   constexpr unsigned kAll = 0xffffffffu;
-  // Launched while the stream kernel runs, on whose results nothing here depends; the join waits for
-  // this kernel alone, so this one ends after the stream has (its pdl_wait).
+  // Launched while the stream kernel runs, on whose results nothing here depends.  What this kernel
+  // does depend on (queries, pages, the join of the call before, which reads the parts that are
+  // written here) has ended before the stream began, for the stream is launched without the programmatic
+  // attribute.  The join waits for this kernel alone, so this one ends after the stream has (its
+  // pdl_wait).
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);

@@ -71,7 +71,9 @@ int current_device();
 // predecessor in the stream drains (set-up of barriers, tensor memory and constant
 // operands overlaps the predecessor's tail); it must execute pdl_wait() before it
 // touches anything the predecessor (or earlier work) produced.  Only kernels that do
-// so are launched with it.
+// so are launched with it, but for one: prefix_attn_kernel waits at its end, and may
+// because the kernel before it uses none of its data and itself starts only when all
+// earlier work has ended (stream_launch in paged_attn.cu).
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                               Args&&... args) {
