@@ -774,7 +774,7 @@ qcf_status qcf_shared_prefix_attn(const qcf_paged_kv* cache, const qcf_paged_bat
   Workspace w;
   const size_t need = workspace_layout(p, b, Hq, c.D, ws, &w);
   if (!ws || ws_bytes < need) return set_error(QCF_ERR_WORKSPACE, "%s: workspace %zu < %zu", who, ws_bytes, need);
-  const AttnArgs a{q, q_stride, cache->k, cache->v, o, lse, Hq, Hq / c.Hkv,
+  const AttnArgs a{q, q_stride, o, lse, Hq, Hq / c.Hkv,
                    static_cast<uint32_t>(((1ull << 32) + Hq / c.Hkv - 1) / (Hq / c.Hkv)), scale * 1.4426950408889634f};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return cache->dtype == QCF_BF16 ? shared_prefix_attn_type<__nv_bfloat16>(cache, c, b, a, p, w, st)

@@ -9,8 +9,6 @@ namespace qcf {
 struct AttnArgs {
   const void* q;
   int64_t q_stride;
-  const void* k;
-  const void* v;
   void* o;
   float* lse;
   int Hq, G;          // G = Hq / Hkv
