@@ -466,8 +466,8 @@ qcf_status qcf_lm_head(const qcf_model* m, const float* x_last, float* logits, i
  * What a program needs after the fused prefill, when several sequences (answers sampled
  * from one request, or several questions) go on from the same context: positions turned
  * into rotations for the layouts and scalings models use, a paged cache that grows with
- * each sequence, and the attention of such a batch, which reads the shared context once
- * for all sequences.  Tensors here are bf16 or fp16 (rotation also fp32); every tensor of
+ * each sequence, and the attention of such a batch, which reads the shared context for many
+ * sequences at a time.  Tensors here are bf16 or fp16 (rotation also fp32); every tensor of
  * one call has the same type. */
 #define QCF_BF16 0
 #define QCF_F16 1
@@ -484,6 +484,11 @@ qcf_status qcf_lm_head(const qcf_model* m, const float* x_last, float* logits, i
  *           and `low` turns: i(t) = R ln(L0 / (2 pi t)) / (2 ln theta),
  *           a = max(0, floor(i(high))), b = min(R/2 - 1, ceil(i(low))),
  *           g = 1 - clamp((k - a) / max(b - a, 0.001), 0, 1)
+ *           The blend ends at the last pair at the latest.  Methods that clamp b at R - 1 let it end
+ *           behind that pair, and so have other rates wherever even the last pair makes more than
+ *           `low` turns over L0 (theta 1e4, R 128, low 1: L0 above 54000; also small R).  Such rates,
+ *           as any others, come in tables that the caller writes: a qcf_rope_table is only its
+ *           cosines and sines.
  * amplitude multiplies cosine and sine (1 for none; a table used to move keys that are
  * already rotated wants 1). */
 #define QCF_ROPE_SCALE_NONE 0
@@ -578,8 +583,11 @@ qcf_status qcf_paged_append(const qcf_paged_kv* cache, const qcf_paged_batch* ba
 
 /* Attention of a batch over its shared prefix and its own tokens: for row i of sequence b at
  * own position p, o[i,h] = sum_j softmax_j(scale * q[i,h] . K_j) V_j over every prefix token
- * and own tokens j <= p, g = h / (Hq/Hkv), one softmax over both.  The prefix is read once
- * for all rows of the batch (a short one once for every 16 of a KV head's score rows).
+ * and own tokens j <= p, g = h / (Hq/Hkv), one softmax over both.
+ * A KV head has Hq / Hkv score rows for each row of the batch.  A long prefix at head dim 64 or 128
+ * is loaded once for every 2 floor(128 Hkv / Hq) rows of the batch (up to 256 score rows); a short
+ * one, one with at most 16 score rows, and any at head dim 16, once for every 16 score rows.  What is
+ * loaded again comes from L2 as far as it fits there.
  *   q    device, rows of Hq heads of D contiguous entries, q_stride entries apart
  *   o    device [n_rows][Hq][D], the cache's type; may be q itself (q_stride = Hq D), and
  *        overlaps nothing else
@@ -587,12 +595,14 @@ qcf_status qcf_paged_append(const qcf_paged_kv* cache, const qcf_paged_batch* ba
  *   ws   device scratch of qcf_shared_prefix_attn_workspace_size() bytes; it needs no clearing;
  *        calls that overlap on the GPU (captured graphs replayed side by side among them) need
  *        separate scratch
- * scale > 0, Hq / Hkv <= 16.  Cache rows behind a length (the rest of a last page, pages not named) may
+ * scale > 0, Hq / Hkv <= 16, n_rows Hq < 2^24; bounds that allow more than about 2^31 tiles of 16
+ * score rows and 32 keys are refused (QCF_ERR_SHAPE).  Cache rows behind a length (the rest of a last page, pages not named) may
  * hold anything, NaN included; a new token whose value holds NaN or infinity may spoil
  * every row of its own sequence.  A page outside the cache sets QCF_DEV_BAD_INDEX, and its
  * keys are left out of the softmax.  Products in the cache's type with fp32 sums, softmax in
- * fp32.  Results repeat bitwise for the same inputs and bounds.  Own tokens are scored 16 rows at a
- * time, for steps and questions; the prefill of a long text is qcf_sparse_causal_attn's work. */
+ * fp32.  Results repeat bitwise for the same inputs and bounds.  Own tokens are loaded
+ * again for every 16 score rows: meant for steps and questions.  New texts of hundreds of rows are right
+ * but slow (4 of 1024 rows over 5120 keys, 32 heads over 8: 622 us, a third of the tensor rate). */
 size_t qcf_shared_prefix_attn_workspace_size(const qcf_paged_kv* cache, const qcf_paged_batch* batch, int Hq);
 qcf_status qcf_shared_prefix_attn(const qcf_paged_kv* cache, const qcf_paged_batch* batch, const void* q,
                                   int64_t q_stride, int Hq, float scale, void* o, float* lse, void* ws, size_t ws_bytes,
