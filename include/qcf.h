@@ -586,8 +586,8 @@ qcf_status qcf_paged_append(const qcf_paged_kv* cache, const qcf_paged_batch* ba
  * and own tokens j <= p, g = h / (Hq/Hkv), one softmax over both.
  * A KV head has Hq / Hkv score rows for each row of the batch.  A long prefix at head dim 64 or 128
  * is loaded once for every 2 floor(128 Hkv / Hq) rows of the batch (up to 256 score rows); a short
- * one, one with at most 16 score rows, and any at head dim 16, once for every 16 score rows.  What is
- * loaded again comes from L2 as far as it fits there.
+ * one, and any at head dim 16 or beside at most 16 score rows, once for every 16 of them.  What is loaded
+ * again comes from L2 as far as it fits there.
  *   q    device, rows of Hq heads of D contiguous entries, q_stride entries apart
  *   o    device [n_rows][Hq][D], the cache's type; may be q itself (q_stride = Hq D), and
  *        overlaps nothing else

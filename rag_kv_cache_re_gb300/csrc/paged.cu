@@ -62,7 +62,8 @@ struct AppendArgs {
 // rows go (one warp per row looks up the sequence, the position and the page).  V: pairs per item
 // (see item_at).  HBM-bound for many rows, 737 MB in 117 us (6.3 TB/s; 177 us with the lookup
 // before the loads), and by that chain of lookups for few: 61 MB of 64 short sequences in 16 us,
-// 16 rows in 3.7.
+// 16 rows in 3.9.  Four CTAs an SM leave 64 registers: pairs of neighbours spill 8 bytes a thread,
+// halves 92, which costs nothing (the 737 MB with halves: 114 us).
 constexpr int kAppendThreads = 256;
 constexpr int kAppendHeads = 4;
 

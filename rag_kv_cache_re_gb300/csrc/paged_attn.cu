@@ -3,7 +3,7 @@
 // With logits x_j = scale q.K_j, any set of keys P is summed up by M = max x_j, L = sum 2^(x_j - M)
 // (x in powers of two) and O = sum 2^(x_j - M) V_j; two sets join by scaling each with
 // 2^(M - max M).  The keys of a row are split into such parts: chunks of the prefix, scored for
-// all rows of the batch together so that its K and V are read once, and chunks of the sequence's
+// all rows of the batch together so that its K and V are read for many of them at once, and chunks of the sequence's
 // own tokens.  A last kernel joins the parts of each row.
 #include <algorithm>
 #include <cmath>
@@ -29,14 +29,14 @@ constexpr int kMostTiles = INT32_MAX - (1 << 20);   // tiles of one call, with r
 // Bound by the K and V bytes; the rings keep 96 KB or more per SM in flight.  386 MB of uneven
 // sequences of head dim 64 in 66 to 71 us (5.4 to 5.8 TB/s), 67 MB of short ones in 20, of which
 // about 5 pass before the first tile is scored.  It serves any number of new rows, but a question of
-// thousands of tokens is work for 128-row tiles.
+// thousands of tokens is work for 128-row tiles (4 of 1024 rows: 622 us the call, 196 the floor).
 template <int D>
 struct StreamCfg {
   static constexpr int COLS = D < 64 ? D : 64, BOXES = D / COLS;
   static constexpr int BOX = kStreamKeys * COLS * 2;   // 32 keys x COLS entries
   static constexpr int TILE = BOXES * BOX;             // a K or V tile
   static constexpr int STAGES = D >= 64 ? 2 : 4;
-  static constexpr int WARPS = D == 128 ? 6 : 12;      // 192 KB of rings (48 KB at head dim 16)
+  static constexpr int WARPS = D == 128 ? 6 : 12;      // 192 KB of rings (96 KB at head dim 16)
   static constexpr int RING = STAGES * 2 * TILE;       // of a warp
   static constexpr int FIXED = WARPS * (RING + STAGES * 8);
 };

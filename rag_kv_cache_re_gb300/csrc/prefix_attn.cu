@@ -1,5 +1,6 @@
 // The shared prefix of a batch on tcgen05 tensor cores (head dims 64 and 128): its K and V are
-// read once for all rows.
+// loaded once for every 256 score rows of a KV head (2 (128 / G) rows of the batch), and by the units
+// of further rows out of L2 as far as they fit.
 //
 // The score rows of one KV head (rows of the batch x the G query heads that share it) are stacked
 // into units of two 128-row tiles, a and b, which share every K and V tile of 128 keys.  The tiles
@@ -27,8 +28,10 @@
 //
 // Bound: HBM below about 285 score rows per KV head, the tensor pipe above.  131072 keys of 8 KV heads
 // against 256 score rows each: 99 us, 5.4 TB/s and 1.39 PFLOP/s at once; 16384 keys against 1564: 80 us,
-// 1.2 PFLOP/s.  A pair of 128 x 128 tiles takes 2860 to 3030 cycles, 2048 of them products: the S
-// products read both operands from shared memory at its full rate.
+// 1.31 PFLOP/s.  A pair of 128 x 128 tiles takes 2860 to 3030 cycles, 2048 of them products: the S
+// products read both operands from shared memory at its full rate.  ptxas, which plans for 168 registers in every
+// warp, spills 12 bytes a thread.  At head dim 64, with half the products to a tile and the same
+// softmax, the call with 131072 keys and 256 score rows a KV head takes 99 us (116 at 128; floor 41).
 #include <algorithm>
 
 #include "paged_attn.cuh"

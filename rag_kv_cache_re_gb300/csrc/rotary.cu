@@ -52,7 +52,8 @@ __device__ __forceinline__ TwoSinCos two_add(const TwoSinCos& a, const TwoSinCos
 // is rounded once.  The parts are of the position itself, so an entry's bits do not depend on the
 // call that fills it.  Thread = (pair, b and part of c): it forms b + c once and uses it for every a,
 // and a warp writes runs of 4 PAIRS bytes.  1024 threads: one CTA per SM has the fewest fp64 values.
-// 131072 positions of 64 pairs, 16 to a CTA: 22.6 us, 3.0 TB/s (32, whole 128-byte lines but twice
+// 131072 positions of 64 pairs, 16 to a CTA: 23 us, 2.9 TB/s.  About 16 of them are the additions and stores:
+// without the fp64 values the kernel takes 18.3, and one that returns behind them 6.2, launch included (32, whole 128-byte lines but twice
 // the fp64 values per SM: 28 us).  8192 positions of 32 pairs: 5.7 us with 8 to a CTA, 8.5 with 16,
 // which fills 64 SMs only.
 constexpr int kTableThreads = 1024;
@@ -113,7 +114,9 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(float* __rest
 // once and serve every head of the chunk, whose loads are all in flight together (and before the
 // position is known).  HBM-bound: 17984 rows of 72 heads of 128 in bf16 take 97.7 us, 6.8 TB/s, the
 // rate of a copy; with the entries unpacked as they come (twice the registers) 152 us, with 8 heads
-// to a thread 224.
+// to a thread 224.  In fp32 eight pairs of four heads are 64 registers of entries: the kernel spills 144
+// bytes a thread and takes 210 us for the same rows (floor 195), neighbours 246.  Runs shorter than 8
+// move fewer bytes an access: heads of 80 turned whole 65 us (floor 61), 32 of the 80 entries 68, 20 of them 75.
 constexpr int kRopeHeads = 4;
 template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(256, 3) rope_apply_kernel(const T* x, int64_t x_stride, T* y, int64_t y_stride, int n, int H,
