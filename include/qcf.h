@@ -596,8 +596,8 @@ qcf_status qcf_paged_append(const qcf_paged_kv* cache, const qcf_paged_batch* ba
  *        calls that overlap on the GPU (captured graphs replayed side by side among them) need
  *        separate scratch
  * scale > 0, Hq / Hkv <= 16, n_rows Hq < 2^24; bounds that allow more than about 2^31 tiles of 16
- * score rows and 32 keys are refused (QCF_ERR_SHAPE).  Cache rows behind a length (the rest of a last page, pages not named) may
- * hold anything, NaN included; a new token whose value holds NaN or infinity may spoil
+ * score rows and 32 keys are refused (QCF_ERR_SHAPE).  Cache rows behind a length (the rest of a last
+ * page, pages not named) may hold anything, NaN included; a new token whose value holds NaN or infinity may spoil
  * every row of its own sequence.  A page outside the cache sets QCF_DEV_BAD_INDEX, and its
  * keys are left out of the softmax.  Products in the cache's type with fp32 sums, softmax in
  * fp32.  Results repeat bitwise for the same inputs and bounds.  Own tokens are loaded

@@ -53,8 +53,8 @@ __device__ __forceinline__ TwoSinCos two_add(const TwoSinCos& a, const TwoSinCos
 // call that fills it.  Thread = (pair, b and part of c): it forms b + c once and uses it for every a,
 // and a warp writes runs of 4 PAIRS bytes.  1024 threads: one CTA per SM has the fewest fp64 values.
 // 131072 positions of 64 pairs, 16 to a CTA: 23 us, 2.9 TB/s.  About 16 of them are the additions and stores:
-// without the fp64 values the kernel takes 18.3, and one that returns behind them 6.2, launch included (32, whole 128-byte lines but twice
-// the fp64 values per SM: 28 us).  8192 positions of 32 pairs: 5.7 us with 8 to a CTA, 8.5 with 16,
+// without the fp64 values the kernel takes 18.3, and one that returns behind them 6.2, launch
+// included (32, whole 128-byte lines but twice the fp64 values per SM: 28 us).  8192 positions of 32 pairs: 5.7 us with 8 to a CTA, 8.5 with 16,
 // which fills 64 SMs only.
 constexpr int kTableThreads = 1024;
 template <int PAIRS>
