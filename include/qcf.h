@@ -608,6 +608,52 @@ qcf_status qcf_shared_prefix_attn(const qcf_paged_kv* cache, const qcf_paged_bat
                                   int64_t q_stride, int Hq, float scale, void* o, float* lse, void* ws, size_t ws_bytes,
                                   void* stream);
 
+/* ------------------------------------------------------------------ whole prompts and chunks of them
+ *
+ * Attention of many new tokens of a sequence at a time.  Both calls take head groups of
+ * Hq / Hkv <= 128, read lengths on the device (a captured graph can be replayed with others
+ * within the bounds) and share these arguments:
+ *   q       device, rows of Hq heads of D contiguous entries, q_stride entries apart
+ *   window  0: every key up to the row's own position; w > 0: the last w of them, its own among them
+ *   o       device [n_rows][Hq][D], the type of q; may be q itself (q_stride = Hq D), and
+ *           overlaps nothing else.  Rows in no sequence are left as they were
+ *   lse     device [n_rows][Hq] fp32 natural-log sum of exp of the scaled logits, or NULL
+ *   ws      device scratch of the matching *_workspace_size() bytes (0: ws may be NULL); it needs
+ *           no clearing; calls that overlap on the GPU (captured graphs replayed side by side
+ *           among them) need separate scratch
+ * scale > 0; n_seq <= 16384; n_rows Hq < 2^24 (QCF_ERR_SHAPE).  Products in the type of q with fp32
+ * sums, softmax in fp32.  Results repeat bitwise for the same inputs and bounds.  A NaN in a query
+ * stays in its row and head; a key or value that holds NaN or infinity may spoil every row of its
+ * own sequence (a prefix token: of the batch), masked or not, and no other. */
+
+/* Causal attention of whole prompts packed one behind the other: rows row_start[b] <= row <
+ * row_start[b + 1] are the tokens of sequence b in order, and token i attends to the tokens
+ * j <= i of its own sequence (i - window < j with a window).
+ *   k, v       device, rows of Hkv heads of D contiguous entries, kv_stride entries apart
+ *   dtype      QCF_BF16 or QCF_F16
+ *   row_start  device [n_seq + 1], ascending
+ *   max_len    bound on a sequence's rows
+ * D a multiple of 8, 8 .. 128 (computed as 64 or 128).  A sequence longer than max_len, or with
+ * rows outside [0, n_rows), is left out and sets QCF_DEV_BAD_INDEX. */
+size_t qcf_packed_causal_attn_workspace_size(int n_seq, int n_rows, int max_len, int Hq, int Hkv, int D);
+qcf_status qcf_packed_causal_attn(const void* q, int64_t q_stride, const void* k, const void* v, int64_t kv_stride,
+                                  int dtype, const int32_t* row_start, int n_seq, int n_rows, int max_len, int Hq,
+                                  int Hkv, int D, float scale, int window, void* o, float* lse, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/* Attention of chunks of new tokens over a paged cache that holds them already
+ * (qcf_paged_append): the arguments and the result of qcf_shared_prefix_attn, but for the window,
+ * which counts positions (prefix_len + own).  Meant for chunks of prompts, alone or among the single
+ * tokens of running sequences; a step of single tokens alone that share a long prefix is
+ * faster through qcf_shared_prefix_attn, which loads the prefix once for many of them.  Cache rows
+ * behind a length (the rest of a last page, pages not named) may hold anything, NaN included.  A page
+ * outside the cache sets QCF_DEV_BAD_INDEX, and its keys are left out of the softmax; a row
+ * left without any key gets o = 0 and lse = -infinity. */
+size_t qcf_paged_chunk_attn_workspace_size(const qcf_paged_kv* cache, const qcf_paged_batch* batch, int Hq);
+qcf_status qcf_paged_chunk_attn(const qcf_paged_kv* cache, const qcf_paged_batch* batch, const void* q, int64_t q_stride,
+                                int Hq, float scale, int window, void* o, float* lse, void* ws, size_t ws_bytes,
+                                void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -143,6 +143,10 @@ PROTOTYPES = {
                              I64, I, P]),
     "qcf_shared_prefix_attn_workspace_size": (SZ, [C.POINTER(PagedKV), C.POINTER(PagedBatch), I]),
     "qcf_shared_prefix_attn": (I, [C.POINTER(PagedKV), C.POINTER(PagedBatch), P, I64, I, F, P, P, P, SZ, P]),
+    "qcf_packed_causal_attn_workspace_size": (SZ, [I, I, I, I, I, I]),
+    "qcf_packed_causal_attn": (I, [P, I64, P, P, I64, I, P, I, I, I, I, I, I, F, I, P, P, P, SZ, P]),
+    "qcf_paged_chunk_attn_workspace_size": (SZ, [C.POINTER(PagedKV), C.POINTER(PagedBatch), I]),
+    "qcf_paged_chunk_attn": (I, [C.POINTER(PagedKV), C.POINTER(PagedBatch), P, I64, I, F, I, P, P, P, SZ, P]),
 }
 
 _lock = threading.Lock()

@@ -33,7 +33,7 @@ enum KernelClass {
   KC_ROPE = 0, KC_ANCHOR, KC_PROFILE, KC_TOPN, KC_GATHER, KC_SCATTER, KC_ATTN, KC_ATTN_COMBINE,
   KC_GEMM_QKV, KC_GEMM_O, KC_GEMM_GU, KC_GEMM_DOWN, KC_GEMM_OTHER, KC_RMSNORM, KC_EMBED,
   KC_LMHEAD, KC_MISC, KC_GEMM_PROBE, KC_ATTN_PROBE, KC_ROPE_APPLY, KC_ROPE_TABLE, KC_APPEND,
-  KC_PREFIX_ATTN, KC_OWN_ATTN, KC_BATCH_COMBINE, KC_COUNT
+  KC_PREFIX_ATTN, KC_OWN_ATTN, KC_BATCH_COMBINE, KC_CHUNK_ATTN, KC_CHUNK_JOIN, KC_PAGES, KC_COUNT
 };
 struct LaunchScope {
   LaunchScope(KernelClass kc, cudaStream_t s);

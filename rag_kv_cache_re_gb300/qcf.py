@@ -577,3 +577,54 @@ def qcf_shared_prefix_attn(cache: PagedKV, batch: PagedBatch, q: torch.Tensor, s
         call("qcf_shared_prefix_attn", cache.ref, batch.ref, q.data_ptr(), qs, Hq, scale, out.data_ptr(),
              None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), nb, _raw_stream(stream, cache.dev))
     return (out, lse) if want_lse else out
+
+
+# ------------------------------------------------------------------ whole prompts and chunks of them
+
+def _attn_out(q: torch.Tensor, out: Optional[torch.Tensor], want_lse: bool, dev: int, stream):
+    if out is None:
+        out = _empty(q.shape, q.dtype, dev, stream)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.get_device() != dev:
+        _bad("out must be contiguous, of the shape, type and device of q")
+    return out, _empty(q.shape[:2], torch.float32, dev, stream) if want_lse else None
+
+
+def qcf_packed_causal_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, row_start: torch.Tensor, max_len: int, scale: float,
+                           window: int = 0, want_lse: bool = False, out: Optional[torch.Tensor] = None, stream=None):
+    """Causal attention of whole prompts packed one behind the other: q [n_rows][Hq][D], k and v
+    [n_rows][Hkv][D] (heads of a row contiguous, any row stride), row_start [n_seq + 1] int32 on the
+    device, max_len a bound on a prompt's tokens.  Returns out (a new tensor unless given; rows of no
+    prompt are not written), with lse if asked."""
+    (n, Hq, D, qs), (nk, Hk, Dk, ks), (nv, Hv, Dv, vs) = _head_rows(q, "q"), _head_rows(k, "k"), _head_rows(v, "v")
+    dev = _here(q)
+    if (nk, Dk) != (n, D) or (nv, Hv, Dv) != (n, Hk, D) or ks != vs or k.dtype != q.dtype or v.dtype != q.dtype:
+        _bad("k and v must have the rows, head dim and type of q, and one row stride")
+    if k.get_device() != dev or v.get_device() != dev or row_start.get_device() != dev:
+        _bad("tensors must be on the current CUDA device")
+    if row_start.dim() != 1 or row_start.numel() < 1:
+        _bad("row_start must hold a start per sequence and the end of the last")
+    _need_i32(row_start, "row_start")
+    out, lse = _attn_out(q, out, want_lse, dev, stream)
+    n_seq = row_start.numel() - 1
+    if n and n_seq:   # empty tensors have no address to pass
+        nb = _lib.lib().qcf_packed_causal_attn_workspace_size(n_seq, n, max_len, Hq, Hk, D)
+        ws = _empty(nb, torch.uint8, dev, stream) if nb else None
+        call("qcf_packed_causal_attn", q.data_ptr(), qs, k.data_ptr(), v.data_ptr(), ks, _DTYPE[q.dtype], row_start.data_ptr(), n_seq, n,
+             max_len, Hq, Hk, D, scale, window, out.data_ptr(), None if lse is None else lse.data_ptr(),
+             None if ws is None else ws.data_ptr(), nb, _raw_stream(stream, dev))
+    return (out, lse) if want_lse else out
+
+
+def qcf_paged_chunk_attn(cache: PagedKV, batch: PagedBatch, q: torch.Tensor, scale: float, window: int = 0, want_lse: bool = False,
+                         out: Optional[torch.Tensor] = None, stream=None):
+    """Attention of chunks of new tokens, q [n_rows][Hq][D], over the batch's prefix and own tokens in
+    pages.  Returns out (a new tensor unless given; padding rows are not written), with lse if asked."""
+    _cache_and_batch(cache, batch)
+    Hq, qs = _batch_rows(cache, batch, q, "q")
+    out, lse = _attn_out(q, out, want_lse, cache.dev, stream)
+    if not batch.empty:
+        nb = _lib.lib().qcf_paged_chunk_attn_workspace_size(cache.ref, batch.ref, Hq)
+        ws = _empty(nb, torch.uint8, cache.dev, stream) if nb else None
+        call("qcf_paged_chunk_attn", cache.ref, batch.ref, q.data_ptr(), qs, Hq, scale, window, out.data_ptr(),
+             None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), nb, _raw_stream(stream, cache.dev))
+    return (out, lse) if want_lse else out
