@@ -63,6 +63,7 @@ typedef enum qcf_status {
 /* Device status word bits (qcf_query_status). */
 #define QCF_DEV_TIMEOUT 0x1u
 #define QCF_DEV_BAD_INDEX 0x2u
+#define QCF_DEV_NO_PAGES 0x4u
 
 /* ------------------------------------------------------------------ library */
 
@@ -653,6 +654,56 @@ size_t qcf_paged_chunk_attn_workspace_size(const qcf_paged_kv* cache, const qcf_
 qcf_status qcf_paged_chunk_attn(const qcf_paged_kv* cache, const qcf_paged_batch* batch, const void* q, int64_t q_stride,
                                 int Hq, float scale, int window, void* o, float* lse, void* ws, size_t ws_bytes,
                                 void* stream);
+
+/* ------------------------------------------------------------------ the pages of a cache
+ *
+ * Sequences whose tokens lie in pages, the same page ids in every layer's cache, with counts, tables
+ * and lengths on the device (page_table and kv_len as qcf_paged_batch reads them; a shared prefix is
+ * a sequence like any other, its row of the table the prefix_pages):
+ *   refs        device [n_pages]: rows of the table that hold the page; 0: free
+ *   page_table  device [n_seq][table_stride]; row b holds ceil(kv_len[b] / page_size) pages, what is
+ *               behind them has no meaning and is left as it is
+ *   kv_len      device [n_seq]
+ * New pages are the lowest ids that were free before the call, in the order of its arguments:
+ * pages given back by a call serve the next one.  A call does all it was asked or nothing: an
+ * argument that its description rules out sets QCF_DEV_BAD_INDEX, too few free pages
+ * QCF_DEV_NO_PAGES, and nothing has changed.  A page id outside the cache in a row that is only given
+ * back or shared sets QCF_DEV_BAD_INDEX and is not counted.  Copies move whole entries; rows behind a length may hold anything.
+ *   ws  device scratch of qcf_pages_workspace_size(pool, n) bytes; it needs no clearing; calls
+ *       that overlap on the GPU need separate scratch (and may not share a pool)
+ * n <= n_seq <= 65535, table_stride <= 2^20, 1 to 256 caches of one layout; refs 16-byte aligned,
+ * the other tables 4. */
+typedef struct qcf_page_pool {
+  const qcf_paged_kv* caches;  /* HOST [n_caches]: every layer's */
+  int n_caches;
+  int32_t* refs;
+  int32_t* page_table;
+  int table_stride;
+  int32_t* kv_len;
+  int n_seq;
+} qcf_page_pool;
+
+/* Scratch of a call with n arguments (qcf_pages_compact: n = 0); 0 for a pool that is refused. */
+size_t qcf_pages_workspace_size(const qcf_page_pool* pool, int n);
+
+/* Sequence dst[i] goes on from src[i] for i < n (src, dst device [n]): what dst held is given back, it
+ * takes the length of src, holds its full pages together with it, and has a copy of the page that src holds
+ * in part.  Every dst once, and none of them a src; a src any number of times. */
+qcf_status qcf_pages_fork(const qcf_page_pool* pool, const int32_t* src, const int32_t* dst, int n, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/* Sequence seqs[i] (seqs NULL: i) gets the length new_len[i] for i < n, 0 <= new_len <= table_stride *
+ * page_size (device [n]): pages behind it are given back, missing ones taken (their rows hold
+ * anything).  Where the length changes and the last page that stays is held in part, and by others too,
+ * its rows are copied to a new page, so that a later append writes into no other sequence.  Every
+ * sequence once. */
+qcf_status qcf_pages_resize(const qcf_page_pool* pool, const int32_t* seqs, const int32_t* new_len, int n, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* Moves the pages in use to the lowest ids: with *n_live (device) pages in use, the k-th of those at
+ * or above n_live goes to the k-th free one below it, rows, counts and tables alike.  Every
+ * holder of a page is a row of the table. */
+qcf_status qcf_pages_compact(const qcf_page_pool* pool, int32_t* n_live, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -16,6 +16,7 @@ STATUS_NAMES = {0: "QCF_OK", 1: "QCF_ERR_INVALID_ARG", 2: "QCF_ERR_SHAPE", 3: "Q
                 8: "QCF_ERR_DEVICE"}
 QCF_DEV_TIMEOUT = 0x1
 QCF_DEV_BAD_INDEX = 0x2
+QCF_DEV_NO_PAGES = 0x4
 QCF_EPI_STORE_BF16 = 0
 QCF_EPI_ADD_F32 = 1
 QCF_LINEAR_W_KN = 0x10
@@ -88,6 +89,11 @@ class PagedBatch(C.Structure):
                 ("table_stride", C.c_int), ("prefix_len", C.c_int), ("prefix_pages", C.c_void_p)]
 
 
+class PagePool(C.Structure):
+    _fields_ = [("caches", C.POINTER(PagedKV)), ("n_caches", C.c_int), ("refs", C.c_void_p), ("page_table", C.c_void_p),
+                ("table_stride", C.c_int), ("kv_len", C.c_void_p), ("n_seq", C.c_int)]
+
+
 P, I, I64, F, D64, SZ = C.c_void_p, C.c_int, C.c_int64, C.c_float, C.c_double, C.c_size_t
 PI32 = C.POINTER(C.c_int32)
 
@@ -147,6 +153,10 @@ PROTOTYPES = {
     "qcf_packed_causal_attn": (I, [P, I64, P, P, I64, I, P, I, I, I, I, I, I, F, I, P, P, P, SZ, P]),
     "qcf_paged_chunk_attn_workspace_size": (SZ, [C.POINTER(PagedKV), C.POINTER(PagedBatch), I]),
     "qcf_paged_chunk_attn": (I, [C.POINTER(PagedKV), C.POINTER(PagedBatch), P, I64, I, F, I, P, P, P, SZ, P]),
+    "qcf_pages_workspace_size": (SZ, [C.POINTER(PagePool), I]),
+    "qcf_pages_fork": (I, [C.POINTER(PagePool), P, P, I, P, SZ, P]),
+    "qcf_pages_resize": (I, [C.POINTER(PagePool), P, P, I, P, SZ, P]),
+    "qcf_pages_compact": (I, [C.POINTER(PagePool), P, P, SZ, P]),
 }
 
 _lock = threading.Lock()

@@ -628,3 +628,80 @@ def qcf_paged_chunk_attn(cache: PagedKV, batch: PagedBatch, q: torch.Tensor, sca
         call("qcf_paged_chunk_attn", cache.ref, batch.ref, q.data_ptr(), qs, Hq, scale, window, out.data_ptr(),
              None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), nb, _raw_stream(stream, cache.dev))
     return (out, lse) if want_lse else out
+
+
+# ------------------------------------------------------------------ the pages of a cache
+
+class PagePool:
+    """The pages of a cache and the sequences that hold them (see qcf_page_pool): `caches` the PagedKV of
+    every layer, all of one layout; refs [n_pages], page_table [n_seq][columns] and kv_len [n_seq] int32 on the
+    device.  page_table and kv_len also serve a PagedBatch."""
+
+    def __init__(self, caches: Sequence[PagedKV], refs: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor):
+        caches = list(caches)
+        if not caches:
+            _bad("a pool needs the cache of a layer at least")
+        self.caches, self.refs, self.page_table, self.kv_len, self.dev = caches, refs, page_table, kv_len, caches[0].dev
+        n_seq = kv_len.numel()
+        _need_i32(kv_len, "kv_len", (n_seq,))
+        _need_i32(refs, "refs", (caches[0].struct.n_pages,))
+        if page_table.dim() != 2 or page_table.shape[0] != n_seq:
+            _bad("page_table must have one row per sequence")
+        _need_i32(page_table, "page_table")
+        if any(t.get_device() != self.dev for t in (refs, page_table, kv_len)) or any(c.dev != self.dev for c in caches):
+            _bad("caches, refs, page_table and kv_len must be on one device")
+        self.n_seq = n_seq
+        self._caches = (_lib.PagedKV * len(caches))(*[c.struct for c in caches])
+        self.struct = _lib.PagePool(self._caches, len(caches), refs.data_ptr(), page_table.data_ptr(), page_table.shape[1], kv_len.data_ptr(),
+                                    n_seq)
+        self.ref = C.byref(self.struct)
+
+    @classmethod
+    def empty(cls, caches: Sequence[PagedKV], n_seq: int, max_len: int) -> "PagePool":
+        """A pool whose pages are all free, for n_seq sequences of up to max_len tokens."""
+        caches = list(caches)
+        if not caches:
+            _bad("a pool needs the cache of a layer at least")
+        dev, cols = caches[0].k.device, max(1, -(-max_len // caches[0].page_size))
+        return cls(caches, *(torch.zeros(shape, dtype=torch.int32, device=dev) for shape in (caches[0].struct.n_pages, (n_seq, cols), n_seq)))
+
+    def _args(self, n: int, *ts: Optional[torch.Tensor]):
+        if self.dev != torch.cuda.current_device():
+            _bad("tensors must be on the current CUDA device")
+        for t in ts:
+            if t is not None:
+                _need_i32(t, "every argument", (n,))
+                if t.get_device() != self.dev:
+                    _bad("tensors must be on the current CUDA device")
+
+    def _scratch(self, n: int, stream):
+        nb = _lib.lib().qcf_pages_workspace_size(self.ref, n)
+        return _empty(max(nb, 1), torch.uint8, self.dev, stream), nb
+
+
+def qcf_pages_fork(pool: PagePool, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+    """Sequences dst[i] (int32 on the device) go on from src[i]: full pages shared, a page held in part copied."""
+    n = src.numel()
+    pool._args(n, src, dst)
+    if n:   # empty tensors have no address to pass
+        ws, nb = pool._scratch(n, stream)
+        call("qcf_pages_fork", pool.ref, src.data_ptr(), dst.data_ptr(), n, ws.data_ptr(), nb, _raw_stream(stream, pool.dev))
+
+
+def qcf_pages_resize(pool: PagePool, new_len: torch.Tensor, seqs: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Sequences seqs[i] (None: 0, 1, ..) get the lengths new_len[i], int32 on the device: pages taken or given back."""
+    n = new_len.numel()
+    pool._args(n, new_len, seqs)
+    if n:
+        ws, nb = pool._scratch(n, stream)
+        call("qcf_pages_resize", pool.ref, None if seqs is None else seqs.data_ptr(), new_len.data_ptr(), n, ws.data_ptr(), nb,
+             _raw_stream(stream, pool.dev))
+
+
+def qcf_pages_compact(pool: PagePool, stream=None) -> torch.Tensor:
+    """Moves the pages in use to the lowest ids; returns how many they are (int32 [1] on the device)."""
+    pool._args(0)
+    live = _empty((1,), torch.int32, pool.dev, stream)
+    ws, nb = pool._scratch(0, stream)
+    call("qcf_pages_compact", pool.ref, live.data_ptr(), ws.data_ptr(), nb, _raw_stream(stream, pool.dev))
+    return live
