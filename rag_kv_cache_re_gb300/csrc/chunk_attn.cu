@@ -5,8 +5,23 @@
 // the keys j <= p (and j > p - window), m a running maximum: one pass over the keys, the sums rescaled
 // when m grows.
 //
-// A CTA takes 64 score rows (new rows x the G query heads of one KV head) of one sequence, 16 to a
-// warp, and walks the key tiles that any of them sees; products on warp tensor cores.
+// Two CTAs of a cluster (a pair) work on one unit: up to four row tiles of 128 score rows (new rows x
+// the G query heads of one KV head) of one sequence, against its key tiles of 128.  A product spans the pair
+// (cta_group::2, 256 rows): row tile x = a, b of both CTAs at once, each holding half of every K
+// tile (64 keys) and of every V tile (half of the columns).  That halves what a CTA loads, keeps and
+// feeds to a product: with K and V whole in one CTA, S = Q K^T reads its operands at the full rate of
+// shared memory (128 bytes a cycle for 64 cycles of products), which the arriving tiles then slow down.
+//
+// Twelve warps a CTA:
+//   warp 0      walks the pair's share of the work and passes units on through a small ring; K producer by
+//               tiled TMA (pages: one box per page and 64 columns), and Q
+//   warp 2      V producer; rows behind a sequence's end are zeroed, since 0 x NaN is NaN
+//   warps 1, 3  in the first CTA, one thread each issues the products of row tile x for both: P_x V, then
+//               S_x = Q_x K^T of the next key tile, the two taking turns
+//   warps 4-7   softmax of a, warps 8-11 of b: thread = score row of this CTA; the weights back to tensor
+//               memory over the scores they came from, the output rescaled only when a row's maximum
+//               grows by more than 2^8; the unit's output at its end
+// Tensor memory columns: S_a 0, S_b 128 (the weights take the first 64 of each), O_a 256, O_b 256 + DP.
 #include <algorithm>
 #include <cmath>
 
@@ -15,16 +30,38 @@
 namespace qcf {
 
 constexpr int kMaxChunkSeqs = 16384;
-constexpr int kChunkRows = 64, kChunkKeys = 64;
+constexpr int kTileKeys = 128;
+constexpr int kTileThreads = 384;
+constexpr int kTileRows = 512;        // score rows of a unit
+// The deal is by cost: so many for a unit, for a key tile of a unit with one row tile in use, with both
+constexpr int kUnitCost = 3, kTileCost1 = 2, kTileCost2 = 3;
+constexpr int kMinCut = 3;            // tiles at least on each side of a cut through a unit
+constexpr int kMinCost = 9;           // dealt to a pair at least
+constexpr int kSegRing = 4;
 
 // What the two entry points differ in: keys and values as rows of one tensor each, or in pages.
 struct ChunkArgs {
   AttnArgs a;
-  const void* k;
-  const void* v;
-  int64_t kv_stride;   // packed: entries from row to row
-  int D, window;
+  int D, window, per;   // per: tokens of a row tile
 };
+struct ChunkParts {     // units cut through: each pair may leave the end of one and the beginning of another
+  int4* rec;            // [pairs]: parts of the unit that begins here and ends elsewhere (0: none), its first row, rows, KV head
+  float2* ml;           // [pairs][2][kTileRows]
+  float* o;             // [pairs][2][kTileRows][D]
+};
+
+template <int DP>
+struct TileCfg {
+  static constexpr int BOXES = DP / 64;
+  static constexpr int QBOX = 128 * 128, QTILE = BOXES * QBOX;          // a CTA's 128 score rows
+  static constexpr int KBOX = 64 * 128, KTILE = BOXES * KBOX;           // its 64 keys
+  static constexpr int VCOLS = DP / 2, VTILE = kTileKeys * VCOLS * 2;   // its columns of 128 values
+  static constexpr int STAGES = DP == 128 ? 4 : 8;
+  static constexpr int OUT = 8 * 4096;                                  // 4 KB for each softmax warp
+  static constexpr int FIXED = 2048;
+  static constexpr int SMEM = 2 * QTILE + STAGES * (KTILE + VTILE) + OUT + FIXED + 1024;
+};
+static_assert(TileCfg<128>::SMEM <= 232448 && TileCfg<64>::SMEM <= 232448, "227 KB of a CTA");
 
 __device__ __forceinline__ SeqSpan chunk_span(const BatchView& b, int seq) {
   if (b.kv_len) return seq_span(b, seq);
@@ -36,207 +73,977 @@ __device__ __forceinline__ SeqSpan chunk_span(const BatchView& b, int seq) {
   return s;
 }
 
-template <typename T, int DP, bool PAGED>
-__global__ void __launch_bounds__(128) chunk_attn_kernel(const PagedView c, const BatchView b, const ChunkArgs p, unsigned int* status) {
-  constexpr int ROW = DP + 8;   // 16 bytes more than a row: eight rows lie in different banks
-  constexpr unsigned kAll = 0xffffffffu;
-  __shared__ __align__(16) T ks[kChunkKeys * ROW], vs[kChunkKeys * ROW];
-  __shared__ unsigned long long gone_s;
-  __shared__ int unit_s[2];
-  const AttnArgs& a = p.a;
+// ------------------------------------------------------------------ pairs of CTAs
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The cluster address of what lies at this shared-memory address in CTA `rank`.
+__device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx_at(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// mbar_wait for arrivals of either CTA.
+__device__ __forceinline__ bool mbar_try_wait_pair(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait_pair(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait_pair(bar, parity)) {
+    if (globaltimer() - t0 > QCF_WAIT_NS) return false;
+  }
+  return true;
+}
+// Tiled loads to this CTA that count on a barrier of either (its cluster address).
+__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+      ::"r"(smem_u32(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+      ::"r"(smem_u32(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// The products of umma_f16 and umma_f16_ts over 256 rows, 128 in each CTA; the descriptors hold in both.
+__device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on this barrier in both CTAs once every product issued by this thread is complete.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+               "h"(static_cast<uint16_t>(3))
+               : "memory");
+}
+// sdesc_mnmajor_sw128 for rows of 32 entries: 64-byte swizzle, atoms of 8 rows in 512 bytes.
+__device__ __forceinline__ uint64_t sdesc_mnmajor_sw64(uint32_t smem_addr) {
+  return static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(1u) << 16 | static_cast<uint64_t>(512u >> 4) << 32 |
+         static_cast<uint64_t>(1u) << 46 | static_cast<uint64_t>(4u) << 61;
+}
+
+// ------------------------------------------------------------------ the deal
+//
+// The units of all sequences, row block by row block and KV head by KV head, lie one behind the other
+// on a line, each as long as its cost.  Pair i takes what lies between i and i + 1 shares of it; a border
+// that falls into a unit cuts it between two key tiles, or is moved to its nearer end where fewer than
+// kMinCut tiles would lie on one side.
+
+struct RowBlock {
+  int i0, ntok;            // tokens of the sequence
+  int t0, end, end_a;      // its key tiles; the end of row tile a's
+  __device__ int tiles() const { return end - t0; }
+};
+__device__ __forceinline__ int tile_of(int prefix, int pos) {
+  return pos < prefix ? pos / kTileKeys : (prefix + kTileKeys - 1) / kTileKeys + (pos - prefix) / kTileKeys;
+}
+__device__ __forceinline__ RowBlock row_block(const BatchView& b, const ChunkArgs& p, int nq, int len, int i) {
+  RowBlock k;
+  k.i0 = i * 4 * p.per;
+  k.ntok = min(4 * p.per, nq - k.i0);
+  const int pos = b.prefix_len + len - nq + k.i0;   // of its first token
+  k.t0 = p.window ? tile_of(b.prefix_len, max(0, pos - p.window + 1)) : 0;
+  k.end = tile_of(b.prefix_len, pos + k.ntok - 1) + 1;
+  k.end_a = tile_of(b.prefix_len, pos + min(k.ntok, 2 * p.per) - 1) + 1;
+  return k;
+}
+__device__ __forceinline__ int tile_cost(const RowBlock& k, int per) { return k.ntok > 2 * per ? kTileCost2 : kTileCost1; }
+__device__ __forceinline__ int64_t unit_cost(const RowBlock& k, int per) {
+  return kUnitCost + static_cast<int64_t>(tile_cost(k, per)) * k.tiles();
+}
+// The tile of a unit before which a border at cost x behind its beginning cuts it.
+__device__ __forceinline__ int cut_at(const RowBlock& k, int per, int64_t x) {
+  const int n = k.tiles();
+  const int t = static_cast<int>(min(max(x - kUnitCost, static_cast<int64_t>(0)) / tile_cost(k, per), static_cast<int64_t>(n)));
+  return t < kMinCut ? 0 : n - t < kMinCut ? n : t;
+}
+
+struct DealStart {
+  int64_t pos, share;   // cost before the row block
+  int seq, block;       // seq -1: nothing for this pair
+};
+
+// One unit, or the part of one, of this pair.
+struct Segment {
+  int seq, row0, ntok, g;      // its first row in the batch, its tokens
+  int pos, len;                // own position of its first token; own tokens of the sequence
+  int t0, nt, nt_a, nt_b;      // first key tile, tiles, those that row tiles a and b see
+  int slot;                    // -1: the whole unit, else where its sums go
+  int end;                     // 1: there are no more
+};
+
+// Sum over the threads before this one, and over all.
+__device__ __forceinline__ int64_t deal_scan(int64_t v, int64_t* met, int64_t* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int unit = blockIdx.x / c.Hkv, g = blockIdx.x - unit * c.Hkv;
-  if (warp == 0) {   // the sequence and row block of this unit
-    int before = 0, seq = -1, block = 0;
-    for (int s0 = 0; s0 < b.n_seq; s0 += 32) {
-      int n = 0;
-      if (s0 + lane < b.n_seq) {
-        const SeqSpan s = chunk_span(b, s0 + lane);
-        if (s.bad && blockIdx.x == 0) flag_status(status, QCF_DEV_BAD_INDEX);
-        n = (s.nq * a.G + kChunkRows - 1) / kChunkRows;
-      }
-      int run = n;
+  int64_t run = v;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kAll, run, o);
-        if (lane >= o) run += v;
-      }
-      const unsigned hit = __ballot_sync(kAll, n > 0 && unit >= before + run - n && unit < before + run);
-      if (hit && seq < 0) {
-        seq = s0 + __ffs(hit) - 1;
-        block = unit - before - __shfl_sync(kAll, run - n, seq - s0);
-      }
-      before += __shfl_sync(kAll, run, 31);
-      if (seq >= 0 && blockIdx.x > 0) break;
-    }
-    if (lane == 0) {
-      unit_s[0] = seq;
-      unit_s[1] = block;
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += u;
   }
   __syncthreads();
-  const int seq = unit_s[0];
-  if (seq < 0) return;
-  const SeqSpan s = chunk_span(b, seq);
-  const int rho0 = unit_s[1] * kChunkRows, end = min(rho0 + kChunkRows, s.nq * a.G);
-  const int r_lo = rho0 + warp * 16 + (lane >> 2), r_hi = r_lo + 8, qc = (lane & 3) * 2;
-  const int prefix = b.prefix_len, old = prefix + s.len - s.nq;   // position of the first new row
-  const int i_lo = min(r_lo, end - 1) / a.G, i_hi = min(r_hi, end - 1) / a.G;
-  const int p_lo = old + i_lo, p_hi = old + i_hi;
-  const int first = p.window ? max(0, old + rho0 / a.G - p.window + 1) : 0, last = old + (end - 1) / a.G;
-  const int low_lo = p.window ? p_lo - p.window : -1, low_hi = p.window ? p_hi - p.window : -1;
-
-  uint32_t qf[DP / 16][4];
-  {
-    const T* ql = static_cast<const T*>(a.q) + (s.row0 + i_lo) * a.q_stride + static_cast<int64_t>(g * a.G + min(r_lo, end - 1) - i_lo * a.G) * p.D;
-    const T* qh = static_cast<const T*>(a.q) + (s.row0 + i_hi) * a.q_stride + static_cast<int64_t>(g * a.G + min(r_hi, end - 1) - i_hi * a.G) * p.D;
+  if (lane == 31) met[warp] = run;
+  __syncthreads();
+  int64_t before = run - v;
+  *total = 0;
 #pragma unroll
-    for (int t = 0; t < DP / 16; ++t) {
-      const int col = t * 16 + qc;
-      qf[t][0] = col < p.D ? *reinterpret_cast<const uint32_t*>(ql + col) : 0u;
-      qf[t][1] = col < p.D ? *reinterpret_cast<const uint32_t*>(qh + col) : 0u;
-      qf[t][2] = col + 8 < p.D ? *reinterpret_cast<const uint32_t*>(ql + col + 8) : 0u;
-      qf[t][3] = col + 8 < p.D ? *reinterpret_cast<const uint32_t*>(qh + col + 8) : 0u;
+  for (int w = 0; w < kTileThreads / 32; ++w) {
+    *total += met[w];
+    if (w < warp) before += met[w];
+  }
+  return before;
+}
+
+// Finds where this pair's share begins; blk: scratch for n_seq + 1 ints.
+__device__ void find_share(const BatchView& b, const ChunkArgs& p, int Hkv, int pair, int pairs, int* blk, int64_t* met, DealStart* start,
+                           unsigned int* status) {
+  const int R = 4 * p.per;
+  const int per_s = (b.n_seq + kTileThreads - 1) / kTileThreads;
+  const int s0 = min(b.n_seq, static_cast<int>(threadIdx.x) * per_s), s1 = min(b.n_seq, s0 + per_s);
+  int64_t mine = 0, all;
+  for (int s = s0; s < s1; ++s) {
+    const SeqSpan q = chunk_span(b, s);
+    if (q.bad && blockIdx.x == 0) flag_status(status, QCF_DEV_BAD_INDEX);
+    blk[s] = (q.nq + R - 1) / R;
+    mine += blk[s];
+  }
+  int64_t at = deal_scan(mine, met, &all);
+  // more row blocks than the rows allow come only of sequences that overlap: nothing is done for them
+  const bool over = all > b.n_rows / R + b.n_seq;
+  if (over && blockIdx.x == 0 && threadIdx.x == 0) flag_status(status, QCF_DEV_BAD_INDEX);
+  const int blocks = over ? 0 : static_cast<int>(all);
+  for (int s = s0; s < s1; ++s) {
+    const int n = blk[s];
+    blk[s] = static_cast<int>(at);
+    at += n;
+  }
+  if (threadIdx.x == 0) {
+    blk[b.n_seq] = blocks;
+    start->seq = -1;
+  }
+  __syncthreads();
+  const int per_b = (blocks + kTileThreads - 1) / kTileThreads;
+  const int b0 = min(blocks, static_cast<int>(threadIdx.x) * per_b), b1 = min(blocks, b0 + per_b);
+  int first = 0;
+  if (b0 < b1) {   // the last sequence that begins at or before block b0
+    int hi = b.n_seq;
+    while (hi - first > 1) {
+      const int mid = (first + hi) >> 1;
+      if (blk[mid] <= b0) first = mid; else hi = mid;
     }
   }
+  // visit(seq, block of it, cost of the block's units)
+  auto walk = [&](auto visit) {
+    int seq = first;
+    SeqSpan q = {};
+    bool known = false;
+    for (int i = b0; i < b1; ++i) {
+      while (i >= blk[seq + 1]) {
+        ++seq;
+        known = false;
+      }
+      if (!known) q = chunk_span(b, seq);
+      known = true;
+      if (visit(seq, i - blk[seq], Hkv * unit_cost(row_block(b, p, q.nq, q.len, i - blk[seq]), p.per))) return;
+    }
+  };
+  int64_t cost = 0, total;
+  walk([&](int, int, int64_t c) {
+    cost += c;
+    return false;
+  });
+  int64_t pos = deal_scan(cost, met, &total);
+  const int64_t share = max((total + pairs - 1) / pairs, static_cast<int64_t>(kMinCost)), want = pair * share;
+  if (pos <= want && want < pos + cost)
+    walk([&](int seq, int i, int64_t c) {
+      if (want >= pos + c) {
+        pos += c;
+        return false;
+      }
+      *start = DealStart{pos, share, seq, i};
+      return true;
+    });
+  __syncthreads();
+}
 
-  constexpr float kLift = kWeightLift<T>;
-  float m_lo = -INFINITY, m_hi = -INFINITY, l_lo = 0.f, l_hi = 0.f;
-  float acc[DP / 8][4];
-#pragma unroll
-  for (int i = 0; i < DP / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-  const int mi = lane >> 3, mr = lane & 7;
-  const uint32_t ka = smem_u32(ks), va = smem_u32(vs);
-  for (int t0 = first / kChunkKeys * kChunkKeys; t0 <= last; t0 += kChunkKeys) {
-    __syncthreads();
-    if (threadIdx.x == 0) gone_s = 0;
-    __syncthreads();
-    for (int e = threadIdx.x; e < kChunkKeys * (DP / 8); e += 128) {
-      const int key = e / (DP / 8), col = e % (DP / 8) * 8, j = t0 + key;
-      uint4 kv = make_uint4(0u, 0u, 0u, 0u), vv = kv;
-      int64_t at = -1;
-      if (j < prefix + s.len) {
-        if constexpr (PAGED) {
-          at = j < prefix ? slot_of(c, b.prefix_pages, j) : slot_of(c, b.page_table + static_cast<int64_t>(seq) * b.table_stride, j - prefix);
-          if (at < 0 && col == 0) {
-            atomicOr(&gone_s, 1ull << key);
-            flag_status(status, QCF_DEV_BAD_INDEX);
+// Walks a pair's share, all lanes of a warp alike; they keep the spans of 32 sequences.
+struct TileWalk {
+  const BatchView& b;
+  const ChunkArgs& p;
+  const int Hkv, pair;
+  int64_t pos, begin, stop, share;
+  int seq, block, g, base;      // base: of the 32 sequences kept
+  int my_row0, my_nq, my_len;   // this lane's
+  int row0, nq, len;            // of seq
+  RowBlock k;
+  bool live;
+  int4 rec;
+
+  __device__ void keep(int from) {
+    base = from;
+    my_nq = 0;
+    if (from + static_cast<int>(threadIdx.x & 31) < b.n_seq) {
+      const SeqSpan s = chunk_span(b, from + (threadIdx.x & 31));
+      my_row0 = s.row0;
+      my_nq = s.nq;
+      my_len = s.len;
+    }
+  }
+  __device__ void enter() {
+    row0 = __shfl_sync(0xffffffffu, my_row0, seq - base);
+    nq = __shfl_sync(0xffffffffu, my_nq, seq - base);
+    len = __shfl_sync(0xffffffffu, my_len, seq - base);
+  }
+  __device__ TileWalk(const BatchView& b_, const ChunkArgs& p_, const DealStart& at, int Hkv_, int pair_) : b(b_), p(p_), Hkv(Hkv_), pair(pair_) {
+    rec = make_int4(0, 0, 0, 0);
+    live = at.seq >= 0;
+    if (!live) return;
+    pos = at.pos;
+    share = at.share;
+    begin = pair * share;
+    stop = begin + share;
+    seq = at.seq;
+    block = at.block;
+    my_row0 = my_len = 0;
+    keep(seq);
+    enter();
+    k = row_block(b, p, nq, len, block);
+    g = static_cast<int>((begin - pos) / unit_cost(k, p.per));
+    pos += g * unit_cost(k, p.per);
+  }
+  // The next sequence with rows.
+  __device__ void next_seq() {
+    while (true) {
+      const unsigned rows = __ballot_sync(0xffffffffu, my_nq > 0), later = seq + 1 - base < 32 ? rows & (0xffffffffu << (seq + 1 - base)) : 0u;
+      if (later) {
+        seq = base + __ffs(later) - 1;
+        enter();
+        return;
+      }
+      if (base + 32 >= b.n_seq) {
+        live = false;
+        return;
+      }
+      keep(base + 32);
+      seq = base - 1;
+    }
+  }
+  __device__ bool next(Segment& s) {
+    while (live) {
+      const int n = k.tiles();
+      const int64_t cost = unit_cost(k, p.per);
+      const int from = pos < begin ? cut_at(k, p.per, begin - pos) : 0, to = pos + cost > stop ? cut_at(k, p.per, stop - pos) : n;
+      const bool some = from < to;
+      if (some) {
+        const bool two = k.ntok > 2 * p.per;
+        s.seq = seq;
+        s.row0 = row0 + k.i0;
+        s.ntok = k.ntok;
+        s.g = g;
+        s.pos = len - nq + k.i0;
+        s.len = len;
+        s.t0 = k.t0 + from;
+        s.nt = to - from;
+        s.nt_a = max(0, min(k.end_a - k.t0, to) - from);
+        s.nt_b = two ? s.nt : 0;
+        s.slot = from == 0 && to == n ? -1 : from > 0 ? 0 : 1;
+        s.end = 0;
+        if (s.slot == 1) {   // how many borders cut this unit: those of the pairs behind this one
+          int parts = 1;
+          for (int64_t at = stop; at < pos + cost; at += share) {
+            const int t = cut_at(k, p.per, at - pos);
+            parts += t > 0 && t < n;
           }
-          if (at >= 0) at += g * c.head_stride;
-        } else {
-          at = (s.row0 + j) * p.kv_stride + static_cast<int64_t>(g) * p.D;
+          rec = make_int4(parts, s.row0, s.ntok, g);
         }
       }
-      if (at >= 0 && col < p.D) {
-        kv = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + at + col);
-        vv = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + at + col);
+      pos += cost;
+      if (pos >= stop) {
+        live = false;
+      } else if (++g == Hkv) {
+        g = 0;
+        if (++block * 4 * p.per >= nq) {
+          block = 0;
+          next_seq();
+        }
+        if (live) k = row_block(b, p, nq, len, block);
       }
-      *reinterpret_cast<uint4*>(ks + key * ROW + col) = kv;
-      *reinterpret_cast<uint4*>(vs + key * ROW + col) = vv;
+      if (some) return true;
     }
-    __syncthreads();
-    const unsigned long long gone = gone_s;
-    float sc[kChunkKeys / 8][4];
-#pragma unroll
-    for (int j = 0; j < kChunkKeys / 8; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
-#pragma unroll
-    for (int t = 0; t < DP / 16; ++t)
-#pragma unroll
-      for (int h = 0; h < kChunkKeys / 16; ++h) {
-        uint32_t b0, b1, b2, b3;
-        ldsm_x4(ka + ((h * 16 + (mi >> 1) * 8 + mr) * ROW + t * 16 + (mi & 1) * 8) * 2, b0, b1, b2, b3);
-        mma_16816<T>(sc[2 * h], qf[t], b0, b1);
-        mma_16816<T>(sc[2 * h + 1], qf[t], b2, b3);
-      }
-    float top_lo = -INFINITY, top_hi = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < kChunkKeys / 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int key = t0 + j * 8 + qc + (e & 1);
-        if (key > (e < 2 ? p_lo : p_hi) || key <= (e < 2 ? low_lo : low_hi) || (gone >> (key - t0) & 1)) sc[j][e] = -INFINITY;
-        if (e < 2) top_lo = fmaxf(top_lo, sc[j][e]); else top_hi = fmaxf(top_hi, sc[j][e]);
-      }
-#pragma unroll
-    for (int o = 1; o <= 2; o <<= 1) {
-      top_lo = fmaxf(top_lo, __shfl_xor_sync(kAll, top_lo, o));
-      top_hi = fmaxf(top_hi, __shfl_xor_sync(kAll, top_hi, o));
-    }
-    const float n_lo = fmaxf(m_lo, top_lo * a.scale_log2 - kLift), n_hi = fmaxf(m_hi, top_hi * a.scale_log2 - kLift);
-    const float f_lo = m_lo == -INFINITY ? 0.f : fast_exp2(m_lo - n_lo), f_hi = m_hi == -INFINITY ? 0.f : fast_exp2(m_hi - n_hi);
-    m_lo = n_lo;
-    m_hi = n_hi;
-    l_lo *= f_lo;
-    l_hi *= f_hi;
-#pragma unroll
-    for (int j = 0; j < DP / 8; ++j) {
-      acc[j][0] *= f_lo;
-      acc[j][1] *= f_lo;
-      acc[j][2] *= f_hi;
-      acc[j][3] *= f_hi;
-    }
-    const float b_lo = m_lo == -INFINITY ? 0.f : -m_lo, b_hi = m_hi == -INFINITY ? 0.f : -m_hi;
-#pragma unroll
-    for (int j = 0; j < kChunkKeys / 8; ++j) {
-      sc[j][0] = fast_exp2(fmaf(sc[j][0], a.scale_log2, b_lo));
-      sc[j][1] = fast_exp2(fmaf(sc[j][1], a.scale_log2, b_lo));
-      sc[j][2] = fast_exp2(fmaf(sc[j][2], a.scale_log2, b_hi));
-      sc[j][3] = fast_exp2(fmaf(sc[j][3], a.scale_log2, b_hi));
-      l_lo += sc[j][0] + sc[j][1];
-      l_hi += sc[j][2] + sc[j][3];
-    }
-    // the weights meet the values in the 16-bit type of both (the MMA's); their sum stays fp32
-#pragma unroll
-    for (int h = 0; h < kChunkKeys / 16; ++h) {
-      const uint32_t pa[4] = {pack2<T>(sc[2 * h][0], sc[2 * h][1]), pack2<T>(sc[2 * h][2], sc[2 * h][3]),
-                              pack2<T>(sc[2 * h + 1][0], sc[2 * h + 1][1]), pack2<T>(sc[2 * h + 1][2], sc[2 * h + 1][3])};
-#pragma unroll
-      for (int dp = 0; dp < DP / 16; ++dp) {
-        uint32_t b0, b1, b2, b3;
-        ldsm_x4_t(va + ((h * 16 + (mi & 1) * 8 + mr) * ROW + dp * 16 + (mi >> 1) * 8) * 2, b0, b1, b2, b3);
-        mma_16816<T>(acc[2 * dp], pa, b0, b1);
-        mma_16816<T>(acc[2 * dp + 1], pa, b2, b3);
-      }
-    }
+    return false;
   }
-#pragma unroll
-  for (int o = 1; o <= 2; o <<= 1) {
-    l_lo += __shfl_xor_sync(kAll, l_lo, o);
-    l_hi += __shfl_xor_sync(kAll, l_hi, o);
+};
+
+// ------------------------------------------------------------------ the kernel
+
+template <typename T>
+constexpr uint32_t idesc_pair(int N, bool b_mn_major) {
+  return std::is_same<T, __half>::value ? idesc_bf16_f32(256, N, b_mn_major) & ~((1u << 7) | (1u << 10)) : idesc_bf16_f32(256, N, b_mn_major);
+}
+
+template <typename T, int DP, bool PAGED>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
+    tile_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ,
+                     const PagedView c, const BatchView b, const ChunkArgs p, const ChunkParts parts, unsigned int* status) {
+  using Cfg = TileCfg<DP>;
+  constexpr int ST = Cfg::STAGES;
+  constexpr unsigned kAll = 0xffffffffu;
+  const AttnArgs& a = p.a;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* qbuf = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  uint8_t* kbuf = qbuf + 2 * Cfg::QTILE;
+  uint8_t* vbuf = kbuf + ST * Cfg::KTILE;
+  uint8_t* obuf = vbuf + ST * Cfg::VTILE;
+  Segment* segs = reinterpret_cast<Segment*>(obuf + Cfg::OUT);
+  DealStart* start = reinterpret_cast<DealStart*>(segs + kSegRing);
+  int64_t* met = reinterpret_cast<int64_t*>(start + 1);
+  // in the first CTA, for both: what its issuers wait for
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(met + kTileThreads / 32);
+  uint64_t* v_full = k_full + ST;
+  uint64_t* q_full = v_full + ST;
+  uint64_t* p_ready = q_full + 1;    // [a, b][first, last 64 keys]
+  // in each CTA
+  uint64_t* k_empty = p_ready + 4;
+  uint64_t* v_empty = k_empty + ST;
+  uint64_t* q_empty = v_empty + ST;
+  uint64_t* s_full = q_empty + 1;    // [a, b]
+  uint64_t* o_done = s_full + 2;     // [a, b]
+  uint64_t* mma_end = o_done + 2;    // [a, b]
+  uint64_t* v_tail = mma_end + 2;
+  uint64_t* seg_full = v_tail + 1;
+  uint64_t* seg_empty = seg_full + kSegRing;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(seg_empty + kSegRing);
+  static_assert(sizeof(Segment) * kSegRing + sizeof(DealStart) + (kTileThreads / 32 + 4 * ST + 24 + 2 * kSegRing) * 8 <= Cfg::FIXED, "fixed part");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank()), pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmQ);
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&k_full[s], 2);
+      mbar_init(&v_full[s], 2);
+      mbar_init(&k_empty[s], 2);
+      mbar_init(&v_empty[s], 2);
+    }
+    mbar_init(q_full, 2);
+    mbar_init(q_empty, 2);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&p_ready[2 * x], 9);       // the softmax warps of both CTAs and the turn
+      mbar_init(&p_ready[2 * x + 1], 8);
+      mbar_init(&s_full[x], 1);
+      mbar_init(&o_done[x], 1);
+      mbar_init(&mma_end[x], 1);
+    }
+    mbar_init(v_tail, 1);
+    for (int s = 0; s < kSegRing; ++s) {
+      mbar_init(&seg_full[s], 1);
+      mbar_init(&seg_empty[s], rank == 0 ? 11 : 9);   // V producer, softmax warps, issuers
+    }
+    fence_mbar_init();
   }
+  if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+  find_share(b, p, c.Hkv, pair, pairs, reinterpret_cast<int*>(kbuf), met, start, status);
+  fence_proxy_async_smem();   // the deal used the rings
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int np = (b.prefix_len + kTileKeys - 1) / kTileKeys;   // tiles of the prefix
+  // A role's next segment; false when a wait ran out.
+  int seg_n = 0;
+  auto next_segment = [&](Segment& s) {
+    const int at = seg_n % kSegRing;
+    if (!mbar_wait(&seg_full[at], (seg_n / kSegRing) & 1)) return false;
+    s = segs[at];
+    ++seg_n;
+    return true;
+  };
+  auto release_segment = [&] { mbar_arrive(&seg_empty[(seg_n - 1) % kSegRing]); };
+
+  if (warp < 4) {
+    // 104 x 128 + 200 x 256 threads: the 168 x 384 registers of the launch
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == 0 || warp == 2) {
+      // ---- the walk, K and Q; V
+      const bool is_k = warp == 0;
+      uint8_t* ring = is_k ? kbuf : vbuf;
+      uint64_t* empty = is_k ? k_empty : v_empty;
+      const uint32_t full = at_rank(is_k ? k_full : v_full, 0), q_full0 = at_rank(q_full, 0);
+      constexpr int TILE_K = Cfg::KTILE, TILE_V = Cfg::VTILE;
+      const int keys = is_k ? 64 : kTileKeys, key0 = is_k ? rank * 64 : 0;   // of a tile, in this CTA
+      const int rows = PAGED ? min(1 << c.page_shift, keys) : keys, boxes = PAGED ? keys / rows : 1;
+      DealStart at0 = *start;
+      if (!is_k) at0.seq = -1;
+      TileWalk walk(b, p, at0, c.Hkv, pair);
+      Segment s;
+      int n = 0, tails = 0, units = 0;
+      bool ok = true;
+      while (ok) {
+        if (is_k) {
+          const bool more = walk.next(s);
+          s.end = !more;
+          const int at = seg_n % kSegRing;
+          if (!__all_sync(kAll, mbar_wait(&seg_empty[at], ((seg_n / kSegRing) & 1) ^ 1u))) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            segs[at] = s;
+            mbar_arrive(&seg_full[at]);
+          }
+          ++seg_n;
+        } else {
+          if (!__all_sync(kAll, next_segment(s))) {
+            ok = false;
+            break;
+          }
+          __syncwarp();
+          if (lane == 0) release_segment();
+        }
+        if (s.end) break;
+        const int32_t* table = PAGED ? b.page_table + static_cast<int64_t>(s.seq) * b.table_stride : nullptr;
+        // this lane's page of tile t: its id, n_pages (which reads as zeros) where there is none
+        auto page_of = [&](int t) {
+          const bool pre = t < np;
+          const int key = (pre ? t : t - np) * kTileKeys + key0 + lane * rows;
+          if (lane >= boxes || key >= (pre ? b.prefix_len : s.len)) return c.n_pages;
+          const int id = (pre ? b.prefix_pages : table)[key >> c.page_shift];
+          if (id >= 0 && id < c.n_pages) return id;
+          flag_status(status, QCF_DEV_BAD_INDEX);
+          return c.n_pages;
+        };
+        int id = PAGED ? page_of(s.t0) : 0;
+        for (int i = 0; i < s.nt; ++i, ++n) {
+          const int st = n % ST, t = s.t0 + i;
+          const int next_id = PAGED && i + 1 < s.nt ? page_of(t + 1) : 0;
+          if (!__all_sync(kAll, mbar_wait_pair(&empty[st], ((n / ST) & 1) ^ 1u))) {
+            ok = false;
+            break;
+          }
+          const bool pre = t < np;
+          const int tk = (pre ? t : t - np) * kTileKeys;   // first key of the tile
+          const int valid = (pre ? b.prefix_len : s.len) - tk;
+          const int stale = valid < kTileKeys ? (PAGED ? min(kTileKeys, (valid + rows - 1) / rows * rows) : kTileKeys) : valid;
+          const bool tail = !is_k && stale > valid;        // rows of the tile that lie behind the end
+          const uint32_t bar = tail ? at_rank(v_tail, rank) : full + st * 8;
+          uint8_t* dst = ring + st * (is_k ? TILE_K : TILE_V);
+          if (lane == 0) mbar_arrive_expect_tx_at(bar, is_k ? TILE_K : TILE_V);
+          __syncwarp();
+          if (lane < boxes) {
+            if (is_k) {
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int rho = half ? r_hi : r_lo;
-    if (rho >= end) continue;
-    const float m = half ? m_hi : m_lo, l = half ? l_hi : l_lo, inv = l == 0.f ? 0.f : 1.f / l;
-    const int i = half ? i_hi : i_lo;
-    const int64_t place = static_cast<int64_t>(s.row0 + i) * a.Hq + g * a.G + rho - i * a.G;
-    T* o = static_cast<T*>(a.o) + place * p.D;
+              for (int h = 0; h < Cfg::BOXES; ++h) {
+                if constexpr (PAGED)
+                  tma_load_4d_pair(dst + h * Cfg::KBOX + lane * rows * 128, &tmK, bar, h * 64, (tk + key0) & ((1 << c.page_shift) - 1), s.g, id);
+                else
+                  tma_load_3d_pair(dst + h * Cfg::KBOX, &tmK, bar, h * 64, s.g, s.row0 - s.pos + tk + key0);
+              }
+            } else {
+              if constexpr (PAGED)
+                tma_load_4d_pair(dst + lane * rows * Cfg::VCOLS * 2, &tmV, bar, rank * Cfg::VCOLS, tk & ((1 << c.page_shift) - 1), s.g, id);
+              else
+                tma_load_3d_pair(dst, &tmV, bar, rank * Cfg::VCOLS, s.g, s.row0 - s.pos + tk);
+            }
+          }
+          id = next_id;
+          if (is_k && i == 0) {   // the unit's Q: rows behind the sequence belong to others or are zeros, and go nowhere
+            if (!__all_sync(kAll, mbar_wait_pair(q_empty, (units & 1) ^ 1u))) {
+              ok = false;
+              break;
+            }
+            const int nb = s.ntok > 2 * p.per ? 2 : 1;
+            if (lane == 0) mbar_arrive_expect_tx_at(q_full0, nb * Cfg::BOXES * p.per * a.G * 128);
+            __syncwarp();
+            if (lane < nb * Cfg::BOXES)
+              tma_load_3d_pair(qbuf + lane * Cfg::QBOX, &tmQ, q_full0, lane % Cfg::BOXES * 64, s.g * a.G,
+                               s.row0 + (2 * (lane / Cfg::BOXES) + rank) * p.per);
+            ++units;
+          }
+          if (tail) {
+            if (!__all_sync(kAll, mbar_wait(v_tail, tails++ & 1))) {
+              ok = false;
+              break;
+            }
+            constexpr int CH = Cfg::VCOLS / 8;   // 16-byte pieces of a row
+            for (int e = lane; e < (stale - valid) * CH; e += 32)
+              *reinterpret_cast<uint4*>(dst + valid * Cfg::VCOLS * 2 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(full + st * 8);
+          }
+        }
+      }
+      if (!ok && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
+      if (rank == 0) {   // no copy of this warp, or its like in the other CTA, is in flight when the CTAs end
+        for (int e = max(0, n - ST); e < n; ++e)
+          if (!mbar_wait_pair(&(is_k ? k_full : v_full)[e % ST], (e / ST) & 1) && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
+        if (is_k && units > 0 && !mbar_wait_pair(q_full, (units - 1) & 1) && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
+        if (is_k && lane == 0 && parts.rec) parts.rec[pair] = walk.rec;
+      }
+    } else if (lane == 0) {
+      const int x = warp >> 1;
+      if (rank == 0) {
+        // ---- MMA issuer of row tile x of both CTAs
+        constexpr uint32_t idesc_s = idesc_pair<T>(kTileKeys, false);
+        constexpr uint32_t idesc_o = idesc_pair<T>(DP, true);
+        constexpr int V_STEP = 16 * Cfg::VCOLS * 2;   // 16 keys of V
+        int n = 0, k = 0;    // key tiles, segments so far
+        uint32_t used = 0;   // weight tiles taken so far
+        bool ok = true;
+        Segment s;
+        const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(qbuf + x * Cfg::QTILE));
+        const uint64_t k_desc = sdesc_kmajor_sw128(smem_u32(kbuf));
+        const uint64_t v_desc = DP == 128 ? sdesc_mnmajor_sw128(smem_u32(vbuf), 16) : sdesc_mnmajor_sw64(smem_u32(vbuf));
+        const uint32_t k_empty1 = at_rank(k_empty, 1), v_empty1 = at_rank(v_empty, 1), q_empty1 = at_rank(q_empty, 1);
+        // The turn: the barrier of a tile's first weights also counts one arrival of the other issuer,
+        // made four products (256 cycles) before the end of its block, which covers what this thread
+        // then takes to see it.
+        auto pass = [&](bool due) {
+          if (due) mbar_arrive(&p_ready[2 * (1 - x)]);
+        };
+        auto wait_k = [&](int tile) { return mbar_wait_pair(&k_full[tile % ST], (tile / ST) & 1); };
+        auto wait_v = [&](int tile) { return mbar_wait_pair(&v_full[tile % ST], (tile / ST) & 1); };
+        auto scores = [&](int tile, bool due, bool last) {   // S_x = Q_x K^T
+          const uint64_t kd = k_desc + tile % ST * (Cfg::KTILE >> 4);
 #pragma unroll
-    for (int j = 0; j < DP / 8; ++j)
-      if (j * 8 + qc < p.D) *reinterpret_cast<uint32_t*>(o + j * 8 + qc) = pack2<T>(acc[j][2 * half] * inv, acc[j][2 * half + 1] * inv);
-    if (a.lse && qc == 0) a.lse[place] = (m + log2f(l)) * 0.69314718055994531f;
+          for (int kk = 0; kk < DP / 16; ++kk) {
+            if (kk == DP / 16 - 4) pass(due);
+            const uint64_t q_at = ((kk >> 2) * Cfg::QBOX + (kk & 3) * 32) >> 4, k_at = ((kk >> 2) * Cfg::KBOX + (kk & 3) * 32) >> 4;
+            umma_f16_pair(tmem + x * 128, q_desc + q_at, kd + k_at, idesc_s, kk > 0 ? 1u : 0u);
+          }
+          umma_commit_pair(&s_full[x]);
+          umma_commit_pair(&k_empty[tile % ST]);
+          if (last) umma_commit_pair(q_empty);
+        };
+        while (true) {
+          if (!(ok = next_segment(s))) break;
+          release_segment();
+          if (s.end) break;
+          const int mine = x ? s.nt_b : s.nt_a;
+          if (!(ok = mbar_wait_pair(q_full, k++ & 1))) break;
+          if (mine > 0) {
+            if (!(ok = wait_k(n))) break;
+            tc_fence_after();
+            scores(n, false, mine == 1);
+          } else {
+            mbar_arrive(q_empty);
+            mbar_arrive_at(q_empty1);
+          }
+          for (int i = 0; i < mine; ++i) {
+            const bool more = i + 1 < mine;
+            if (!(ok = wait_v(n + i) && (!more || wait_k(n + i + 1)))) break;
+            const uint64_t vd = v_desc + (n + i) % ST * (Cfg::VTILE >> 4);
+            auto weigh = [&](int half) {   // O_x += P_x V over 64 keys
+              tc_fence_after();
+#pragma unroll
+              for (int kk = half * (kTileKeys / 32); kk < (half + 1) * (kTileKeys / 32); ++kk)
+                umma_f16_ts_pair(tmem + 256 + x * DP, tmem + x * 128 + kk * 8, vd + kk * (V_STEP >> 4), idesc_o, (i > 0 || kk > 0) ? 1u : 0u);
+            };
+            // a begins, b follows while a has tiles left; who is alone gives itself the turn
+            if (x == 0 ? i == 0 || s.nt_b == 0 : i >= s.nt_a) mbar_arrive(&p_ready[2 * x]);
+            const bool due = x == 0 ? s.nt_b > 0 : i + 1 < s.nt_a;
+            if (!(ok = mbar_wait_pair(&p_ready[2 * x], used & 1))) break;
+            weigh(0);
+            if (!(ok = mbar_wait_pair(&p_ready[2 * x + 1], used & 1))) break;
+            weigh(1);
+            ++used;
+            if (more) {
+              scores(n + i + 1, due, i + 2 == mine);
+            } else {
+              pass(due);
+              umma_commit_pair(&o_done[x]);
+            }
+            umma_commit_pair(&v_empty[(n + i) % ST]);   // after the scores: a commit costs this thread more than a product
+          }
+          if (!ok) break;
+          for (int i = mine; i < s.nt; ++i) {   // tiles that only the other row tile sees: hand them on
+            const int st = (n + i) % ST;
+            if (!(ok = wait_k(n + i))) break;
+            mbar_arrive(&k_empty[st]);
+            mbar_arrive_at(k_empty1 + st * 8);
+            if (!(ok = wait_v(n + i))) break;
+            mbar_arrive(&v_empty[st]);
+            mbar_arrive_at(v_empty1 + st * 8);
+          }
+          if (!ok) break;
+          n += s.nt;
+        }
+        if (!ok) flag_status(status, QCF_DEV_TIMEOUT);
+        umma_commit_pair(&mma_end[x]);   // nothing runs on tensor memory once it is freed
+      }
+    }
+  } else {
+    // ---- softmax: thread = score row of tile x
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    const int x = (warp - 4) >> 2, quarter = warp & 3;
+    const int rho = quarter * 32 + lane, pl = div_g(a, rho), place = 2 * x + rank;   // place: of the row tile in the unit
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_tm = tmem + lane_base + x * 128, o_tm = tmem + lane_base + 256 + x * DP;
+    const uint32_t ready = at_rank(p_ready, 0) + 16 * x;
+    uint8_t* out = obuf + (warp - 4) * 4096;
+    uint32_t seen = 0, ends = 0;
+    bool ok = true;
+    Segment s;
+    while (true) {
+      if (!__all_sync(kAll, next_segment(s))) {
+        ok = false;
+        break;
+      }
+      __syncwarp();
+      if (lane == 0) release_segment();
+      if (s.end) break;
+      const int mine = x ? s.nt_b : s.nt_a;
+      if (x && mine == 0) continue;
+      const int tok = place * p.per + pl, own = s.pos + min(tok, s.ntok - 1);   // this row's token; its position (a row of none: the last's)
+      const bool real = pl < p.per && tok < s.ntok;
+      const int32_t* table = PAGED ? b.page_table + static_cast<int64_t>(s.seq) * b.table_stride : nullptr;
+      auto page_bad = [&](int t) {   // the page of this lane's 8 keys of tile t lies outside the cache
+        const bool pre = t < np;
+        const int key = (pre ? t : t - np) * kTileKeys + lane * 8;
+        if (lane >= kTileKeys / 8 || key >= (pre ? b.prefix_len : s.len)) return false;
+        const int id = (pre ? b.prefix_pages : table)[key >> c.page_shift];
+        return id < 0 || id >= c.n_pages;
+      };
+      float m = -INFINITY, l = 0.f;
+      bool bad = PAGED && mine > 0 && page_bad(s.t0);
+      for (int i = 0; i < mine; ++i) {
+        const int t = s.t0 + i;
+        const unsigned bad8 = PAGED ? __ballot_sync(kAll, bad) : 0u;
+        if constexpr (PAGED) bad = i + 1 < mine && page_bad(t + 1);
+        if (!__all_sync(kAll, mbar_wait(&s_full[x], seen++ & 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float sv[kTileKeys];
+        tmem_ld128(s_tm, sv);
+        // keys of the tile that this row sees: [low, high)
+        const bool pre = t < np;
+        const int last = pre ? b.prefix_len : own + 1, high = last - (pre ? t : t - np) * kTileKeys;
+        const int low = p.window ? (pre ? b.prefix_len : 0) + own + 1 - p.window - (pre ? t : t - np) * kTileKeys : 0;
+        if (__any_sync(kAll, high < kTileKeys || low > 0)) {
+#pragma unroll
+          for (int j = 0; j < kTileKeys; ++j)
+            if (j >= high || j < low) sv[j] = -INFINITY;
+        }
+        if (bad8) {
+#pragma unroll
+          for (int j = 0; j < kTileKeys; ++j)
+            if (bad8 >> (j / 8) & 1) sv[j] = -INFINITY;
+        }
+        // 64 weights from the logits; they leave in two halves, so that P V of the first 64 keys runs
+        // under the powers of the others
+        const Pair scale2 = make_pair2(a.scale_log2, a.scale_log2);
+        Pair sum[2];
+        uint32_t pk[32];
+        auto weights = [&](int half, float base) {
+          const Pair nm2 = make_pair2(-base, -base);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int j = half * 64 + 2 * e;
+            float p0, p1;
+            split(fma2(make_pair2(sv[j], sv[j + 1]), scale2, nm2), p0, p1);
+            p0 = fast_exp2(p0);
+            p1 = fast_exp2(p1);
+            sum[e & 1] = add2(sum[e & 1], make_pair2(p0, p1));
+            pk[e] = pack2<T>(p0, p1);
+          }
+        };
+        // The first half is weighed with the maximum so far, the tile's own found meanwhile (the
+        // special-function unit paces the powers, the comparisons fill its gaps): the maximum
+        // moves only by more than 2^8, so after a unit's first tiles it nearly always stands.
+        sum[0] = sum[1] = make_pair2(0.f, 0.f);
+        weights(0, m == -INFINITY ? 0.f : m);
+        float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+        for (int j = 4; j < kTileKeys - 4; j += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], sv[j + e], sv[j + 4 + e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], sv[kTileKeys - 4 + e]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+        const bool grow = top > m + (8.0f + kWeightLift<T>);
+        if (__any_sync(kAll, grow)) {
+          const float m_new = grow ? top - kWeightLift<T> : m;
+          if (i > 0) {   // the full S of this tile says that every earlier product has been added to O
+            const float f = m == -INFINITY ? 0.f : fast_exp2(m - m_new);
+#pragma unroll 1
+            for (int cc = 0; cc < DP / 32; ++cc) {
+              float ov[32];
+              tmem_ld32(o_tm + cc * 32, ov);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] *= f;
+              tmem_st32(o_tm + cc * 32, ov);
+            }
+            l *= f;
+          }
+          m = m_new;
+          sum[0] = sum[1] = make_pair2(0.f, 0.f);
+          weights(0, m == -INFINITY ? 0.f : m);
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (half == 1) weights(1, m == -INFINITY ? 0.f : m);
+          tmem_st32u(s_tm + half * 32, pk);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(ready + 8 * half);
+        }
+        float l0, l1;
+        split(add2(sum[0], sum[1]), l0, l1);
+        l += l0 + l1;
+      }
+      if (!ok) break;
+
+      // ---- the unit's output, through 4 KB of shared memory so that whole lines leave
+      if (mine > 0) {
+        if (!__all_sync(kAll, mbar_wait(&o_done[x], ends++ & 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+      }
+      const int rows = min(max(s.ntok - place * p.per, 0), p.per) * a.G;   // score rows of this CTA's tile
+      if (s.slot >= 0) {
+        const int64_t at = (static_cast<int64_t>(pair) * 2 + s.slot) * kTileRows + place * p.per * a.G;   // rows of the unit in order
+        if (real) parts.ml[at + rho] = make_float2(m, l);
+        if (mine > 0) {
+#pragma unroll 1
+          for (int cc = 0; cc < DP / 32; ++cc) {
+            float ov[32];
+            tmem_ld32(o_tm + cc * 32, ov);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(out + sw128_off(lane, e)) = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int r = e * 4 + (lane >> 3), row = quarter * 32 + r, col = cc * 32 + (lane & 7) * 4;
+              if (row < rows && col < p.D)
+                *reinterpret_cast<float4*>(parts.o + (at + row) * p.D + col) = *reinterpret_cast<const float4*>(out + sw128_off(r, lane & 7));
+            }
+            __syncwarp();
+          }
+        }
+      } else {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t first = static_cast<int64_t>(s.row0 + place * p.per) * a.Hq + s.g * a.G;   // head of score row 0
+        if (a.lse && real) a.lse[first + static_cast<int64_t>(pl) * a.Hq + rho - pl * a.G] = (m + log2f(l)) * 0.69314718055994531f;
+#pragma unroll 1
+        for (int cc = 0; cc < DP / 64; ++cc) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float ov[32];
+            tmem_ld32(o_tm + cc * 64 + h * 32, ov);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint4 w;
+              w.x = pack2<T>(ov[8 * e] * inv, ov[8 * e + 1] * inv);
+              w.y = pack2<T>(ov[8 * e + 2] * inv, ov[8 * e + 3] * inv);
+              w.z = pack2<T>(ov[8 * e + 4] * inv, ov[8 * e + 5] * inv);
+              w.w = pack2<T>(ov[8 * e + 6] * inv, ov[8 * e + 7] * inv);
+              *reinterpret_cast<uint4*>(out + sw128_off(lane, h * 4 + e)) = w;
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int r = e * 4 + (lane >> 3), row = quarter * 32 + r, col = cc * 64 + (lane & 7) * 8, tl = div_g(a, row);
+            if (row < rows && col < p.D)
+              *reinterpret_cast<uint4*>(static_cast<T*>(a.o) + (first + static_cast<int64_t>(tl) * a.Hq + row - tl * a.G) * p.D + col) =
+                  *reinterpret_cast<const uint4*>(out + sw128_off(r, lane & 7));
+          }
+          __syncwarp();
+        }
+      }
+      tc_fence_before();
+    }
+    if (!ok && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  // in both CTAs: the commits that arrive here have all done so when the last has
+  if (threadIdx.x < 2 && !mbar_wait_pair(&mma_end[threadIdx.x], 0)) flag_status(status, QCF_DEV_TIMEOUT);
+  __syncwarp();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ joining the parts
+//
+// A warp joins the parts of one score row of a unit that was cut: the one that its first pair left, and
+// those of the pairs behind it.
+constexpr int kJoinWarps = 8, kJoinRows = 16;
+template <typename T>
+__global__ void __launch_bounds__(kJoinWarps * 32) tile_join_kernel(const ChunkArgs p, const ChunkParts parts) {
+  pdl_wait();
+  const int4 rec = parts.rec[blockIdx.x];
+  if (rec.x <= 1) return;
+  const AttnArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool has = lane * 4 < p.D;
+  for (int r = blockIdx.y * kJoinRows + warp; r < min(static_cast<int>(blockIdx.y + 1) * kJoinRows, rec.z * a.G); r += kJoinWarps) {
+    float M = -INFINITY, L = 0.f, sum[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int BATCH = 4;
+    for (int i0 = 0; i0 < rec.x; i0 += BATCH) {
+      float2 ml[BATCH];
+      float4 v[BATCH];
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) {   // behind the end the last part again: loads without branches stay together
+        const int i = min(i0 + j, rec.x - 1);
+        const int64_t at = (static_cast<int64_t>(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * kTileRows + r;
+        ml[j] = parts.ml[at];
+        v[j] = *reinterpret_cast<const float4*>(parts.o + at * p.D + (has ? lane * 4 : 0));
+      }
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j)
+        if (i0 + j < rec.x && ml[j].y != 0.f) {   // a part without keys for this row has no sums
+          const float top = fmaxf(M, ml[j].x);
+          const float f = ml[j].x == -INFINITY ? 1.f : fast_exp2(ml[j].x - top), e = M == -INFINITY ? 0.f : fast_exp2(M - top);
+          M = top;
+          L = fmaf(ml[j].y, f, L * e);
+          sum[0] = fmaf(v[j].x, f, sum[0] * e);
+          sum[1] = fmaf(v[j].y, f, sum[1] * e);
+          sum[2] = fmaf(v[j].z, f, sum[2] * e);
+          sum[3] = fmaf(v[j].w, f, sum[3] * e);
+        }
+    }
+    const int tok = div_g(a, r);
+    const int64_t at = static_cast<int64_t>(rec.y + tok) * a.Hq + rec.w * a.G + r - tok * a.G;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    if (has)
+      *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + at * p.D + lane * 4) = make_uint2(pack2<T>(sum[0] * inv, sum[1] * inv), pack2<T>(sum[2] * inv, sum[3] * inv));
+    if (a.lse && lane == 0) a.lse[at] = (M + log2f(L)) * 0.69314718055994531f;
   }
 }
 
 // ------------------------------------------------------------------ host
 
-// Row blocks of a KV head at most: every sequence may end with a part of one.
-static int64_t most_blocks(const BatchView& b, int G) {
-  const int64_t rows = std::min(b.max_q, b.n_rows);
-  return std::min(b.n_seq * ((rows * G + kChunkRows - 1) / kChunkRows),
-                  (static_cast<int64_t>(b.n_rows) * G + static_cast<int64_t>(b.n_seq) * (kChunkRows - 1)) / kChunkRows);
+static int tile_pairs() { return std::max(1, num_sms() / 2); }
+
+// Whether the bounds allow a unit long enough to be cut.
+static bool may_cut(const BatchView& b, int window) {
+  int64_t tiles = (static_cast<int64_t>(b.prefix_len) + kTileKeys - 1) / kTileKeys + (static_cast<int64_t>(b.max_len) + kTileKeys - 1) / kTileKeys;
+  if (window) tiles = std::min(tiles, (static_cast<int64_t>(window) + kTileRows + kTileKeys - 1) / kTileKeys + 2);
+  return tiles >= 2 * kMinCut;
 }
 
-template <typename T, bool PAGED>
-static cudaError_t chunk_launch(const PagedView& c, const BatchView& b, const ChunkArgs& p, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, most_blocks(b, p.a.G)) * c.Hkv));
-  LaunchScope ls(KC_CHUNK_ATTN, st);
-  if (p.D <= 64)
-    chunk_attn_kernel<T, 64, PAGED><<<grid, 128, 0, st>>>(c, b, p, device_status_ptr());
-  else
-    chunk_attn_kernel<T, 128, PAGED><<<grid, 128, 0, st>>>(c, b, p, device_status_ptr());
-  return cudaGetLastError();
+static size_t parts_layout(const BatchView& b, int D, int window, void* base, ChunkParts* w) {
+  *w = ChunkParts{};
+  if (!may_cut(b, window)) return 0;
+  uint8_t* at = static_cast<uint8_t*>(base);
+  size_t used = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* r = at + used;
+    used += align_up(bytes, 256);
+    return r;
+  };
+  const size_t pairs = tile_pairs(), rows = pairs * 2 * kTileRows;
+  w->rec = reinterpret_cast<int4*>(take(pairs * sizeof(int4)));
+  w->ml = reinterpret_cast<float2*>(take(rows * sizeof(float2)));
+  w->o = reinterpret_cast<float*>(take(rows * D * sizeof(float)));
+  return used;
+}
+
+// Where keys and values are.
+struct ChunkSource {
+  const void* k;
+  const void* v;
+  int64_t kv_stride;   // packed: entries from row to row
+};
+
+template <typename T, int DP, bool PAGED>
+static qcf_status tile_launch(const char* who, const ChunkSource& src, const PagedView& c, const BatchView& b, const ChunkArgs& p, const ChunkParts& w,
+                              cudaStream_t st) {
+  using Cfg = TileCfg<DP>;
+  CUtensorMap tk, tv, tq;
+  const CUtensorMapSwizzle v_swizzle = Cfg::VCOLS == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  const uint64_t qd[3] = {static_cast<uint64_t>(p.D), static_cast<uint64_t>(p.a.Hq), static_cast<uint64_t>(b.n_rows)};
+  const uint64_t qs[2] = {static_cast<uint64_t>(p.D) * 2, static_cast<uint64_t>(p.a.q_stride) * 2};
+  const uint32_t qb[3] = {64, static_cast<uint32_t>(p.a.G), static_cast<uint32_t>(p.per)};
+  bool ok = encode_tmap_3d(&tq, p.a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (PAGED) {
+    ok = ok && encode_pages(&tk, src.k, c, std::min(1 << c.page_shift, 64), 64, CU_TENSOR_MAP_SWIZZLE_128B) &&
+         encode_pages(&tv, src.v, c, std::min(1 << c.page_shift, kTileKeys), Cfg::VCOLS, v_swizzle);
+  } else {
+    const uint64_t d[3] = {static_cast<uint64_t>(p.D), static_cast<uint64_t>(c.Hkv), static_cast<uint64_t>(b.n_rows)};
+    const uint64_t s[2] = {static_cast<uint64_t>(p.D) * 2, static_cast<uint64_t>(src.kv_stride) * 2};
+    const uint32_t kb[3] = {64, 1, 64}, vb[3] = {Cfg::VCOLS, 1, kTileKeys};
+    ok = ok && encode_tmap_3d(&tk, src.k, d, s, kb, CU_TENSOR_MAP_SWIZZLE_128B) && encode_tmap_3d(&tv, src.v, d, s, vb, v_swizzle);
+  }
+  if (!ok) return set_error(QCF_ERR_CUDA, "%s: tensor map encoding failed", who);
+  static PerDevice<cudaError_t> smem_attr;
+  cudaError_t e = smem_attr.get(current_device(), [] {
+    return cudaFuncSetAttribute(tile_attn_kernel<T, DP, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+  });
+  if (e != cudaSuccess) return cuda_error(e, who);
+  {
+    LaunchScope ls(KC_CHUNK_ATTN, st);
+    tile_attn_kernel<T, DP, PAGED><<<2 * tile_pairs(), kTileThreads, Cfg::SMEM, st>>>(tk, tv, tq, c, b, p, w, device_status_ptr());
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_error(e, who);
+  }
+  if (!w.rec) return QCF_OK;
+  LaunchScope ls(KC_CHUNK_JOIN, st);
+  e = launch_pdl(tile_join_kernel<T>, dim3(tile_pairs(), (std::min(4 * p.per * p.a.G, kTileRows) + kJoinRows - 1) / kJoinRows), dim3(kJoinWarps * 32), 0, st, p,
+                 w);
+  return e == cudaSuccess ? QCF_OK : cuda_error(e, who);
+}
+
+template <bool PAGED>
+static qcf_status chunk_launch(const char* who, int dtype, const ChunkSource& src, const PagedView& c, const BatchView& b, ChunkArgs p, void* ws,
+                               size_t ws_bytes, cudaStream_t st) {
+  if (p.window >= static_cast<int64_t>(b.prefix_len) + b.max_len) p.window = 0;   // every key lies inside
+  ChunkParts w;
+  const size_t need = parts_layout(b, p.D, p.window, ws, &w);
+  if (need > 0 && (!ws || ws_bytes < need)) return set_error(QCF_ERR_WORKSPACE, "%s: workspace %zu < %zu", who, ws_bytes, need);
+  if (dtype == QCF_BF16)
+    return p.D <= 64 ? tile_launch<__nv_bfloat16, 64, PAGED>(who, src, c, b, p, w, st) : tile_launch<__nv_bfloat16, 128, PAGED>(who, src, c, b, p, w, st);
+  return p.D <= 64 ? tile_launch<__half, 64, PAGED>(who, src, c, b, p, w, st) : tile_launch<__half, 128, PAGED>(who, src, c, b, p, w, st);
 }
 
 static qcf_status check_sizes(const char* who, const PagedView& c, const BatchView& b, int Hq) {
@@ -293,8 +1100,9 @@ extern "C" {
 size_t qcf_packed_causal_attn_workspace_size(int n_seq, int n_rows, int max_len, int Hq, int Hkv, int D) {
   PagedView c;
   BatchView b;
-  check_packed("qcf_packed_causal_attn_workspace_size", n_seq, n_rows, max_len, Hq, Hkv, D, &c, &b);
-  return 0;
+  if (check_packed("qcf_packed_causal_attn_workspace_size", n_seq, n_rows, max_len, Hq, Hkv, D, &c, &b) != QCF_OK) return 0;
+  ChunkParts w;
+  return n_seq == 0 || n_rows == 0 ? 0 : parts_layout(b, D, 0, nullptr, &w);
 }
 
 qcf_status qcf_packed_causal_attn(const void* q, int64_t q_stride, const void* k, const void* v, int64_t kv_stride, int dtype,
@@ -314,18 +1122,17 @@ qcf_status qcf_packed_causal_attn(const void* q, int64_t q_stride, const void* k
   if ((s = check_chunk(who, c, q, q_stride, Hq, scale, window, o, ws)) != QCF_OK) return s;
   if (n_seq == 0 || n_rows == 0) return QCF_OK;
   b.row_start = row_start;
-  const ChunkArgs p{attn_args(q, q_stride, o, lse, Hq, Hkv, scale), k, v, kv_stride, D, window};
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == QCF_BF16 ? chunk_launch<__nv_bfloat16, false>(c, b, p, st) : chunk_launch<__half, false>(c, b, p, st);
-  return e == cudaSuccess ? QCF_OK : cuda_error(e, "qcf_packed_causal_attn: launch");
+  const ChunkArgs p{attn_args(q, q_stride, o, lse, Hq, Hkv, scale), D, window, 128 / (Hq / Hkv)};
+  return chunk_launch<false>(who, dtype, ChunkSource{k, v, kv_stride}, c, b, p, ws, ws_bytes, static_cast<cudaStream_t>(stream));
 }
 
 size_t qcf_paged_chunk_attn_workspace_size(const qcf_paged_kv* cache, const qcf_paged_batch* batch, int Hq) {
   const char* who = "qcf_paged_chunk_attn_workspace_size";
   PagedView c;
   BatchView b;
-  if (check_paged(who, cache, batch, &c, &b) == QCF_OK) check_sizes(who, c, b, Hq);
-  return 0;
+  if (check_paged(who, cache, batch, &c, &b) != QCF_OK || check_sizes(who, c, b, Hq) != QCF_OK) return 0;
+  ChunkParts w;
+  return b.n_seq == 0 || b.n_rows == 0 ? 0 : parts_layout(b, c.D, 0, nullptr, &w);
 }
 
 qcf_status qcf_paged_chunk_attn(const qcf_paged_kv* cache, const qcf_paged_batch* batch, const void* q, int64_t q_stride, int Hq,
@@ -338,10 +1145,8 @@ qcf_status qcf_paged_chunk_attn(const qcf_paged_kv* cache, const qcf_paged_batch
   if (s == QCF_OK) s = check_chunk(who, c, q, q_stride, Hq, scale, window, o, ws);
   if (s != QCF_OK) return s;
   if (b.n_seq == 0 || b.n_rows == 0) return QCF_OK;
-  const ChunkArgs p{attn_args(q, q_stride, o, lse, Hq, c.Hkv, scale), cache->k, cache->v, 0, c.D, window};
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = cache->dtype == QCF_BF16 ? chunk_launch<__nv_bfloat16, true>(c, b, p, st) : chunk_launch<__half, true>(c, b, p, st);
-  return e == cudaSuccess ? QCF_OK : cuda_error(e, "qcf_paged_chunk_attn: launch");
+  const ChunkArgs p{attn_args(q, q_stride, o, lse, Hq, c.Hkv, scale), c.D, window, 128 / (Hq / c.Hkv)};
+  return chunk_launch<true>(who, cache->dtype, ChunkSource{cache->k, cache->v, 0}, c, b, p, ws, ws_bytes, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
