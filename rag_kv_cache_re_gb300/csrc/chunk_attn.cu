@@ -89,30 +89,16 @@ __device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
 }
+// Arrivals at a barrier of either CTA.  What they announce lies in tensor memory or comes by TMA, which have
+// ordering of their own: without a scope the arrival orders no other memory across the pair (a release for the
+// cluster is a memory barrier of 500 cycles or more, and made every weight tile wait for it).
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_expect_tx_at(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// mbar_wait for arrivals of either CTA.
-__device__ __forceinline__ bool mbar_try_wait_pair(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait_pair(bar, parity)) return true;
-  const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait_pair(bar, parity)) {
-    if (globaltimer() - t0 > QCF_WAIT_NS) return false;
-  }
-  return true;
-}
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 // Tiled loads to this CTA that count on a barrier of either (its cluster address).
 __device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
   asm volatile(
@@ -558,7 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         for (int i = 0; i < s.nt; ++i, ++n) {
           const int st = n % ST, t = s.t0 + i;
           const int next_id = PAGED && i + 1 < s.nt ? page_of(t + 1) : 0;
-          if (!__all_sync(kAll, mbar_wait_pair(&empty[st], ((n / ST) & 1) ^ 1u))) {
+          if (!__all_sync(kAll, mbar_wait(&empty[st], ((n / ST) & 1) ^ 1u))) {
             ok = false;
             break;
           }
@@ -589,7 +575,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
           }
           id = next_id;
           if (is_k && i == 0) {   // the unit's Q: rows behind the sequence belong to others or are zeros, and go nowhere
-            if (!__all_sync(kAll, mbar_wait_pair(q_empty, (units & 1) ^ 1u))) {
+            if (!__all_sync(kAll, mbar_wait(q_empty, (units & 1) ^ 1u))) {
               ok = false;
               break;
             }
@@ -611,15 +597,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
               *reinterpret_cast<uint4*>(dst + valid * Cfg::VCOLS * 2 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_at(full + st * 8);
+            if (lane == 0) {
+              fence_cluster();   // the zeros are written by ordinary stores, and the first CTA issues what reads them
+              mbar_arrive_at(full + st * 8);
+            }
           }
         }
       }
       if (!ok && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
       if (rank == 0) {   // no copy of this warp, or its like in the other CTA, is in flight when the CTAs end
         for (int e = max(0, n - ST); e < n; ++e)
-          if (!mbar_wait_pair(&(is_k ? k_full : v_full)[e % ST], (e / ST) & 1) && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
-        if (is_k && units > 0 && !mbar_wait_pair(q_full, (units - 1) & 1) && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
+          if (!mbar_wait(&(is_k ? k_full : v_full)[e % ST], (e / ST) & 1) && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
+        if (is_k && units > 0 && !mbar_wait(q_full, (units - 1) & 1) && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
         if (is_k && lane == 0 && parts.rec) parts.rec[pair] = walk.rec;
       }
     } else if (lane == 0) {
@@ -643,8 +632,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         auto pass = [&](bool due) {
           if (due) mbar_arrive(&p_ready[2 * (1 - x)]);
         };
-        auto wait_k = [&](int tile) { return mbar_wait_pair(&k_full[tile % ST], (tile / ST) & 1); };
-        auto wait_v = [&](int tile) { return mbar_wait_pair(&v_full[tile % ST], (tile / ST) & 1); };
+        auto wait_k = [&](int tile) { return mbar_wait(&k_full[tile % ST], (tile / ST) & 1); };
+        auto wait_v = [&](int tile) { return mbar_wait(&v_full[tile % ST], (tile / ST) & 1); };
         auto scores = [&](int tile, bool due, bool last) {   // S_x = Q_x K^T
           const uint64_t kd = k_desc + tile % ST * (Cfg::KTILE >> 4);
 #pragma unroll
@@ -662,7 +651,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
           release_segment();
           if (s.end) break;
           const int mine = x ? s.nt_b : s.nt_a;
-          if (!(ok = mbar_wait_pair(q_full, k++ & 1))) break;
+          if (!(ok = mbar_wait(q_full, k++ & 1))) break;
           if (mine > 0) {
             if (!(ok = wait_k(n))) break;
             tc_fence_after();
@@ -674,6 +663,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
           for (int i = 0; i < mine; ++i) {
             const bool more = i + 1 < mine;
             if (!(ok = wait_v(n + i) && (!more || wait_k(n + i + 1)))) break;
+            const int t = s.t0 + i;
+            if ((t < np ? b.prefix_len - t * kTileKeys : s.len - (t - np) * kTileKeys) < kTileKeys) fence_cluster();   // zeros of the V producers
             const uint64_t vd = v_desc + (n + i) % ST * (Cfg::VTILE >> 4);
             auto weigh = [&](int half) {   // O_x += P_x V over 64 keys
               tc_fence_after();
@@ -684,9 +675,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             // a begins, b follows while a has tiles left; who is alone gives itself the turn
             if (x == 0 ? i == 0 || s.nt_b == 0 : i >= s.nt_a) mbar_arrive(&p_ready[2 * x]);
             const bool due = x == 0 ? s.nt_b > 0 : i + 1 < s.nt_a;
-            if (!(ok = mbar_wait_pair(&p_ready[2 * x], used & 1))) break;
+            if (!(ok = mbar_wait(&p_ready[2 * x], used & 1))) break;
             weigh(0);
-            if (!(ok = mbar_wait_pair(&p_ready[2 * x + 1], used & 1))) break;
+            if (!(ok = mbar_wait(&p_ready[2 * x + 1], used & 1))) break;
             weigh(1);
             ++used;
             if (more) {
@@ -905,7 +896,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   tc_fence_before();
   __syncthreads();
   // in both CTAs: the commits that arrive here have all done so when the last has
-  if (threadIdx.x < 2 && !mbar_wait_pair(&mma_end[threadIdx.x], 0)) flag_status(status, QCF_DEV_TIMEOUT);
+  if (threadIdx.x < 2 && !mbar_wait(&mma_end[threadIdx.x], 0)) flag_status(status, QCF_DEV_TIMEOUT);
   __syncwarp();
   cluster_sync();
   if (warp == 1) {
