@@ -120,25 +120,28 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 // The products of umma_f16 and umma_f16_ts over 256 rows, 128 in each CTA; the descriptors hold in both.
-__device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// A whole warp runs the issuing code, so that descriptors stay in uniform registers, and `one` lane of it issues.
+__device__ __forceinline__ void umma_f16_pair(bool one, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(one))
       : "memory");
 }
-__device__ __forceinline__ void umma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void umma_f16_ts_pair(bool one, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(one))
       : "memory");
 }
 // Arrives on this barrier in both CTAs once every product issued by this thread is complete.
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
-               "h"(static_cast<uint16_t>(3))
-               : "memory");
+__device__ __forceinline__ void umma_commit_pair(bool one, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %2, 0;\n"
+      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3)), "r"(static_cast<uint32_t>(one))
+      : "memory");
 }
 // sdesc_mnmajor_sw128 for rows of 32 entries: 64-byte swizzle, atoms of 8 rows in 512 bytes.
 __device__ __forceinline__ uint64_t sdesc_mnmajor_sw64(uint32_t smem_addr) {
@@ -611,99 +614,103 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         if (is_k && units > 0 && !mbar_wait(q_full, (units - 1) & 1) && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
         if (is_k && lane == 0 && parts.rec) parts.rec[pair] = walk.rec;
       }
-    } else if (lane == 0) {
-      const int x = warp >> 1;
-      if (rank == 0) {
-        // ---- MMA issuer of row tile x of both CTAs
-        constexpr uint32_t idesc_s = idesc_pair<T>(kTileKeys, false);
-        constexpr uint32_t idesc_o = idesc_pair<T>(DP, true);
-        constexpr int V_STEP = 16 * Cfg::VCOLS * 2;   // 16 keys of V
-        int n = 0, k = 0;    // key tiles, segments so far
-        uint32_t used = 0;   // weight tiles taken so far
-        bool ok = true;
-        Segment s;
-        const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(qbuf + x * Cfg::QTILE));
-        const uint64_t k_desc = sdesc_kmajor_sw128(smem_u32(kbuf));
-        const uint64_t v_desc = DP == 128 ? sdesc_mnmajor_sw128(smem_u32(vbuf), 16) : sdesc_mnmajor_sw64(smem_u32(vbuf));
-        const uint32_t k_empty1 = at_rank(k_empty, 1), v_empty1 = at_rank(v_empty, 1), q_empty1 = at_rank(q_empty, 1);
-        // The turn: the barrier of a tile's first weights also counts one arrival of the other issuer,
-        // made four products (256 cycles) before the end of its block, which covers what this thread
-        // then takes to see it.
-        auto pass = [&](bool due) {
-          if (due) mbar_arrive(&p_ready[2 * (1 - x)]);
-        };
-        auto wait_k = [&](int tile) { return mbar_wait(&k_full[tile % ST], (tile / ST) & 1); };
-        auto wait_v = [&](int tile) { return mbar_wait(&v_full[tile % ST], (tile / ST) & 1); };
-        auto scores = [&](int tile, bool due, bool last) {   // S_x = Q_x K^T
-          const uint64_t kd = k_desc + tile % ST * (Cfg::KTILE >> 4);
+    } else if (rank == 0) {
+      // ---- MMA issuer of row tile x of both CTAs
+      const int x = __shfl_sync(kAll, warp >> 1, 0);
+      const bool one = lane == 0;
+      constexpr uint32_t idesc_s = idesc_pair<T>(kTileKeys, false);
+      constexpr uint32_t idesc_o = idesc_pair<T>(DP, true);
+      constexpr int V_STEP = 16 * Cfg::VCOLS * 2;   // 16 keys of V
+      int n = 0, k = 0;    // key tiles, segments so far
+      uint32_t used = 0;   // weight tiles taken so far
+      bool ok = true;
+      Segment s;
+      const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(qbuf + x * Cfg::QTILE));
+      const uint64_t k_desc = sdesc_kmajor_sw128(smem_u32(kbuf));
+      const uint64_t v_desc = DP == 128 ? sdesc_mnmajor_sw128(smem_u32(vbuf), 16) : sdesc_mnmajor_sw64(smem_u32(vbuf));
+      const uint32_t k_empty1 = at_rank(k_empty, 1), v_empty1 = at_rank(v_empty, 1), q_empty1 = at_rank(q_empty, 1);
+      // The turn: the barrier of a tile's first weights also counts one arrival of the other issuer,
+      // made four products (256 cycles) before the end of its block, which covers what this warp
+      // then takes to see it.
+      auto pass = [&](bool due) {
+        if (due && one) mbar_arrive(&p_ready[2 * (1 - x)]);
+      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kAll, mbar_wait(bar, parity)) != 0; };
+      auto wait_k = [&](int tile) { return wait(&k_full[tile % ST], (tile / ST) & 1); };
+      auto wait_v = [&](int tile) { return wait(&v_full[tile % ST], (tile / ST) & 1); };
+      auto scores = [&](int tile, bool due, bool last) {   // S_x = Q_x K^T
+        const uint64_t kd = k_desc + tile % ST * (Cfg::KTILE >> 4);
 #pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk) {
-            if (kk == DP / 16 - 4) pass(due);
-            const uint64_t q_at = ((kk >> 2) * Cfg::QBOX + (kk & 3) * 32) >> 4, k_at = ((kk >> 2) * Cfg::KBOX + (kk & 3) * 32) >> 4;
-            umma_f16_pair(tmem + x * 128, q_desc + q_at, kd + k_at, idesc_s, kk > 0 ? 1u : 0u);
-          }
-          umma_commit_pair(&s_full[x]);
-          umma_commit_pair(&k_empty[tile % ST]);
-          if (last) umma_commit_pair(q_empty);
-        };
-        while (true) {
-          if (!(ok = next_segment(s))) break;
-          release_segment();
-          if (s.end) break;
-          const int mine = x ? s.nt_b : s.nt_a;
-          if (!(ok = mbar_wait(q_full, k++ & 1))) break;
-          if (mine > 0) {
-            if (!(ok = wait_k(n))) break;
+        for (int kk = 0; kk < DP / 16; ++kk) {
+          if (kk == DP / 16 - 4) pass(due);
+          const uint64_t q_at = ((kk >> 2) * Cfg::QBOX + (kk & 3) * 32) >> 4, k_at = ((kk >> 2) * Cfg::KBOX + (kk & 3) * 32) >> 4;
+          umma_f16_pair(one, tmem + x * 128, q_desc + q_at, kd + k_at, idesc_s, kk > 0 ? 1u : 0u);
+        }
+        umma_commit_pair(one, &s_full[x]);
+        umma_commit_pair(one, &k_empty[tile % ST]);
+        if (last) umma_commit_pair(one, q_empty);
+      };
+      while (true) {
+        if (!(ok = __all_sync(kAll, next_segment(s)))) break;
+        __syncwarp();
+        if (one) release_segment();
+        if (s.end) break;
+        // alike in all lanes, which the compiler cannot see in what comes from memory
+        const int t0 = __shfl_sync(kAll, s.t0, 0), nt = __shfl_sync(kAll, s.nt, 0), len = __shfl_sync(kAll, s.len, 0);
+        const int nt_a = __shfl_sync(kAll, s.nt_a, 0), nt_b = __shfl_sync(kAll, s.nt_b, 0), mine = x ? nt_b : nt_a;
+        if (!(ok = wait(q_full, k++ & 1))) break;
+        if (mine > 0) {
+          if (!(ok = wait_k(n))) break;
+          tc_fence_after();
+          scores(n, false, mine == 1);
+        } else if (one) {
+          mbar_arrive(q_empty);
+          mbar_arrive_at(q_empty1);
+        }
+        for (int i = 0; i < mine; ++i) {
+          const bool more = i + 1 < mine;
+          if (!(ok = wait_v(n + i) && (!more || wait_k(n + i + 1)))) break;
+          const int t = t0 + i;
+          if ((t < np ? b.prefix_len - t * kTileKeys : len - (t - np) * kTileKeys) < kTileKeys) fence_cluster();   // zeros of the V producers
+          const uint64_t vd = v_desc + (n + i) % ST * (Cfg::VTILE >> 4);
+          auto weigh = [&](int half) {   // O_x += P_x V over 64 keys
             tc_fence_after();
-            scores(n, false, mine == 1);
-          } else {
-            mbar_arrive(q_empty);
-            mbar_arrive_at(q_empty1);
-          }
-          for (int i = 0; i < mine; ++i) {
-            const bool more = i + 1 < mine;
-            if (!(ok = wait_v(n + i) && (!more || wait_k(n + i + 1)))) break;
-            const int t = s.t0 + i;
-            if ((t < np ? b.prefix_len - t * kTileKeys : s.len - (t - np) * kTileKeys) < kTileKeys) fence_cluster();   // zeros of the V producers
-            const uint64_t vd = v_desc + (n + i) % ST * (Cfg::VTILE >> 4);
-            auto weigh = [&](int half) {   // O_x += P_x V over 64 keys
-              tc_fence_after();
 #pragma unroll
-              for (int kk = half * (kTileKeys / 32); kk < (half + 1) * (kTileKeys / 32); ++kk)
-                umma_f16_ts_pair(tmem + 256 + x * DP, tmem + x * 128 + kk * 8, vd + kk * (V_STEP >> 4), idesc_o, (i > 0 || kk > 0) ? 1u : 0u);
-            };
-            // a begins, b follows while a has tiles left; who is alone gives itself the turn
-            if (x == 0 ? i == 0 || s.nt_b == 0 : i >= s.nt_a) mbar_arrive(&p_ready[2 * x]);
-            const bool due = x == 0 ? s.nt_b > 0 : i + 1 < s.nt_a;
-            if (!(ok = mbar_wait(&p_ready[2 * x], used & 1))) break;
-            weigh(0);
-            if (!(ok = mbar_wait(&p_ready[2 * x + 1], used & 1))) break;
-            weigh(1);
-            ++used;
-            if (more) {
-              scores(n + i + 1, due, i + 2 == mine);
-            } else {
-              pass(due);
-              umma_commit_pair(&o_done[x]);
-            }
-            umma_commit_pair(&v_empty[(n + i) % ST]);   // after the scores: a commit costs this thread more than a product
+            for (int kk = half * (kTileKeys / 32); kk < (half + 1) * (kTileKeys / 32); ++kk)
+              umma_f16_ts_pair(one, tmem + 256 + x * DP, tmem + x * 128 + kk * 8, vd + kk * (V_STEP >> 4), idesc_o, (i > 0 || kk > 0) ? 1u : 0u);
+          };
+          // a begins, b follows while a has tiles left; who is alone gives itself the turn
+          if ((x == 0 ? i == 0 || nt_b == 0 : i >= nt_a) && one) mbar_arrive(&p_ready[2 * x]);
+          const bool due = x == 0 ? nt_b > 0 : i + 1 < nt_a;
+          if (!(ok = wait(&p_ready[2 * x], used & 1))) break;
+          weigh(0);
+          if (!(ok = wait(&p_ready[2 * x + 1], used & 1))) break;
+          weigh(1);
+          ++used;
+          if (more) {
+            scores(n + i + 1, due, i + 2 == mine);
+          } else {
+            pass(due);
+            umma_commit_pair(one, &o_done[x]);
           }
-          if (!ok) break;
-          for (int i = mine; i < s.nt; ++i) {   // tiles that only the other row tile sees: hand them on
-            const int st = (n + i) % ST;
-            if (!(ok = wait_k(n + i))) break;
+          umma_commit_pair(one, &v_empty[(n + i) % ST]);   // after the scores: a commit costs more than a product
+        }
+        if (!ok) break;
+        for (int i = mine; i < nt; ++i) {   // tiles that only the other row tile sees: hand them on
+          const int st = (n + i) % ST;
+          if (!(ok = wait_k(n + i) && wait_v(n + i))) break;
+          if (one) {
             mbar_arrive(&k_empty[st]);
             mbar_arrive_at(k_empty1 + st * 8);
-            if (!(ok = wait_v(n + i))) break;
             mbar_arrive(&v_empty[st]);
             mbar_arrive_at(v_empty1 + st * 8);
           }
-          if (!ok) break;
-          n += s.nt;
         }
-        if (!ok) flag_status(status, QCF_DEV_TIMEOUT);
-        umma_commit_pair(&mma_end[x]);   // nothing runs on tensor memory once it is freed
+        if (!ok) break;
+        n += nt;
       }
+      if (!ok && one) flag_status(status, QCF_DEV_TIMEOUT);
+      umma_commit_pair(one, &mma_end[x]);   // nothing runs on tensor memory once it is freed
     }
   } else {
     // ---- softmax: thread = score row of tile x
