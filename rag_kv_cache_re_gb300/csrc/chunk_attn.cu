@@ -143,6 +143,17 @@ __device__ __forceinline__ void umma_commit_pair(bool one, uint64_t* bar) {
       "h"(static_cast<uint16_t>(3)), "r"(static_cast<uint32_t>(one))
       : "memory");
 }
+// 32 lanes x 16 consecutive 32-bit columns from registers into tensor memory; tmem_wait_st() before others may read them.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+      "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])),
+      "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15]))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // sdesc_mnmajor_sw128 for rows of 32 entries: 64-byte swizzle, atoms of 8 rows in 512 bytes.
 __device__ __forceinline__ uint64_t sdesc_mnmajor_sw64(uint32_t smem_addr) {
   return static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(1u) << 16 | static_cast<uint64_t>(512u >> 4) << 32 |
@@ -771,29 +782,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
           for (int j = 0; j < kTileKeys; ++j)
             if (bad8 >> (j / 8) & 1) sv[j] = -INFINITY;
         }
-        // 64 weights from the logits; they leave in two halves, so that P V of the first 64 keys runs
-        // under the powers of the others
-        const Pair scale2 = make_pair2(a.scale_log2, a.scale_log2);
-        Pair sum[2];
-        uint32_t pk[32];
-        auto weights = [&](int half, float base) {
-          const Pair nm2 = make_pair2(-base, -base);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int j = half * 64 + 2 * e;
-            float p0, p1;
-            split(fma2(make_pair2(sv[j], sv[j + 1]), scale2, nm2), p0, p1);
-            p0 = fast_exp2(p0);
-            p1 = fast_exp2(p1);
-            sum[e & 1] = add2(sum[e & 1], make_pair2(p0, p1));
-            pk[e] = pack2<T>(p0, p1);
-          }
-        };
-        // The first half is weighed with the maximum so far, the tile's own found meanwhile (the
-        // special-function unit paces the powers, the comparisons fill its gaps): the maximum
-        // moves only by more than 2^8, so after a unit's first tiles it nearly always stands.
-        sum[0] = sum[1] = make_pair2(0.f, 0.f);
-        weights(0, m == -INFINITY ? 0.f : m);
         float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
         for (int j = 4; j < kTileKeys - 4; j += 8)
@@ -808,26 +796,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
           if (i > 0) {   // the full S of this tile says that every earlier product has been added to O
             const float f = m == -INFINITY ? 0.f : fast_exp2(m - m_new);
 #pragma unroll 1
-            for (int cc = 0; cc < DP / 32; ++cc) {
-              float ov[32];
-              tmem_ld32(o_tm + cc * 32, ov);
+            for (int cc = 0; cc < DP / 16; ++cc) {
+              float ov[16];
+              tmem_ld16(o_tm + cc * 16, ov);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) ov[e] *= f;
-              tmem_st32(o_tm + cc * 32, ov);
+              for (int e = 0; e < 16; ++e) ov[e] *= f;
+              tmem_st16(o_tm + cc * 16, ov);
             }
+            tmem_wait_st();
             l *= f;
           }
           m = m_new;
-          sum[0] = sum[1] = make_pair2(0.f, 0.f);
-          weights(0, m == -INFINITY ? 0.f : m);
         }
+        // The weights leave in two halves, so that P V of the first 64 keys runs under the powers of the others.
+        // A weight takes the place of its logit: with the first half weighed before the maximum was
+        // known, and kept in case it had moved, registers left few powers under way at a time
+        // (1200 cycles to the weights of a tile).
+        const float base = m == -INFINITY ? 0.f : -m;
+        const Pair scale2 = make_pair2(a.scale_log2, a.scale_log2), base2 = make_pair2(base, base);
+        Pair sum[2];
+        sum[0] = sum[1] = make_pair2(0.f, 0.f);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (half == 1) weights(1, m == -INFINITY ? 0.f : m);
-          tmem_st32u(s_tm + half * 32, pk);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_at(ready + 8 * half);
+        for (int part = 0; part < 4; ++part) {
+          float pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int j = part * 32 + 2 * e;
+            float p0, p1;
+            split(fma2(make_pair2(sv[j], sv[j + 1]), scale2, base2), p0, p1);
+            p0 = fast_exp2(p0);
+            p1 = fast_exp2(p1);
+            sum[e & 1] = add2(sum[e & 1], make_pair2(p0, p1));
+            pk[e] = __uint_as_float(pack2<T>(p0, p1));
+          }
+          tmem_st16(s_tm + part * 16, pk);
+          if (part & 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(ready + 8 * (part >> 1));
+          }
         }
         float l0, l1;
         split(add2(sum[0], sum[1]), l0, l1);
