@@ -16,11 +16,13 @@
 //   warp 0      walks the pair's share of the work and passes units on through a small ring; K producer by
 //               tiled TMA (pages: one box per page and 64 columns), and Q
 //   warp 2      V producer; rows behind a sequence's end are zeroed, since 0 x NaN is NaN
-//   warps 1, 3  in the first CTA, one thread each issues the products of row tile x for both: P_x V, then
+//   warps 1, 3  in the first CTA, one lane each issues the products of row tile x for both: P_x V, then
 //               S_x = Q_x K^T of the next key tile, the two taking turns
 //   warps 4-7   softmax of a, warps 8-11 of b: thread = score row of this CTA; the weights back to tensor
 //               memory over the scores they came from, the output rescaled only when a row's maximum
 //               grows by more than 2^8; the unit's output at its end
+// A unit with rows in a alone (single tokens, short questions) takes its key tiles by turns: b has the
+// even ones and a the odd ones of the same rows, and the output joins the two.
 // Tensor memory columns: S_a 0, S_b 128 (the weights take the first 64 of each), O_a 256, O_b 256 + DP.
 #include <algorithm>
 #include <cmath>
@@ -56,10 +58,10 @@ struct TileCfg {
   static constexpr int QBOX = 128 * 128, QTILE = BOXES * QBOX;          // a CTA's 128 score rows
   static constexpr int KBOX = 64 * 128, KTILE = BOXES * KBOX;           // its 64 keys
   static constexpr int VCOLS = DP / 2, VTILE = kTileKeys * VCOLS * 2;   // its columns of 128 values
-  static constexpr int STAGES = DP == 128 ? 4 : 8;
-  static constexpr int OUT = 8 * 4096;                                  // 4 KB for each softmax warp
-  static constexpr int FIXED = 2048;
-  static constexpr int SMEM = 2 * QTILE + STAGES * (KTILE + VTILE) + OUT + FIXED + 1024;
+  static constexpr int STAGES = DP == 128 ? 3 : 8;
+  static constexpr int OBOX = 128 * 128, OTILE = BOXES * OBOX;          // output of 128 score rows, 64 columns to a box
+  static constexpr int FIXED = 3072;
+  static constexpr int SMEM = 2 * QTILE + STAGES * (KTILE + VTILE) + 2 * OTILE + FIXED;
 };
 static_assert(TileCfg<128>::SMEM <= 232448 && TileCfg<64>::SMEM <= 232448, "227 KB of a CTA");
 
@@ -112,6 +114,19 @@ __device__ __forceinline__ void tma_load_4d_pair(void* smem_dst, const CUtensorM
       ::"r"(smem_u32(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
+               ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(smem_src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+// The shared memory of this thread's bulk stores has been read.
+__device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// Eight bits for each of the lowest four.
+__device__ __forceinline__ uint32_t bytes_of(unsigned b) {
+  return (b & 1u) * 0xffu | (b >> 1 & 1u) * 0xff00u | (b >> 2 & 1u) * 0xff0000u | (b >> 3 & 1u) * 0xff000000u;
+}
+// The lowest n bits, none below 0 and all from 32 on.
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols) : "memory");
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -185,83 +200,88 @@ __device__ __forceinline__ RowBlock row_block(const BatchView& b, const ChunkArg
   k.end_a = tile_of(b.prefix_len, pos + min(k.ntok, 2 * p.per) - 1) + 1;
   return k;
 }
-__device__ __forceinline__ int tile_cost(const RowBlock& k, int per) { return k.ntok > 2 * per ? kTileCost2 : kTileCost1; }
-__device__ __forceinline__ int64_t unit_cost(const RowBlock& k, int per) {
-  return kUnitCost + static_cast<int64_t>(tile_cost(k, per)) * k.tiles();
+__device__ __forceinline__ bool two_tiles(const RowBlock& k, int per) { return k.ntok > 2 * per; }
+__device__ __forceinline__ int unit_cost(const RowBlock& k, int per) {
+  return kUnitCost + (two_tiles(k, per) ? kTileCost2 : kTileCost1) * k.tiles();
 }
 // The tile of a unit before which a border at cost x behind its beginning cuts it.
-__device__ __forceinline__ int cut_at(const RowBlock& k, int per, int64_t x) {
-  const int n = k.tiles();
-  const int t = static_cast<int>(min(max(x - kUnitCost, static_cast<int64_t>(0)) / tile_cost(k, per), static_cast<int64_t>(n)));
+__device__ __forceinline__ int cut_at(const RowBlock& k, int per, int x) {
+  const int n = k.tiles(), y = max(x - kUnitCost, 0);
+  const int t = min(two_tiles(k, per) ? y / kTileCost2 : y / kTileCost1, n);
   return t < kMinCut ? 0 : n - t < kMinCut ? n : t;
 }
 
 struct DealStart {
-  int64_t pos, share;   // cost before the row block
   int seq, block;       // seq -1: nothing for this pair
+  int pos, share;       // cost before the row block
 };
 
 // One unit, or the part of one, of this pair.
 struct Segment {
   int seq, row0, ntok, g;      // its first row in the batch, its tokens
   int pos, len;                // own position of its first token; own tokens of the sequence
-  int t0, nt, nt_a, nt_b;      // first key tile, tiles, those that row tiles a and b see
+  int t0, nt, nt_a, nt_b;      // first key tile, tiles, those of row tiles a and b
+  int split;                   // 1: no rows in b, so it takes the even tiles of a's rows, a the odd ones
   int slot;                    // -1: the whole unit, else where its sums go
   int end;                     // 1: there are no more
 };
 
-// Sum over the threads before this one, and over all.
-__device__ __forceinline__ int64_t deal_scan(int64_t v, int64_t* met, int64_t* total) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t run = v;
+// The deal is found by the softmax warps, while others set up barriers and tensor memory.
+constexpr int kDealThreads = 256;
+__device__ __forceinline__ void deal_sync() { bar_sync(7, kDealThreads); }
+// Sum over the threads before this one, and over all; met: 8 ints of its own for each use.
+__device__ __forceinline__ int deal_scan(int tid, int v, int* met, int* total) {
+  const int warp = tid >> 5, lane = tid & 31;
+  int run = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, run, o);
+    const int u = __shfl_up_sync(0xffffffffu, run, o);
     if (lane >= o) run += u;
   }
-  __syncthreads();
   if (lane == 31) met[warp] = run;
-  __syncthreads();
-  int64_t before = run - v;
+  deal_sync();
+  int before = run - v;
   *total = 0;
 #pragma unroll
-  for (int w = 0; w < kTileThreads / 32; ++w) {
-    *total += met[w];
-    if (w < warp) before += met[w];
+  for (int w = 0; w < kDealThreads / 32; ++w) {
+    const int u = met[w];
+    *total += u;
+    if (w < warp) before += u;
   }
   return before;
 }
 
 // Finds where this pair's share begins; blk: scratch for n_seq + 1 ints.
-__device__ void find_share(const BatchView& b, const ChunkArgs& p, int Hkv, int pair, int pairs, int* blk, int64_t* met, DealStart* start,
+__device__ void find_share(int tid, const BatchView& b, const ChunkArgs& p, int Hkv, int pair, int pairs, int* blk, int* met, DealStart* start,
                            unsigned int* status) {
-  const int R = 4 * p.per;
-  const int per_s = (b.n_seq + kTileThreads - 1) / kTileThreads;
-  const int s0 = min(b.n_seq, static_cast<int>(threadIdx.x) * per_s), s1 = min(b.n_seq, s0 + per_s);
-  int64_t mine = 0, all;
+  const int R = 4 * p.per, most = b.n_rows / R + b.n_seq;   // row blocks at most
+  const int per_s = (b.n_seq + kDealThreads - 1) / kDealThreads;
+  const int s0 = min(b.n_seq, tid * per_s), s1 = min(b.n_seq, s0 + per_s);
+  int mine = 0, all, total;
   for (int s = s0; s < s1; ++s) {
     const SeqSpan q = chunk_span(b, s);
     if (q.bad && blockIdx.x == 0) flag_status(status, QCF_DEV_BAD_INDEX);
-    blk[s] = (q.nq + R - 1) / R;
-    mine += blk[s];
+    const int n = (q.nq + R - 1) / R;
+    blk[s] = n;
+    mine = min(mine + n, most + 1);
   }
-  int64_t at = deal_scan(mine, met, &all);
+  int at = deal_scan(tid, mine, met, &all);   // no overflow: 256 (most + 1) < 2^31
   // more row blocks than the rows allow come only of sequences that overlap: nothing is done for them
-  const bool over = all > b.n_rows / R + b.n_seq;
-  if (over && blockIdx.x == 0 && threadIdx.x == 0) flag_status(status, QCF_DEV_BAD_INDEX);
-  const int blocks = over ? 0 : static_cast<int>(all);
+  const bool over = all > most;
+  if (over && blockIdx.x == 0 && tid == 0) flag_status(status, QCF_DEV_BAD_INDEX);
+  const int blocks = over ? 0 : all;
   for (int s = s0; s < s1; ++s) {
     const int n = blk[s];
-    blk[s] = static_cast<int>(at);
+    blk[s] = at;
     at += n;
   }
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     blk[b.n_seq] = blocks;
     start->seq = -1;
   }
-  __syncthreads();
-  const int per_b = (blocks + kTileThreads - 1) / kTileThreads;
-  const int b0 = min(blocks, static_cast<int>(threadIdx.x) * per_b), b1 = min(blocks, b0 + per_b);
+  deal_sync();
+  const int per_b = (blocks + kDealThreads - 1) / kDealThreads;
+  const int b0 = min(blocks, tid * per_b), b1 = min(blocks, b0 + per_b);
   int first = 0;
   if (b0 < b1) {   // the last sequence that begins at or before block b0
     int hi = b.n_seq;
@@ -285,23 +305,23 @@ __device__ void find_share(const BatchView& b, const ChunkArgs& p, int Hkv, int 
       if (visit(seq, i - blk[seq], Hkv * unit_cost(row_block(b, p, q.nq, q.len, i - blk[seq]), p.per))) return;
     }
   };
-  int64_t cost = 0, total;
-  walk([&](int, int, int64_t c) {
+  int cost = 0;
+  walk([&](int, int, int c) {
     cost += c;
     return false;
   });
-  int64_t pos = deal_scan(cost, met, &total);
-  const int64_t share = max((total + pairs - 1) / pairs, static_cast<int64_t>(kMinCost)), want = pair * share;
+  int pos = deal_scan(tid, cost, met + 8, &total);
+  const int share = max((total + pairs - 1) / pairs, kMinCost);
+  const int64_t want = static_cast<int64_t>(pair) * share;
   if (pos <= want && want < pos + cost)
-    walk([&](int seq, int i, int64_t c) {
+    walk([&](int seq, int i, int c) {
       if (want >= pos + c) {
         pos += c;
         return false;
       }
-      *start = DealStart{pos, share, seq, i};
+      *start = DealStart{seq, i, pos, share};
       return true;
     });
-  __syncthreads();
 }
 
 // Walks a pair's share, all lanes of a warp alike; they keep the spans of 32 sequences.
@@ -309,7 +329,7 @@ struct TileWalk {
   const BatchView& b;
   const ChunkArgs& p;
   const int Hkv, pair;
-  int64_t pos, begin, stop, share;
+  int pos, begin, stop, share;
   int seq, block, g, base;      // base: of the 32 sequences kept
   int my_row0, my_nq, my_len;   // this lane's
   int row0, nq, len;            // of seq
@@ -346,7 +366,7 @@ struct TileWalk {
     keep(seq);
     enter();
     k = row_block(b, p, nq, len, block);
-    g = static_cast<int>((begin - pos) / unit_cost(k, p.per));
+    g = (begin - pos) / unit_cost(k, p.per);
     pos += g * unit_cost(k, p.per);
   }
   // The next sequence with rows.
@@ -369,11 +389,11 @@ struct TileWalk {
   __device__ bool next(Segment& s) {
     while (live) {
       const int n = k.tiles();
-      const int64_t cost = unit_cost(k, p.per);
+      const int cost = unit_cost(k, p.per);
       const int from = pos < begin ? cut_at(k, p.per, begin - pos) : 0, to = pos + cost > stop ? cut_at(k, p.per, stop - pos) : n;
       const bool some = from < to;
       if (some) {
-        const bool two = k.ntok > 2 * p.per;
+        const bool two = two_tiles(k, p.per);
         s.seq = seq;
         s.row0 = row0 + k.i0;
         s.ntok = k.ntok;
@@ -382,13 +402,14 @@ struct TileWalk {
         s.len = len;
         s.t0 = k.t0 + from;
         s.nt = to - from;
-        s.nt_a = max(0, min(k.end_a - k.t0, to) - from);
-        s.nt_b = two ? s.nt : 0;
+        s.split = !two;
+        s.nt_a = two ? max(0, min(k.end_a - k.t0, to) - from) : s.nt / 2;
+        s.nt_b = s.nt - (two ? 0 : s.nt_a);
         s.slot = from == 0 && to == n ? -1 : from > 0 ? 0 : 1;
         s.end = 0;
         if (s.slot == 1) {   // how many borders cut this unit: those of the pairs behind this one
           int parts = 1;
-          for (int64_t at = stop; at < pos + cost; at += share) {
+          for (int at = stop; at < pos + cost; at += share) {
             const int t = cut_at(k, p.per, at - pos);
             parts += t > 0 && t < n;
           }
@@ -422,22 +443,22 @@ constexpr uint32_t idesc_pair(int N, bool b_mn_major) {
 template <typename T, int DP, bool PAGED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     tile_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ,
-                     const PagedView c, const BatchView b, const ChunkArgs p, const ChunkParts parts, unsigned int* status) {
+                     const __grid_constant__ CUtensorMap tmO, const PagedView c, const BatchView b, const ChunkArgs p, const ChunkParts parts,
+                     unsigned int* status) {
   using Cfg = TileCfg<DP>;
   constexpr int ST = Cfg::STAGES;
   constexpr unsigned kAll = 0xffffffffu;
   const AttnArgs& a = p.a;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_addr = smem_u32(smem_raw);
-  uint8_t* qbuf = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  extern __shared__ __align__(1024) uint8_t qbuf[];
   uint8_t* kbuf = qbuf + 2 * Cfg::QTILE;
   uint8_t* vbuf = kbuf + ST * Cfg::KTILE;
   uint8_t* obuf = vbuf + ST * Cfg::VTILE;
-  Segment* segs = reinterpret_cast<Segment*>(obuf + Cfg::OUT);
+  float2* donated = reinterpret_cast<float2*>(obuf + 2 * Cfg::OTILE);   // [128]: maximum and sum of a's rows for b
+  Segment* segs = reinterpret_cast<Segment*>(donated + 128);
   DealStart* start = reinterpret_cast<DealStart*>(segs + kSegRing);
-  int64_t* met = reinterpret_cast<int64_t*>(start + 1);
+  int* met = reinterpret_cast<int*>(start + 1);
   // in the first CTA, for both: what its issuers wait for
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(met + kTileThreads / 32);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(met + 16);
   uint64_t* v_full = k_full + ST;
   uint64_t* q_full = v_full + ST;
   uint64_t* p_ready = q_full + 1;    // [a, b][first, last 64 keys]
@@ -452,7 +473,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   uint64_t* seg_full = v_tail + 1;
   uint64_t* seg_empty = seg_full + kSegRing;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(seg_empty + kSegRing);
-  static_assert(sizeof(Segment) * kSegRing + sizeof(DealStart) + (kTileThreads / 32 + 4 * ST + 24 + 2 * kSegRing) * 8 <= Cfg::FIXED, "fixed part");
+  static_assert(sizeof(Segment) * kSegRing % 8 == 0 && sizeof(DealStart) % 8 == 0, "barriers");
+  static_assert(128 * 8 + sizeof(Segment) * kSegRing + sizeof(DealStart) + 64 + (4 * ST + 24 + 2 * kSegRing) * 8 <= Cfg::FIXED, "fixed part");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank()), pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
@@ -460,6 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
     tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmO);
     for (int s = 0; s < ST; ++s) {
       mbar_init(&k_full[s], 2);
       mbar_init(&v_full[s], 2);
@@ -483,8 +506,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
-  find_share(b, p, c.Hkv, pair, pairs, reinterpret_cast<int*>(kbuf), met, start, status);
-  fence_proxy_async_smem();   // the deal used the rings
+  pdl_wait();
+  if (warp >= 4) {
+    find_share(threadIdx.x - 128, b, p, c.Hkv, pair, pairs, reinterpret_cast<int*>(kbuf), met, start, status);
+    fence_proxy_async_smem();   // the deal used the rings
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -495,7 +521,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   int seg_n = 0;
   auto next_segment = [&](Segment& s) {
     const int at = seg_n % kSegRing;
-    if (!mbar_wait(&seg_full[at], (seg_n / kSegRing) & 1)) return false;
+    // longer than the walk's own waits take to run out: it still passes an end on, so that all warps see the same segments
+    bool there = false;
+    for (int i = 0; i < 5 && !there; ++i) there = mbar_wait(&seg_full[at], (seg_n / kSegRing) & 1);
+    if (!there) return false;
     s = segs[at];
     ++seg_n;
     return true;
@@ -593,12 +622,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
               ok = false;
               break;
             }
-            const int nb = s.ntok > 2 * p.per ? 2 : 1;
-            if (lane == 0) mbar_arrive_expect_tx_at(q_full0, nb * Cfg::BOXES * p.per * a.G * 128);
+            if (lane == 0) mbar_arrive_expect_tx_at(q_full0, 2 * Cfg::BOXES * p.per * a.G * 128);
             __syncwarp();
-            if (lane < nb * Cfg::BOXES)
+            if (lane < 2 * Cfg::BOXES)
               tma_load_3d_pair(qbuf + lane * Cfg::QBOX, &tmQ, q_full0, lane % Cfg::BOXES * 64, s.g * a.G,
-                               s.row0 + (2 * (lane / Cfg::BOXES) + rank) * p.per);
+                               s.row0 + (s.split ? rank : 2 * (lane / Cfg::BOXES) + rank) * p.per);
             ++units;
           }
           if (tail) {
@@ -619,6 +647,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         }
       }
       if (!ok && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
+      if (!ok && is_k) {
+        const int at = seg_n % kSegRing;
+        if (__all_sync(kAll, mbar_wait(&seg_empty[at], ((seg_n / kSegRing) & 1) ^ 1u)) && lane == 0) {
+          segs[at].end = 1;
+          mbar_arrive(&seg_full[at]);
+        }
+      }
       if (rank == 0) {   // no copy of this warp, or its like in the other CTA, is in flight when the CTAs end
         for (int e = max(0, n - ST); e < n; ++e)
           if (!mbar_wait(&(is_k ? k_full : v_full)[e % ST], (e / ST) & 1) && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
@@ -669,21 +704,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         // alike in all lanes, which the compiler cannot see in what comes from memory
         const int t0 = __shfl_sync(kAll, s.t0, 0), nt = __shfl_sync(kAll, s.nt, 0), len = __shfl_sync(kAll, s.len, 0);
         const int nt_a = __shfl_sync(kAll, s.nt_a, 0), nt_b = __shfl_sync(kAll, s.nt_b, 0), mine = x ? nt_b : nt_a;
+        const int split = __shfl_sync(kAll, s.split, 0), step = 1 + split;
+        auto hand_on = [&](int tile) {   // one that the other row tile alone takes
+          if (!(wait_k(tile) && wait_v(tile))) return false;
+          const int st = tile % ST;
+          if (one) {
+            mbar_arrive(&k_empty[st]);
+            mbar_arrive_at(k_empty1 + st * 8);
+            mbar_arrive(&v_empty[st]);
+            mbar_arrive_at(v_empty1 + st * 8);
+          }
+          return true;
+        };
         if (!(ok = wait(q_full, k++ & 1))) break;
-        if (mine > 0) {
-          if (!(ok = wait_k(n))) break;
+        int at = n;   // tile
+        if (split && x == 0) ok = hand_on(at++);
+        if (mine > 0 && ok) {
+          if (!(ok = wait_k(at))) break;
           tc_fence_after();
-          scores(n, false, mine == 1);
+          scores(at, false, mine == 1);
         } else if (one) {
           mbar_arrive(q_empty);
           mbar_arrive_at(q_empty1);
         }
-        for (int i = 0; i < mine; ++i) {
+        for (int i = 0; i < mine && ok; ++i) {
           const bool more = i + 1 < mine;
-          if (!(ok = wait_v(n + i) && (!more || wait_k(n + i + 1)))) break;
-          const int t = t0 + i;
+          if (!(ok = wait_v(at) && (!more || wait_k(at + step)))) break;
+          const int t = t0 + at - n;
           if ((t < np ? b.prefix_len - t * kTileKeys : len - (t - np) * kTileKeys) < kTileKeys) fence_cluster();   // zeros of the V producers
-          const uint64_t vd = v_desc + (n + i) % ST * (Cfg::VTILE >> 4);
+          const uint64_t vd = v_desc + at % ST * (Cfg::VTILE >> 4);
           auto weigh = [&](int half) {   // O_x += P_x V over 64 keys
             tc_fence_after();
 #pragma unroll
@@ -691,32 +740,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
               umma_f16_ts_pair(one, tmem + 256 + x * DP, tmem + x * 128 + kk * 8, vd + kk * (V_STEP >> 4), idesc_o, (i > 0 || kk > 0) ? 1u : 0u);
           };
           // a begins, b follows while a has tiles left; who is alone gives itself the turn
-          if ((x == 0 ? i == 0 || nt_b == 0 : i >= nt_a) && one) mbar_arrive(&p_ready[2 * x]);
-          const bool due = x == 0 ? nt_b > 0 : i + 1 < nt_a;
+          if ((x == 0 ? i == 0 : i >= nt_a) && one) mbar_arrive(&p_ready[2 * x]);
+          const bool due = x == 0 || i + 1 < nt_a;
           if (!(ok = wait(&p_ready[2 * x], used & 1))) break;
           weigh(0);
           if (!(ok = wait(&p_ready[2 * x + 1], used & 1))) break;
           weigh(1);
           ++used;
           if (more) {
-            scores(n + i + 1, due, i + 2 == mine);
+            scores(at + step, due, i + 2 == mine);
           } else {
             pass(due);
             umma_commit_pair(one, &o_done[x]);
           }
-          umma_commit_pair(one, &v_empty[(n + i) % ST]);   // after the scores: a commit costs more than a product
+          umma_commit_pair(one, &v_empty[at % ST]);   // after the scores: a commit costs more than a product
+          if (split && at + 1 < n + nt) ok = hand_on(at + 1);
+          at += step;
         }
         if (!ok) break;
-        for (int i = mine; i < nt; ++i) {   // tiles that only the other row tile sees: hand them on
-          const int st = (n + i) % ST;
-          if (!(ok = wait_k(n + i) && wait_v(n + i))) break;
-          if (one) {
-            mbar_arrive(&k_empty[st]);
-            mbar_arrive_at(k_empty1 + st * 8);
-            mbar_arrive(&v_empty[st]);
-            mbar_arrive_at(v_empty1 + st * 8);
-          }
-        }
+        if (!split)
+          for (; at < n + nt && ok; ++at) ok = hand_on(at);
         if (!ok) break;
         n += nt;
       }
@@ -727,13 +770,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     // ---- softmax: thread = score row of tile x
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int x = (warp - 4) >> 2, quarter = warp & 3;
-    const int rho = quarter * 32 + lane, pl = div_g(a, rho), place = 2 * x + rank;   // place: of the row tile in the unit
+    const int rho = quarter * 32 + lane, pl = div_g(a, rho);
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_tm = tmem + lane_base + x * 128, o_tm = tmem + lane_base + 256 + x * DP;
     const uint32_t ready = at_rank(p_ready, 0) + 16 * x;
-    uint8_t* out = obuf + (warp - 4) * 4096;
+    uint8_t* obox = obuf + x * Cfg::OTILE;   // the tile's boxes of output
     uint32_t seen = 0, ends = 0;
-    bool ok = true;
+    bool ok = true, stored = false;
     Segment s;
     while (true) {
       if (!__all_sync(kAll, next_segment(s))) {
@@ -743,10 +786,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       __syncwarp();
       if (lane == 0) release_segment();
       if (s.end) break;
-      const int mine = x ? s.nt_b : s.nt_a;
-      if (x && mine == 0) continue;
+      const int mine = x ? s.nt_b : s.nt_a, step = 1 + s.split, t_mine = s.t0 + (s.split & (x ^ 1));
+      const int place = s.split ? rank : 2 * x + rank;   // of the row tile in the unit
       const int tok = place * p.per + pl, own = s.pos + min(tok, s.ntok - 1);   // this row's token; its position (a row of none: the last's)
-      const bool real = pl < p.per && tok < s.ntok;
       const int32_t* table = PAGED ? b.page_table + static_cast<int64_t>(s.seq) * b.table_stride : nullptr;
       auto page_bad = [&](int t) {   // the page of this lane's 8 keys of tile t lies outside the cache
         const bool pre = t < np;
@@ -756,15 +798,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         return id < 0 || id >= c.n_pages;
       };
       float m = -INFINITY, l = 0.f;
-      bool bad = PAGED && mine > 0 && page_bad(s.t0);
+      bool bad = PAGED && mine > 0 && page_bad(t_mine);
       for (int i = 0; i < mine; ++i) {
-        const int t = s.t0 + i;
+        const int t = t_mine + i * step;
         const unsigned bad8 = PAGED ? __ballot_sync(kAll, bad) : 0u;
-        if constexpr (PAGED) bad = i + 1 < mine && page_bad(t + 1);
-        if (!__all_sync(kAll, mbar_wait(&s_full[x], seen++ & 1))) {
-          ok = false;
-          break;
-        }
+        if constexpr (PAGED) bad = i + 1 < mine && page_bad(t + step);
+        ok = ok && __all_sync(kAll, mbar_wait(&s_full[x], seen++ & 1));   // a warp whose wait ran out still meets the others
         tc_fence_after();
         float sv[kTileKeys];
         tmem_ld128(s_tm, sv);
@@ -772,15 +811,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         const bool pre = t < np;
         const int last = pre ? b.prefix_len : own + 1, high = last - (pre ? t : t - np) * kTileKeys;
         const int low = p.window ? (pre ? b.prefix_len : 0) + own + 1 - p.window - (pre ? t : t - np) * kTileKeys : 0;
-        if (__any_sync(kAll, high < kTileKeys || low > 0)) {
+        if (__any_sync(kAll, high < kTileKeys || low > 0 || bad8)) {
+          // one bit to each key: comparisons of every key with both ends took 1500 cycles
 #pragma unroll
-          for (int j = 0; j < kTileKeys; ++j)
-            if (j >= high || j < low) sv[j] = -INFINITY;
-        }
-        if (bad8) {
+          for (int w = 0; w < kTileKeys / 32; ++w) {
+            uint32_t see = bits_below(high - 32 * w) & ~bits_below(low - 32 * w);
+            if constexpr (PAGED) see &= ~bytes_of(bad8 >> (4 * w));
 #pragma unroll
-          for (int j = 0; j < kTileKeys; ++j)
-            if (bad8 >> (j / 8) & 1) sv[j] = -INFINITY;
+            for (int j = 0; j < 32; ++j)
+              if (!(see >> j & 1u)) sv[32 * w + j] = -INFINITY;
+          }
         }
         float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
@@ -809,9 +849,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
           m = m_new;
         }
         // The weights leave in two halves, so that P V of the first 64 keys runs under the powers of the others.
-        // A weight takes the place of its logit: with the first half weighed before the maximum was
-        // known, and kept in case it had moved, registers left few powers under way at a time
-        // (1200 cycles to the weights of a tile).
         const float base = m == -INFINITY ? 0.f : -m;
         const Pair scale2 = make_pair2(a.scale_log2, a.scale_log2), base2 = make_pair2(base, base);
         Pair sum[2];
@@ -841,71 +878,152 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         split(add2(sum[0], sum[1]), l0, l1);
         l += l0 + l1;
       }
-      if (!ok) break;
 
-      // ---- the unit's output, through 4 KB of shared memory so that whole lines leave
+      // ---- the unit's output
+      const int rows = min(max(s.ntok - place * p.per, 0), p.per) * a.G;   // score rows of this CTA's tile
+      const bool cut = s.slot >= 0, real = rho < rows;
+      const bool whole = rows == p.per * a.G && rows > 96 && !cut;         // so all four warps have rows
+      const int64_t first = static_cast<int64_t>(s.row0 + place * p.per) * a.Hq + s.g * a.G;                // head of score row 0
+      const int64_t part = (static_cast<int64_t>(pair) * 2 + s.slot) * kTileRows + place * p.per * a.G;     // cut: rows of the unit in order
+      uint8_t* out = obox + quarter * 32 * 128;   // this warp's rows of the first box
+      if (stored) {   // the stores of the unit before have read the boxes
+        if (rho == 0) bulk_wait_read0();
+        bar_sync(1 + x, 128);
+        stored = false;
+      }
+      auto leave = [&] {   // statistics, of the whole unit or this part of it
+        if (!real) return;
+        if (cut)
+          parts.ml[part + rho] = make_float2(m, l);
+        else if (a.lse)
+          a.lse[first + static_cast<int64_t>(pl) * a.Hq + rho - pl * a.G] = (m + log2f(l)) * 0.69314718055994531f;
+      };
       if (mine > 0) {
-        if (!__all_sync(kAll, mbar_wait(&o_done[x], ends++ & 1))) {
-          ok = false;
-          break;
-        }
+        ok = ok && __all_sync(kAll, mbar_wait(&o_done[x], ends++ & 1));
         tc_fence_after();
       }
-      const int rows = min(max(s.ntok - place * p.per, 0), p.per) * a.G;   // score rows of this CTA's tile
-      if (s.slot >= 0) {
-        const int64_t at = (static_cast<int64_t>(pair) * 2 + s.slot) * kTileRows + place * p.per * a.G;   // rows of the unit in order
-        if (real) parts.ml[at + rho] = make_float2(m, l);
-        if (mine > 0) {
-#pragma unroll 1
-          for (int cc = 0; cc < DP / 32; ++cc) {
-            float ov[32];
-            tmem_ld32(o_tm + cc * 32, ov);
+      if (rows <= quarter * 32) continue;   // none of this warp's (in a's as in b's of the same rows)
+      if (!cut && !s.split) {
+        leave();
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        float ov[DP];
+        if constexpr (DP == 128) tmem_ld128(o_tm, ov); else tmem_ld64(o_tm, ov);
+        tc_fence_before();
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<float4*>(out + sw128_off(lane, e)) = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int r = e * 4 + (lane >> 3), row = quarter * 32 + r, col = cc * 32 + (lane & 7) * 4;
-              if (row < rows && col < p.D)
-                *reinterpret_cast<float4*>(parts.o + (at + row) * p.D + col) = *reinterpret_cast<const float4*>(out + sw128_off(r, lane & 7));
-            }
-            __syncwarp();
-          }
+        for (int e = 0; e < DP / 8; ++e) {
+          uint4 w;
+          w.x = pack2<T>(ov[8 * e] * inv, ov[8 * e + 1] * inv);
+          w.y = pack2<T>(ov[8 * e + 2] * inv, ov[8 * e + 3] * inv);
+          w.z = pack2<T>(ov[8 * e + 4] * inv, ov[8 * e + 5] * inv);
+          w.w = pack2<T>(ov[8 * e + 6] * inv, ov[8 * e + 7] * inv);
+          *reinterpret_cast<uint4*>(out + (e >> 3) * Cfg::OBOX + sw128_off(lane, e & 7)) = w;
         }
       } else {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t first = static_cast<int64_t>(s.row0 + place * p.per) * a.Hq + s.g * a.G;   // head of score row 0
-        if (a.lse && real) a.lse[first + static_cast<int64_t>(pl) * a.Hq + rho - pl * a.G] = (m + log2f(l)) * 0.69314718055994531f;
+        // a's rows of a split unit go to b, 32 bits each, half of the columns at a time; sums of a cut unit to the parts
+        constexpr int WIDE = DP / 2;
+        float mine_f = 1.f, other_f = 0.f;
+        const bool donor = s.split && x == 0;
+        const uint8_t* theirs = obuf + quarter * 32 * 128;
+        if (donor) donated[rho] = make_float2(m, l);
 #pragma unroll 1
-        for (int cc = 0; cc < DP / 64; ++cc) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float ov[32];
-            tmem_ld32(o_tm + cc * 64 + h * 32, ov);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint4 w;
-              w.x = pack2<T>(ov[8 * e] * inv, ov[8 * e + 1] * inv);
-              w.y = pack2<T>(ov[8 * e + 2] * inv, ov[8 * e + 3] * inv);
-              w.z = pack2<T>(ov[8 * e + 4] * inv, ov[8 * e + 5] * inv);
-              w.w = pack2<T>(ov[8 * e + 6] * inv, ov[8 * e + 7] * inv);
-              *reinterpret_cast<uint4*>(out + sw128_off(lane, h * 4 + e)) = w;
+        for (int cc = 0; cc < 2; ++cc) {
+          if (s.split && !donor) {
+            bar_sync(3 + quarter, 64);
+            if (cc == 0) {
+              const float2 ml = donated[rho];
+              const float top = fmaxf(m, ml.x);
+              mine_f = m == -INFINITY ? 0.f : fast_exp2(m - top);
+              other_f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top);
+              l = l * (m == -INFINITY ? 1.f : mine_f) + ml.y * (ml.x == -INFINITY ? 1.f : other_f);   // without keys: 0, or NaN
+              m = top;
             }
           }
-          __syncwarp();
+          if (cc == 0 && !donor) {
+            leave();
+            if (!cut) {
+              const float inv = l == 0.f ? 0.f : 1.f / l;
+              mine_f *= inv;
+              other_f *= inv;
+            }
+          }
+#pragma unroll 1
+          for (int h = 0; h < WIDE / 32; ++h) {
+            const int col0 = cc * WIDE + h * 32;
+            float ov[32];
+            if (mine > 0) {
+              tmem_ld32(o_tm + col0, ov);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] = 0.f;
+            }
+            if (s.split && !donor) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 v = *reinterpret_cast<const float4*>(theirs + h * Cfg::OBOX + sw128_off(lane, e));
+                ov[4 * e] = fmaf(ov[4 * e], mine_f, v.x * other_f);
+                ov[4 * e + 1] = fmaf(ov[4 * e + 1], mine_f, v.y * other_f);
+                ov[4 * e + 2] = fmaf(ov[4 * e + 2], mine_f, v.z * other_f);
+                ov[4 * e + 3] = fmaf(ov[4 * e + 3], mine_f, v.w * other_f);
+              }
+            }
+            if (donor || cut) {
+              uint8_t* to = out + (donor ? h * Cfg::OBOX : 0);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<float4*>(to + sw128_off(lane, e)) = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+              if (!donor) {
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const int r = e * 4 + (lane >> 3), row = quarter * 32 + r, col = col0 + (lane & 7) * 4;
+                  if (row < rows && col < p.D)
+                    *reinterpret_cast<float4*>(parts.o + (part + row) * p.D + col) = *reinterpret_cast<const float4*>(to + sw128_off(r, lane & 7));
+                }
+                __syncwarp();
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint4 w;
+                w.x = pack2<T>(ov[8 * e], ov[8 * e + 1]);
+                w.y = pack2<T>(ov[8 * e + 2], ov[8 * e + 3]);
+                w.z = pack2<T>(ov[8 * e + 4], ov[8 * e + 5]);
+                w.w = pack2<T>(ov[8 * e + 6], ov[8 * e + 7]);
+                *reinterpret_cast<uint4*>(out + (col0 >> 6) * Cfg::OBOX + sw128_off(lane, (col0 >> 3 & 7) + e)) = w;
+              }
+            }
+          }
+          if (donor) bar_sync(3 + quarter, 64);     // written
+          if (s.split) bar_sync(3 + quarter, 64);   // read
+        }
+        tc_fence_before();
+        if (donor || cut) continue;
+      }
+      if (whole) {   // every row of the tile: tiled stores, which run on while the next unit does
+        fence_proxy_async_smem();
+        bar_sync(1 + x, 128);
+        if (rho == 0) {
+#pragma unroll
+          for (int h = 0; h < Cfg::BOXES; ++h)
+            tma_store_3d(&tmO, obox + h * Cfg::OBOX, h * 64, s.g * a.G, s.row0 + place * p.per);
+          bulk_commit_group();
+        }
+        stored = true;
+      } else {       // rows behind the sequence's end belong to others
+        __syncwarp();
+#pragma unroll 1
+        for (int h = 0; h < Cfg::BOXES; ++h)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int r = e * 4 + (lane >> 3), row = quarter * 32 + r, col = cc * 64 + (lane & 7) * 8, tl = div_g(a, row);
+            const int r = e * 4 + (lane >> 3), row = quarter * 32 + r, col = h * 64 + (lane & 7) * 8, tl = div_g(a, row);
             if (row < rows && col < p.D)
               *reinterpret_cast<uint4*>(static_cast<T*>(a.o) + (first + static_cast<int64_t>(tl) * a.Hq + row - tl * a.G) * p.D + col) =
-                  *reinterpret_cast<const uint4*>(out + sw128_off(r, lane & 7));
+                  *reinterpret_cast<const uint4*>(out + h * Cfg::OBOX + sw128_off(r, lane & 7));
           }
-          __syncwarp();
-        }
+        __syncwarp();
       }
-      tc_fence_before();
     }
+    if (rho == 0) bulk_wait_group0();   // the stores are done before this kernel counts as complete
     if (!ok && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
   }
   tc_fence_before();
@@ -970,14 +1088,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tile_join_kernel(const ChunkA
 
 // ------------------------------------------------------------------ host
 
-static int tile_pairs() { return std::max(1, num_sms() / 2); }
-
+// Key tiles of a unit at most.
+static int64_t most_tiles(const BatchView& b) {
+  return (static_cast<int64_t>(b.prefix_len) + kTileKeys - 1) / kTileKeys + (static_cast<int64_t>(b.max_len) + kTileKeys - 1) / kTileKeys;
+}
 // Whether the bounds allow a unit long enough to be cut.
 static bool may_cut(const BatchView& b, int window) {
-  int64_t tiles = (static_cast<int64_t>(b.prefix_len) + kTileKeys - 1) / kTileKeys + (static_cast<int64_t>(b.max_len) + kTileKeys - 1) / kTileKeys;
+  int64_t tiles = most_tiles(b);
   if (window) tiles = std::min(tiles, (static_cast<int64_t>(window) + kTileRows + kTileKeys - 1) / kTileKeys + 2);
   return tiles >= 2 * kMinCut;
 }
+
+static int tile_pairs() { return std::max(1, num_sms() / 2); }
 
 static size_t parts_layout(const BatchView& b, int D, int window, void* base, ChunkParts* w) {
   *w = ChunkParts{};
@@ -1007,12 +1129,13 @@ template <typename T, int DP, bool PAGED>
 static qcf_status tile_launch(const char* who, const ChunkSource& src, const PagedView& c, const BatchView& b, const ChunkArgs& p, const ChunkParts& w,
                               cudaStream_t st) {
   using Cfg = TileCfg<DP>;
-  CUtensorMap tk, tv, tq;
+  CUtensorMap tk, tv, tq, to;
   const CUtensorMapSwizzle v_swizzle = Cfg::VCOLS == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   const uint64_t qd[3] = {static_cast<uint64_t>(p.D), static_cast<uint64_t>(p.a.Hq), static_cast<uint64_t>(b.n_rows)};
   const uint64_t qs[2] = {static_cast<uint64_t>(p.D) * 2, static_cast<uint64_t>(p.a.q_stride) * 2};
   const uint32_t qb[3] = {64, static_cast<uint32_t>(p.a.G), static_cast<uint32_t>(p.per)};
-  bool ok = encode_tmap_3d(&tq, p.a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B);
+  const uint64_t os[2] = {static_cast<uint64_t>(p.D) * 2, static_cast<uint64_t>(p.a.Hq) * p.D * 2};
+  bool ok = encode_tmap_3d(&tq, p.a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B) && encode_tmap_3d(&to, p.a.o, qd, os, qb, CU_TENSOR_MAP_SWIZZLE_128B);
   if (PAGED) {
     ok = ok && encode_pages(&tk, src.k, c, std::min(1 << c.page_shift, 64), 64, CU_TENSOR_MAP_SWIZZLE_128B) &&
          encode_pages(&tv, src.v, c, std::min(1 << c.page_shift, kTileKeys), Cfg::VCOLS, v_swizzle);
@@ -1030,8 +1153,9 @@ static qcf_status tile_launch(const char* who, const ChunkSource& src, const Pag
   if (e != cudaSuccess) return cuda_error(e, who);
   {
     LaunchScope ls(KC_CHUNK_ATTN, st);
-    tile_attn_kernel<T, DP, PAGED><<<2 * tile_pairs(), kTileThreads, Cfg::SMEM, st>>>(tk, tv, tq, c, b, p, w, device_status_ptr());
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_error(e, who);
+    e = launch_pdl(tile_attn_kernel<T, DP, PAGED>, dim3(2 * tile_pairs()), dim3(kTileThreads), Cfg::SMEM, st, tk, tv, tq, to, c, b, p, w,
+                   device_status_ptr());
+    if (e != cudaSuccess) return cuda_error(e, who);
   }
   if (!w.rec) return QCF_OK;
   LaunchScope ls(KC_CHUNK_JOIN, st);
@@ -1057,6 +1181,11 @@ static qcf_status check_sizes(const char* who, const PagedView& c, const BatchVi
   if (Hq <= 0 || Hq % c.Hkv || Hq / c.Hkv > 128) return set_error(QCF_ERR_SHAPE, "%s: Hq=%d Hkv=%d", who, Hq, c.Hkv);
   if (static_cast<int64_t>(b.n_rows) * Hq > INT32_MAX / 128)
     return set_error(QCF_ERR_SHAPE, "%s: %d rows of %d heads are too many for one call", who, b.n_rows, Hq);
+  // the deal counts costs in 31 bits, with room for a share more
+  const int R = 4 * (128 / (Hq / c.Hkv));
+  const double blocks = std::min(static_cast<double>(b.n_seq) * ((std::min(b.max_q, b.n_rows) + R - 1) / R), static_cast<double>(b.n_rows) / R + b.n_seq);
+  if (blocks * c.Hkv * (kUnitCost + kTileCost2 * static_cast<double>(most_tiles(b))) > INT32_MAX / 2)
+    return set_error(QCF_ERR_SHAPE, "%s: the bounds allow more work than one call takes", who);
   return QCF_OK;
 }
 
