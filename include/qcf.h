@@ -622,7 +622,8 @@ qcf_status qcf_shared_prefix_attn(const qcf_paged_kv* cache, const qcf_paged_bat
  *   ws      device scratch of the matching *_workspace_size() bytes (0: ws may be NULL); it needs
  *           no clearing; calls that overlap on the GPU (captured graphs replayed side by side
  *           among them) need separate scratch
- * scale > 0; n_seq <= 16384; n_rows Hq < 2^24 (QCF_ERR_SHAPE).  Products in the type of q with fp32
+ * scale > 0; n_seq <= 8000; n_rows Hq < 2^24; bounds that allow more than about 2^28 key tiles of
+ * 128 for 512 score rows each are refused (QCF_ERR_SHAPE).  Products in the type of q with fp32
  * sums, softmax in fp32.  Results repeat bitwise for the same inputs and bounds.  A NaN in a query
  * stays in its row and head; a key or value that holds NaN or infinity may spoil every row of its
  * own sequence (a prefix token: of the batch), masked or not, and no other. */

@@ -21,8 +21,8 @@
 //   warps 4-7   softmax of a, warps 8-11 of b: thread = score row of this CTA; the weights back to tensor
 //               memory over the scores they came from, the output rescaled only when a row's maximum
 //               grows by more than 2^8; the unit's output at its end
-// A unit with rows in a alone (single tokens, short questions) takes its key tiles by turns: b has the
-// even ones and a the odd ones of the same rows, and the output joins the two.
+// A unit with rows in a alone (single tokens, short questions) takes its key tiles by turns: a has the
+// even ones and b the odd ones of the same rows, and the output joins the two.
 // Tensor memory columns: S_a 0, S_b 128 (the weights take the first 64 of each), O_a 256, O_b 256 + DP.
 #include <algorithm>
 #include <cmath>
@@ -31,7 +31,7 @@
 
 namespace qcf {
 
-constexpr int kMaxChunkSeqs = 16384;
+constexpr int kMaxChunkSeqs = 8000;   // the deal keeps 12 bytes of each where the rings will be
 constexpr int kTileKeys = 128;
 constexpr int kTileThreads = 384;
 constexpr int kTileRows = 512;        // score rows of a unit
@@ -49,7 +49,7 @@ struct ChunkArgs {
 struct ChunkParts {     // units cut through: each pair may leave the end of one and the beginning of another
   int4* rec;            // [pairs]: parts of the unit that begins here and ends elsewhere (0: none), its first row, rows, KV head
   float2* ml;           // [pairs][2][kTileRows]
-  float* o;             // [pairs][2][kTileRows][D]
+  float* o;             // [pairs][2][kTileRows][D]; rows of a unit: 128 to each of its row tiles
 };
 
 template <int DP>
@@ -59,7 +59,7 @@ struct TileCfg {
   static constexpr int KBOX = 64 * 128, KTILE = BOXES * KBOX;           // its 64 keys
   static constexpr int VCOLS = DP / 2, VTILE = kTileKeys * VCOLS * 2;   // its columns of 128 values
   static constexpr int STAGES = DP == 128 ? 3 : 8;
-  static constexpr int OBOX = 128 * 128, OTILE = BOXES * OBOX;          // output of 128 score rows, 64 columns to a box
+  static constexpr int OBOX = 128 * 128, OTILE = 2 * OBOX;              // output of 128 score rows, 128 bytes of each to a box
   static constexpr int FIXED = 3072;
   static constexpr int SMEM = 2 * QTILE + STAGES * (KTILE + VTILE) + 2 * OTILE + FIXED;
 };
@@ -124,6 +124,10 @@ __device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.
 // Eight bits for each of the lowest four.
 __device__ __forceinline__ uint32_t bytes_of(unsigned b) {
   return (b & 1u) * 0xffu | (b >> 1 & 1u) * 0xff00u | (b >> 2 & 1u) * 0xff0000u | (b >> 3 & 1u) * 0xff000000u;
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
 }
 // The lowest n bits, none below 0 and all from 32 on.
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
@@ -214,6 +218,8 @@ __device__ __forceinline__ int cut_at(const RowBlock& k, int per, int x) {
 struct DealStart {
   int seq, block;       // seq -1: nothing for this pair
   int pos, share;       // cost before the row block
+  int row0, nq, len;    // of the sequence
+  int unused;
 };
 
 // One unit, or the part of one, of this pair.
@@ -221,7 +227,7 @@ struct Segment {
   int seq, row0, ntok, g;      // its first row in the batch, its tokens
   int pos, len;                // own position of its first token; own tokens of the sequence
   int t0, nt, nt_a, nt_b;      // first key tile, tiles, those of row tiles a and b
-  int split;                   // 1: no rows in b, so it takes the even tiles of a's rows, a the odd ones
+  int split;                   // 1: no rows in b, so it takes the odd tiles of a's rows, a the even ones
   int slot;                    // -1: the whole unit, else where its sums go
   int end;                     // 1: there are no more
 };
@@ -251,18 +257,22 @@ __device__ __forceinline__ int deal_scan(int tid, int v, int* met, int* total) {
   return before;
 }
 
-// Finds where this pair's share begins; blk: scratch for n_seq + 1 ints.
+// Finds where this pair's share begins; blk: scratch for 3 n_seq + 1 ints.
 __device__ void find_share(int tid, const BatchView& b, const ChunkArgs& p, int Hkv, int pair, int pairs, int* blk, int* met, DealStart* start,
                            unsigned int* status) {
   const int R = 4 * p.per, most = b.n_rows / R + b.n_seq;   // row blocks at most
   const int per_s = (b.n_seq + kDealThreads - 1) / kDealThreads;
   const int s0 = min(b.n_seq, tid * per_s), s1 = min(b.n_seq, s0 + per_s);
+  int* nqs = blk + b.n_seq + 1;
+  int* lens = nqs + b.n_seq;
   int mine = 0, all, total;
   for (int s = s0; s < s1; ++s) {
     const SeqSpan q = chunk_span(b, s);
     if (q.bad && blockIdx.x == 0) flag_status(status, QCF_DEV_BAD_INDEX);
     const int n = (q.nq + R - 1) / R;
     blk[s] = n;
+    nqs[s] = q.nq;
+    lens[s] = q.len;
     mine = min(mine + n, most + 1);
   }
   int at = deal_scan(tid, mine, met, &all);   // no overflow: 256 (most + 1) < 2^31
@@ -293,16 +303,9 @@ __device__ void find_share(int tid, const BatchView& b, const ChunkArgs& p, int 
   // visit(seq, block of it, cost of the block's units)
   auto walk = [&](auto visit) {
     int seq = first;
-    SeqSpan q = {};
-    bool known = false;
     for (int i = b0; i < b1; ++i) {
-      while (i >= blk[seq + 1]) {
-        ++seq;
-        known = false;
-      }
-      if (!known) q = chunk_span(b, seq);
-      known = true;
-      if (visit(seq, i - blk[seq], Hkv * unit_cost(row_block(b, p, q.nq, q.len, i - blk[seq]), p.per))) return;
+      while (i >= blk[seq + 1]) ++seq;
+      if (visit(seq, i - blk[seq], Hkv * unit_cost(row_block(b, p, nqs[seq], lens[seq], i - blk[seq]), p.per))) return;
     }
   };
   int cost = 0;
@@ -319,7 +322,7 @@ __device__ void find_share(int tid, const BatchView& b, const ChunkArgs& p, int 
         pos += c;
         return false;
       }
-      *start = DealStart{seq, i, pos, share};
+      *start = DealStart{seq, i, pos, share, b.row_start[seq], nqs[seq], lens[seq], 0};
       return true;
     });
 }
@@ -364,7 +367,9 @@ struct TileWalk {
     block = at.block;
     my_row0 = my_len = 0;
     keep(seq);
-    enter();
+    row0 = at.row0;
+    nq = at.nq;
+    len = at.len;
     k = row_block(b, p, nq, len, block);
     g = (begin - pos) / unit_cost(k, p.per);
     pos += g * unit_cost(k, p.per);
@@ -403,8 +408,8 @@ struct TileWalk {
         s.t0 = k.t0 + from;
         s.nt = to - from;
         s.split = !two;
-        s.nt_a = two ? max(0, min(k.end_a - k.t0, to) - from) : s.nt / 2;
-        s.nt_b = s.nt - (two ? 0 : s.nt_a);
+        s.nt_a = two ? max(0, min(k.end_a - k.t0, to) - from) : (s.nt + 1) / 2;
+        s.nt_b = two ? s.nt : s.nt / 2;
         s.slot = from == 0 && to == n ? -1 : from > 0 ? 0 : 1;
         s.end = 0;
         if (s.slot == 1) {   // how many borders cut this unit: those of the pairs behind this one
@@ -443,7 +448,7 @@ constexpr uint32_t idesc_pair(int N, bool b_mn_major) {
 template <typename T, int DP, bool PAGED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     tile_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ,
-                     const __grid_constant__ CUtensorMap tmO, const PagedView c, const BatchView b, const ChunkArgs p, const ChunkParts parts,
+                     const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmP, const PagedView c, const BatchView b, const ChunkArgs p, const ChunkParts parts,
                      unsigned int* status) {
   using Cfg = TileCfg<DP>;
   constexpr int ST = Cfg::STAGES;
@@ -532,8 +537,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   auto release_segment = [&] { mbar_arrive(&seg_empty[(seg_n - 1) % kSegRing]); };
 
   if (warp < 4) {
-    // 104 x 128 + 200 x 256 threads: the 168 x 384 registers of the launch
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    // 88 x 128 + 208 x 256 threads: the 168 x 384 registers of the launch
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0 || warp == 2) {
       // ---- the walk, K and Q; V
       const bool is_k = warp == 0;
@@ -674,7 +679,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(qbuf + x * Cfg::QTILE));
       const uint64_t k_desc = sdesc_kmajor_sw128(smem_u32(kbuf));
       const uint64_t v_desc = DP == 128 ? sdesc_mnmajor_sw128(smem_u32(vbuf), 16) : sdesc_mnmajor_sw64(smem_u32(vbuf));
-      const uint32_t k_empty1 = at_rank(k_empty, 1), v_empty1 = at_rank(v_empty, 1), q_empty1 = at_rank(q_empty, 1);
+      const uint32_t q_empty1 = at_rank(q_empty, 1);
       // The turn: the barrier of a tile's first weights also counts one arrival of the other issuer,
       // made four products (256 cycles) before the end of its block, which covers what this warp
       // then takes to see it.
@@ -705,21 +710,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         const int t0 = __shfl_sync(kAll, s.t0, 0), nt = __shfl_sync(kAll, s.nt, 0), len = __shfl_sync(kAll, s.len, 0);
         const int nt_a = __shfl_sync(kAll, s.nt_a, 0), nt_b = __shfl_sync(kAll, s.nt_b, 0), mine = x ? nt_b : nt_a;
         const int split = __shfl_sync(kAll, s.split, 0), step = 1 + split;
-        auto hand_on = [&](int tile) {   // one that the other row tile alone takes
-          if (!(wait_k(tile) && wait_v(tile))) return false;
-          const int st = tile % ST;
-          if (one) {
-            mbar_arrive(&k_empty[st]);
-            mbar_arrive_at(k_empty1 + st * 8);
-            mbar_arrive(&v_empty[st]);
-            mbar_arrive_at(v_empty1 + st * 8);
-          }
+        if (!(ok = wait(q_full, k++ & 1))) break;
+        // Every use of a stage is emptied by both issuers, also by the one whose row tile does not see the tile: that
+        // one hands it on as soon as it is there.
+        auto hand_k = [&](int tile) {
+          if (!wait_k(tile)) return false;
+          umma_commit_pair(one, &k_empty[tile % ST]);
           return true;
         };
-        if (!(ok = wait(q_full, k++ & 1))) break;
-        int at = n;   // tile
-        if (split && x == 0) ok = hand_on(at++);
-        if (mine > 0 && ok) {
+        auto hand_v = [&](int tile) {
+          if (!wait_v(tile)) return false;
+          umma_commit_pair(one, &v_empty[tile % ST]);
+          return true;
+        };
+        auto hand = [&](int tile) { return tile >= n + nt || (hand_k(tile) && hand_v(tile)); };
+        const bool late = split && x;   // b's tiles of a split unit begin with the second
+        int at = n + late;              // tile
+        if (late && !(ok = hand_k(n))) break;
+        if (mine > 0) {
           if (!(ok = wait_k(at))) break;
           tc_fence_after();
           scores(at, false, mine == 1);
@@ -727,9 +735,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
           mbar_arrive(q_empty);
           mbar_arrive_at(q_empty1);
         }
-        for (int i = 0; i < mine && ok; ++i) {
+        if (late && !(ok = hand_v(n))) break;
+        if (split && !(ok = hand(at + 1))) break;
+        for (int i = 0; i < mine; ++i) {
           const bool more = i + 1 < mine;
-          if (!(ok = wait_v(at) && (!more || wait_k(at + step)))) break;
+          if (!(ok = wait_v(at))) break;
           const int t = t0 + at - n;
           if ((t < np ? b.prefix_len - t * kTileKeys : len - (t - np) * kTileKeys) < kTileKeys) fence_cluster();   // zeros of the V producers
           const uint64_t vd = v_desc + at % ST * (Cfg::VTILE >> 4);
@@ -741,25 +751,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
           };
           // a begins, b follows while a has tiles left; who is alone gives itself the turn
           if ((x == 0 ? i == 0 : i >= nt_a) && one) mbar_arrive(&p_ready[2 * x]);
-          const bool due = x == 0 || i + 1 < nt_a;
+          const bool due = x == 0 ? i < nt_b : i + 1 < nt_a;
           if (!(ok = wait(&p_ready[2 * x], used & 1))) break;
           weigh(0);
           if (!(ok = wait(&p_ready[2 * x + 1], used & 1))) break;
           weigh(1);
           ++used;
           if (more) {
+            if (!(ok = wait_k(at + step))) break;
             scores(at + step, due, i + 2 == mine);
           } else {
             pass(due);
             umma_commit_pair(one, &o_done[x]);
           }
           umma_commit_pair(one, &v_empty[at % ST]);   // after the scores: a commit costs more than a product
-          if (split && at + 1 < n + nt) ok = hand_on(at + 1);
+          if (split && more && !(ok = hand(at + 3))) break;
           at += step;
         }
         if (!ok) break;
         if (!split)
-          for (; at < n + nt && ok; ++at) ok = hand_on(at);
+          for (; at < n + nt && ok; ++at) ok = hand(at);
         if (!ok) break;
         n += nt;
       }
@@ -768,7 +779,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     }
   } else {
     // ---- softmax: thread = score row of tile x
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int x = (warp - 4) >> 2, quarter = warp & 3;
     const int rho = quarter * 32 + lane, pl = div_g(a, rho);
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
@@ -786,7 +797,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       __syncwarp();
       if (lane == 0) release_segment();
       if (s.end) break;
-      const int mine = x ? s.nt_b : s.nt_a, step = 1 + s.split, t_mine = s.t0 + (s.split & (x ^ 1));
+      const int mine = x ? s.nt_b : s.nt_a, step = 1 + s.split, t_mine = s.t0 + (s.split & x);
       const int place = s.split ? rank : 2 * x + rank;   // of the row tile in the unit
       const int tok = place * p.per + pl, own = s.pos + min(tok, s.ntok - 1);   // this row's token; its position (a row of none: the last's)
       const int32_t* table = PAGED ? b.page_table + static_cast<int64_t>(s.seq) * b.table_stride : nullptr;
@@ -881,125 +892,113 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
 
       // ---- the unit's output
       const int rows = min(max(s.ntok - place * p.per, 0), p.per) * a.G;   // score rows of this CTA's tile
-      const bool cut = s.slot >= 0, real = rho < rows;
-      const bool whole = rows == p.per * a.G && rows > 96 && !cut;         // so all four warps have rows
-      const int64_t first = static_cast<int64_t>(s.row0 + place * p.per) * a.Hq + s.g * a.G;                // head of score row 0
-      const int64_t part = (static_cast<int64_t>(pair) * 2 + s.slot) * kTileRows + place * p.per * a.G;     // cut: rows of the unit in order
+      const bool cut = s.slot >= 0, real = rho < rows, few = rows <= 32;
+      const bool tiled = !few && (cut || rows == p.per * a.G);             // stored by whole tiles, all four warps together
+      const int64_t first = static_cast<int64_t>(s.row0 + place * p.per) * a.Hq + s.g * a.G;            // head of score row 0
+      const int64_t part = ((static_cast<int64_t>(pair) * 2 + max(s.slot, 0)) * 4 + place) * 128;       // cut: row 0 of the tile's sums
       uint8_t* out = obox + quarter * 32 * 128;   // this warp's rows of the first box
-      if (stored) {   // the stores of the unit before have read the boxes
+      auto boxes_free = [&] {   // tiled stores have read the boxes
         if (rho == 0) bulk_wait_read0();
         bar_sync(1 + x, 128);
-        stored = false;
-      }
-      auto leave = [&] {   // statistics, of the whole unit or this part of it
-        if (!real) return;
-        if (cut)
-          parts.ml[part + rho] = make_float2(m, l);
-        else if (a.lse)
-          a.lse[first + static_cast<int64_t>(pl) * a.Hq + rho - pl * a.G] = (m + log2f(l)) * 0.69314718055994531f;
       };
+      if (stored) boxes_free();
+      stored = false;
       if (mine > 0) {
         ok = ok && __all_sync(kAll, mbar_wait(&o_done[x], ends++ & 1));
         tc_fence_after();
       }
-      if (rows <= quarter * 32) continue;   // none of this warp's (in a's as in b's of the same rows)
-      if (!cut && !s.split) {
-        leave();
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        float ov[DP];
-        if constexpr (DP == 128) tmem_ld128(o_tm, ov); else tmem_ld64(o_tm, ov);
-        tc_fence_before();
-#pragma unroll
-        for (int e = 0; e < DP / 8; ++e) {
-          uint4 w;
-          w.x = pack2<T>(ov[8 * e] * inv, ov[8 * e + 1] * inv);
-          w.y = pack2<T>(ov[8 * e + 2] * inv, ov[8 * e + 3] * inv);
-          w.z = pack2<T>(ov[8 * e + 4] * inv, ov[8 * e + 5] * inv);
-          w.w = pack2<T>(ov[8 * e + 6] * inv, ov[8 * e + 7] * inv);
-          *reinterpret_cast<uint4*>(out + (e >> 3) * Cfg::OBOX + sw128_off(lane, e & 7)) = w;
+      float mine_f = 1.f, other_f = 0.f;
+      if (s.split) {   // b takes a's sums, too
+        if (x == 0) {
+          donated[rho] = make_float2(m, l);
+          tc_fence_before();
+          bar_sync(3 + quarter, 64);
+          bar_sync(3 + quarter, 64);   // they have been read
+          continue;
         }
-      } else {
-        // a's rows of a split unit go to b, 32 bits each, half of the columns at a time; sums of a cut unit to the parts
-        constexpr int WIDE = DP / 2;
-        float mine_f = 1.f, other_f = 0.f;
-        const bool donor = s.split && x == 0;
-        const uint8_t* theirs = obuf + quarter * 32 * 128;
-        if (donor) donated[rho] = make_float2(m, l);
-#pragma unroll 1
-        for (int cc = 0; cc < 2; ++cc) {
-          if (s.split && !donor) {
-            bar_sync(3 + quarter, 64);
-            if (cc == 0) {
-              const float2 ml = donated[rho];
-              const float top = fmaxf(m, ml.x);
-              mine_f = m == -INFINITY ? 0.f : fast_exp2(m - top);
-              other_f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top);
-              l = l * (m == -INFINITY ? 1.f : mine_f) + ml.y * (ml.x == -INFINITY ? 1.f : other_f);   // without keys: 0, or NaN
-              m = top;
-            }
-          }
-          if (cc == 0 && !donor) {
-            leave();
-            if (!cut) {
-              const float inv = l == 0.f ? 0.f : 1.f / l;
-              mine_f *= inv;
-              other_f *= inv;
-            }
-          }
-#pragma unroll 1
-          for (int h = 0; h < WIDE / 32; ++h) {
-            const int col0 = cc * WIDE + h * 32;
-            float ov[32];
-            if (mine > 0) {
-              tmem_ld32(o_tm + col0, ov);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) ov[e] = 0.f;
-            }
-            if (s.split && !donor) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 v = *reinterpret_cast<const float4*>(theirs + h * Cfg::OBOX + sw128_off(lane, e));
-                ov[4 * e] = fmaf(ov[4 * e], mine_f, v.x * other_f);
-                ov[4 * e + 1] = fmaf(ov[4 * e + 1], mine_f, v.y * other_f);
-                ov[4 * e + 2] = fmaf(ov[4 * e + 2], mine_f, v.z * other_f);
-                ov[4 * e + 3] = fmaf(ov[4 * e + 3], mine_f, v.w * other_f);
-              }
-            }
-            if (donor || cut) {
-              uint8_t* to = out + (donor ? h * Cfg::OBOX : 0);
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<float4*>(to + sw128_off(lane, e)) = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
-              if (!donor) {
-                __syncwarp();
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const int r = e * 4 + (lane >> 3), row = quarter * 32 + r, col = col0 + (lane & 7) * 4;
-                  if (row < rows && col < p.D)
-                    *reinterpret_cast<float4*>(parts.o + (part + row) * p.D + col) = *reinterpret_cast<const float4*>(to + sw128_off(r, lane & 7));
-                }
-                __syncwarp();
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint4 w;
-                w.x = pack2<T>(ov[8 * e], ov[8 * e + 1]);
-                w.y = pack2<T>(ov[8 * e + 2], ov[8 * e + 3]);
-                w.z = pack2<T>(ov[8 * e + 4], ov[8 * e + 5]);
-                w.w = pack2<T>(ov[8 * e + 6], ov[8 * e + 7]);
-                *reinterpret_cast<uint4*>(out + (col0 >> 6) * Cfg::OBOX + sw128_off(lane, (col0 >> 3 & 7) + e)) = w;
-              }
-            }
-          }
-          if (donor) bar_sync(3 + quarter, 64);     // written
-          if (s.split) bar_sync(3 + quarter, 64);   // read
-        }
-        tc_fence_before();
-        if (donor || cut) continue;
+        bar_sync(3 + quarter, 64);
+        tc_fence_after();
+        const float2 ml = donated[rho];
+        const float top = fmaxf(m, ml.x);
+        mine_f = m == -INFINITY ? 0.f : fast_exp2(m - top);
+        other_f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top);
+        l = l * (m == -INFINITY ? 1.f : mine_f) + ml.y * (ml.x == -INFINITY ? 1.f : other_f);   // without keys: 0, or NaN
+        m = top;
       }
-      if (whole) {   // every row of the tile: tiled stores, which run on while the next unit does
+      if (real) {
+        if (cut)
+          parts.ml[part + rho] = make_float2(m, l);
+        else if (a.lse)
+          a.lse[first + static_cast<int64_t>(pl) * a.Hq + rho - pl * a.G] = (m + log2f(l)) * 0.69314718055994531f;
+      }
+      if (!cut) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        mine_f *= inv;
+        other_f *= inv;
+      }
+      stored = tiled;
+      if (rows <= quarter * 32) {   // none of this warp's, which still meets the others
+        if (s.split) bar_sync(3 + quarter, 64);
+        if (tiled) {
+          bar_sync(1 + x, 128);
+          if (cut && DP == 128) {
+            bar_sync(1 + x, 128);
+            bar_sync(1 + x, 128);
+          }
+        }
+        continue;
+      }
+#pragma unroll 1
+      for (int c0 = 0; c0 < DP; c0 += 64) {
+        float ov[64];
+        tmem_ld64(o_tm + c0, ov);
+        // nothing of b without a tile of its own, or where this part of a unit has none for a
+#pragma unroll
+        for (int e = 0; e < 64; ++e) ov[e] = mine > 0 ? ov[e] * mine_f : 0.f;
+        if (s.split) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            float oa[16];
+            tmem_ld16(tmem + lane_base + 256 + c0 + h * 16, oa);   // a has a tile at least
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ov[h * 16 + e] = fmaf(oa[e], other_f, ov[h * 16 + e]);
+          }
+        }
+        if (c0 + 64 >= DP) {
+          tc_fence_before();
+          if (s.split) bar_sync(3 + quarter, 64);
+        }
+        if (few) {   // rows go straight out
+          if (real && cut) {
+            float* o = parts.o + (part + rho) * p.D + c0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (c0 + e * 4 < p.D) *reinterpret_cast<float4*>(o + e * 4) = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+          } else if (real) {
+            T* o = static_cast<T*>(a.o) + (first + static_cast<int64_t>(pl) * a.Hq + rho - pl * a.G) * p.D + c0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (c0 + e * 8 < p.D) *reinterpret_cast<uint4*>(o + e * 8) = pack8<T>(ov + 8 * e);
+          }
+        } else if (cut) {   // 32 columns of 32 bits to a box
+          if (c0 > 0) boxes_free();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            *reinterpret_cast<float4*>(out + (e >> 3) * Cfg::OBOX + sw128_off(lane, e & 7)) = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+          fence_proxy_async_smem();
+          bar_sync(1 + x, 128);
+          if (rho == 0) {
+            tma_store_2d(&tmP, obox, c0, static_cast<int>(part));
+            if (c0 + 32 < p.D) tma_store_2d(&tmP, obox + Cfg::OBOX, c0 + 32, static_cast<int>(part));
+            bulk_commit_group();
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(out + (c0 >> 6) * Cfg::OBOX + sw128_off(lane, e)) = pack8<T>(ov + 8 * e);
+        }
+      }
+      if (few || cut) continue;
+      if (tiled) {   // every row of the tile: stores that run on while the next unit does
         fence_proxy_async_smem();
         bar_sync(1 + x, 128);
         if (rho == 0) {
@@ -1008,7 +1007,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             tma_store_3d(&tmO, obox + h * Cfg::OBOX, h * 64, s.g * a.G, s.row0 + place * p.per);
           bulk_commit_group();
         }
-        stored = true;
       } else {       // rows behind the sequence's end belong to others
         __syncwarp();
 #pragma unroll 1
@@ -1052,6 +1050,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tile_join_kernel(const ChunkA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool has = lane * 4 < p.D;
   for (int r = blockIdx.y * kJoinRows + warp; r < min(static_cast<int>(blockIdx.y + 1) * kJoinRows, rec.z * a.G); r += kJoinWarps) {
+    const int tok = div_g(a, r), tile = tok / p.per, in_unit = tile * 128 + r - tile * p.per * a.G;
     float M = -INFINITY, L = 0.f, sum[4] = {0.f, 0.f, 0.f, 0.f};
     constexpr int BATCH = 4;
     for (int i0 = 0; i0 < rec.x; i0 += BATCH) {
@@ -1060,7 +1059,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tile_join_kernel(const ChunkA
 #pragma unroll
       for (int j = 0; j < BATCH; ++j) {   // behind the end the last part again: loads without branches stay together
         const int i = min(i0 + j, rec.x - 1);
-        const int64_t at = (static_cast<int64_t>(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * kTileRows + r;
+        const int64_t at = (static_cast<int64_t>(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * kTileRows + in_unit;
         ml[j] = parts.ml[at];
         v[j] = *reinterpret_cast<const float4*>(parts.o + at * p.D + (has ? lane * 4 : 0));
       }
@@ -1077,7 +1076,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tile_join_kernel(const ChunkA
           sum[3] = fmaf(v[j].w, f, sum[3] * e);
         }
     }
-    const int tok = div_g(a, r);
     const int64_t at = static_cast<int64_t>(rec.y + tok) * a.Hq + rec.w * a.G + r - tok * a.G;
     const float inv = L == 0.f ? 0.f : 1.f / L;
     if (has)
@@ -1129,13 +1127,18 @@ template <typename T, int DP, bool PAGED>
 static qcf_status tile_launch(const char* who, const ChunkSource& src, const PagedView& c, const BatchView& b, const ChunkArgs& p, const ChunkParts& w,
                               cudaStream_t st) {
   using Cfg = TileCfg<DP>;
-  CUtensorMap tk, tv, tq, to;
+  CUtensorMap tk, tv, tq, to, tp;
   const CUtensorMapSwizzle v_swizzle = Cfg::VCOLS == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   const uint64_t qd[3] = {static_cast<uint64_t>(p.D), static_cast<uint64_t>(p.a.Hq), static_cast<uint64_t>(b.n_rows)};
   const uint64_t qs[2] = {static_cast<uint64_t>(p.D) * 2, static_cast<uint64_t>(p.a.q_stride) * 2};
   const uint32_t qb[3] = {64, static_cast<uint32_t>(p.a.G), static_cast<uint32_t>(p.per)};
   const uint64_t os[2] = {static_cast<uint64_t>(p.D) * 2, static_cast<uint64_t>(p.a.Hq) * p.D * 2};
   bool ok = encode_tmap_3d(&tq, p.a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B) && encode_tmap_3d(&to, p.a.o, qd, os, qb, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (w.rec)   // sums of the parts: rows of D columns, boxes of 128 rows and 32 columns
+    ok = ok && encode_tmap_2d(&tp, w.o, p.D, static_cast<uint64_t>(tile_pairs()) * 2 * kTileRows, static_cast<uint64_t>(p.D) * 4, 32, 128,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
+  else
+    tp = to;     // never used
   if (PAGED) {
     ok = ok && encode_pages(&tk, src.k, c, std::min(1 << c.page_shift, 64), 64, CU_TENSOR_MAP_SWIZZLE_128B) &&
          encode_pages(&tv, src.v, c, std::min(1 << c.page_shift, kTileKeys), Cfg::VCOLS, v_swizzle);
@@ -1153,7 +1156,7 @@ static qcf_status tile_launch(const char* who, const ChunkSource& src, const Pag
   if (e != cudaSuccess) return cuda_error(e, who);
   {
     LaunchScope ls(KC_CHUNK_ATTN, st);
-    e = launch_pdl(tile_attn_kernel<T, DP, PAGED>, dim3(2 * tile_pairs()), dim3(kTileThreads), Cfg::SMEM, st, tk, tv, tq, to, c, b, p, w,
+    e = launch_pdl(tile_attn_kernel<T, DP, PAGED>, dim3(2 * tile_pairs()), dim3(kTileThreads), Cfg::SMEM, st, tk, tv, tq, to, tp, c, b, p, w,
                    device_status_ptr());
     if (e != cudaSuccess) return cuda_error(e, who);
   }

@@ -22,7 +22,7 @@ SHARED = [(dict(q=None), ARG), (dict(o=None), ARG), (dict(scale=0.0), ARG), (dic
 
 @pytest.mark.parametrize("kw,expect", SHARED + [
     (dict(), OK), (dict(k=None), ARG), (dict(v=None), ARG), (dict(start=None), ARG), (dict(dtype=2), ARG), (dict(dtype=-1), ARG), (dict(n_seq=-1), SHAPE),
-    (dict(n_seq=16385), SHAPE), (dict(n_rows=-1), SHAPE), (dict(max_len=-1), SHAPE), (dict(n_rows=1 << 20), SHAPE), (dict(Hkv=0), SHAPE), (dict(D=0), SHAPE),
+    (dict(n_seq=8001), SHAPE), (dict(n_rows=-1), SHAPE), (dict(max_len=-1), SHAPE), (dict(n_rows=1 << 20), SHAPE), (dict(Hkv=0), SHAPE), (dict(D=0), SHAPE),
     (dict(D=12), SHAPE), (dict(D=136, qs=8192, kvs=8192), SHAPE), (dict(D=80), OK), (dict(D=8), OK), (dict(kvs=1016), SHAPE), (dict(kvs=1028), ALIGN), (dict(k=P + 8), ALIGN),
     (dict(v=P + 8), ALIGN)])
 def test_packed_arguments(L, kw, expect):  # noqa: F811
@@ -53,7 +53,7 @@ def test_chunk_arguments(L, kw, expect):  # noqa: F811
 
 def test_chunk_sizes(L):  # noqa: F811
     assert chunk(L, None, batch(L)) == ARG and chunk(L, cache(L), None) == ARG
-    assert chunk(L, cache(L), batch(L, n_seq=16385)) == SHAPE
+    assert chunk(L, cache(L), batch(L, n_seq=8001)) == SHAPE
     assert chunk(L, cache(L), batch(L, n_rows=1 << 20)) == SHAPE
 
 
