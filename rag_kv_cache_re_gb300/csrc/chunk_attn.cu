@@ -45,6 +45,7 @@ constexpr int kSegRing = 4;
 struct ChunkArgs {
   AttnArgs a;
   int D, window, per;   // per: tokens of a row tile
+  int group;            // sequences of at most so many new rows share a prefix as a group; 0: none does
 };
 struct ChunkParts {     // units cut through: each pair may leave the end of one and the beginning of another
   int4* rec;            // [pairs]: parts of the unit that begins here and ends elsewhere (0: none), its first row, rows, KV head
@@ -186,6 +187,47 @@ __device__ __forceinline__ uint64_t sdesc_mnmajor_sw64(uint32_t smem_addr) {
 // that falls into a unit cuts it between two key tiles, or is moved to its nearer end where fewer than
 // kMinCut tiles would lie on one side.
 
+// A run of sequences with a few new rows each (single tokens) within 32 aligned ones goes as a group: its
+// rows lie side by side in the batch and make one unit, which reads the shared prefix once for all of them and
+// then each one's own tiles, which the rows of the others do not see.  (44 single tokens of 32 heads over a prefix of 5120 tokens
+// among chunks of 2640: 423 us for the call with a unit to each.)  It stands in the place of its
+// first sequence; its length is kept as -1 - (32 own tiles + (sequences - 1)).
+struct Span {
+  int row0, nq, len;   // nq 0: no rows, or those of a group that began before
+};
+__device__ __forceinline__ int group_size(int len) { return ((-1 - len) & 31) + 1; }
+__device__ __forceinline__ int group_tiles(int len) { return (-1 - len) >> 5; }
+__device__ __forceinline__ int warp_scan(int v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (static_cast<int>(threadIdx.x & 31) >= o) v += u;
+  }
+  return v;
+}
+// Of sequence base + lane, base a multiple of 32; all lanes of a warp together.
+__device__ __forceinline__ Span span_at(const BatchView& b, const ChunkArgs& p, int base, bool* bad) {
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31, seq = base + lane;
+  SeqSpan q = {0, 0, 0, false};
+  if (seq < b.n_seq) q = chunk_span(b, seq);
+  *bad = q.bad;
+  Span s{q.row0, q.nq, q.len};
+  if (p.group == 0) return s;
+  const bool small = seq < b.n_seq && !q.bad && q.nq <= p.group;
+  const unsigned in = __ballot_sync(kAll, small), rows = __ballot_sync(kAll, small && q.nq > 0);
+  const int tiles = small && q.nq > 0 ? (q.len + kTileKeys - 1) / kTileKeys : 0;
+  const int nq_sum = warp_scan(small ? q.nq : 0), tile_sum = warp_scan(tiles);
+  const unsigned gap_below = ~in & ((1u << lane) - 1u), gap_above = ~in >> lane;
+  const int first = 32 - __clz(gap_below), end = gap_above ? lane + __ffs(gap_above) - 1 : 32;   // the run of this lane
+  const int nq_run = __shfl_sync(kAll, nq_sum, max(end - 1, 0)) - nq_sum + q.nq;
+  const int tile_run = __shfl_sync(kAll, tile_sum, max(end - 1, 0)) - tile_sum + tiles;
+  const unsigned run = small ? (0xffffffffu >> (32 - (end - first))) << first : 0u;
+  if (__popc(rows & run) < 2) return s;
+  if (lane == first) return Span{q.row0, nq_run, -1 - (tile_run * 32 + end - first - 1)};
+  return Span{q.row0, 0, q.len};
+}
+
 struct RowBlock {
   int i0, ntok;            // tokens of the sequence
   int t0, end, end_a;      // its key tiles; the end of row tile a's
@@ -198,6 +240,11 @@ __device__ __forceinline__ RowBlock row_block(const BatchView& b, const ChunkArg
   RowBlock k;
   k.i0 = i * 4 * p.per;
   k.ntok = min(4 * p.per, nq - k.i0);
+  if (len < 0) {
+    k.t0 = 0;
+    k.end = k.end_a = (b.prefix_len + kTileKeys - 1) / kTileKeys + group_tiles(len);
+    return k;
+  }
   const int pos = b.prefix_len + len - nq + k.i0;   // of its first token
   k.t0 = p.window ? tile_of(b.prefix_len, max(0, pos - p.window + 1)) : 0;
   k.end = tile_of(b.prefix_len, pos + k.ntok - 1) + 1;
@@ -218,14 +265,14 @@ __device__ __forceinline__ int cut_at(const RowBlock& k, int per, int x) {
 struct DealStart {
   int seq, block;       // seq -1: nothing for this pair
   int pos, share;       // cost before the row block
-  int row0, nq, len;    // of the sequence
+  int row0, nq, len;    // of the sequence or group
   int unused;
 };
 
 // One unit, or the part of one, of this pair.
 struct Segment {
   int seq, row0, ntok, g;      // its first row in the batch, its tokens
-  int pos, len;                // own position of its first token; own tokens of the sequence
+  int pos, len;                // own position of its first token; own tokens of the sequence (or a group's, see Span)
   int t0, nt, nt_a, nt_b;      // first key tile, tiles, those of row tiles a and b
   int split;                   // 1: no rows in b, so it takes the odd tiles of a's rows, a the even ones
   int slot;                    // -1: the whole unit, else where its sums go
@@ -266,15 +313,18 @@ __device__ void find_share(int tid, const BatchView& b, const ChunkArgs& p, int 
   int* nqs = blk + b.n_seq + 1;
   int* lens = nqs + b.n_seq;
   int mine = 0, all, total;
-  for (int s = s0; s < s1; ++s) {
-    const SeqSpan q = chunk_span(b, s);
-    if (q.bad && blockIdx.x == 0) flag_status(status, QCF_DEV_BAD_INDEX);
-    const int n = (q.nq + R - 1) / R;
-    blk[s] = n;
-    nqs[s] = q.nq;
-    lens[s] = q.len;
-    mine = min(mine + n, most + 1);
+  for (int s = tid; s - (tid & 31) < b.n_seq; s += kDealThreads) {
+    bool bad;
+    const Span q = span_at(b, p, s - (tid & 31), &bad);
+    if (bad && blockIdx.x == 0) flag_status(status, QCF_DEV_BAD_INDEX);
+    if (s < b.n_seq) {
+      blk[s] = (q.nq + R - 1) / R;
+      nqs[s] = q.nq;
+      lens[s] = q.len;
+    }
   }
+  deal_sync();
+  for (int s = s0; s < s1; ++s) mine = min(mine + blk[s], most + 1);
   int at = deal_scan(tid, mine, met, &all);   // no overflow: 256 (most + 1) < 2^31
   // more row blocks than the rows allow come only of sequences that overlap: nothing is done for them
   const bool over = all > most;
@@ -342,13 +392,11 @@ struct TileWalk {
 
   __device__ void keep(int from) {
     base = from;
-    my_nq = 0;
-    if (from + static_cast<int>(threadIdx.x & 31) < b.n_seq) {
-      const SeqSpan s = chunk_span(b, from + (threadIdx.x & 31));
-      my_row0 = s.row0;
-      my_nq = s.nq;
-      my_len = s.len;
-    }
+    bool bad;
+    const Span s = span_at(b, p, from, &bad);
+    my_row0 = s.row0;
+    my_nq = s.nq;
+    my_len = s.len;
   }
   __device__ void enter() {
     row0 = __shfl_sync(0xffffffffu, my_row0, seq - base);
@@ -365,8 +413,7 @@ struct TileWalk {
     stop = begin + share;
     seq = at.seq;
     block = at.block;
-    my_row0 = my_len = 0;
-    keep(seq);
+    keep(seq & ~31);
     row0 = at.row0;
     nq = at.nq;
     len = at.len;
@@ -403,7 +450,7 @@ struct TileWalk {
         s.row0 = row0 + k.i0;
         s.ntok = k.ntok;
         s.g = g;
-        s.pos = len - nq + k.i0;
+        s.pos = len < 0 ? 0 : len - nq + k.i0;
         s.len = len;
         s.t0 = k.t0 + from;
         s.nt = to - from;
@@ -536,6 +583,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   };
   auto release_segment = [&] { mbar_arrive(&seg_empty[(seg_n - 1) % kSegRing]); };
 
+  // The sequences of a grouped unit, one to a lane: own tokens, first own tile.
+  int sub_len = 0, sub_tile = 0;
+  auto open_group = [&](const Segment& s) {
+    if (!PAGED || s.len >= 0) return;
+    int tiles = 0;
+    if (lane < group_size(s.len)) {
+      const SeqSpan q = seq_span(b, s.seq + lane);
+      sub_len = q.len;
+      tiles = q.nq > 0 ? (q.len + kTileKeys - 1) / kTileKeys : 0;
+    }
+    sub_tile = warp_scan(tiles) - tiles;
+  };
+  struct KeyTile {
+    int seq;        // whose own tokens (-1: the prefix)
+    int key0, len;  // its first key; keys there are
+  };
+  auto key_tile = [&](const Segment& s, int t) {
+    if (t < np) return KeyTile{-1, t * kTileKeys, b.prefix_len};
+    if (!PAGED || s.len >= 0) return KeyTile{s.seq, (t - np) * kTileKeys, s.len};
+    const int sub = max(__popc(__ballot_sync(kAll, lane < group_size(s.len) && sub_tile <= t - np)) - 1, 0);
+    return KeyTile{s.seq + sub, (t - np - __shfl_sync(kAll, sub_tile, sub)) * kTileKeys, __shfl_sync(kAll, sub_len, sub)};
+  };
+  auto pages_of_tile = [&](const KeyTile& k) { return k.seq < 0 ? b.prefix_pages : b.page_table + static_cast<int64_t>(k.seq) * b.table_stride; };
+
   if (warp < 4) {
     // 88 x 128 + 208 x 256 threads: the 168 x 384 registers of the launch
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -577,28 +648,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
           if (lane == 0) release_segment();
         }
         if (s.end) break;
-        const int32_t* table = PAGED ? b.page_table + static_cast<int64_t>(s.seq) * b.table_stride : nullptr;
-        // this lane's page of tile t: its id, n_pages (which reads as zeros) where there is none
-        auto page_of = [&](int t) {
-          const bool pre = t < np;
-          const int key = (pre ? t : t - np) * kTileKeys + key0 + lane * rows;
-          if (lane >= boxes || key >= (pre ? b.prefix_len : s.len)) return c.n_pages;
-          const int id = (pre ? b.prefix_pages : table)[key >> c.page_shift];
+        open_group(s);
+        // this lane's page of a tile: its id, n_pages (which reads as zeros) where there is none
+        auto page_of = [&](const KeyTile& k) {
+          const int key = k.key0 + key0 + lane * rows;
+          if (lane >= boxes || key >= k.len) return c.n_pages;
+          const int id = pages_of_tile(k)[key >> c.page_shift];
           if (id >= 0 && id < c.n_pages) return id;
           flag_status(status, QCF_DEV_BAD_INDEX);
           return c.n_pages;
         };
-        int id = PAGED ? page_of(s.t0) : 0;
+        KeyTile ahead = key_tile(s, s.t0);
+        int next_id = PAGED ? page_of(ahead) : 0;
         for (int i = 0; i < s.nt; ++i, ++n) {
-          const int st = n % ST, t = s.t0 + i;
-          const int next_id = PAGED && i + 1 < s.nt ? page_of(t + 1) : 0;
+          const int st = n % ST, id = next_id;
+          const KeyTile k = ahead;
+          if (i + 1 < s.nt) {
+            ahead = key_tile(s, s.t0 + i + 1);
+            if (PAGED) next_id = page_of(ahead);
+          }
           if (!__all_sync(kAll, mbar_wait(&empty[st], ((n / ST) & 1) ^ 1u))) {
             ok = false;
             break;
           }
-          const bool pre = t < np;
-          const int tk = (pre ? t : t - np) * kTileKeys;   // first key of the tile
-          const int valid = (pre ? b.prefix_len : s.len) - tk;
+          const int tk = k.key0, valid = k.len - tk;
           const int stale = valid < kTileKeys ? (PAGED ? min(kTileKeys, (valid + rows - 1) / rows * rows) : kTileKeys) : valid;
           const bool tail = !is_k && stale > valid;        // rows of the tile that lie behind the end
           const uint32_t bar = tail ? at_rank(v_tail, rank) : full + st * 8;
@@ -621,7 +694,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                 tma_load_3d_pair(dst, &tmV, bar, rank * Cfg::VCOLS, s.g, s.row0 - s.pos + tk);
             }
           }
-          id = next_id;
           if (is_k && i == 0) {   // the unit's Q: rows behind the sequence belong to others or are zeros, and go nowhere
             if (!__all_sync(kAll, mbar_wait(q_empty, (units & 1) ^ 1u))) {
               ok = false;
@@ -707,9 +779,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         if (one) release_segment();
         if (s.end) break;
         // alike in all lanes, which the compiler cannot see in what comes from memory
-        const int t0 = __shfl_sync(kAll, s.t0, 0), nt = __shfl_sync(kAll, s.nt, 0), len = __shfl_sync(kAll, s.len, 0);
+        const int t0 = __shfl_sync(kAll, s.t0, 0), nt = __shfl_sync(kAll, s.nt, 0);
         const int nt_a = __shfl_sync(kAll, s.nt_a, 0), nt_b = __shfl_sync(kAll, s.nt_b, 0), mine = x ? nt_b : nt_a;
         const int split = __shfl_sync(kAll, s.split, 0), step = 1 + split;
+        open_group(s);
         if (!(ok = wait(q_full, k++ & 1))) break;
         // Every use of a stage is emptied by both issuers, also by the one whose row tile does not see the tile: that
         // one hands it on as soon as it is there.
@@ -740,8 +813,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         for (int i = 0; i < mine; ++i) {
           const bool more = i + 1 < mine;
           if (!(ok = wait_v(at))) break;
-          const int t = t0 + at - n;
-          if ((t < np ? b.prefix_len - t * kTileKeys : len - (t - np) * kTileKeys) < kTileKeys) fence_cluster();   // zeros of the V producers
+          const KeyTile kt = key_tile(s, t0 + at - n);
+          if (kt.len - kt.key0 < kTileKeys) fence_cluster();   // zeros of the V producers
           const uint64_t vd = v_desc + at % ST * (Cfg::VTILE >> 4);
           auto weigh = [&](int half) {   // O_x += P_x V over 64 keys
             tc_fence_after();
@@ -799,29 +872,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       if (s.end) break;
       const int mine = x ? s.nt_b : s.nt_a, step = 1 + s.split, t_mine = s.t0 + (s.split & x);
       const int place = s.split ? rank : 2 * x + rank;   // of the row tile in the unit
-      const int tok = place * p.per + pl, own = s.pos + min(tok, s.ntok - 1);   // this row's token; its position (a row of none: the last's)
-      const int32_t* table = PAGED ? b.page_table + static_cast<int64_t>(s.seq) * b.table_stride : nullptr;
-      auto page_bad = [&](int t) {   // the page of this lane's 8 keys of tile t lies outside the cache
-        const bool pre = t < np;
-        const int key = (pre ? t : t - np) * kTileKeys + lane * 8;
-        if (lane >= kTileKeys / 8 || key >= (pre ? b.prefix_len : s.len)) return false;
-        const int id = (pre ? b.prefix_pages : table)[key >> c.page_shift];
+      // this row's token, sequence and own position (a row of none: the last token's)
+      const int tok = place * p.per + pl;
+      int seq = s.seq, own = s.pos + min(tok, s.ntok - 1);
+      open_group(s);
+      if (PAGED && s.len < 0) {
+        int from = 0x7fffffff, nq = 0, sub = 0;   // of this lane's sequence: its first token in the group, its rows
+        if (lane < group_size(s.len)) {
+          from = b.row_start[s.seq + lane] - s.row0;
+          nq = b.row_start[s.seq + lane + 1] - s.row0 - from;
+        }
+        const int mine_tok = min(tok, s.ntok - 1);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+          if (__shfl_sync(kAll, from, sub + o) <= mine_tok) sub += o;
+        seq = s.seq + sub;
+        own = __shfl_sync(kAll, sub_len, sub) - __shfl_sync(kAll, nq, sub) + mine_tok - __shfl_sync(kAll, from, sub);
+      }
+      auto page_bad = [&](const KeyTile& k) {   // the page of this lane's 8 keys of a tile lies outside the cache
+        const int key = k.key0 + lane * 8;
+        if (lane >= kTileKeys / 8 || key >= k.len) return false;
+        const int id = pages_of_tile(k)[key >> c.page_shift];
         return id < 0 || id >= c.n_pages;
       };
       float m = -INFINITY, l = 0.f;
-      bool bad = PAGED && mine > 0 && page_bad(t_mine);
+      KeyTile ahead = key_tile(s, t_mine);
+      bool bad = PAGED && mine > 0 && page_bad(ahead);
       for (int i = 0; i < mine; ++i) {
-        const int t = t_mine + i * step;
+        const KeyTile k = ahead;
         const unsigned bad8 = PAGED ? __ballot_sync(kAll, bad) : 0u;
-        if constexpr (PAGED) bad = i + 1 < mine && page_bad(t + step);
+        if (i + 1 < mine) {
+          ahead = key_tile(s, t_mine + (i + 1) * step);
+          if constexpr (PAGED) bad = page_bad(ahead);
+        }
         ok = ok && __all_sync(kAll, mbar_wait(&s_full[x], seen++ & 1));   // a warp whose wait ran out still meets the others
         tc_fence_after();
         float sv[kTileKeys];
         tmem_ld128(s_tm, sv);
         // keys of the tile that this row sees: [low, high)
-        const bool pre = t < np;
-        const int last = pre ? b.prefix_len : own + 1, high = last - (pre ? t : t - np) * kTileKeys;
-        const int low = p.window ? (pre ? b.prefix_len : 0) + own + 1 - p.window - (pre ? t : t - np) * kTileKeys : 0;
+        const int high = k.seq < 0 ? k.len - k.key0 : k.seq == seq ? own + 1 - k.key0 : 0;
+        const int low = p.window ? (k.seq < 0 ? b.prefix_len : 0) + own + 1 - p.window - k.key0 : 0;
         if (__any_sync(kAll, high < kTileKeys || low > 0 || bad8)) {
           // one bit to each key: comparisons of every key with both ends took 1500 cycles
 #pragma unroll
@@ -937,66 +1027,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         other_f *= inv;
       }
       stored = tiled;
-      if (rows <= quarter * 32) {   // none of this warp's, which still meets the others
-        if (s.split) bar_sync(3 + quarter, 64);
-        if (tiled) {
-          bar_sync(1 + x, 128);
-          if (cut && DP == 128) {
-            bar_sync(1 + x, 128);
-            bar_sync(1 + x, 128);
-          }
-        }
-        continue;
-      }
+      const bool busy = rows > quarter * 32;   // this warp has rows
+      // 32 columns at a time in a short loop: unrolled, its code came from memory for 2000 to 5000 cycles a unit
 #pragma unroll 1
-      for (int c0 = 0; c0 < DP; c0 += 64) {
-        float ov[64];
-        tmem_ld64(o_tm + c0, ov);
-        // nothing of b without a tile of its own, or where this part of a unit has none for a
+      for (int c0 = 0; c0 < DP; c0 += 32) {
+        if (cut && tiled && c0 >= 64 && !(c0 & 32)) boxes_free();
+        if (busy) {
+          float ov[32];
+          tmem_ld32(o_tm + c0, ov);
+          // nothing of b without a tile of its own, or where this part of a unit has none for a
 #pragma unroll
-        for (int e = 0; e < 64; ++e) ov[e] = mine > 0 ? ov[e] * mine_f : 0.f;
-        if (s.split) {
+          for (int e = 0; e < 32; ++e) ov[e] = mine > 0 ? ov[e] * mine_f : 0.f;
+          if (s.split) {
+            float oa[32];
+            tmem_ld32(tmem + lane_base + 256 + c0, oa);   // a has a tile at least
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            float oa[16];
-            tmem_ld16(tmem + lane_base + 256 + c0 + h * 16, oa);   // a has a tile at least
-#pragma unroll
-            for (int e = 0; e < 16; ++e) ov[h * 16 + e] = fmaf(oa[e], other_f, ov[h * 16 + e]);
+            for (int e = 0; e < 32; ++e) ov[e] = fmaf(oa[e], other_f, ov[e]);
           }
-        }
-        if (c0 + 64 >= DP) {
-          tc_fence_before();
-          if (s.split) bar_sync(3 + quarter, 64);
-        }
-        if (few) {   // rows go straight out
-          if (real && cut) {
-            float* o = parts.o + (part + rho) * p.D + c0;
+          if (cut) {   // 32 columns of 32 bits to a box
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (c0 + e * 4 < p.D) *reinterpret_cast<float4*>(o + e * 4) = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
-          } else if (real) {
+            for (int e = 0; e < 8; ++e) {
+              const float4 v = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+              if (tiled)
+                *reinterpret_cast<float4*>(out + (c0 >> 5 & 1) * Cfg::OBOX + sw128_off(lane, e)) = v;
+              else if (real && c0 + e * 4 < p.D)   // few rows go straight out
+                *reinterpret_cast<float4*>(parts.o + (part + rho) * p.D + c0 + e * 4) = v;
+            }
+          } else {
             T* o = static_cast<T*>(a.o) + (first + static_cast<int64_t>(pl) * a.Hq + rho - pl * a.G) * p.D + c0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (c0 + e * 8 < p.D) *reinterpret_cast<uint4*>(o + e * 8) = pack8<T>(ov + 8 * e);
+            for (int e = 0; e < 4; ++e) {
+              const uint4 v = pack8<T>(ov + 8 * e);
+              if (!few)
+                *reinterpret_cast<uint4*>(out + (c0 >> 6) * Cfg::OBOX + sw128_off(lane, (c0 >> 3 & 7) + e)) = v;
+              else if (real && c0 + e * 8 < p.D)
+                *reinterpret_cast<uint4*>(o + e * 8) = v;
+            }
           }
-        } else if (cut) {   // 32 columns of 32 bits to a box
-          if (c0 > 0) boxes_free();
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            *reinterpret_cast<float4*>(out + (e >> 3) * Cfg::OBOX + sw128_off(lane, e & 7)) = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+        }
+        if (cut && tiled && (c0 & 32)) {
           fence_proxy_async_smem();
           bar_sync(1 + x, 128);
           if (rho == 0) {
-            tma_store_2d(&tmP, obox, c0, static_cast<int>(part));
-            if (c0 + 32 < p.D) tma_store_2d(&tmP, obox + Cfg::OBOX, c0 + 32, static_cast<int>(part));
+            tma_store_2d(&tmP, obox, c0 - 32, static_cast<int>(part));
+            if (c0 < p.D) tma_store_2d(&tmP, obox + Cfg::OBOX, c0, static_cast<int>(part));
             bulk_commit_group();
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(out + (c0 >> 6) * Cfg::OBOX + sw128_off(lane, e)) = pack8<T>(ov + 8 * e);
         }
       }
+      tc_fence_before();
+      if (s.split) bar_sync(3 + quarter, 64);   // a's sums have been read
       if (few || cut) continue;
       if (tiled) {   // every row of the tile: stores that run on while the next unit does
         fence_proxy_async_smem();
@@ -1007,7 +1087,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             tma_store_3d(&tmO, obox + h * Cfg::OBOX, h * 64, s.g * a.G, s.row0 + place * p.per);
           bulk_commit_group();
         }
-      } else {       // rows behind the sequence's end belong to others
+      } else if (busy) {   // rows behind the sequence's end belong to others
         __syncwarp();
 #pragma unroll 1
         for (int h = 0; h < Cfg::BOXES; ++h)
@@ -1090,18 +1170,23 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tile_join_kernel(const ChunkA
 static int64_t most_tiles(const BatchView& b) {
   return (static_cast<int64_t>(b.prefix_len) + kTileKeys - 1) / kTileKeys + (static_cast<int64_t>(b.max_len) + kTileKeys - 1) / kTileKeys;
 }
+// New rows of a sequence that may go in a group (0: none does): where a prefix of four tiles or more is read once for the
+// group, and 32 of them fill no more than a unit.  max_len: the length of a Span holds its own tiles.
+static int group_rows(const BatchView& b, int window, int per) {
+  return window == 0 && b.prefix_len >= 4 * kTileKeys && b.max_len <= 1 << 27 ? 4 * per / 32 : 0;
+}
 // Whether the bounds allow a unit long enough to be cut.
-static bool may_cut(const BatchView& b, int window) {
+static bool may_cut(const BatchView& b, int window, int group) {
   int64_t tiles = most_tiles(b);
   if (window) tiles = std::min(tiles, (static_cast<int64_t>(window) + kTileRows + kTileKeys - 1) / kTileKeys + 2);
-  return tiles >= 2 * kMinCut;
+  return group > 0 || tiles >= 2 * kMinCut;
 }
 
 static int tile_pairs() { return std::max(1, num_sms() / 2); }
 
-static size_t parts_layout(const BatchView& b, int D, int window, void* base, ChunkParts* w) {
+static size_t parts_layout(const BatchView& b, int D, int window, int group, void* base, ChunkParts* w) {
   *w = ChunkParts{};
-  if (!may_cut(b, window)) return 0;
+  if (!may_cut(b, window, group)) return 0;
   uint8_t* at = static_cast<uint8_t*>(base);
   size_t used = 0;
   auto take = [&](size_t bytes) {
@@ -1172,7 +1257,7 @@ static qcf_status chunk_launch(const char* who, int dtype, const ChunkSource& sr
                                size_t ws_bytes, cudaStream_t st) {
   if (p.window >= static_cast<int64_t>(b.prefix_len) + b.max_len) p.window = 0;   // every key lies inside
   ChunkParts w;
-  const size_t need = parts_layout(b, p.D, p.window, ws, &w);
+  const size_t need = parts_layout(b, p.D, p.window, p.group, ws, &w);
   if (need > 0 && (!ws || ws_bytes < need)) return set_error(QCF_ERR_WORKSPACE, "%s: workspace %zu < %zu", who, ws_bytes, need);
   if (dtype == QCF_BF16)
     return p.D <= 64 ? tile_launch<__nv_bfloat16, 64, PAGED>(who, src, c, b, p, w, st) : tile_launch<__nv_bfloat16, 128, PAGED>(who, src, c, b, p, w, st);
@@ -1240,7 +1325,7 @@ size_t qcf_packed_causal_attn_workspace_size(int n_seq, int n_rows, int max_len,
   BatchView b;
   if (check_packed("qcf_packed_causal_attn_workspace_size", n_seq, n_rows, max_len, Hq, Hkv, D, &c, &b) != QCF_OK) return 0;
   ChunkParts w;
-  return n_seq == 0 || n_rows == 0 ? 0 : parts_layout(b, D, 0, nullptr, &w);
+  return n_seq == 0 || n_rows == 0 ? 0 : parts_layout(b, D, 0, 0, nullptr, &w);
 }
 
 qcf_status qcf_packed_causal_attn(const void* q, int64_t q_stride, const void* k, const void* v, int64_t kv_stride, int dtype,
@@ -1260,7 +1345,7 @@ qcf_status qcf_packed_causal_attn(const void* q, int64_t q_stride, const void* k
   if ((s = check_chunk(who, c, q, q_stride, Hq, scale, window, o, ws)) != QCF_OK) return s;
   if (n_seq == 0 || n_rows == 0) return QCF_OK;
   b.row_start = row_start;
-  const ChunkArgs p{attn_args(q, q_stride, o, lse, Hq, Hkv, scale), D, window, 128 / (Hq / Hkv)};
+  const ChunkArgs p{attn_args(q, q_stride, o, lse, Hq, Hkv, scale), D, window, 128 / (Hq / Hkv), 0};
   return chunk_launch<false>(who, dtype, ChunkSource{k, v, kv_stride}, c, b, p, ws, ws_bytes, static_cast<cudaStream_t>(stream));
 }
 
@@ -1270,7 +1355,7 @@ size_t qcf_paged_chunk_attn_workspace_size(const qcf_paged_kv* cache, const qcf_
   BatchView b;
   if (check_paged(who, cache, batch, &c, &b) != QCF_OK || check_sizes(who, c, b, Hq) != QCF_OK) return 0;
   ChunkParts w;
-  return b.n_seq == 0 || b.n_rows == 0 ? 0 : parts_layout(b, c.D, 0, nullptr, &w);
+  return b.n_seq == 0 || b.n_rows == 0 ? 0 : parts_layout(b, c.D, 0, group_rows(b, 0, 128 / (Hq / c.Hkv)), nullptr, &w);
 }
 
 qcf_status qcf_paged_chunk_attn(const qcf_paged_kv* cache, const qcf_paged_batch* batch, const void* q, int64_t q_stride, int Hq,
@@ -1283,7 +1368,8 @@ qcf_status qcf_paged_chunk_attn(const qcf_paged_kv* cache, const qcf_paged_batch
   if (s == QCF_OK) s = check_chunk(who, c, q, q_stride, Hq, scale, window, o, ws);
   if (s != QCF_OK) return s;
   if (b.n_seq == 0 || b.n_rows == 0) return QCF_OK;
-  const ChunkArgs p{attn_args(q, q_stride, o, lse, Hq, c.Hkv, scale), c.D, window, 128 / (Hq / c.Hkv)};
+  const int per = 128 / (Hq / c.Hkv);
+  const ChunkArgs p{attn_args(q, q_stride, o, lse, Hq, c.Hkv, scale), c.D, window, per, group_rows(b, window, per)};
   return chunk_launch<true>(who, cache->dtype, ChunkSource{cache->k, cache->v, 0}, c, b, p, ws, ws_bytes, static_cast<cudaStream_t>(stream));
 }
 

@@ -235,6 +235,69 @@ def test_chunk_long(Q, new, lens, prefix, Hq, Hkv, D):
     check_chunk(Q, bt, Hq, window=2500)
 
 
+GROUPS = [  # runs of short sequences before, between and behind longer ones, some without rows, over a prefix of several tiles
+    ([1] * 40, [(i * 53) % 700 + 1 for i in range(40)]),
+    ([1, 0, 1, 300, 1, 1, 0, 0, 2, 1, 50, 1], [200, 7, 129, 400, 1, 128, 5, 900, 256, 384, 90, 33]),
+    ([2, 1, 3, 4] * 20, [(i * 37) % 300 + 4 for i in range(80)]), ([0, 0, 1, 0], [9, 0, 300, 4]), ([1, 0, 0, 1] + [0] * 60 + [1, 1], [60 + i for i in range(66)])]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page,layout,dtype", [
+    (32, 8, 128, 16, "rows", "bf16"), (16, 1, 64, 64, "heads", "f16"), (7, 1, 128, 8, "heads", "bf16"), (4, 4, 128, 128, "rows", "f16"), (24, 1, 16, 32, "rows", "bf16")])
+@pytest.mark.parametrize("prefix", [512, 1301])
+@pytest.mark.parametrize("new,lens", GROUPS)
+def test_chunk_groups_of_short_sequences(Q, Hq, Hkv, D, page, layout, dtype, prefix, new, lens):
+    bt = R.Batch(new, lens, prefix, Hkv, D, page, layout, TYPES[dtype], seed=len(new) + D, pad=3, lead=1).fill()
+    check_chunk(Q, bt, Hq)
+    check_chunk(Q, bt, Hq, window=prefix)
+
+
+def test_chunk_groups_leave_out_bad_sequences_and_pages(Q):
+    new, lens = [1] * 12 + [40] + [1] * 3, [100 + 9 * i for i in range(16)]
+    bt = R.Batch(new, lens, 700, 2, 128, 16, "rows", torch.bfloat16, seed=2).fill()
+    q = bt.randn(bt.n_rows, 8, 128)
+    cache, batch = bt.bind(Q)
+    ref, rlse = Q.qcf_paged_chunk_attn(cache, batch, q, 0.1, want_lse=True)
+    bt.kv_len[5] = 0                               # fewer tokens than new rows
+    out = torch.full_like(ref, 7.0)
+    Q.qcf_paged_chunk_attn(cache, batch, q, 0.1, out=out)
+    assert Q.qcf_query_status() == 2
+    assert torch.all(out[5] == 7.0)
+    bt.kv_len[5] = lens[5]
+    o, e, tol, ltol = P.batch_attention(bt, q, 0.1)
+    keep = [i for i in range(bt.n_rows) if i != 5]
+    within(out[keep], o[keep], tol[keep], "beside a bad sequence")
+    was = int(bt.table[7, 1])
+    bt.table[7, 1] = -3                            # tokens 16 .. 31 of one of them
+    got, lse = Q.qcf_paged_chunk_attn(cache, batch, q, 0.1, want_lse=True)
+    assert Q.qcf_query_status() == 2
+    bt.table[7, 1] = was
+    o, e, tol, ltol = P.batch_attention(bt, q, 0.1, 0, {7: range(16, 32)})
+    within(got, o, tol, "with a bad page")
+    within(lse, e, ltol, "lse with a bad page")
+    assert torch.equal(Q.qcf_paged_chunk_attn(cache, batch, q, 0.1), ref) and rlse.shape == lse.shape
+
+
+def test_chunk_groups_of_many(Q):
+    """Hundreds of single tokens, a cache that changes under a captured call."""
+    lens = [(i * 29) % 260 + 1 for i in range(300)]
+    bt = R.Batch([1] * 300, lens, 2000, 4, 64, 32, "rows", torch.float16, seed=5, pad=2, table_cols=9).fill()
+    check_chunk(Q, bt, 16, max_len=288)
+    q = bt.randn(bt.n_rows, 16, 64)
+    cache, batch = bt.bind(Q, max_len=288)
+    out = torch.zeros_like(q)
+    Q.qcf_paged_chunk_attn(cache, batch, q, 0.1, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Q.qcf_paged_chunk_attn(cache, batch, q, 0.1, out=out)
+    for step in (1, 40, 100):
+        bt.lens = [max(1, n - step) for n in lens]
+        bt.kv_len.copy_(torch.tensor(bt.lens, dtype=torch.int32))
+        graph.replay()
+        o, _, tol, _ = P.batch_attention(bt, q, 0.1)
+        within(out[:300], o[:300], tol[:300], f"{step} fewer")
+
+
 def test_chunk_agrees_with_the_shared_prefix_call(Q):
     """Two ways through the same batch: each within its tolerance of the same values."""
     bt = R.Batch([30, 1, 64], [200, 90, 64], 1500, 8, 128, 16, "rows", torch.bfloat16, seed=3).fill()
