@@ -206,6 +206,7 @@ __device__ __forceinline__ int warp_scan(int v) {
   return v;
 }
 // Of sequence base + lane, base a multiple of 32; all lanes of a warp together.
+template <bool PAGED>
 __device__ __forceinline__ Span span_at(const BatchView& b, const ChunkArgs& p, int base, bool* bad) {
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31, seq = base + lane;
@@ -213,7 +214,7 @@ __device__ __forceinline__ Span span_at(const BatchView& b, const ChunkArgs& p, 
   if (seq < b.n_seq) q = chunk_span(b, seq);
   *bad = q.bad;
   Span s{q.row0, q.nq, q.len};
-  if (p.group == 0) return s;
+  if (!PAGED || p.group == 0) return s;
   const bool small = seq < b.n_seq && !q.bad && q.nq <= p.group;
   const unsigned in = __ballot_sync(kAll, small), rows = __ballot_sync(kAll, small && q.nq > 0);
   const int tiles = small && q.nq > 0 ? (q.len + kTileKeys - 1) / kTileKeys : 0;
@@ -236,11 +237,12 @@ struct RowBlock {
 __device__ __forceinline__ int tile_of(int prefix, int pos) {
   return pos < prefix ? pos / kTileKeys : (prefix + kTileKeys - 1) / kTileKeys + (pos - prefix) / kTileKeys;
 }
+template <bool PAGED>
 __device__ __forceinline__ RowBlock row_block(const BatchView& b, const ChunkArgs& p, int nq, int len, int i) {
   RowBlock k;
   k.i0 = i * 4 * p.per;
   k.ntok = min(4 * p.per, nq - k.i0);
-  if (len < 0) {
+  if (PAGED && len < 0) {
     k.t0 = 0;
     k.end = k.end_a = (b.prefix_len + kTileKeys - 1) / kTileKeys + group_tiles(len);
     return k;
@@ -305,6 +307,7 @@ __device__ __forceinline__ int deal_scan(int tid, int v, int* met, int* total) {
 }
 
 // Finds where this pair's share begins; blk: scratch for 3 n_seq + 1 ints.
+template <bool PAGED>
 __device__ void find_share(int tid, const BatchView& b, const ChunkArgs& p, int Hkv, int pair, int pairs, int* blk, int* met, DealStart* start,
                            unsigned int* status) {
   const int R = 4 * p.per, most = b.n_rows / R + b.n_seq;   // row blocks at most
@@ -315,7 +318,7 @@ __device__ void find_share(int tid, const BatchView& b, const ChunkArgs& p, int 
   int mine = 0, all, total;
   for (int s = tid; s - (tid & 31) < b.n_seq; s += kDealThreads) {
     bool bad;
-    const Span q = span_at(b, p, s - (tid & 31), &bad);
+    const Span q = span_at<PAGED>(b, p, s - (tid & 31), &bad);
     if (bad && blockIdx.x == 0) flag_status(status, QCF_DEV_BAD_INDEX);
     if (s < b.n_seq) {
       blk[s] = (q.nq + R - 1) / R;
@@ -355,7 +358,7 @@ __device__ void find_share(int tid, const BatchView& b, const ChunkArgs& p, int 
     int seq = first;
     for (int i = b0; i < b1; ++i) {
       while (i >= blk[seq + 1]) ++seq;
-      if (visit(seq, i - blk[seq], Hkv * unit_cost(row_block(b, p, nqs[seq], lens[seq], i - blk[seq]), p.per))) return;
+      if (visit(seq, i - blk[seq], Hkv * unit_cost(row_block<PAGED>(b, p, nqs[seq], lens[seq], i - blk[seq]), p.per))) return;
     }
   };
   int cost = 0;
@@ -378,6 +381,7 @@ __device__ void find_share(int tid, const BatchView& b, const ChunkArgs& p, int 
 }
 
 // Walks a pair's share, all lanes of a warp alike; they keep the spans of 32 sequences.
+template <bool PAGED>
 struct TileWalk {
   const BatchView& b;
   const ChunkArgs& p;
@@ -393,7 +397,7 @@ struct TileWalk {
   __device__ void keep(int from) {
     base = from;
     bool bad;
-    const Span s = span_at(b, p, from, &bad);
+    const Span s = span_at<PAGED>(b, p, from, &bad);
     my_row0 = s.row0;
     my_nq = s.nq;
     my_len = s.len;
@@ -417,7 +421,7 @@ struct TileWalk {
     row0 = at.row0;
     nq = at.nq;
     len = at.len;
-    k = row_block(b, p, nq, len, block);
+    k = row_block<PAGED>(b, p, nq, len, block);
     g = (begin - pos) / unit_cost(k, p.per);
     pos += g * unit_cost(k, p.per);
   }
@@ -450,7 +454,7 @@ struct TileWalk {
         s.row0 = row0 + k.i0;
         s.ntok = k.ntok;
         s.g = g;
-        s.pos = len < 0 ? 0 : len - nq + k.i0;
+        s.pos = PAGED && len < 0 ? 0 : len - nq + k.i0;
         s.len = len;
         s.t0 = k.t0 + from;
         s.nt = to - from;
@@ -477,7 +481,7 @@ struct TileWalk {
           block = 0;
           next_seq();
         }
-        if (live) k = row_block(b, p, nq, len, block);
+        if (live) k = row_block<PAGED>(b, p, nq, len, block);
       }
       if (some) return true;
     }
@@ -560,7 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
   pdl_wait();
   if (warp >= 4) {
-    find_share(threadIdx.x - 128, b, p, c.Hkv, pair, pairs, reinterpret_cast<int*>(kbuf), met, start, status);
+    find_share<PAGED>(threadIdx.x - 128, b, p, c.Hkv, pair, pairs, reinterpret_cast<int*>(kbuf), met, start, status);
     fence_proxy_async_smem();   // the deal used the rings
   }
   tc_fence_before();
@@ -621,7 +625,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       const int rows = PAGED ? min(1 << c.page_shift, keys) : keys, boxes = PAGED ? keys / rows : 1;
       DealStart at0 = *start;
       if (!is_k) at0.seq = -1;
-      TileWalk walk(b, p, at0, c.Hkv, pair);
+      TileWalk<PAGED> walk(b, p, at0, c.Hkv, pair);
       Segment s;
       int n = 0, tails = 0, units = 0;
       bool ok = true;
@@ -1027,56 +1031,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         other_f *= inv;
       }
       stored = tiled;
-      const bool busy = rows > quarter * 32;   // this warp has rows
-      // 32 columns at a time in a short loop: unrolled, its code came from memory for 2000 to 5000 cycles a unit
-#pragma unroll 1
-      for (int c0 = 0; c0 < DP; c0 += 32) {
-        if (cut && tiled && c0 >= 64 && !(c0 & 32)) boxes_free();
-        if (busy) {
-          float ov[32];
-          tmem_ld32(o_tm + c0, ov);
-          // nothing of b without a tile of its own, or where this part of a unit has none for a
-#pragma unroll
-          for (int e = 0; e < 32; ++e) ov[e] = mine > 0 ? ov[e] * mine_f : 0.f;
-          if (s.split) {
-            float oa[32];
-            tmem_ld32(tmem + lane_base + 256 + c0, oa);   // a has a tile at least
-#pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = fmaf(oa[e], other_f, ov[e]);
-          }
-          if (cut) {   // 32 columns of 32 bits to a box
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 v = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
-              if (tiled)
-                *reinterpret_cast<float4*>(out + (c0 >> 5 & 1) * Cfg::OBOX + sw128_off(lane, e)) = v;
-              else if (real && c0 + e * 4 < p.D)   // few rows go straight out
-                *reinterpret_cast<float4*>(parts.o + (part + rho) * p.D + c0 + e * 4) = v;
-            }
-          } else {
-            T* o = static_cast<T*>(a.o) + (first + static_cast<int64_t>(pl) * a.Hq + rho - pl * a.G) * p.D + c0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint4 v = pack8<T>(ov + 8 * e);
-              if (!few)
-                *reinterpret_cast<uint4*>(out + (c0 >> 6) * Cfg::OBOX + sw128_off(lane, (c0 >> 3 & 7) + e)) = v;
-              else if (real && c0 + e * 8 < p.D)
-                *reinterpret_cast<uint4*>(o + e * 8) = v;
-            }
+      if (rows <= quarter * 32) {   // none of this warp's, which still meets the others
+        if (s.split) bar_sync(3 + quarter, 64);
+        if (tiled) {
+          bar_sync(1 + x, 128);
+          if (cut && DP == 128) {
+            bar_sync(1 + x, 128);
+            bar_sync(1 + x, 128);
           }
         }
-        if (cut && tiled && (c0 & 32)) {
+        continue;
+      }
+#pragma unroll 1
+      for (int c0 = 0; c0 < DP; c0 += 64) {
+        float ov[64];
+        tmem_ld64(o_tm + c0, ov);
+        // nothing of b without a tile of its own, or where this part of a unit has none for a
+#pragma unroll
+        for (int e = 0; e < 64; ++e) ov[e] = mine > 0 ? ov[e] * mine_f : 0.f;
+        if (s.split) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            float oa[16];
+            tmem_ld16(tmem + lane_base + 256 + c0 + h * 16, oa);   // a has a tile at least
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ov[h * 16 + e] = fmaf(oa[e], other_f, ov[h * 16 + e]);
+          }
+        }
+        if (c0 + 64 >= DP) {
+          tc_fence_before();
+          if (s.split) bar_sync(3 + quarter, 64);
+        }
+        if (few) {   // rows go straight out
+          if (real && cut) {
+            float* o = parts.o + (part + rho) * p.D + c0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (c0 + e * 4 < p.D) *reinterpret_cast<float4*>(o + e * 4) = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+          } else if (real) {
+            T* o = static_cast<T*>(a.o) + (first + static_cast<int64_t>(pl) * a.Hq + rho - pl * a.G) * p.D + c0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (c0 + e * 8 < p.D) *reinterpret_cast<uint4*>(o + e * 8) = pack8<T>(ov + 8 * e);
+          }
+        } else if (cut) {   // 32 columns of 32 bits to a box
+          if (c0 > 0) boxes_free();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            *reinterpret_cast<float4*>(out + (e >> 3) * Cfg::OBOX + sw128_off(lane, e & 7)) = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
           fence_proxy_async_smem();
           bar_sync(1 + x, 128);
           if (rho == 0) {
-            tma_store_2d(&tmP, obox, c0 - 32, static_cast<int>(part));
-            if (c0 < p.D) tma_store_2d(&tmP, obox + Cfg::OBOX, c0, static_cast<int>(part));
+            tma_store_2d(&tmP, obox, c0, static_cast<int>(part));
+            if (c0 + 32 < p.D) tma_store_2d(&tmP, obox + Cfg::OBOX, c0 + 32, static_cast<int>(part));
             bulk_commit_group();
           }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(out + (c0 >> 6) * Cfg::OBOX + sw128_off(lane, e)) = pack8<T>(ov + 8 * e);
         }
       }
-      tc_fence_before();
-      if (s.split) bar_sync(3 + quarter, 64);   // a's sums have been read
       if (few || cut) continue;
       if (tiled) {   // every row of the tile: stores that run on while the next unit does
         fence_proxy_async_smem();
@@ -1087,7 +1101,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             tma_store_3d(&tmO, obox + h * Cfg::OBOX, h * 64, s.g * a.G, s.row0 + place * p.per);
           bulk_commit_group();
         }
-      } else if (busy) {   // rows behind the sequence's end belong to others
+      } else {       // rows behind the sequence's end belong to others
         __syncwarp();
 #pragma unroll 1
         for (int h = 0; h < Cfg::BOXES; ++h)
