@@ -655,6 +655,7 @@ class PagePool:
         self.struct = _lib.PagePool(self._caches, len(caches), refs.data_ptr(), page_table.data_ptr(), page_table.shape[1], kv_len.data_ptr(),
                                     n_seq)
         self.ref = C.byref(self.struct)
+        self._ws_bytes: Dict[int, int] = {}
 
     @classmethod
     def empty(cls, caches: Sequence[PagedKV], n_seq: int, max_len: int) -> "PagePool":
@@ -665,43 +666,45 @@ class PagePool:
         dev, cols = caches[0].k.device, max(1, -(-max_len // caches[0].page_size))
         return cls(caches, *(torch.zeros(shape, dtype=torch.int32, device=dev) for shape in (caches[0].struct.n_pages, (n_seq, cols), n_seq)))
 
-    def _args(self, n: int, *ts: Optional[torch.Tensor]):
+    def _list(self, t: torch.Tensor, n: int) -> int:
+        """The address of an argument of n entries."""
+        if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or t.get_device() != self.dev:
+            _bad(f"every argument must be a contiguous int32 tensor of {n} entries on the pool's device")
+        return t.data_ptr()
+
+    def _scratch(self, n: int, stream) -> Tuple[torch.Tensor, int]:
+        """Scratch of a call with n arguments, and its size: a function of the layout and n alone."""
         if self.dev != torch.cuda.current_device():
             _bad("tensors must be on the current CUDA device")
-        for t in ts:
-            if t is not None:
-                _need_i32(t, "every argument", (n,))
-                if t.get_device() != self.dev:
-                    _bad("tensors must be on the current CUDA device")
-
-    def _scratch(self, n: int, stream):
-        nb = _lib.lib().qcf_pages_workspace_size(self.ref, n)
+        nb = self._ws_bytes.get(n)
+        if nb is None:
+            nb = _lib.lib().qcf_pages_workspace_size(self.ref, n)
+            if nb:
+                self._ws_bytes[n] = nb
         return _empty(max(nb, 1), torch.uint8, self.dev, stream), nb
 
 
 def qcf_pages_fork(pool: PagePool, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
     """Sequences dst[i] (int32 on the device) go on from src[i]: full pages shared, a page held in part copied."""
     n = src.numel()
-    pool._args(n, src, dst)
+    a, b = pool._list(src, n), pool._list(dst, n)
     if n:   # empty tensors have no address to pass
         ws, nb = pool._scratch(n, stream)
-        call("qcf_pages_fork", pool.ref, src.data_ptr(), dst.data_ptr(), n, ws.data_ptr(), nb, _raw_stream(stream, pool.dev))
+        call("qcf_pages_fork", pool.ref, a, b, n, ws.data_ptr(), nb, _raw_stream(stream, pool.dev))
 
 
 def qcf_pages_resize(pool: PagePool, new_len: torch.Tensor, seqs: Optional[torch.Tensor] = None, stream=None) -> None:
     """Sequences seqs[i] (None: 0, 1, ..) get the lengths new_len[i], int32 on the device: pages taken or given back."""
     n = new_len.numel()
-    pool._args(n, new_len, seqs)
+    b, a = pool._list(new_len, n), None if seqs is None else pool._list(seqs, n)
     if n:
         ws, nb = pool._scratch(n, stream)
-        call("qcf_pages_resize", pool.ref, None if seqs is None else seqs.data_ptr(), new_len.data_ptr(), n, ws.data_ptr(), nb,
-             _raw_stream(stream, pool.dev))
+        call("qcf_pages_resize", pool.ref, a, b, n, ws.data_ptr(), nb, _raw_stream(stream, pool.dev))
 
 
 def qcf_pages_compact(pool: PagePool, stream=None) -> torch.Tensor:
     """Moves the pages in use to the lowest ids; returns how many they are (int32 [1] on the device)."""
-    pool._args(0)
-    live = _empty((1,), torch.int32, pool.dev, stream)
     ws, nb = pool._scratch(0, stream)
+    live = _empty((1,), torch.int32, pool.dev, stream)
     call("qcf_pages_compact", pool.ref, live.data_ptr(), ws.data_ptr(), nb, _raw_stream(stream, pool.dev))
     return live
