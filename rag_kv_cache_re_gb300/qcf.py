@@ -511,6 +511,18 @@ class PagedBatch:
                 self._ws_bytes[key] = nb
         return nb
 
+    def chunk_workspace_size(self, cache: PagedKV, Hq: int) -> int:
+        """qcf_paged_chunk_attn_workspace_size, kept alike."""
+        if self.empty:
+            return 0
+        key = (cache.page_size, cache.Hkv, cache.D, -Hq)
+        nb = self._ws_bytes.get(key)
+        if nb is None:
+            nb = _lib.lib().qcf_paged_chunk_attn_workspace_size(cache.ref, self.ref, Hq)
+            if nb:
+                self._ws_bytes[key] = nb
+        return nb
+
 
 def _batch_rows(cache: PagedKV, batch: PagedBatch, t: torch.Tensor, what: str):
     """(H, row stride) of a tensor that holds the batch's rows in the cache's type and head dim."""
@@ -623,7 +635,7 @@ def qcf_paged_chunk_attn(cache: PagedKV, batch: PagedBatch, q: torch.Tensor, sca
     Hq, qs = _batch_rows(cache, batch, q, "q")
     out, lse = _attn_out(q, out, want_lse, cache.dev, stream)
     if not batch.empty:
-        nb = _lib.lib().qcf_paged_chunk_attn_workspace_size(cache.ref, batch.ref, Hq)
+        nb = batch.chunk_workspace_size(cache, Hq)
         ws = _empty(nb, torch.uint8, cache.dev, stream) if nb else None
         call("qcf_paged_chunk_attn", cache.ref, batch.ref, q.data_ptr(), qs, Hq, scale, window, out.data_ptr(),
              None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), nb, _raw_stream(stream, cache.dev))
@@ -635,7 +647,8 @@ def qcf_paged_chunk_attn(cache: PagedKV, batch: PagedBatch, q: torch.Tensor, sca
 class PagePool:
     """The pages of a cache and the sequences that hold them (see qcf_page_pool): `caches` the PagedKV of
     every layer, all of one layout; refs [n_pages], page_table [n_seq][columns] and kv_len [n_seq] int32 on the
-    device.  page_table and kv_len also serve a PagedBatch."""
+    device.  page_table and kv_len also serve a PagedBatch.  Calls with one pool are made on one stream, or
+    ordered by the caller: each changes the pool, and they share its scratch."""
 
     def __init__(self, caches: Sequence[PagedKV], refs: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor):
         caches = list(caches)
@@ -655,7 +668,11 @@ class PagePool:
         self.struct = _lib.PagePool(self._caches, len(caches), refs.data_ptr(), page_table.data_ptr(), page_table.shape[1], kv_len.data_ptr(),
                                     n_seq)
         self.ref = C.byref(self.struct)
-        self._ws_bytes: Dict[int, int] = {}
+        # Scratch for as many arguments as there are sequences.  One for the pool's life: its calls never overlap, for
+        # each changes the pool.  (0 for a layout the library refuses, as every call then will.)
+        self._nb = _lib.lib().qcf_pages_workspace_size(self.ref, n_seq)
+        self._ws = torch.empty(max(self._nb, 1), dtype=torch.uint8, device=refs.device)
+        self._ws_ptr = self._ws.data_ptr()
 
     @classmethod
     def empty(cls, caches: Sequence[PagedKV], n_seq: int, max_len: int) -> "PagePool":
@@ -672,16 +689,9 @@ class PagePool:
             _bad(f"every argument must be a contiguous int32 tensor of {n} entries on the pool's device")
         return t.data_ptr()
 
-    def _scratch(self, n: int, stream) -> Tuple[torch.Tensor, int]:
-        """Scratch of a call with n arguments, and its size: a function of the layout and n alone."""
+    def _here(self):
         if self.dev != torch.cuda.current_device():
             _bad("tensors must be on the current CUDA device")
-        nb = self._ws_bytes.get(n)
-        if nb is None:
-            nb = _lib.lib().qcf_pages_workspace_size(self.ref, n)
-            if nb:
-                self._ws_bytes[n] = nb
-        return _empty(max(nb, 1), torch.uint8, self.dev, stream), nb
 
 
 def qcf_pages_fork(pool: PagePool, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
@@ -689,8 +699,8 @@ def qcf_pages_fork(pool: PagePool, src: torch.Tensor, dst: torch.Tensor, stream=
     n = src.numel()
     a, b = pool._list(src, n), pool._list(dst, n)
     if n:   # empty tensors have no address to pass
-        ws, nb = pool._scratch(n, stream)
-        call("qcf_pages_fork", pool.ref, a, b, n, ws.data_ptr(), nb, _raw_stream(stream, pool.dev))
+        pool._here()
+        call("qcf_pages_fork", pool.ref, a, b, n, pool._ws_ptr, pool._nb, _raw_stream(stream, pool.dev))
 
 
 def qcf_pages_resize(pool: PagePool, new_len: torch.Tensor, seqs: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -698,13 +708,13 @@ def qcf_pages_resize(pool: PagePool, new_len: torch.Tensor, seqs: Optional[torch
     n = new_len.numel()
     b, a = pool._list(new_len, n), None if seqs is None else pool._list(seqs, n)
     if n:
-        ws, nb = pool._scratch(n, stream)
-        call("qcf_pages_resize", pool.ref, a, b, n, ws.data_ptr(), nb, _raw_stream(stream, pool.dev))
+        pool._here()
+        call("qcf_pages_resize", pool.ref, a, b, n, pool._ws_ptr, pool._nb, _raw_stream(stream, pool.dev))
 
 
 def qcf_pages_compact(pool: PagePool, stream=None) -> torch.Tensor:
     """Moves the pages in use to the lowest ids; returns how many they are (int32 [1] on the device)."""
-    ws, nb = pool._scratch(0, stream)
+    pool._here()
     live = _empty((1,), torch.int32, pool.dev, stream)
-    call("qcf_pages_compact", pool.ref, live.data_ptr(), ws.data_ptr(), nb, _raw_stream(stream, pool.dev))
+    call("qcf_pages_compact", pool.ref, live.data_ptr(), pool._ws_ptr, pool._nb, _raw_stream(stream, pool.dev))
     return live
