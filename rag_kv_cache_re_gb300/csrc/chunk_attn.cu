@@ -1133,27 +1133,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
 // ------------------------------------------------------------------ joining the parts
 //
 // A warp joins the parts of one score row of a unit that was cut: the one that its first pair left, and
-// those of the pairs behind it.
-constexpr int kJoinWarps = 8, kJoinRows = 16;
+// those of the pairs behind it.  The rows of all cut units, few or many, are dealt out over the warps.
+// (A CTA to every 16 rows that a pair might have left: the call with 64 rows over 5120 keys 26.7 us, for JOIN_US.)
+constexpr int kJoinThreads = 256, kMaxPairs = kJoinThreads;
 template <typename T>
-__global__ void __launch_bounds__(kJoinWarps * 32) tile_join_kernel(const ChunkArgs p, const ChunkParts parts) {
-  pdl_wait();
-  const int4 rec = parts.rec[blockIdx.x];
-  if (rec.x <= 1) return;
+__global__ void __launch_bounds__(kJoinThreads) tile_join_kernel(const ChunkArgs p, const ChunkParts parts, int pairs) {
+  constexpr int WARPS = kJoinThreads / 32, BATCH = 8;
+  __shared__ int4 rec_s[kMaxPairs];
+  __shared__ int first_s[kMaxPairs + 1];   // rows of cut units before each pair's
+  __shared__ int sums[WARPS];
   const AttnArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  {
+    const int4 rec = static_cast<int>(threadIdx.x) < pairs ? parts.rec[threadIdx.x] : make_int4(0, 0, 0, 0);
+    const int mine = rec.x > 1 ? rec.z * a.G : 0;
+    const int run = warp_scan(mine);
+    if (lane == 31) sums[warp] = run;
+    rec_s[threadIdx.x] = rec;
+    __syncthreads();
+    int before = run - mine;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) before += w < warp ? sums[w] : 0;
+    first_s[threadIdx.x] = before;
+    if (threadIdx.x == kJoinThreads - 1) first_s[kMaxPairs] = before + mine;
+    __syncthreads();
+  }
+  const int total = first_s[kMaxPairs];
   const bool has = lane * 4 < p.D;
-  for (int r = blockIdx.y * kJoinRows + warp; r < min(static_cast<int>(blockIdx.y + 1) * kJoinRows, rec.z * a.G); r += kJoinWarps) {
-    const int tok = div_g(a, r), tile = tok / p.per, in_unit = tile * 128 + r - tile * p.per * a.G;
+  for (int row = blockIdx.x * WARPS + warp; row < total; row += gridDim.x * WARPS) {
+    int pair = 0;   // the last one whose rows begin at or before this one: rows there are only of pairs that cut a unit
+#pragma unroll
+    for (int o = kMaxPairs / 2; o > 0; o >>= 1)
+      if (first_s[pair + o] <= row) pair += o;
+    const int4 rec = rec_s[pair];
+    const int r = row - first_s[pair], tok = div_g(a, r), tile = tok / p.per, in_unit = tile * 128 + r - tile * p.per * a.G;
     float M = -INFINITY, L = 0.f, sum[4] = {0.f, 0.f, 0.f, 0.f};
-    constexpr int BATCH = 4;
     for (int i0 = 0; i0 < rec.x; i0 += BATCH) {
       float2 ml[BATCH];
       float4 v[BATCH];
 #pragma unroll
       for (int j = 0; j < BATCH; ++j) {   // behind the end the last part again: loads without branches stay together
         const int i = min(i0 + j, rec.x - 1);
-        const int64_t at = (static_cast<int64_t>(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * kTileRows + in_unit;
+        const int64_t at = (static_cast<int64_t>(pair + i) * 2 + (i == 0 ? 1 : 0)) * kTileRows + in_unit;
         ml[j] = parts.ml[at];
         v[j] = *reinterpret_cast<const float4*>(parts.o + at * p.D + (has ? lane * 4 : 0));
       }
@@ -1196,7 +1218,7 @@ static bool may_cut(const BatchView& b, int window, int group) {
   return group > 0 || tiles >= 2 * kMinCut;
 }
 
-static int tile_pairs() { return std::max(1, num_sms() / 2); }
+static int tile_pairs() { return std::min(std::max(1, num_sms() / 2), kMaxPairs); }
 
 static size_t parts_layout(const BatchView& b, int D, int window, int group, void* base, ChunkParts* w) {
   *w = ChunkParts{};
@@ -1261,8 +1283,7 @@ static qcf_status tile_launch(const char* who, const ChunkSource& src, const Pag
   }
   if (!w.rec) return QCF_OK;
   LaunchScope ls(KC_CHUNK_JOIN, st);
-  e = launch_pdl(tile_join_kernel<T>, dim3(tile_pairs(), (std::min(4 * p.per * p.a.G, kTileRows) + kJoinRows - 1) / kJoinRows), dim3(kJoinWarps * 32), 0, st, p,
-                 w);
+  e = launch_pdl(tile_join_kernel<T>, dim3(num_sms() * 4), dim3(kJoinThreads), 0, st, p, w, tile_pairs());
   return e == cudaSuccess ? QCF_OK : cuda_error(e, who);
 }
 

@@ -54,66 +54,66 @@ struct CopyShape {
   bool rows_outer, dense;                         // [row][head] or [head][row]; a page has no gaps
 };
 
-// Sum of v over the block, and over the threads before this one; `met` holds 33 ints.
-__device__ __forceinline__ int block_scan(int v, int* met, int* total) {
+// Sum of v over the threads before this one, and over the block.  met: 32 entries, of its own for calls that follow
+// each other without a barrier between (every warp adds the warps' sums for itself, which saves two).
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* met, int64_t* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int run = v;
+  int64_t run = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, run, o);
+    const int64_t u = __shfl_up_sync(0xffffffffu, run, o);
     if (lane >= o) run += u;
   }
-  __syncthreads();   // the last use of met is over
   if (lane == 31) met[warp] = run;
   __syncthreads();
-  if (warp == 0) {
-    int w = met[lane];
+  int64_t w = met[lane];
+  const int64_t own = w;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += u;
-    }
-    met[lane] = w;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += u;
   }
-  __syncthreads();
-  *total = met[31];
-  return run - v + (warp > 0 ? met[warp - 1] : 0);
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  return run - v + __shfl_sync(0xffffffffu, w - own, warp);
 }
 
-constexpr int kIdsPerThread = 16, kIdsPerPass = kPlanThreads * kIdsPerThread;
-// The counts of this thread's ids [base, base + 16); -1 behind the end.
+// A pass over the counts: a warp has 512 ids in a row, a lane every 32nd of them, so that loads and lists are coalesced and
+// ranks are votes.
+constexpr int kIdsPerLane = 16, kIdsPerPass = kPlanThreads * kIdsPerLane;
+__device__ __forceinline__ int64_t id_at(int64_t base, int e) { return base + (threadIdx.x >> 5) * (32 * kIdsPerLane) + e * 32 + (threadIdx.x & 31); }
+// The counts of this lane's ids; -1 behind the end.
 __device__ __forceinline__ void load_refs(const PoolView& p, int64_t base, int* r) {
 #pragma unroll
-  for (int q = 0; q < kIdsPerThread / 4; ++q) {
-    if (base + 4 * q + 3 < p.n_pages) {
-      const int4 v = *reinterpret_cast<const int4*>(p.refs + base + 4 * q);
-      r[4 * q] = v.x; r[4 * q + 1] = v.y; r[4 * q + 2] = v.z; r[4 * q + 3] = v.w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) r[4 * q + e] = base + 4 * q + e < p.n_pages ? p.refs[base + 4 * q + e] : -1;
-    }
+  for (int e = 0; e < kIdsPerLane; ++e) {
+    const int64_t id = id_at(base, e);
+    r[e] = id < p.n_pages ? p.refs[id] : -1;
   }
 }
 
-// The lowest `want` free ids, ascending, into list; how many there are, at most want.
-__device__ int take_free(const PoolView& p, int want, int32_t* list, int* met) {
-  int found = 0;
+// The lowest `want` free ids, ascending, into list; how many there are, at most want.  r: the counts of the first pass.
+__device__ int take_free(const PoolView& p, int want, int32_t* list, int64_t* met, int* r) {
+  const unsigned below = (1u << (threadIdx.x & 31)) - 1u;
+  int64_t found = 0;
   for (int64_t base = 0; base < p.n_pages && found < want; base += kIdsPerPass) {
-    const int64_t mine = base + static_cast<int64_t>(threadIdx.x) * kIdsPerThread;
-    int r[kIdsPerThread], n = 0, total;
-    load_refs(p, mine, r);
+    if (base > 0) load_refs(p, base, r);
+    int n = 0;
 #pragma unroll
-    for (int e = 0; e < kIdsPerThread; ++e) n += r[e] == 0;
-    int at = found + block_scan(n, met, &total);
+    for (int e = 0; e < kIdsPerLane; ++e) n += __popc(__ballot_sync(0xffffffffu, r[e] == 0));
+    int64_t total;
+    // a warp's count once, in its last lane
+    const int64_t before = block_scan((threadIdx.x & 31) == 31 ? n : 0, met, &total);
+    int64_t at = found + __shfl_sync(0xffffffffu, before, 31);
 #pragma unroll
-    for (int e = 0; e < kIdsPerThread; ++e)
-      if (r[e] == 0) {
-        if (at < want) list[at] = static_cast<int>(mine) + e;
-        ++at;
-      }
+    for (int e = 0; e < kIdsPerLane; ++e) {
+      const unsigned free = __ballot_sync(0xffffffffu, r[e] == 0);
+      const int64_t place = at + __popc(free & below);
+      if (r[e] == 0 && place < want) list[place] = static_cast<int>(id_at(base, e));
+      at += __popc(free);
+    }
     found += total;
+    __syncthreads();   // met may be written again
   }
-  return min(found, want);
+  return static_cast<int>(min(found, static_cast<int64_t>(want)));
 }
 
 __device__ __forceinline__ int pages_of(const PoolView& p, int len) { return (len + (1 << p.page_shift) - 1) >> p.page_shift; }
@@ -125,8 +125,10 @@ __device__ __forceinline__ bool mark(unsigned* set, int b) { return atomicOr(&se
 template <bool FORK>
 __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(const PoolView p, const int32_t* a, const int32_t* b, const PlanView out,
                                                                   unsigned int* status) {
-  __shared__ int met[33];
+  __shared__ int64_t met[2][32];
   __shared__ unsigned named[2048];
+  int r[kIdsPerLane];
+  load_refs(p, 0, r);   // on their way while the arguments are read
   const int words = (p.n_seq + 31) / 32, most = p.table_stride << p.page_shift;
   for (int i = threadIdx.x; i < words; i += kPlanThreads) named[i] = 0;
   __syncthreads();
@@ -172,15 +174,18 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(const PoolView
         take = (split ? 1 : 0) + it.add1 - it.add0;
       }
     }
-    bad |= __syncthreads_or(wrong);
-    int total;
-    it.first = wanted + block_scan(take, met, &total);
-    wanted = min(wanted + static_cast<int64_t>(total), static_cast<int64_t>(p.n_pages) + 1);
-    copies += __syncthreads_count(it.copy_col >= 0);
+    // new pages, and above them copies and wrong arguments, in one sum
+    int64_t total;
+    const int64_t before = block_scan(take | static_cast<int64_t>(it.copy_col >= 0) << 32 | static_cast<int64_t>(wrong) << 48, met[0], &total);
+    it.first = wanted + static_cast<int>(before & 0xffffffff);
+    wanted = static_cast<int>(min(wanted + (total & 0xffffffff), static_cast<int64_t>(p.n_pages) + 1));
+    copies += static_cast<int>(total >> 32 & 0xffff);
+    bad |= total >> 48 != 0;
     if (i < p.n) out.items[i] = it;
+    __syncthreads();   // met may be written again
   }
   const bool over = wanted > p.n_pages;
-  const int found = bad || over ? 0 : take_free(p, wanted, out.list, met);
+  const int found = bad || over ? 0 : take_free(p, wanted, out.list, met[1], r);
   if (threadIdx.x == 0) {
     const bool few = !bad && (over || found < wanted);
     if (bad) flag_status(status, QCF_DEV_BAD_INDEX);
@@ -191,48 +196,52 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(const PoolView
 
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PoolView p, const PlanView out, int32_t* n_live,
                                                                     unsigned int* status) {
-  __shared__ int met[33];
+  __shared__ int64_t met[2][32];
+  const unsigned below = (1u << (threadIdx.x & 31)) - 1u;
+  const bool last = (threadIdx.x & 31) == 31;
+  int r[kIdsPerLane];
+  int64_t total;
+  int count = 0;
+  for (int64_t base = 0; base < p.n_pages; base += kIdsPerPass) {
+    load_refs(p, base, r);
+#pragma unroll
+    for (int e = 0; e < kIdsPerLane; ++e) count += r[e] > 0;
+  }
   const int most = p.table_stride << p.page_shift;
   bool bad = false;
   for (int i = threadIdx.x; i < p.n_seq; i += kPlanThreads) {
     const int len = p.kv_len[i];
     bad |= len < 0 || len > most;
   }
-  bad = __syncthreads_or(bad);
-  int live = 0, total;
-  for (int64_t base = 0; base < p.n_pages; base += kIdsPerPass) {
-    int r[kIdsPerThread];
-    load_refs(p, base + static_cast<int64_t>(threadIdx.x) * kIdsPerThread, r);
-#pragma unroll
-    for (int e = 0; e < kIdsPerThread; ++e) live += r[e] > 0;
-  }
-  block_scan(live, met, &total);
-  live = total;
+  block_scan(count | static_cast<int64_t>(bad) << 32, met[0], &total);
+  bad = total >> 32 != 0;
+  const int live = static_cast<int>(total & 0xffffffff);
   int holes = 0, moves = 0;   // below `live` there are as many free pages as live ones above
   for (int64_t base = 0; base < p.n_pages; base += kIdsPerPass) {
-    const int64_t mine = base + static_cast<int64_t>(threadIdx.x) * kIdsPerThread;
-    int r[kIdsPerThread], h = 0, m = 0;
-    load_refs(p, mine, r);
+    if (p.n_pages > kIdsPerPass) load_refs(p, base, r);   // one pass has them still
+    int h = 0, m = 0;
 #pragma unroll
-    for (int e = 0; e < kIdsPerThread; ++e) {
-      const int64_t id = mine + e;
-      h += id < live && r[e] <= 0 && id < p.n_pages;
-      m += id >= live && r[e] > 0;
+    for (int e = 0; e < kIdsPerLane; ++e) {
+      const int64_t id = id_at(base, e);
+      h += __popc(__ballot_sync(0xffffffffu, id < live && r[e] <= 0));
+      m += __popc(__ballot_sync(0xffffffffu, id >= live && r[e] > 0));
     }
-    int ha = holes + block_scan(h, met, &total);
-    holes += total;
-    int ma = moves + block_scan(m, met, &total);
-    moves += total;
+    const int64_t before = __shfl_sync(0xffffffffu, block_scan(last ? h | static_cast<int64_t>(m) << 32 : 0, met[1], &total), 31);
+    int ha = holes + static_cast<int>(before & 0xffffffff), ma = moves + static_cast<int>(before >> 32);
 #pragma unroll
-    for (int e = 0; e < kIdsPerThread; ++e) {
-      const int64_t id = mine + e;
-      if (id >= p.n_pages) continue;
-      if (id < live && r[e] <= 0) out.list[ha++] = static_cast<int>(id);
-      if (id >= live) {
-        out.map[id] = r[e] > 0 ? ma : -1;
-        if (r[e] > 0) out.list2[ma++] = static_cast<int>(id);
-      }
+    for (int e = 0; e < kIdsPerLane; ++e) {
+      const int64_t id = id_at(base, e);
+      const bool hole = id < live && r[e] <= 0, move = id >= live && r[e] > 0;   // -1 behind the last page: neither
+      const unsigned hs = __ballot_sync(0xffffffffu, hole), ms = __ballot_sync(0xffffffffu, move);
+      if (hole) out.list[ha + __popc(hs & below)] = static_cast<int>(id);
+      if (move) out.list2[ma + __popc(ms & below)] = static_cast<int>(id);
+      if (id >= live && id < p.n_pages) out.map[id] = move ? ma + __popc(ms & below) : -1;
+      ha += __popc(hs);
+      ma += __popc(ms);
     }
+    holes += static_cast<int>(total & 0xffffffff);
+    moves += static_cast<int>(total >> 32);
+    __syncthreads();   // met may be written again
   }
   if (threadIdx.x == 0) {
     if (bad) flag_status(status, QCF_DEV_BAD_INDEX);
