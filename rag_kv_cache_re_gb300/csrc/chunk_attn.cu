@@ -1134,7 +1134,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
 //
 // A warp joins the parts of one score row of a unit that was cut: the one that its first pair left, and
 // those of the pairs behind it.  The rows of all cut units, few or many, are dealt out over the warps.
-// (A CTA to every 16 rows that a pair might have left: the call with 64 rows over 5120 keys 26.7 us, for JOIN_US.)
+// (A CTA to every 16 rows that a pair might have left: the call with 64 rows over 5120 keys 26.7 us for 22.2.)
 constexpr int kJoinThreads = 256, kMaxPairs = kJoinThreads;
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) tile_join_kernel(const ChunkArgs p, const ChunkParts parts, int pairs) {

@@ -56,64 +56,68 @@ struct CopyShape {
 
 // Sum of v over the threads before this one, and over the block.  met: 32 entries, of its own for calls that follow
 // each other without a barrier between (every warp adds the warps' sums for itself, which saves two).
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* met, int64_t* total) {
+template <typename I>
+__device__ __forceinline__ I block_scan(I v, I* met, I* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t run = v;
+  I run = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, run, o);
+    const I u = __shfl_up_sync(0xffffffffu, run, o);
     if (lane >= o) run += u;
   }
   if (lane == 31) met[warp] = run;
   __syncthreads();
-  int64_t w = met[lane];
-  const int64_t own = w;
+  I w = met[lane];
+  const I own = w;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, w, o);
+    const I u = __shfl_up_sync(0xffffffffu, w, o);
     if (lane >= o) w += u;
   }
   *total = __shfl_sync(0xffffffffu, w, 31);
   return run - v + __shfl_sync(0xffffffffu, w - own, warp);
 }
 
-// A pass over the counts: a warp has 512 ids in a row, a lane every 32nd of them, so that loads and lists are coalesced and
-// ranks are votes.
-constexpr int kIdsPerLane = 16, kIdsPerPass = kPlanThreads * kIdsPerLane;
-__device__ __forceinline__ int64_t id_at(int64_t base, int e) { return base + (threadIdx.x >> 5) * (32 * kIdsPerLane) + e * 32 + (threadIdx.x & 31); }
+// A pass over the counts: a warp has N x 32 ids in a row, a lane every 32nd of them, so that loads and lists are coalesced
+// and ranks are votes.
+template <int N>
+__device__ __forceinline__ int64_t id_at(int64_t base, int e) { return base + (threadIdx.x >> 5) * (32 * N) + e * 32 + (threadIdx.x & 31); }
 // The counts of this lane's ids; -1 behind the end.
+template <int N>
 __device__ __forceinline__ void load_refs(const PoolView& p, int64_t base, int* r) {
 #pragma unroll
-  for (int e = 0; e < kIdsPerLane; ++e) {
-    const int64_t id = id_at(base, e);
+  for (int e = 0; e < N; ++e) {
+    const int64_t id = id_at<N>(base, e);
     r[e] = id < p.n_pages ? p.refs[id] : -1;
   }
 }
 
-// The lowest `want` free ids, ascending, into list; how many there are, at most want.  r: the counts of the first pass.
-__device__ int take_free(const PoolView& p, int want, int32_t* list, int64_t* met, int* r) {
+// The lowest `want` free ids, ascending, into list; how many there are, at most want.  r: the counts of the first pass.  Free
+// pages are mostly found early: short passes, the next one's counts on their way.
+constexpr int kFreeIds = 4;
+__device__ int take_free(const PoolView& p, int want, int32_t* list, int* met, int* r) {
   const unsigned below = (1u << (threadIdx.x & 31)) - 1u;
-  int64_t found = 0;
-  for (int64_t base = 0; base < p.n_pages && found < want; base += kIdsPerPass) {
-    if (base > 0) load_refs(p, base, r);
-    int n = 0;
+  int found = 0;
+  for (int64_t base = 0; base < p.n_pages && found < want; base += kPlanThreads * kFreeIds) {
+    int next[kFreeIds];
+    load_refs<kFreeIds>(p, base + kPlanThreads * kFreeIds, next);
+    int n = 0, total;
 #pragma unroll
-    for (int e = 0; e < kIdsPerLane; ++e) n += __popc(__ballot_sync(0xffffffffu, r[e] == 0));
-    int64_t total;
+    for (int e = 0; e < kFreeIds; ++e) n += __popc(__ballot_sync(0xffffffffu, r[e] == 0));
     // a warp's count once, in its last lane
-    const int64_t before = block_scan((threadIdx.x & 31) == 31 ? n : 0, met, &total);
-    int64_t at = found + __shfl_sync(0xffffffffu, before, 31);
+    int at = found + __shfl_sync(0xffffffffu, block_scan((threadIdx.x & 31) == 31 ? n : 0, met, &total), 31);
 #pragma unroll
-    for (int e = 0; e < kIdsPerLane; ++e) {
+    for (int e = 0; e < kFreeIds; ++e) {
       const unsigned free = __ballot_sync(0xffffffffu, r[e] == 0);
-      const int64_t place = at + __popc(free & below);
-      if (r[e] == 0 && place < want) list[place] = static_cast<int>(id_at(base, e));
+      const int place = at + __popc(free & below);
+      if (r[e] == 0 && place < want) list[place] = static_cast<int>(id_at<kFreeIds>(base, e));
       at += __popc(free);
+      r[e] = next[e];
     }
     found += total;
     __syncthreads();   // met may be written again
   }
-  return static_cast<int>(min(found, static_cast<int64_t>(want)));
+  return min(found, want);
 }
 
 __device__ __forceinline__ int pages_of(const PoolView& p, int len) { return (len + (1 << p.page_shift) - 1) >> p.page_shift; }
@@ -122,70 +126,75 @@ __device__ __forceinline__ int pages_of(const PoolView& p, int len) { return (le
 __device__ __forceinline__ bool mark(unsigned* set, int b) { return atomicOr(&set[b >> 5], 1u << (b & 31)) >> (b & 31) & 1u; }
 
 // FORK: a = sources, b = destinations.  Otherwise (resize): a = sequences (NULL: 0, 1, ..), b = new lengths.
+// Bound by the chain of loads an argument takes (itself, its sequence's length, the table, the count of a page): 2 us, beside 2 of
+// the launch.
 template <bool FORK>
 __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(const PoolView p, const int32_t* a, const int32_t* b, const PlanView out,
                                                                   unsigned int* status) {
-  __shared__ int64_t met[2][32];
+  __shared__ int64_t sums[32];
+  __shared__ int met[32];
   __shared__ unsigned named[2048];
-  int r[kIdsPerLane];
-  load_refs(p, 0, r);   // on their way while the arguments are read
   const int words = (p.n_seq + 31) / 32, most = p.table_stride << p.page_shift;
   for (int i = threadIdx.x; i < words; i += kPlanThreads) named[i] = 0;
+  pdl_wait();
   __syncthreads();
   bool bad = false;
-  for (int i = threadIdx.x; i < p.n; i += kPlanThreads) {   // each sequence written once
-    const int seq = FORK ? b[i] : a ? a[i] : i;
-    bad |= seq < 0 || seq >= p.n_seq || mark(named, seq);
+  PlanItem mine = {};   // of the first 1024 arguments, which are mostly all
+  auto read = [&](int i, PlanItem& it) {
+    it.seq = FORK ? b[i] : a ? a[i] : i;
+    it.from = FORK ? a[i] : it.seq;
+    it.copy_col = -1;
+    const int to = FORK ? 0 : b[i];
+    if (it.seq < 0 || it.seq >= p.n_seq || it.from < 0 || it.from >= p.n_seq || to < 0 || to > most) return false;
+    const int now = p.kv_len[it.seq], src = p.kv_len[it.from];
+    if (mark(named, it.seq) || now < 0 || now > most || src < 0 || src > most) return false;   // each sequence is written once
+    const int kept = FORK ? src : min(now, to), part = kept & ((1 << p.page_shift) - 1);
+    it.len = FORK ? src : to;
+    it.keep = kept >> p.page_shift;
+    if (part > 0 && (FORK || now != to)) {
+      // a page held in part is copied: by fork always, by resize where others hold it too
+      const int page = p.table[static_cast<int64_t>(it.from) * p.table_stride + it.keep];
+      if (page < 0 || page >= p.n_pages) return false;
+      if (FORK || p.refs[page] > 1) {
+        it.copy_src = page;
+        it.copy_col = it.keep;
+        it.copy_rows = part;
+      }
+    }
+    it.drop1 = pages_of(p, now);
+    it.drop0 = FORK ? 0 : min(pages_of(p, to), it.drop1);
+    it.add0 = FORK ? 0 : it.drop1;
+    it.add1 = FORK ? 0 : max(pages_of(p, to), it.drop1);
+    return true;
+  };
+  for (int i = threadIdx.x; i < p.n; i += kPlanThreads) {
+    PlanItem it = {};
+    bad |= !read(i, it);
+    if (i == threadIdx.x) mine = it; else out.items[i] = it;
   }
+  int r[kFreeIds];
+  load_refs<kFreeIds>(p, 0, r);   // on their way under the sums
   bad = __syncthreads_or(bad);
   int wanted = 0, copies = 0;
   for (int i0 = 0; i0 < p.n && !bad; i0 += kPlanThreads) {
     const int i = i0 + threadIdx.x;
     PlanItem it = {};
-    int take = 0;
-    bool wrong = false;
-    it.copy_col = -1;
-    if (i < p.n) {
-      it.seq = FORK ? b[i] : a ? a[i] : i;
-      it.from = FORK ? a[i] : it.seq;
-      const int to = FORK ? 0 : b[i];
-      wrong = it.from < 0 || it.from >= p.n_seq || (FORK && (named[it.from >> 5] >> (it.from & 31) & 1u)) || to < 0 || to > most;
-      const int now = p.kv_len[it.seq], src = wrong ? 0 : p.kv_len[it.from];
-      wrong |= now < 0 || now > most || src < 0 || src > most;
-      if (!wrong) {
-        const int kept = FORK ? src : min(now, to), part = kept & ((1 << p.page_shift) - 1);
-        it.len = FORK ? src : to;
-        it.keep = kept >> p.page_shift;
-        // a page held in part is copied: fork; resize where the length changes and others hold it too
-        bool split = part > 0 && (FORK || now != to);
-        if (split) {
-          it.copy_src = p.table[static_cast<int64_t>(it.from) * p.table_stride + it.keep];
-          wrong = it.copy_src < 0 || it.copy_src >= p.n_pages;
-          split = !wrong && (FORK || p.refs[it.copy_src] > 1);
-        }
-        if (split) {
-          it.copy_col = it.keep;
-          it.copy_rows = part;
-        }
-        it.drop1 = pages_of(p, now);
-        it.drop0 = FORK ? 0 : min(pages_of(p, to), it.drop1);
-        it.add0 = FORK ? 0 : it.drop1;
-        it.add1 = FORK ? 0 : max(pages_of(p, to), it.drop1);
-        take = (split ? 1 : 0) + it.add1 - it.add0;
-      }
-    }
+    if (i < p.n) it = i0 == 0 ? mine : out.items[i];
+    const bool copied = i < p.n && it.copy_col >= 0;
+    const bool wrong = FORK && i < p.n && (named[it.from >> 5] >> (it.from & 31) & 1u);   // a source that is written
+    const int take = i < p.n ? (copied ? 1 : 0) + it.add1 - it.add0 : 0;
     // new pages, and above them copies and wrong arguments, in one sum
     int64_t total;
-    const int64_t before = block_scan(take | static_cast<int64_t>(it.copy_col >= 0) << 32 | static_cast<int64_t>(wrong) << 48, met[0], &total);
+    const int64_t before = block_scan(take | static_cast<int64_t>(copied) << 32 | static_cast<int64_t>(wrong) << 48, sums, &total);
     it.first = wanted + static_cast<int>(before & 0xffffffff);
     wanted = static_cast<int>(min(wanted + (total & 0xffffffff), static_cast<int64_t>(p.n_pages) + 1));
     copies += static_cast<int>(total >> 32 & 0xffff);
     bad |= total >> 48 != 0;
     if (i < p.n) out.items[i] = it;
-    __syncthreads();   // met may be written again
+    if (i0 + kPlanThreads < p.n) __syncthreads();   // sums may be written again
   }
   const bool over = wanted > p.n_pages;
-  const int found = bad || over ? 0 : take_free(p, wanted, out.list, met[1], r);
+  const int found = bad || over ? 0 : take_free(p, wanted, out.list, met, r);
   if (threadIdx.x == 0) {
     const bool few = !bad && (over || found < wanted);
     if (bad) flag_status(status, QCF_DEV_BAD_INDEX);
@@ -194,18 +203,20 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(const PoolView
   }
 }
 
+constexpr int kCompactIds = 16, kCompactPass = kPlanThreads * kCompactIds;
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PoolView p, const PlanView out, int32_t* n_live,
                                                                     unsigned int* status) {
   __shared__ int64_t met[2][32];
   const unsigned below = (1u << (threadIdx.x & 31)) - 1u;
   const bool last = (threadIdx.x & 31) == 31;
-  int r[kIdsPerLane];
+  int r[kCompactIds];
   int64_t total;
   int count = 0;
-  for (int64_t base = 0; base < p.n_pages; base += kIdsPerPass) {
-    load_refs(p, base, r);
+  pdl_wait();
+  for (int64_t base = 0; base < p.n_pages; base += kCompactPass) {
+    load_refs<kCompactIds>(p, base, r);
 #pragma unroll
-    for (int e = 0; e < kIdsPerLane; ++e) count += r[e] > 0;
+    for (int e = 0; e < kCompactIds; ++e) count += r[e] > 0;
   }
   const int most = p.table_stride << p.page_shift;
   bool bad = false;
@@ -217,20 +228,20 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PoolVi
   bad = total >> 32 != 0;
   const int live = static_cast<int>(total & 0xffffffff);
   int holes = 0, moves = 0;   // below `live` there are as many free pages as live ones above
-  for (int64_t base = 0; base < p.n_pages; base += kIdsPerPass) {
-    if (p.n_pages > kIdsPerPass) load_refs(p, base, r);   // one pass has them still
+  for (int64_t base = 0; base < p.n_pages; base += kCompactPass) {
+    if (p.n_pages > kCompactPass) load_refs<kCompactIds>(p, base, r);   // one pass has them still
     int h = 0, m = 0;
 #pragma unroll
-    for (int e = 0; e < kIdsPerLane; ++e) {
-      const int64_t id = id_at(base, e);
+    for (int e = 0; e < kCompactIds; ++e) {
+      const int64_t id = id_at<kCompactIds>(base, e);
       h += __popc(__ballot_sync(0xffffffffu, id < live && r[e] <= 0));
       m += __popc(__ballot_sync(0xffffffffu, id >= live && r[e] > 0));
     }
     const int64_t before = __shfl_sync(0xffffffffu, block_scan(last ? h | static_cast<int64_t>(m) << 32 : 0, met[1], &total), 31);
     int ha = holes + static_cast<int>(before & 0xffffffff), ma = moves + static_cast<int>(before >> 32);
 #pragma unroll
-    for (int e = 0; e < kIdsPerLane; ++e) {
-      const int64_t id = id_at(base, e);
+    for (int e = 0; e < kCompactIds; ++e) {
+      const int64_t id = id_at<kCompactIds>(base, e);
       const bool hole = id < live && r[e] <= 0, move = id >= live && r[e] > 0;   // -1 behind the last page: neither
       const unsigned hs = __ballot_sync(0xffffffffu, hole), ms = __ballot_sync(0xffffffffu, move);
       if (hole) out.list[ha + __popc(hs & below)] = static_cast<int>(id);
@@ -448,8 +459,7 @@ template <bool FORK>
 static qcf_status pages_launch(const char* who, const PoolCall& k, const int32_t* a, const int32_t* b, cudaStream_t st) {
   {
     LaunchScope ls(KC_PAGES, st);
-    pages_plan_kernel<FORK><<<1, kPlanThreads, 0, st>>>(k.p, a, b, k.plan, device_status_ptr());
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_pdl(pages_plan_kernel<FORK>, dim3(1), dim3(kPlanThreads), 0, st, k.p, a, b, k.plan, device_status_ptr());
     if (e != cudaSuccess) return cuda_error(e, who);
   }
   LaunchScope ls(KC_PAGES, st);
@@ -496,8 +506,7 @@ qcf_status qcf_pages_compact(const qcf_page_pool* pool, int32_t* n_live, void* w
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   {
     LaunchScope ls(KC_PAGES, st);
-    compact_plan_kernel<<<1, kPlanThreads, 0, st>>>(k.p, k.plan, n_live, device_status_ptr());
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_pdl(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, k.p, k.plan, n_live, device_status_ptr());
     if (e != cudaSuccess) return cuda_error(e, "qcf_pages_compact: launch");
   }
   LaunchScope ls(KC_PAGES, st);
