@@ -24,6 +24,15 @@
 // A unit with rows in a alone (single tokens, short questions) takes its key tiles by turns: a has the
 // even ones and b the odd ones of the same rows, and the output joins the two.
 // Tensor memory columns: S_a 0, S_b 128 (the weights take the first 64 of each), O_a 256, O_b 256 + DP.
+//
+// Bound: a causal prompt of 17984 tokens, 64 heads over 8: 3.32 to 3.39 ms, 1.57 to 1.60 PFLOP/s (cuBLAS: 1.89 in bursts, 1.72 kept up
+// under the power limit, where this kernel runs too).  A pair of row tiles takes 2700 to 2900 cycles a key tile, 2048 of them products.
+// One row tile's own chain is as long: S 512, its arrival 150, the softmax's two halves 1100 and 450, the
+// arrival at the issuer 220, the last products 256.  Two row tiles are what fits tensor memory at head dim 128; at 64, with
+// half the products to the same softmax, the powers bound (16384 tokens, 32 heads over 8: 1184 us, 0.93 PFLOP/s).
+// A unit costs another 5000 cycles (queries, the first scores, a masked tile, the output), which bounds many short prompts:
+// ten of 512 tokens 40.5 us, floor 15.7.  Small calls: the launch 2.5 us, the deal 2.5, loads and one tile 4, code
+// that is fetched as it runs the first time: four questions of up to 64 tokens 13.7 us.
 #include <algorithm>
 #include <cmath>
 
@@ -35,9 +44,12 @@ constexpr int kMaxChunkSeqs = 8000;   // the deal keeps 12 bytes of each where t
 constexpr int kTileKeys = 128;
 constexpr int kTileThreads = 384;
 constexpr int kTileRows = 512;        // score rows of a unit
-// The deal is by cost: so many for a unit, for a key tile of a unit with one row tile in use, with both
+// The deal is by cost: so many for a unit, for a key tile of a unit with one row tile in use (1680 cycles), with both (2800).
 constexpr int kUnitCost = 3, kTileCost1 = 2, kTileCost2 = 3;
-constexpr int kMinCut = 3;            // tiles at least on each side of a cut through a unit
+// Tiles at least on each side of a cut through a unit: a cut costs the sums' way out and the join.  2 parts of 512
+// rows: 8 us of the call.  Prompts of 1024 / 2048 / 4096 tokens, 64 rows over 5120 keys, in us: 3 tiles 26.8 / 52.0 / 123.1, 22.6;
+// 4 24.7 / 51.3 / 122.4, 23.8; 6 21.9 / 51.9 / 118.0, 24.4; 8 21.9 / 52.2 / 117.2, 26.0.
+constexpr int kMinCut = 3;
 constexpr int kMinCost = 9;           // dealt to a pair at least
 constexpr int kSegRing = 4;
 
@@ -190,7 +202,7 @@ __device__ __forceinline__ uint64_t sdesc_mnmajor_sw64(uint32_t smem_addr) {
 // A run of sequences with a few new rows each (single tokens) within 32 aligned ones goes as a group: its
 // rows lie side by side in the batch and make one unit, which reads the shared prefix once for all of them and
 // then each one's own tiles, which the rows of the others do not see.  (44 single tokens of 32 heads over a prefix of 5120 tokens
-// among chunks of 2640: 423 us for the call with a unit to each.)  It stands in the place of its
+// among chunks of 2640: 336 us for the call, 423 with a unit to each.)  It stands in the place of its
 // first sequence; its length is kept as -1 - (32 own tiles + (sequences - 1)).
 struct Span {
   int row0, nq, len;   // nq 0: no rows, or those of a group that began before
@@ -917,7 +929,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         const int high = k.seq < 0 ? k.len - k.key0 : k.seq == seq ? own + 1 - k.key0 : 0;
         const int low = p.window ? (k.seq < 0 ? b.prefix_len : 0) + own + 1 - p.window - k.key0 : 0;
         if (__any_sync(kAll, high < kTileKeys || low > 0 || bad8)) {
-          // one bit to each key: comparisons of every key with both ends took 1500 cycles
+          // one bit to each key: 800 cycles; comparisons of every key with both ends took 1500, skipping keys by eights more
 #pragma unroll
           for (int w = 0; w < kTileKeys / 32; ++w) {
             uint32_t see = bits_below(high - 32 * w) & ~bits_below(low - 32 * w);
