@@ -73,7 +73,7 @@ struct TileCfg {
   static constexpr int VCOLS = DP / 2, VTILE = kTileKeys * VCOLS * 2;   // its columns of 128 values
   static constexpr int STAGES = DP == 128 ? 3 : 8;
   static constexpr int OBOX = 128 * 128, OTILE = 2 * OBOX;              // output of 128 score rows, 128 bytes of each to a box
-  static constexpr int FIXED = 3072;
+  static constexpr int FIXED = 3 * 1024;
   static constexpr int SMEM = 2 * QTILE + STAGES * (KTILE + VTILE) + 2 * OTILE + FIXED;
 };
 static_assert(TileCfg<128>::SMEM <= 232448 && TileCfg<64>::SMEM <= 232448, "227 KB of a CTA");
@@ -167,6 +167,15 @@ __device__ __forceinline__ void umma_f16_ts_pair(bool one, uint32_t d_tmem, uint
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(one))
       : "memory");
 }
+// umma_f16_ts_pair that leaves the rows with a set bit in `off` (128 of the first CTA, 128 of the second) as they are.
+__device__ __forceinline__ void umma_f16_ts_pair_rows(bool one, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, const uint32_t* off) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n setp.eq.b32 p, 0, 0;\n setp.ne.b32 e, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8, %9, %10, %11, %12}, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(static_cast<uint32_t>(one)), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]), "r"(off[4]),
+      "r"(off[5]), "r"(off[6]), "r"(off[7])
+      : "memory");
+}
 // Arrives on this barrier in both CTAs once every product issued by this thread is complete.
 __device__ __forceinline__ void umma_commit_pair(bool one, uint64_t* bar) {
   asm volatile(
@@ -201,8 +210,10 @@ __device__ __forceinline__ uint64_t sdesc_mnmajor_sw64(uint32_t smem_addr) {
 
 // A run of sequences with a few new rows each (single tokens) within 32 aligned ones goes as a group: its
 // rows lie side by side in the batch and make one unit, which reads the shared prefix once for all of them and
-// then each one's own tiles, which the rows of the others do not see.  (44 single tokens of 32 heads over a prefix of 5120 tokens
-// among chunks of 2640: 336 us for the call, 423 with a unit to each.)  It stands in the place of its
+// then each one's own tiles, which the rows of the others do not see: their weights are 0, and their sums
+// are left out of the product, for 0 x NaN is NaN and one sequence's values must not spoil another.  (44
+// single tokens of 32 heads over a prefix of 5120 tokens among chunks of 2640: 386 us for the call, 423 with
+// a unit to each; 342 with all rows in the products of all tiles.)  It stands in the place of its
 // first sequence; its length is kept as -1 - (32 own tiles + (sequences - 1)).
 struct Span {
   int row0, nq, len;   // nq 0: no rows, or those of a group that began before
@@ -218,7 +229,7 @@ __device__ __forceinline__ int warp_scan(int v) {
   return v;
 }
 // Of sequence base + lane, base a multiple of 32; all lanes of a warp together.
-template <bool PAGED>
+template <bool GROUPS>
 __device__ __forceinline__ Span span_at(const BatchView& b, const ChunkArgs& p, int base, bool* bad) {
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31, seq = base + lane;
@@ -226,7 +237,7 @@ __device__ __forceinline__ Span span_at(const BatchView& b, const ChunkArgs& p, 
   if (seq < b.n_seq) q = chunk_span(b, seq);
   *bad = q.bad;
   Span s{q.row0, q.nq, q.len};
-  if (!PAGED || p.group == 0) return s;
+  if (!GROUPS) return s;
   const bool small = seq < b.n_seq && !q.bad && q.nq <= p.group;
   const unsigned in = __ballot_sync(kAll, small), rows = __ballot_sync(kAll, small && q.nq > 0);
   const int tiles = small && q.nq > 0 ? (q.len + kTileKeys - 1) / kTileKeys : 0;
@@ -249,12 +260,12 @@ struct RowBlock {
 __device__ __forceinline__ int tile_of(int prefix, int pos) {
   return pos < prefix ? pos / kTileKeys : (prefix + kTileKeys - 1) / kTileKeys + (pos - prefix) / kTileKeys;
 }
-template <bool PAGED>
+template <bool GROUPS>
 __device__ __forceinline__ RowBlock row_block(const BatchView& b, const ChunkArgs& p, int nq, int len, int i) {
   RowBlock k;
   k.i0 = i * 4 * p.per;
   k.ntok = min(4 * p.per, nq - k.i0);
-  if (PAGED && len < 0) {
+  if (GROUPS && len < 0) {
     k.t0 = 0;
     k.end = k.end_a = (b.prefix_len + kTileKeys - 1) / kTileKeys + group_tiles(len);
     return k;
@@ -319,7 +330,7 @@ __device__ __forceinline__ int deal_scan(int tid, int v, int* met, int* total) {
 }
 
 // Finds where this pair's share begins; blk: scratch for 3 n_seq + 1 ints.
-template <bool PAGED>
+template <bool GROUPS>
 __device__ void find_share(int tid, const BatchView& b, const ChunkArgs& p, int Hkv, int pair, int pairs, int* blk, int* met, DealStart* start,
                            unsigned int* status) {
   const int R = 4 * p.per, most = b.n_rows / R + b.n_seq;   // row blocks at most
@@ -330,7 +341,7 @@ __device__ void find_share(int tid, const BatchView& b, const ChunkArgs& p, int 
   int mine = 0, all, total;
   for (int s = tid; s - (tid & 31) < b.n_seq; s += kDealThreads) {
     bool bad;
-    const Span q = span_at<PAGED>(b, p, s - (tid & 31), &bad);
+    const Span q = span_at<GROUPS>(b, p, s - (tid & 31), &bad);
     if (bad && blockIdx.x == 0) flag_status(status, QCF_DEV_BAD_INDEX);
     if (s < b.n_seq) {
       blk[s] = (q.nq + R - 1) / R;
@@ -370,7 +381,7 @@ __device__ void find_share(int tid, const BatchView& b, const ChunkArgs& p, int 
     int seq = first;
     for (int i = b0; i < b1; ++i) {
       while (i >= blk[seq + 1]) ++seq;
-      if (visit(seq, i - blk[seq], Hkv * unit_cost(row_block<PAGED>(b, p, nqs[seq], lens[seq], i - blk[seq]), p.per))) return;
+      if (visit(seq, i - blk[seq], Hkv * unit_cost(row_block<GROUPS>(b, p, nqs[seq], lens[seq], i - blk[seq]), p.per))) return;
     }
   };
   int cost = 0;
@@ -393,7 +404,7 @@ __device__ void find_share(int tid, const BatchView& b, const ChunkArgs& p, int 
 }
 
 // Walks a pair's share, all lanes of a warp alike; they keep the spans of 32 sequences.
-template <bool PAGED>
+template <bool GROUPS>
 struct TileWalk {
   const BatchView& b;
   const ChunkArgs& p;
@@ -409,7 +420,7 @@ struct TileWalk {
   __device__ void keep(int from) {
     base = from;
     bool bad;
-    const Span s = span_at<PAGED>(b, p, from, &bad);
+    const Span s = span_at<GROUPS>(b, p, from, &bad);
     my_row0 = s.row0;
     my_nq = s.nq;
     my_len = s.len;
@@ -433,7 +444,7 @@ struct TileWalk {
     row0 = at.row0;
     nq = at.nq;
     len = at.len;
-    k = row_block<PAGED>(b, p, nq, len, block);
+    k = row_block<GROUPS>(b, p, nq, len, block);
     g = (begin - pos) / unit_cost(k, p.per);
     pos += g * unit_cost(k, p.per);
   }
@@ -466,7 +477,7 @@ struct TileWalk {
         s.row0 = row0 + k.i0;
         s.ntok = k.ntok;
         s.g = g;
-        s.pos = PAGED && len < 0 ? 0 : len - nq + k.i0;
+        s.pos = GROUPS && len < 0 ? 0 : len - nq + k.i0;
         s.len = len;
         s.t0 = k.t0 + from;
         s.nt = to - from;
@@ -493,7 +504,7 @@ struct TileWalk {
           block = 0;
           next_seq();
         }
-        if (live) k = row_block<PAGED>(b, p, nq, len, block);
+        if (live) k = row_block<GROUPS>(b, p, nq, len, block);
       }
       if (some) return true;
     }
@@ -508,7 +519,8 @@ constexpr uint32_t idesc_pair(int N, bool b_mn_major) {
   return std::is_same<T, __half>::value ? idesc_bf16_f32(256, N, b_mn_major) & ~((1u << 7) | (1u << 10)) : idesc_bf16_f32(256, N, b_mn_major);
 }
 
-template <typename T, int DP, bool PAGED>
+// GROUPS: a kernel of its own, for what groups need in the issuing warps costs other calls 3 %.
+template <typename T, int DP, bool PAGED, bool GROUPS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     tile_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmP, const PagedView c, const BatchView b, const ChunkArgs p, const ChunkParts parts,
@@ -576,7 +588,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
   pdl_wait();
   if (warp >= 4) {
-    find_share<PAGED>(threadIdx.x - 128, b, p, c.Hkv, pair, pairs, reinterpret_cast<int*>(kbuf), met, start, status);
+    find_share<GROUPS>(threadIdx.x - 128, b, p, c.Hkv, pair, pairs, reinterpret_cast<int*>(kbuf), met, start, status);
     fence_proxy_async_smem();   // the deal used the rings
   }
   tc_fence_before();
@@ -599,14 +611,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   };
   auto release_segment = [&] { mbar_arrive(&seg_empty[(seg_n - 1) % kSegRing]); };
 
-  // The sequences of a grouped unit, one to a lane: own tokens, first own tile.
-  int sub_len = 0, sub_tile = 0;
+  // The sequences of a grouped unit, one to a lane: own tokens, first own tile, first token in the unit, new rows.
+  int sub_len = 0, sub_tile = 0, sub_tok = 0, sub_nq = 0;
   auto open_group = [&](const Segment& s) {
-    if (!PAGED || s.len >= 0) return;
+    if (!GROUPS || s.len >= 0) return;
     int tiles = 0;
+    sub_tok = 0x7fffffff;
     if (lane < group_size(s.len)) {
       const SeqSpan q = seq_span(b, s.seq + lane);
       sub_len = q.len;
+      sub_tok = q.row0 - s.row0;
+      sub_nq = q.nq;
       tiles = q.nq > 0 ? (q.len + kTileKeys - 1) / kTileKeys : 0;
     }
     sub_tile = warp_scan(tiles) - tiles;
@@ -617,7 +632,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   };
   auto key_tile = [&](const Segment& s, int t) {
     if (t < np) return KeyTile{-1, t * kTileKeys, b.prefix_len};
-    if (!PAGED || s.len >= 0) return KeyTile{s.seq, (t - np) * kTileKeys, s.len};
+    if (!GROUPS || s.len >= 0) return KeyTile{s.seq, (t - np) * kTileKeys, s.len};
     const int sub = max(__popc(__ballot_sync(kAll, lane < group_size(s.len) && sub_tile <= t - np)) - 1, 0);
     return KeyTile{s.seq + sub, (t - np - __shfl_sync(kAll, sub_tile, sub)) * kTileKeys, __shfl_sync(kAll, sub_len, sub)};
   };
@@ -637,7 +652,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       const int rows = PAGED ? min(1 << c.page_shift, keys) : keys, boxes = PAGED ? keys / rows : 1;
       DealStart at0 = *start;
       if (!is_k) at0.seq = -1;
-      TileWalk<PAGED> walk(b, p, at0, c.Hkv, pair);
+      TileWalk<GROUPS> walk(b, p, at0, c.Hkv, pair);
       Segment s;
       int n = 0, tails = 0, units = 0;
       bool ok = true;
@@ -832,11 +847,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
           const KeyTile kt = key_tile(s, t0 + at - n);
           if (kt.len - kt.key0 < kTileKeys) fence_cluster();   // zeros of the V producers
           const uint64_t vd = v_desc + at % ST * (Cfg::VTILE >> 4);
+          const bool grouped = GROUPS && s.len < 0, others = grouped && kt.seq >= 0;   // others: rows that do not see these keys
+          uint32_t off[8];
+          if (others) {
+            const int sub = kt.seq - s.seq, tok = __shfl_sync(kAll, sub_tok, sub), tok_end = tok + __shfl_sync(kAll, sub_nq, sub);
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+              const int t0 = (split ? w >> 2 : 2 * x + (w >> 2)) * p.per, row0 = 32 * (w & 3);   // the row tile's first token, the word's first row
+              const uint32_t on = bits_below((min(tok_end, t0 + p.per) - t0) * a.G - row0) & ~bits_below((tok - t0) * a.G - row0);
+              off[w] = __reduce_or_sync(kAll, ~on);   // the same in all lanes: this leaves it in a uniform register, which the products take
+            }
+          }
+          const uint32_t onto = grouped || i > 0 ? 1u : 0u;   // the softmax warps have cleared the sums of a group
           auto weigh = [&](int half) {   // O_x += P_x V over 64 keys
             tc_fence_after();
+            if (others) {
+#pragma unroll
+              for (int kk = half * (kTileKeys / 32); kk < (half + 1) * (kTileKeys / 32); ++kk)
+                umma_f16_ts_pair_rows(one, tmem + 256 + x * DP, tmem + x * 128 + kk * 8, vd + kk * (V_STEP >> 4), idesc_o, off);
+              return;
+            }
 #pragma unroll
             for (int kk = half * (kTileKeys / 32); kk < (half + 1) * (kTileKeys / 32); ++kk)
-              umma_f16_ts_pair(one, tmem + 256 + x * DP, tmem + x * 128 + kk * 8, vd + kk * (V_STEP >> 4), idesc_o, (i > 0 || kk > 0) ? 1u : 0u);
+              umma_f16_ts_pair(one, tmem + 256 + x * DP, tmem + x * 128 + kk * 8, vd + kk * (V_STEP >> 4), idesc_o, kk > 0 ? 1u : onto);
           };
           // a begins, b follows while a has tiles left; who is alone gives itself the turn
           if ((x == 0 ? i == 0 : i >= nt_a) && one) mbar_arrive(&p_ready[2 * x]);
@@ -892,18 +925,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       const int tok = place * p.per + pl;
       int seq = s.seq, own = s.pos + min(tok, s.ntok - 1);
       open_group(s);
-      if (PAGED && s.len < 0) {
-        int from = 0x7fffffff, nq = 0, sub = 0;   // of this lane's sequence: its first token in the group, its rows
-        if (lane < group_size(s.len)) {
-          from = b.row_start[s.seq + lane] - s.row0;
-          nq = b.row_start[s.seq + lane + 1] - s.row0 - from;
-        }
+      if (GROUPS && s.len < 0) {
+        int sub = 0;
         const int mine_tok = min(tok, s.ntok - 1);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
-          if (__shfl_sync(kAll, from, sub + o) <= mine_tok) sub += o;
+          if (__shfl_sync(kAll, sub_tok, sub + o) <= mine_tok) sub += o;
         seq = s.seq + sub;
-        own = __shfl_sync(kAll, sub_len, sub) - __shfl_sync(kAll, nq, sub) + mine_tok - __shfl_sync(kAll, from, sub);
+        own = __shfl_sync(kAll, sub_len, sub) - __shfl_sync(kAll, sub_nq, sub) + mine_tok - __shfl_sync(kAll, sub_tok, sub);
+        if (mine > 0) {   // own tiles leave other rows' sums as they are: all begin with 0
+#pragma unroll 1
+          for (int cc = 0; cc < DP / 16; ++cc) {
+            const float zero[16] = {};
+            tmem_st16(o_tm + cc * 16, zero);
+          }
+          tmem_wait_st();
+        }
       }
       auto page_bad = [&](const KeyTile& k) {   // the page of this lane's 8 keys of a tile lies outside the cache
         const int key = k.key0 + lane * 8;
@@ -1256,7 +1293,7 @@ struct ChunkSource {
   int64_t kv_stride;   // packed: entries from row to row
 };
 
-template <typename T, int DP, bool PAGED>
+template <typename T, int DP, bool PAGED, bool GROUPS>
 static qcf_status tile_launch(const char* who, const ChunkSource& src, const PagedView& c, const BatchView& b, const ChunkArgs& p, const ChunkParts& w,
                               cudaStream_t st) {
   using Cfg = TileCfg<DP>;
@@ -1284,12 +1321,12 @@ static qcf_status tile_launch(const char* who, const ChunkSource& src, const Pag
   if (!ok) return set_error(QCF_ERR_CUDA, "%s: tensor map encoding failed", who);
   static PerDevice<cudaError_t> smem_attr;
   cudaError_t e = smem_attr.get(current_device(), [] {
-    return cudaFuncSetAttribute(tile_attn_kernel<T, DP, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+    return cudaFuncSetAttribute(tile_attn_kernel<T, DP, PAGED, GROUPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
   });
   if (e != cudaSuccess) return cuda_error(e, who);
   {
     LaunchScope ls(KC_CHUNK_ATTN, st);
-    e = launch_pdl(tile_attn_kernel<T, DP, PAGED>, dim3(2 * tile_pairs()), dim3(kTileThreads), Cfg::SMEM, st, tk, tv, tq, to, tp, c, b, p, w,
+    e = launch_pdl(tile_attn_kernel<T, DP, PAGED, GROUPS>, dim3(2 * tile_pairs()), dim3(kTileThreads), Cfg::SMEM, st, tk, tv, tq, to, tp, c, b, p, w,
                    device_status_ptr());
     if (e != cudaSuccess) return cuda_error(e, who);
   }
@@ -1299,6 +1336,15 @@ static qcf_status tile_launch(const char* who, const ChunkSource& src, const Pag
   return e == cudaSuccess ? QCF_OK : cuda_error(e, who);
 }
 
+template <typename T, bool PAGED>
+static qcf_status tile_launch_type(const char* who, const ChunkSource& src, const PagedView& c, const BatchView& b, const ChunkArgs& p, const ChunkParts& w,
+                                   cudaStream_t st) {
+  if constexpr (PAGED)
+    if (p.group > 0)
+      return p.D <= 64 ? tile_launch<T, 64, PAGED, true>(who, src, c, b, p, w, st) : tile_launch<T, 128, PAGED, true>(who, src, c, b, p, w, st);
+  return p.D <= 64 ? tile_launch<T, 64, PAGED, false>(who, src, c, b, p, w, st) : tile_launch<T, 128, PAGED, false>(who, src, c, b, p, w, st);
+}
+
 template <bool PAGED>
 static qcf_status chunk_launch(const char* who, int dtype, const ChunkSource& src, const PagedView& c, const BatchView& b, ChunkArgs p, void* ws,
                                size_t ws_bytes, cudaStream_t st) {
@@ -1306,9 +1352,8 @@ static qcf_status chunk_launch(const char* who, int dtype, const ChunkSource& sr
   ChunkParts w;
   const size_t need = parts_layout(b, p.D, p.window, p.group, ws, &w);
   if (need > 0 && (!ws || ws_bytes < need)) return set_error(QCF_ERR_WORKSPACE, "%s: workspace %zu < %zu", who, ws_bytes, need);
-  if (dtype == QCF_BF16)
-    return p.D <= 64 ? tile_launch<__nv_bfloat16, 64, PAGED>(who, src, c, b, p, w, st) : tile_launch<__nv_bfloat16, 128, PAGED>(who, src, c, b, p, w, st);
-  return p.D <= 64 ? tile_launch<__half, 64, PAGED>(who, src, c, b, p, w, st) : tile_launch<__half, 128, PAGED>(who, src, c, b, p, w, st);
+  if (dtype == QCF_BF16) return tile_launch_type<__nv_bfloat16, PAGED>(who, src, c, b, p, w, st);
+  return tile_launch_type<__half, PAGED>(who, src, c, b, p, w, st);
 }
 
 static qcf_status check_sizes(const char* who, const PagedView& c, const BatchView& b, int Hq) {

@@ -277,6 +277,26 @@ def test_chunk_groups_leave_out_bad_sequences_and_pages(Q):
     assert torch.equal(Q.qcf_paged_chunk_attn(cache, batch, q, 0.1), ref) and rlse.shape == lse.shape
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (16, 1, 64), (7, 1, 128)])
+def test_chunk_groups_keep_one_sequences_nan_to_itself(Q, Hq, Hkv, D):
+    """NaN and infinity in keys and values of some sequences of a group: the others' rows have the bits they have without."""
+    new, lens = [1, 1, 2, 1, 1, 0, 1, 3, 1, 1], [300, 5, 129, 640, 1, 9, 128, 77, 200, 256]
+    bt = R.Batch(new, lens, 900, Hkv, D, 16, "rows", torch.bfloat16, seed=4).fill()
+    q = bt.randn(bt.n_rows, Hq, D)
+    cache, batch = bt.bind(Q)
+    ref, rlse = Q.qcf_paged_chunk_attn(cache, batch, q, 0.1, want_lse=True)
+    o, _, tol, _ = P.batch_attention(bt, q, 0.1)
+    within(ref, o, tol, "before")
+    for b, j, what, value in ((0, 299, bt.v, float("nan")), (3, 0, bt.v, float("inf")), (6, 127, bt.k, float("nan")), (7, 10, bt.v, float("-inf"))):
+        page, row = (int(t[j]) for t in bt.own_at(b))
+        bt.rows(what)[page, row] = value
+    got, lse = Q.qcf_paged_chunk_attn(cache, batch, q, 0.1, want_lse=True)
+    hurt = {0, 3, 6, 7}
+    for b, r, n in bt.spans():
+        same = torch.equal(got[r: r + n], ref[r: r + n]) and torch.equal(lse[r: r + n], rlse[r: r + n])
+        assert same != (b in hurt) or n == 0, f"sequence {b}"
+
+
 def test_chunk_groups_of_many(Q):
     """Hundreds of single tokens, a cache that changes under a captured call."""
     lens = [(i * 29) % 260 + 1 for i in range(300)]
