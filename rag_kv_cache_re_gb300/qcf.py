@@ -593,7 +593,9 @@ def qcf_shared_prefix_attn(cache: PagedKV, batch: PagedBatch, q: torch.Tensor, s
 
 # ------------------------------------------------------------------ whole prompts and chunks of them
 
-def _attn_out(q: torch.Tensor, out: Optional[torch.Tensor], want_lse: bool, dev: int, stream):
+def _attn_out(q: torch.Tensor, out: Optional[torch.Tensor], want_lse: bool, dev: int, stream, *counts: int):
+    if not all(-2**31 <= int(n) < 2**31 for n in counts):
+        _bad("max_len and window must be 32-bit counts")
     if out is None:
         out = _empty(q.shape, q.dtype, dev, stream)
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.get_device() != dev:
@@ -616,7 +618,7 @@ def qcf_packed_causal_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ro
     if row_start.dim() != 1 or row_start.numel() < 1:
         _bad("row_start must hold a start per sequence and the end of the last")
     _need_i32(row_start, "row_start")
-    out, lse = _attn_out(q, out, want_lse, dev, stream)
+    out, lse = _attn_out(q, out, want_lse, dev, stream, max_len, window)
     n_seq = row_start.numel() - 1
     if n and n_seq:   # empty tensors have no address to pass
         nb = _lib.lib().qcf_packed_causal_attn_workspace_size(n_seq, n, max_len, Hq, Hk, D)
@@ -633,7 +635,7 @@ def qcf_paged_chunk_attn(cache: PagedKV, batch: PagedBatch, q: torch.Tensor, sca
     pages.  Returns out (a new tensor unless given; padding rows are not written), with lse if asked."""
     _cache_and_batch(cache, batch)
     Hq, qs = _batch_rows(cache, batch, q, "q")
-    out, lse = _attn_out(q, out, want_lse, cache.dev, stream)
+    out, lse = _attn_out(q, out, want_lse, cache.dev, stream, window)
     if not batch.empty:
         nb = batch.chunk_workspace_size(cache, Hq)
         ws = _empty(nb, torch.uint8, cache.dev, stream) if nb else None
@@ -648,7 +650,8 @@ class PagePool:
     """The pages of a cache and the sequences that hold them (see qcf_page_pool): `caches` the PagedKV of
     every layer, all of one layout; refs [n_pages], page_table [n_seq][columns] and kv_len [n_seq] int32 on the
     device.  page_table and kv_len also serve a PagedBatch.  Calls with one pool are made on one stream, or
-    ordered by the caller: each changes the pool, and they share its scratch."""
+    ordered by the caller: each changes the pool, and they share its scratch.  A pool outlives the graphs
+    that hold calls of it."""
 
     def __init__(self, caches: Sequence[PagedKV], refs: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor):
         caches = list(caches)
@@ -673,6 +676,7 @@ class PagePool:
         self._nb = _lib.lib().qcf_pages_workspace_size(self.ref, n_seq)
         self._ws = torch.empty(max(self._nb, 1), dtype=torch.uint8, device=refs.device)
         self._ws_ptr = self._ws.data_ptr()
+        self._streams = {_raw_stream(None, self.dev)}   # that the allocator knows to use the scratch
 
     @classmethod
     def empty(cls, caches: Sequence[PagedKV], n_seq: int, max_len: int) -> "PagePool":
@@ -689,9 +693,15 @@ class PagePool:
             _bad(f"every argument must be a contiguous int32 tensor of {n} entries on the pool's device")
         return t.data_ptr()
 
-    def _here(self):
+    def _here(self, stream) -> int:
+        """The stream of a call that is about to be made."""
         if self.dev != torch.cuda.current_device():
             _bad("tensors must be on the current CUDA device")
+        raw = _raw_stream(stream, self.dev)
+        if raw not in self._streams:
+            self._ws.record_stream(torch.cuda.current_stream(self.dev) if stream is None else stream)
+            self._streams.add(raw)
+        return raw
 
 
 def qcf_pages_fork(pool: PagePool, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
@@ -699,8 +709,8 @@ def qcf_pages_fork(pool: PagePool, src: torch.Tensor, dst: torch.Tensor, stream=
     n = src.numel()
     a, b = pool._list(src, n), pool._list(dst, n)
     if n:   # empty tensors have no address to pass
-        pool._here()
-        call("qcf_pages_fork", pool.ref, a, b, n, pool._ws_ptr, pool._nb, _raw_stream(stream, pool.dev))
+        raw = pool._here(stream)
+        call("qcf_pages_fork", pool.ref, a, b, n, pool._ws_ptr, pool._nb, raw)
 
 
 def qcf_pages_resize(pool: PagePool, new_len: torch.Tensor, seqs: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -708,13 +718,13 @@ def qcf_pages_resize(pool: PagePool, new_len: torch.Tensor, seqs: Optional[torch
     n = new_len.numel()
     b, a = pool._list(new_len, n), None if seqs is None else pool._list(seqs, n)
     if n:
-        pool._here()
-        call("qcf_pages_resize", pool.ref, a, b, n, pool._ws_ptr, pool._nb, _raw_stream(stream, pool.dev))
+        raw = pool._here(stream)
+        call("qcf_pages_resize", pool.ref, a, b, n, pool._ws_ptr, pool._nb, raw)
 
 
 def qcf_pages_compact(pool: PagePool, stream=None) -> torch.Tensor:
     """Moves the pages in use to the lowest ids; returns how many they are (int32 [1] on the device)."""
-    pool._here()
+    raw = pool._here(stream)
     live = _empty((1,), torch.int32, pool.dev, stream)
-    call("qcf_pages_compact", pool.ref, live.data_ptr(), pool._ws_ptr, pool._nb, _raw_stream(stream, pool.dev))
+    call("qcf_pages_compact", pool.ref, live.data_ptr(), pool._ws_ptr, pool._nb, raw)
     return live
