@@ -646,9 +646,9 @@ qcf_status qcf_packed_causal_attn(const void* q, int64_t q_stride, const void* k
 /* Attention of chunks of new tokens over a paged cache that holds them already
  * (qcf_paged_append): the arguments and the result of qcf_shared_prefix_attn, but for the window,
  * which counts positions (prefix_len + own).  Meant for chunks of prompts, alone or among the single
- * tokens of running sequences (4 of 1024 rows over 5120 keys, 32 heads over 8: 261 us, 623 by that call).  A
+ * tokens of running sequences (4 of 1024 rows over 5120 keys, 32 heads over 8: 257 us, 623 by that call).  A
  * step of single tokens or short questions alone is faster there (64 single tokens over 5120 keys: 37 us, 64
- * here; questions of 33 to 64 rows over 16384: 100 and 132).  Cache rows
+ * here; questions of 33 to 64 rows over 16384: 99 and 122).  Cache rows
  * behind a length (the rest of a last page, pages not named) may hold anything, NaN included.  A page
  * outside the cache sets QCF_DEV_BAD_INDEX, and its keys are left out of the softmax; a row
  * left without any key gets o = 0 and lse = -infinity. */

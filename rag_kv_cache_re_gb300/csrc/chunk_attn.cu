@@ -25,14 +25,15 @@
 // even ones and b the odd ones of the same rows, and the output joins the two.
 // Tensor memory columns: S_a 0, S_b 128 (the weights take the first 64 of each), O_a 256, O_b 256 + DP.
 //
-// Bound: a causal prompt of 17984 tokens, 64 heads over 8: 3.32 to 3.39 ms, 1.57 to 1.60 PFLOP/s (cuBLAS: 1.89 in bursts, 1.72 kept up
-// under the power limit, where this kernel runs too).  A pair of row tiles takes 2700 to 2900 cycles a key tile, 2048 of them products.
-// One row tile's own chain is as long: S 512, its arrival 150, the softmax's two halves 1100 and 450, the
-// arrival at the issuer 220, the last products 256.  Two row tiles are what fits tensor memory at head dim 128; at 64, with
-// half the products to the same softmax, the powers bound (16384 tokens, 32 heads over 8: 1184 us, 0.93 PFLOP/s).
-// A unit costs another 5000 cycles (queries, the first scores, a masked tile, the output), which bounds many short prompts:
-// ten of 512 tokens 40.5 us, floor 15.7.  Small calls: the launch 2.5 us, the deal 2.5, loads and one tile 4, code
-// that is fetched as it runs the first time: four questions of up to 64 tokens 13.7 us.
+// Bound: a causal prompt of 17984 tokens, 64 heads over 8: 3.11 to 3.21 ms, 1.65 to 1.70 PFLOP/s (cuBLAS:
+// 1.89 in bursts, 1.72 kept up under the power limit, where this kernel runs too).  A pair of row tiles takes
+// 2550 to 2750 cycles a key tile, 2048 of them products.  One row tile's own chain is as long: S 512, its
+// arrival 150, the softmax's two halves 1100 and 450, the arrival at the issuer 220, the last products 256.  Two row
+// tiles are what fits tensor memory at head dim 128; at 64, with half the products to the same softmax,
+// the powers bound (16384 tokens, 32 heads over 8: 1090 us, 1.01 PFLOP/s).  A unit costs another 5000 cycles
+// (queries, the first scores, a masked tile, the output), which bounds many short prompts: ten of 512 tokens
+// 38 us, floor 15.7.  Small calls: the launch 2.5 us, the deal 2.5, loads and one tile 4, code that is
+// fetched as it runs the first time: four questions of up to 64 tokens 13.7 us.
 #include <algorithm>
 #include <cmath>
 
@@ -44,8 +45,10 @@ constexpr int kMaxChunkSeqs = 8000;   // the deal keeps 12 bytes of each where t
 constexpr int kTileKeys = 128;
 constexpr int kTileThreads = 384;
 constexpr int kTileRows = 512;        // score rows of a unit
-// The deal is by cost: so many for a unit, for a key tile of a unit with one row tile in use (1680 cycles), with both (2800).
-constexpr int kUnitCost = 3, kTileCost1 = 2, kTileCost2 = 3;
+// The deal is by cost: so many for a unit, for a key tile of a unit with one row tile in use (1680 cycles), with both
+// (2700), and for those of a group, whose own tiles come from pages met nowhere else (the mixed step below 277 us; dealt
+// like other tiles 340, at 4 and 5 290).
+constexpr int kUnitCost = 3, kTileCost1 = 2, kTileCost2 = 3, kGroupCost1 = 3, kGroupCost2 = 4;
 // Tiles at least on each side of a cut through a unit: a cut costs the sums' way out and the join.  2 parts of 512
 // rows: 8 us of the call.  Prompts of 1024 / 2048 / 4096 tokens, 64 rows over 5120 keys, in us: 3 tiles 26.8 / 52.0 / 123.1, 22.6;
 // 4 24.7 / 51.3 / 122.4, 23.8; 6 21.9 / 51.9 / 118.0, 24.4; 8 21.9 / 52.2 / 117.2, 26.0.
@@ -212,8 +215,8 @@ __device__ __forceinline__ uint64_t sdesc_mnmajor_sw64(uint32_t smem_addr) {
 // rows lie side by side in the batch and make one unit, which reads the shared prefix once for all of them and
 // then each one's own tiles, which the rows of the others do not see: their weights are 0, and their sums
 // are left out of the product, for 0 x NaN is NaN and one sequence's values must not spoil another.  (44
-// single tokens of 32 heads over a prefix of 5120 tokens among chunks of 2640: 386 us for the call, 423 with
-// a unit to each; 342 with all rows in the products of all tiles.)  It stands in the place of its
+// single tokens of 32 heads over a prefix of 5120 tokens among chunks of 2640: 280 us for the call, 402 with
+// a unit to each.)  It stands in the place of its
 // first sequence; its length is kept as -1 - (32 own tiles + (sequences - 1)).
 struct Span {
   int row0, nq, len;   // nq 0: no rows, or those of a group that began before
@@ -255,11 +258,13 @@ __device__ __forceinline__ Span span_at(const BatchView& b, const ChunkArgs& p, 
 struct RowBlock {
   int i0, ntok;            // tokens of the sequence
   int t0, end, end_a;      // its key tiles; the end of row tile a's
+  int cost;                // of a key tile
   __device__ int tiles() const { return end - t0; }
 };
 __device__ __forceinline__ int tile_of(int prefix, int pos) {
   return pos < prefix ? pos / kTileKeys : (prefix + kTileKeys - 1) / kTileKeys + (pos - prefix) / kTileKeys;
 }
+__device__ __forceinline__ bool two_tiles(const RowBlock& k, int per) { return k.ntok > 2 * per; }
 template <bool GROUPS>
 __device__ __forceinline__ RowBlock row_block(const BatchView& b, const ChunkArgs& p, int nq, int len, int i) {
   RowBlock k;
@@ -268,22 +273,20 @@ __device__ __forceinline__ RowBlock row_block(const BatchView& b, const ChunkArg
   if (GROUPS && len < 0) {
     k.t0 = 0;
     k.end = k.end_a = (b.prefix_len + kTileKeys - 1) / kTileKeys + group_tiles(len);
+    k.cost = two_tiles(k, p.per) ? kGroupCost2 : kGroupCost1;
     return k;
   }
   const int pos = b.prefix_len + len - nq + k.i0;   // of its first token
   k.t0 = p.window ? tile_of(b.prefix_len, max(0, pos - p.window + 1)) : 0;
   k.end = tile_of(b.prefix_len, pos + k.ntok - 1) + 1;
   k.end_a = tile_of(b.prefix_len, pos + min(k.ntok, 2 * p.per) - 1) + 1;
+  k.cost = two_tiles(k, p.per) ? kTileCost2 : kTileCost1;
   return k;
 }
-__device__ __forceinline__ bool two_tiles(const RowBlock& k, int per) { return k.ntok > 2 * per; }
-__device__ __forceinline__ int unit_cost(const RowBlock& k, int per) {
-  return kUnitCost + (two_tiles(k, per) ? kTileCost2 : kTileCost1) * k.tiles();
-}
+__device__ __forceinline__ int unit_cost(const RowBlock& k) { return kUnitCost + k.cost * k.tiles(); }
 // The tile of a unit before which a border at cost x behind its beginning cuts it.
-__device__ __forceinline__ int cut_at(const RowBlock& k, int per, int x) {
-  const int n = k.tiles(), y = max(x - kUnitCost, 0);
-  const int t = min(two_tiles(k, per) ? y / kTileCost2 : y / kTileCost1, n);
+__device__ __forceinline__ int cut_at(const RowBlock& k, int x) {
+  const int n = k.tiles(), t = min(max(x - kUnitCost, 0) / k.cost, n);
   return t < kMinCut ? 0 : n - t < kMinCut ? n : t;
 }
 
@@ -303,6 +306,24 @@ struct Segment {
   int slot;                    // -1: the whole unit, else where its sums go
   int end;                     // 1: there are no more
 };
+
+// What comes from memory is alike in all lanes of a warp, which the compiler cannot see: from one lane it knows, and keeps
+// addresses, descriptors and loop bounds once for the warp instead of once for each lane (17984 tokens 3.30 -> 3.16 ms).
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ void make_uniform(Segment& s) {
+  s.seq = uniform(s.seq);
+  s.row0 = uniform(s.row0);
+  s.ntok = uniform(s.ntok);
+  s.g = uniform(s.g);
+  s.pos = uniform(s.pos);
+  s.len = uniform(s.len);
+  s.t0 = uniform(s.t0);
+  s.nt = uniform(s.nt);
+  s.nt_a = uniform(s.nt_a);
+  s.nt_b = uniform(s.nt_b);
+  s.split = uniform(s.split);
+  s.slot = uniform(s.slot);
+}
 
 // The deal is found by the softmax warps, while others set up barriers and tensor memory.
 constexpr int kDealThreads = 256;
@@ -381,7 +402,7 @@ __device__ void find_share(int tid, const BatchView& b, const ChunkArgs& p, int 
     int seq = first;
     for (int i = b0; i < b1; ++i) {
       while (i >= blk[seq + 1]) ++seq;
-      if (visit(seq, i - blk[seq], Hkv * unit_cost(row_block<GROUPS>(b, p, nqs[seq], lens[seq], i - blk[seq]), p.per))) return;
+      if (visit(seq, i - blk[seq], Hkv * unit_cost(row_block<GROUPS>(b, p, nqs[seq], lens[seq], i - blk[seq])))) return;
     }
   };
   int cost = 0;
@@ -445,8 +466,8 @@ struct TileWalk {
     nq = at.nq;
     len = at.len;
     k = row_block<GROUPS>(b, p, nq, len, block);
-    g = (begin - pos) / unit_cost(k, p.per);
-    pos += g * unit_cost(k, p.per);
+    g = (begin - pos) / unit_cost(k);
+    pos += g * unit_cost(k);
   }
   // The next sequence with rows.
   __device__ void next_seq() {
@@ -468,8 +489,8 @@ struct TileWalk {
   __device__ bool next(Segment& s) {
     while (live) {
       const int n = k.tiles();
-      const int cost = unit_cost(k, p.per);
-      const int from = pos < begin ? cut_at(k, p.per, begin - pos) : 0, to = pos + cost > stop ? cut_at(k, p.per, stop - pos) : n;
+      const int cost = unit_cost(k);
+      const int from = pos < begin ? cut_at(k, begin - pos) : 0, to = pos + cost > stop ? cut_at(k, stop - pos) : n;
       const bool some = from < to;
       if (some) {
         const bool two = two_tiles(k, p.per);
@@ -489,7 +510,7 @@ struct TileWalk {
         if (s.slot == 1) {   // how many borders cut this unit: those of the pairs behind this one
           int parts = 1;
           for (int at = stop; at < pos + cost; at += share) {
-            const int t = cut_at(k, p.per, at - pos);
+            const int t = cut_at(k, at - pos);
             parts += t > 0 && t < n;
           }
           rec = make_int4(parts, s.row0, s.ntok, g);
@@ -519,12 +540,12 @@ constexpr uint32_t idesc_pair(int N, bool b_mn_major) {
   return std::is_same<T, __half>::value ? idesc_bf16_f32(256, N, b_mn_major) & ~((1u << 7) | (1u << 10)) : idesc_bf16_f32(256, N, b_mn_major);
 }
 
-// GROUPS: a kernel of its own, for what groups need in the issuing warps costs other calls 3 %.
+// GROUPS: a kernel of its own, for what groups need in the issuing warps costs other calls 1 to 4 %.
 template <typename T, int DP, bool PAGED, bool GROUPS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     tile_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ,
-                     const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmP, const PagedView c, const BatchView b, const ChunkArgs p, const ChunkParts parts,
-                     unsigned int* status) {
+                     const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmP, const PagedView c, const BatchView b,
+                     const ChunkArgs p, const ChunkParts parts, unsigned int* status) {
   using Cfg = TileCfg<DP>;
   constexpr int ST = Cfg::STAGES;
   constexpr unsigned kAll = 0xffffffffu;
@@ -556,7 +577,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   static_assert(sizeof(Segment) * kSegRing % 8 == 0 && sizeof(DealStart) % 8 == 0, "barriers");
   static_assert(128 * 8 + sizeof(Segment) * kSegRing + sizeof(DealStart) + 64 + (4 * ST + 24 + 2 * kSegRing) * 8 <= Cfg::FIXED, "fixed part");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank()), pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tmK);
@@ -679,6 +700,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
           if (lane == 0) release_segment();
         }
         if (s.end) break;
+        make_uniform(s);
         open_group(s);
         // this lane's page of a tile: its id, n_pages (which reads as zeros) where there is none
         auto page_of = [&](const KeyTile& k) {
@@ -770,7 +792,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       }
     } else if (rank == 0) {
       // ---- MMA issuer of row tile x of both CTAs
-      const int x = __shfl_sync(kAll, warp >> 1, 0);
+      const int x = warp >> 1;
       const bool one = lane == 0;
       constexpr uint32_t idesc_s = idesc_pair<T>(kTileKeys, false);
       constexpr uint32_t idesc_o = idesc_pair<T>(DP, true);
@@ -809,10 +831,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         __syncwarp();
         if (one) release_segment();
         if (s.end) break;
-        // alike in all lanes, which the compiler cannot see in what comes from memory
-        const int t0 = __shfl_sync(kAll, s.t0, 0), nt = __shfl_sync(kAll, s.nt, 0);
-        const int nt_a = __shfl_sync(kAll, s.nt_a, 0), nt_b = __shfl_sync(kAll, s.nt_b, 0), mine = x ? nt_b : nt_a;
-        const int split = __shfl_sync(kAll, s.split, 0), step = 1 + split;
+        make_uniform(s);
+        const int t0 = s.t0, nt = s.nt, nt_a = s.nt_a, nt_b = s.nt_b, mine = x ? nt_b : nt_a, split = s.split, step = 1 + split;
         open_group(s);
         if (!(ok = wait(q_full, k++ & 1))) break;
         // Every use of a stage is emptied by both issuers, also by the one whose row tile does not see the tile: that
@@ -841,54 +861,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         }
         if (late && !(ok = hand_v(n))) break;
         if (split && !(ok = hand(at + 1))) break;
-        for (int i = 0; i < mine; ++i) {
-          const bool more = i + 1 < mine;
-          if (!(ok = wait_v(at))) break;
-          const KeyTile kt = key_tile(s, t0 + at - n);
-          if (kt.len - kt.key0 < kTileKeys) fence_cluster();   // zeros of the V producers
-          const uint64_t vd = v_desc + at % ST * (Cfg::VTILE >> 4);
-          const bool grouped = GROUPS && s.len < 0, others = grouped && kt.seq >= 0;   // others: rows that do not see these keys
-          uint32_t off[8];
-          if (others) {
-            const int sub = kt.seq - s.seq, tok = __shfl_sync(kAll, sub_tok, sub), tok_end = tok + __shfl_sync(kAll, sub_nq, sub);
-#pragma unroll
-            for (int w = 0; w < 8; ++w) {
-              const int t0 = (split ? w >> 2 : 2 * x + (w >> 2)) * p.per, row0 = 32 * (w & 3);   // the row tile's first token, the word's first row
-              const uint32_t on = bits_below((min(tok_end, t0 + p.per) - t0) * a.G - row0) & ~bits_below((tok - t0) * a.G - row0);
-              off[w] = __reduce_or_sync(kAll, ~on);   // the same in all lanes: this leaves it in a uniform register, which the products take
-            }
-          }
-          const uint32_t onto = grouped || i > 0 ? 1u : 0u;   // the softmax warps have cleared the sums of a group
-          auto weigh = [&](int half) {   // O_x += P_x V over 64 keys
-            tc_fence_after();
+        // of a group or not, told apart outside the loop: a choice in it costs other units 4 %
+        auto tiles = [&](auto in_group) {
+          constexpr bool IN_GROUP = decltype(in_group)::value;
+          for (int i = 0; i < mine; ++i) {
+            const bool more = i + 1 < mine;
+            if (!(ok = wait_v(at))) break;
+            const KeyTile kt = key_tile(s, t0 + at - n);
+            if (kt.len - kt.key0 < kTileKeys) fence_cluster();   // zeros of the V producers
+            const uint64_t vd = v_desc + at % ST * (Cfg::VTILE >> 4);
+            const bool others = IN_GROUP && t0 + at - n >= np;   // others: rows that do not see these keys
+            uint32_t off[8];
             if (others) {
-#pragma unroll
-              for (int kk = half * (kTileKeys / 32); kk < (half + 1) * (kTileKeys / 32); ++kk)
-                umma_f16_ts_pair_rows(one, tmem + 256 + x * DP, tmem + x * 128 + kk * 8, vd + kk * (V_STEP >> 4), idesc_o, off);
-              return;
+              const int sub = kt.seq - s.seq, tok = __shfl_sync(kAll, sub_tok, sub), tok_end = tok + __shfl_sync(kAll, sub_nq, sub);
+  #pragma unroll
+              for (int w = 0; w < 8; ++w) {
+                const int t0 = (split ? w >> 2 : 2 * x + (w >> 2)) * p.per, row0 = 32 * (w & 3);   // the row tile's first token, the word's first row
+                const uint32_t on = bits_below((min(tok_end, t0 + p.per) - t0) * a.G - row0) & ~bits_below((tok - t0) * a.G - row0);
+                off[w] = __reduce_or_sync(kAll, ~on);   // the same in all lanes: this leaves it in a uniform register, which the products take
+              }
             }
-#pragma unroll
-            for (int kk = half * (kTileKeys / 32); kk < (half + 1) * (kTileKeys / 32); ++kk)
-              umma_f16_ts_pair(one, tmem + 256 + x * DP, tmem + x * 128 + kk * 8, vd + kk * (V_STEP >> 4), idesc_o, kk > 0 ? 1u : onto);
-          };
-          // a begins, b follows while a has tiles left; who is alone gives itself the turn
-          if ((x == 0 ? i == 0 : i >= nt_a) && one) mbar_arrive(&p_ready[2 * x]);
-          const bool due = x == 0 ? i < nt_b : i + 1 < nt_a;
-          if (!(ok = wait(&p_ready[2 * x], used & 1))) break;
-          weigh(0);
-          if (!(ok = wait(&p_ready[2 * x + 1], used & 1))) break;
-          weigh(1);
-          ++used;
-          if (more) {
-            if (!(ok = wait_k(at + step))) break;
-            scores(at + step, due, i + 2 == mine);
-          } else {
-            pass(due);
-            umma_commit_pair(one, &o_done[x]);
+            const uint32_t onto = IN_GROUP || i > 0 ? 1u : 0u;   // the softmax warps have cleared the sums of a group
+            auto weigh = [&](int half) {   // O_x += P_x V over 64 keys
+              tc_fence_after();
+              if (others) {
+  #pragma unroll
+                for (int kk = half * (kTileKeys / 32); kk < (half + 1) * (kTileKeys / 32); ++kk)
+                  umma_f16_ts_pair_rows(one, tmem + 256 + x * DP, tmem + x * 128 + kk * 8, vd + kk * (V_STEP >> 4), idesc_o, off);
+                return;
+              }
+  #pragma unroll
+              for (int kk = half * (kTileKeys / 32); kk < (half + 1) * (kTileKeys / 32); ++kk)
+                umma_f16_ts_pair(one, tmem + 256 + x * DP, tmem + x * 128 + kk * 8, vd + kk * (V_STEP >> 4), idesc_o, kk > 0 ? 1u : onto);
+            };
+            // a begins, b follows while a has tiles left; who is alone gives itself the turn
+            if ((x == 0 ? i == 0 : i >= nt_a) && one) mbar_arrive(&p_ready[2 * x]);
+            const bool due = x == 0 ? i < nt_b : i + 1 < nt_a;
+            if (!(ok = wait(&p_ready[2 * x], used & 1))) break;
+            weigh(0);
+            if (!(ok = wait(&p_ready[2 * x + 1], used & 1))) break;
+            weigh(1);
+            ++used;
+            if (more) {
+              if (!(ok = wait_k(at + step))) break;
+              scores(at + step, due, i + 2 == mine);
+            } else {
+              pass(due);
+              umma_commit_pair(one, &o_done[x]);
+            }
+            umma_commit_pair(one, &v_empty[at % ST]);   // after the scores: a commit costs more than a product
+            if (split && more && !(ok = hand(at + 3))) break;
+            at += step;
           }
-          umma_commit_pair(one, &v_empty[at % ST]);   // after the scores: a commit costs more than a product
-          if (split && more && !(ok = hand(at + 3))) break;
-          at += step;
+        };
+        if constexpr (GROUPS) {
+          if (s.len < 0) tiles(std::true_type{}); else tiles(std::false_type{});
+        } else {
+          tiles(std::false_type{});
         }
         if (!ok) break;
         if (!split)
@@ -919,6 +948,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       __syncwarp();
       if (lane == 0) release_segment();
       if (s.end) break;
+      make_uniform(s);
       const int mine = x ? s.nt_b : s.nt_a, step = 1 + s.split, t_mine = s.t0 + (s.split & x);
       const int place = s.split ? rank : 2 * x + rank;   // of the row tile in the unit
       // this row's token, sequence and own position (a row of none: the last token's)
@@ -960,10 +990,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         }
         ok = ok && __all_sync(kAll, mbar_wait(&s_full[x], seen++ & 1));   // a warp whose wait ran out still meets the others
         tc_fence_after();
-        float sv[kTileKeys];
-        tmem_ld128(s_tm, sv);
         // keys of the tile that this row sees: [low, high)
         const int high = k.seq < 0 ? k.len - k.key0 : k.seq == seq ? own + 1 - k.key0 : 0;
+        if (GROUPS && s.len < 0 && !__any_sync(kAll, high > 0)) {   // none of the warp's: the products leave its rows out
+          if (lane == 0) {
+            mbar_arrive_at(ready);
+            mbar_arrive_at(ready + 8);
+          }
+          continue;
+        }
+        float sv[kTileKeys];
+        tmem_ld128(s_tm, sv);
         const int low = p.window ? (k.seq < 0 ? b.prefix_len : 0) + own + 1 - p.window - k.key0 : 0;
         if (__any_sync(kAll, high < kTileKeys || low > 0 || bad8)) {
           // one bit to each key: 800 cycles; comparisons of every key with both ends took 1500, skipping keys by eights more
@@ -1258,7 +1295,7 @@ static int64_t most_tiles(const BatchView& b) {
 // New rows of a sequence that may go in a group (0: none does): where a prefix of four tiles or more is read once for the
 // group, and 32 of them fill no more than a unit.  max_len: the length of a Span holds its own tiles.
 static int group_rows(const BatchView& b, int window, int per) {
-  return window == 0 && b.prefix_len >= 4 * kTileKeys && b.max_len <= 1 << 27 ? 4 * per / 32 : 0;
+  return window == 0 && b.n_seq > 1 && b.prefix_len >= 4 * kTileKeys && b.max_len <= 1 << 27 ? 4 * per / 32 : 0;
 }
 // Whether the bounds allow a unit long enough to be cut.
 static bool may_cut(const BatchView& b, int window, int group) {
