@@ -992,7 +992,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         tc_fence_after();
         // keys of the tile that this row sees: [low, high)
         const int high = k.seq < 0 ? k.len - k.key0 : k.seq == seq ? own + 1 - k.key0 : 0;
-        if (GROUPS && s.len < 0 && !__any_sync(kAll, high > 0)) {   // none of the warp's: the products leave its rows out
+        if (GROUPS && k.seq >= 0 && s.len < 0 && !__any_sync(kAll, seq == k.seq)) {   // others' keys: the products leave the warp's rows out
           if (lane == 0) {
             mbar_arrive_at(ready);
             mbar_arrive_at(ready + 8);
@@ -1401,7 +1401,7 @@ static qcf_status check_sizes(const char* who, const PagedView& c, const BatchVi
   // the deal counts costs in 31 bits, with room for a share more
   const int R = 4 * (128 / (Hq / c.Hkv));
   const double blocks = std::min(static_cast<double>(b.n_seq) * ((std::min(b.max_q, b.n_rows) + R - 1) / R), static_cast<double>(b.n_rows) / R + b.n_seq);
-  if (blocks * c.Hkv * (kUnitCost + kTileCost2 * static_cast<double>(most_tiles(b))) > INT32_MAX / 2)
+  if (blocks * c.Hkv * (kUnitCost + kGroupCost2 * static_cast<double>(most_tiles(b))) > INT32_MAX / 2)
     return set_error(QCF_ERR_SHAPE, "%s: the bounds allow more work than one call takes", who);
   return QCF_OK;
 }

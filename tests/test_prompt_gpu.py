@@ -297,6 +297,20 @@ def test_chunk_groups_keep_one_sequences_nan_to_itself(Q, Hq, Hkv, D):
         assert same != (b in hurt) or n == 0, f"sequence {b}"
 
 
+@pytest.mark.parametrize("D,dtype", [(128, "bf16"), (64, "f16")])
+@pytest.mark.parametrize("at", range(112, 145, 8))
+def test_chunk_groups_with_rows_before_and_behind_a_tile(Q, D, dtype, at):
+    """New rows of a group's sequence on both sides of a key tile's border, in more than one warp: the rows before it see
+    none of the tile's keys."""
+    bt = R.Batch([16, 8, 16, 16, 1, 16], [40, 8, at, at + 3, 300, 16 + at], 700, 4, D, 16, "rows", TYPES[dtype], seed=at).fill()
+    q = bt.randn(bt.n_rows, 4, D)
+    cache, batch = bt.bind(Q)
+    got, lse = Q.qcf_paged_chunk_attn(cache, batch, q, 0.1, want_lse=True)
+    o, e, tol, ltol = P.batch_attention(bt, q, 0.1)
+    within(got, o, tol, "o")
+    within(lse, e, ltol, "lse")
+
+
 def test_chunk_groups_of_many(Q):
     """Hundreds of single tokens, a cache that changes under a captured call."""
     lens = [(i * 29) % 260 + 1 for i in range(300)]
