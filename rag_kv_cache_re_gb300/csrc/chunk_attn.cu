@@ -1204,6 +1204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     if (rho == 0) bulk_wait_group0();   // the stores are done before this kernel counts as complete
     if (!ok && lane == 0) flag_status(status, QCF_DEV_TIMEOUT);
   }
+  pdl_launch_dependents();   // the join comes up as pairs end
   tc_fence_before();
   __syncthreads();
   // in both CTAs: the commits that arrive here have all done so when the last has

@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(const PoolView
   const int words = (p.n_seq + 31) / 32, most = p.table_stride << p.page_shift;
   for (int i = threadIdx.x; i < words; i += kPlanThreads) named[i] = 0;
   pdl_wait();
+  pdl_launch_dependents();   // what applies the plan comes up meanwhile (turnover 11.3 -> 10.9 us)
   __syncthreads();
   bool bad = false;
   PlanItem mine = {};   // of the first 1024 arguments, which are mostly all
@@ -213,6 +214,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PoolVi
   int64_t total;
   int count = 0;
   pdl_wait();
+  pdl_launch_dependents();
   for (int64_t base = 0; base < p.n_pages; base += kCompactPass) {
     load_refs<kCompactIds>(p, base, r);
 #pragma unroll

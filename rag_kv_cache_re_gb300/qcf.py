@@ -8,6 +8,7 @@ ordered on the current stream.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 from typing import Dict, List, Optional, Sequence, Tuple
 
 import numpy as np
@@ -603,6 +604,12 @@ def _attn_out(q: torch.Tensor, out: Optional[torch.Tensor], want_lse: bool, dev:
     return out, _empty(q.shape[:2], torch.float32, dev, stream) if want_lse else None
 
 
+@functools.lru_cache(maxsize=1024)
+def _packed_workspace(dev: int, *sizes: int) -> int:
+    """qcf_packed_causal_attn_workspace_size: a function of the sizes and the device alone."""
+    return _lib.lib().qcf_packed_causal_attn_workspace_size(*sizes)
+
+
 def qcf_packed_causal_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, row_start: torch.Tensor, max_len: int, scale: float,
                            window: int = 0, want_lse: bool = False, out: Optional[torch.Tensor] = None, stream=None):
     """Causal attention of whole prompts packed one behind the other: q [n_rows][Hq][D], k and v
@@ -621,7 +628,7 @@ def qcf_packed_causal_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ro
     out, lse = _attn_out(q, out, want_lse, dev, stream, max_len, window)
     n_seq = row_start.numel() - 1
     if n and n_seq:   # empty tensors have no address to pass
-        nb = _lib.lib().qcf_packed_causal_attn_workspace_size(n_seq, n, max_len, Hq, Hk, D)
+        nb = _packed_workspace(dev, n_seq, n, max_len, Hq, Hk, D)
         ws = _empty(nb, torch.uint8, dev, stream) if nb else None
         call("qcf_packed_causal_attn", q.data_ptr(), qs, k.data_ptr(), v.data_ptr(), ks, _DTYPE[q.dtype], row_start.data_ptr(), n_seq, n,
              max_len, Hq, Hk, D, scale, window, out.data_ptr(), None if lse is None else lse.data_ptr(),
