@@ -622,7 +622,7 @@ qcf_status qcf_shared_prefix_attn(const qcf_paged_kv* cache, const qcf_paged_bat
  *   ws      device scratch of the matching *_workspace_size() bytes (0: ws may be NULL); it needs
  *           no clearing; calls that overlap on the GPU (captured graphs replayed side by side
  *           among them) need separate scratch
- * scale > 0; n_seq <= 8000; n_rows Hq < 2^24; bounds that allow more than about 2^28 key tiles of
+ * scale > 0; n_seq <= 8000; n_rows Hq < 2^24; bounds that allow more than about 2^27 key tiles of
  * 128 for 512 score rows each are refused (QCF_ERR_SHAPE).  Products in the type of q with fp32
  * sums, softmax in fp32.  Results repeat bitwise for the same inputs and bounds.  A NaN in a query
  * stays in its row and head; a key or value that holds NaN or infinity may spoil every row of its
@@ -647,8 +647,8 @@ qcf_status qcf_packed_causal_attn(const void* q, int64_t q_stride, const void* k
  * (qcf_paged_append): the arguments and the result of qcf_shared_prefix_attn, but for the window,
  * which counts positions (prefix_len + own).  Meant for chunks of prompts, alone or among the single
  * tokens of running sequences (4 of 1024 rows over 5120 keys, 32 heads over 8: 257 us, 623 by that call).  A
- * step of single tokens or short questions alone is faster there (64 single tokens over 5120 keys: 37 us, 64
- * here; questions of 33 to 64 rows over 16384: 99 and 122).  Cache rows
+ * step of single tokens or short questions alone is faster there (64 single tokens over 5120 keys: 37 us, 56
+ * here; questions of 33 to 64 rows over 16384: 99 and 106).  Cache rows
  * behind a length (the rest of a last page, pages not named) may hold anything, NaN included.  A page
  * outside the cache sets QCF_DEV_BAD_INDEX, and its keys are left out of the softmax; a row
  * left without any key gets o = 0 and lse = -infinity. */

@@ -46,14 +46,14 @@ constexpr int kTileKeys = 128;
 constexpr int kTileThreads = 384;
 constexpr int kTileRows = 512;        // score rows of a unit
 // The deal is by cost: so many for a unit, for a key tile of a unit with one row tile in use (1680 cycles), with both
-// (2700), and for those of a group, whose own tiles come from pages met nowhere else (the mixed step below 277 us; dealt
-// like other tiles 340, at 4 and 5 290).
-constexpr int kUnitCost = 3, kTileCost1 = 2, kTileCost2 = 3, kGroupCost1 = 3, kGroupCost2 = 4;
+// (2650), and for those of a group, whose own tiles come from pages met nowhere else.  (The mixed step below 273 us, dealt
+// like other tiles 294, at 6 and 8 280; 1024 rows and 100 single tokens of up to 4000 own keys 277, 267, 319.)
+constexpr int kUnitCost = 6, kTileCost1 = 4, kTileCost2 = 6, kGroupCost1 = 5, kGroupCost2 = 7;
 // Tiles at least on each side of a cut through a unit: a cut costs the sums' way out and the join.  2 parts of 512
 // rows: 8 us of the call.  Prompts of 1024 / 2048 / 4096 tokens, 64 rows over 5120 keys, in us: 3 tiles 26.8 / 52.0 / 123.1, 22.6;
 // 4 24.7 / 51.3 / 122.4, 23.8; 6 21.9 / 51.9 / 118.0, 24.4; 8 21.9 / 52.2 / 117.2, 26.0.
 constexpr int kMinCut = 3;
-constexpr int kMinCost = 9;           // dealt to a pair at least
+constexpr int kMinCost = 18;           // dealt to a pair at least
 constexpr int kSegRing = 4;
 
 // What the two entry points differ in: keys and values as rows of one tensor each, or in pages.
@@ -74,8 +74,10 @@ struct TileCfg {
   static constexpr int QBOX = 128 * 128, QTILE = BOXES * QBOX;          // a CTA's 128 score rows
   static constexpr int KBOX = 64 * 128, KTILE = BOXES * KBOX;           // its 64 keys
   static constexpr int VCOLS = DP / 2, VTILE = kTileKeys * VCOLS * 2;   // its columns of 128 values
-  static constexpr int STAGES = DP == 128 ? 3 : 8;
-  static constexpr int OBOX = 128 * 128, OTILE = 2 * OBOX;              // output of 128 score rows, 128 bytes of each to a box
+  // 4 and one box of output: 3 and two take 1 % less where many rows share a tile, and 10 to 16 % more where few do
+  // (8 questions of 33 to 64 rows over 16384 keys 123 us for 107, one row over 65536 70 for 59).
+  static constexpr int STAGES = DP == 128 ? 4 : 8;
+  static constexpr int OBOX = 128 * 128, OBOXES = DP == 128 ? 1 : 2, OTILE = OBOXES * OBOX;   // output of 128 score rows, 128 bytes of each to a box
   static constexpr int FIXED = 3 * 1024;
   static constexpr int SMEM = 2 * QTILE + STAGES * (KTILE + VTILE) + 2 * OTILE + FIXED;
 };
@@ -215,7 +217,7 @@ __device__ __forceinline__ uint64_t sdesc_mnmajor_sw64(uint32_t smem_addr) {
 // rows lie side by side in the batch and make one unit, which reads the shared prefix once for all of them and
 // then each one's own tiles, which the rows of the others do not see: their weights are 0, and their sums
 // are left out of the product, for 0 x NaN is NaN and one sequence's values must not spoil another.  (44
-// single tokens of 32 heads over a prefix of 5120 tokens among chunks of 2640: 280 us for the call, 402 with
+// single tokens of 32 heads over a prefix of 5120 tokens among chunks of 2640: 273 us for the call, 402 with
 // a unit to each.)  It stands in the place of its
 // first sequence; its length is kept as -1 - (32 own tiles + (sequences - 1)).
 struct Span {
@@ -1119,13 +1121,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       stored = tiled;
       if (rows <= quarter * 32) {   // none of this warp's, which still meets the others
         if (s.split) bar_sync(3 + quarter, 64);
-        if (tiled) {
-          bar_sync(1 + x, 128);
-          if (cut && DP == 128) {
-            bar_sync(1 + x, 128);
-            bar_sync(1 + x, 128);
-          }
-        }
+        if (tiled)   // cut: a whole tile has no such warp
+          for (int i = 0; i < (Cfg::OBOXES == 1 ? 2 * (DP / 32) - 1 : 1); ++i) bar_sync(1 + x, 128);
         continue;
       }
 #pragma unroll 1
@@ -1161,44 +1158,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
               if (c0 + e * 8 < p.D) *reinterpret_cast<uint4*>(o + e * 8) = pack8<T>(ov + 8 * e);
           }
         } else if (cut) {   // 32 columns of 32 bits to a box
-          if (c0 > 0) boxes_free();
+          static_assert(Cfg::OBOXES == 1 || DP == 64, "boxes are free");
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            *reinterpret_cast<float4*>(out + (e >> 3) * Cfg::OBOX + sw128_off(lane, e & 7)) = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
-          fence_proxy_async_smem();
-          bar_sync(1 + x, 128);
-          if (rho == 0) {
-            tma_store_2d(&tmP, obox, c0, static_cast<int>(part));
-            if (c0 + 32 < p.D) tma_store_2d(&tmP, obox + Cfg::OBOX, c0 + 32, static_cast<int>(part));
-            bulk_commit_group();
+          for (int h = 0; h < 2; ++h) {
+            if (Cfg::OBOXES == 1 && c0 + h > 0) boxes_free();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float* f = ov + 32 * h + 4 * e;
+              *reinterpret_cast<float4*>(out + h * (Cfg::OTILE - Cfg::OBOX) + sw128_off(lane, e)) = make_float4(f[0], f[1], f[2], f[3]);
+            }
+            if (Cfg::OBOXES == 2 && h == 0) continue;
+            fence_proxy_async_smem();
+            bar_sync(1 + x, 128);
+            if (rho == 0) {
+#pragma unroll
+              for (int g = Cfg::OBOXES == 2 ? 0 : h; g <= h; ++g)
+                if (c0 + 32 * g < p.D) tma_store_2d(&tmP, obox + g * (Cfg::OTILE - Cfg::OBOX), c0 + 32 * g, static_cast<int>(part));
+              bulk_commit_group();
+            }
           }
         } else {
+          if (tiled && c0 > 0) boxes_free();
 #pragma unroll
-          for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(out + (c0 >> 6) * Cfg::OBOX + sw128_off(lane, e)) = pack8<T>(ov + 8 * e);
-        }
-      }
-      if (few || cut) continue;
-      if (tiled) {   // every row of the tile: stores that run on while the next unit does
-        fence_proxy_async_smem();
-        bar_sync(1 + x, 128);
-        if (rho == 0) {
+          for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(out + sw128_off(lane, e)) = pack8<T>(ov + 8 * e);
+          if (tiled) {   // every row of the tile: stores that run on while the next unit does
+            fence_proxy_async_smem();
+            bar_sync(1 + x, 128);
+            if (rho == 0) {
+              tma_store_3d(&tmO, obox, c0, s.g * a.G, s.row0 + place * p.per);
+              bulk_commit_group();
+            }
+          } else {       // rows behind the sequence's end belong to others
+            __syncwarp();
 #pragma unroll
-          for (int h = 0; h < Cfg::BOXES; ++h)
-            tma_store_3d(&tmO, obox + h * Cfg::OBOX, h * 64, s.g * a.G, s.row0 + place * p.per);
-          bulk_commit_group();
-        }
-      } else {       // rows behind the sequence's end belong to others
-        __syncwarp();
-#pragma unroll 1
-        for (int h = 0; h < Cfg::BOXES; ++h)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int r = e * 4 + (lane >> 3), row = quarter * 32 + r, col = h * 64 + (lane & 7) * 8, tl = div_g(a, row);
-            if (row < rows && col < p.D)
-              *reinterpret_cast<uint4*>(static_cast<T*>(a.o) + (first + static_cast<int64_t>(tl) * a.Hq + row - tl * a.G) * p.D + col) =
-                  *reinterpret_cast<const uint4*>(out + h * Cfg::OBOX + sw128_off(r, lane & 7));
+            for (int e = 0; e < 8; ++e) {
+              const int r = e * 4 + (lane >> 3), row = quarter * 32 + r, col = c0 + (lane & 7) * 8, tl = div_g(a, row);
+              if (row < rows && col < p.D)
+                *reinterpret_cast<uint4*>(static_cast<T*>(a.o) + (first + static_cast<int64_t>(tl) * a.Hq + row - tl * a.G) * p.D + col) =
+                    *reinterpret_cast<const uint4*>(out + sw128_off(r, lane & 7));
+            }
+            __syncwarp();
           }
-        __syncwarp();
+        }
       }
     }
     if (rho == 0) bulk_wait_group0();   // the stores are done before this kernel counts as complete
