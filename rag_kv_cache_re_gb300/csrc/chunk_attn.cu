@@ -53,7 +53,7 @@ constexpr int kUnitCost = 6, kTileCost1 = 4, kTileCost2 = 6, kGroupCost1 = 5, kG
 // rows: 8 us of the call.  Prompts of 1024 / 2048 / 4096 tokens, 64 rows over 5120 keys, in us: 3 tiles 26.8 / 52.0 / 123.1, 22.6;
 // 4 24.7 / 51.3 / 122.4, 23.8; 6 21.9 / 51.9 / 118.0, 24.4; 8 21.9 / 52.2 / 117.2, 26.0.
 constexpr int kMinCut = 3;
-constexpr int kMinCost = 18;           // dealt to a pair at least
+constexpr int kMinCost = 18;          // dealt to a pair at least
 constexpr int kSegRing = 4;
 
 // What the two entry points differ in: keys and values as rows of one tensor each, or in pages.
@@ -77,7 +77,7 @@ struct TileCfg {
   // 4 and one box of output: 3 and two take 1 % less where many rows share a tile, and 10 to 16 % more where few do
   // (8 questions of 33 to 64 rows over 16384 keys 123 us for 107, one row over 65536 70 for 59).
   static constexpr int STAGES = DP == 128 ? 4 : 8;
-  static constexpr int OBOX = 128 * 128, OBOXES = DP == 128 ? 1 : 2, OTILE = OBOXES * OBOX;   // output of 128 score rows, 128 bytes of each to a box
+  static constexpr int OBOX = 128 * 128, OBOXES = DP == 128 ? 1 : 2, OTILE = OBOXES * OBOX;   // output: 128 bytes of 128 rows to a box
   static constexpr int FIXED = 3 * 1024;
   static constexpr int SMEM = 2 * QTILE + STAGES * (KTILE + VTILE) + 2 * OTILE + FIXED;
 };
@@ -1121,8 +1121,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       stored = tiled;
       if (rows <= quarter * 32) {   // none of this warp's, which still meets the others
         if (s.split) bar_sync(3 + quarter, 64);
-        if (tiled)   // cut: a whole tile has no such warp
-          for (int i = 0; i < (Cfg::OBOXES == 1 ? 2 * (DP / 32) - 1 : 1); ++i) bar_sync(1 + x, 128);
+        if (tiled) {
+          bar_sync(1 + x, 128);
+          if (Cfg::OBOXES == 1)   // cut: a whole tile has no such warp
+            for (int i = 1; i < 2 * (DP / 32) - 1; ++i) bar_sync(1 + x, 128);
+        }
         continue;
       }
 #pragma unroll 1
@@ -1157,49 +1160,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             for (int e = 0; e < 8; ++e)
               if (c0 + e * 8 < p.D) *reinterpret_cast<uint4*>(o + e * 8) = pack8<T>(ov + 8 * e);
           }
-        } else if (cut) {   // 32 columns of 32 bits to a box
-          static_assert(Cfg::OBOXES == 1 || DP == 64, "boxes are free");
+        } else if (cut && Cfg::OBOXES == 1) {   // 32 columns of 32 bits at a time
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (Cfg::OBOXES == 1 && c0 + h > 0) boxes_free();
+            if (c0 + h > 0) boxes_free();
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const float* f = ov + 32 * h + 4 * e;
-              *reinterpret_cast<float4*>(out + h * (Cfg::OTILE - Cfg::OBOX) + sw128_off(lane, e)) = make_float4(f[0], f[1], f[2], f[3]);
+              *reinterpret_cast<float4*>(out + sw128_off(lane, e)) = make_float4(f[0], f[1], f[2], f[3]);
             }
-            if (Cfg::OBOXES == 2 && h == 0) continue;
             fence_proxy_async_smem();
             bar_sync(1 + x, 128);
-            if (rho == 0) {
-#pragma unroll
-              for (int g = Cfg::OBOXES == 2 ? 0 : h; g <= h; ++g)
-                if (c0 + 32 * g < p.D) tma_store_2d(&tmP, obox + g * (Cfg::OTILE - Cfg::OBOX), c0 + 32 * g, static_cast<int>(part));
+            if (rho == 0 && c0 + 32 * h < p.D) {
+              tma_store_2d(&tmP, obox, c0 + 32 * h, static_cast<int>(part));
               bulk_commit_group();
             }
+          }
+        } else if (cut) {   // or two boxes of them
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            *reinterpret_cast<float4*>(out + (e >> 3) * Cfg::OBOX + sw128_off(lane, e & 7)) = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+          fence_proxy_async_smem();
+          bar_sync(1 + x, 128);
+          if (rho == 0) {
+            tma_store_2d(&tmP, obox, c0, static_cast<int>(part));
+            if (c0 + 32 < p.D) tma_store_2d(&tmP, obox + Cfg::OBOX, c0 + 32, static_cast<int>(part));
+            bulk_commit_group();
           }
         } else {
-          if (tiled && c0 > 0) boxes_free();
+          if (Cfg::OBOXES == 1 && tiled && c0 > 0) boxes_free();
 #pragma unroll
           for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(out + sw128_off(lane, e)) = pack8<T>(ov + 8 * e);
-          if (tiled) {   // every row of the tile: stores that run on while the next unit does
-            fence_proxy_async_smem();
-            bar_sync(1 + x, 128);
-            if (rho == 0) {
-              tma_store_3d(&tmO, obox, c0, s.g * a.G, s.row0 + place * p.per);
-              bulk_commit_group();
-            }
-          } else {       // rows behind the sequence's end belong to others
-            __syncwarp();
+          if constexpr (Cfg::OBOXES == 1) {
+            if (tiled) {   // every row of the tile: stores that run on while the next unit does
+              fence_proxy_async_smem();
+              bar_sync(1 + x, 128);
+              if (rho == 0) {
+                tma_store_3d(&tmO, obox, c0, s.g * a.G, s.row0 + place * p.per);
+                bulk_commit_group();
+              }
+            } else {       // rows behind the sequence's end belong to others
+              __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int r = e * 4 + (lane >> 3), row = quarter * 32 + r, col = c0 + (lane & 7) * 8, tl = div_g(a, row);
-              if (row < rows && col < p.D)
-                *reinterpret_cast<uint4*>(static_cast<T*>(a.o) + (first + static_cast<int64_t>(tl) * a.Hq + row - tl * a.G) * p.D + col) =
-                    *reinterpret_cast<const uint4*>(out + sw128_off(r, lane & 7));
+              for (int e = 0; e < 8; ++e) {
+                const int r = e * 4 + (lane >> 3), row = quarter * 32 + r, col = c0 + (lane & 7) * 8, tl = div_g(a, row);
+                if (row < rows && col < p.D)
+                  *reinterpret_cast<uint4*>(static_cast<T*>(a.o) + (first + static_cast<int64_t>(tl) * a.Hq + row - tl * a.G) * p.D + col) =
+                      *reinterpret_cast<const uint4*>(out + sw128_off(r, lane & 7));
+              }
+              __syncwarp();
             }
-            __syncwarp();
           }
         }
+      }
+      if (Cfg::OBOXES == 1 || few || cut) continue;   // head dim 64: all columns in one box, after the loop (in it, as above, the call takes 7 % more)
+      if (tiled) {   // every row of the tile: stores that run on while the next unit does
+        fence_proxy_async_smem();
+        bar_sync(1 + x, 128);
+        if (rho == 0) {
+#pragma unroll
+          for (int h = 0; h < Cfg::BOXES; ++h)
+            tma_store_3d(&tmO, obox + h * Cfg::OBOX, h * 64, s.g * a.G, s.row0 + place * p.per);
+          bulk_commit_group();
+        }
+      } else {       // rows behind the sequence's end belong to others
+        __syncwarp();
+#pragma unroll 1
+        for (int h = 0; h < Cfg::BOXES; ++h)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int r = e * 4 + (lane >> 3), row = quarter * 32 + r, col = h * 64 + (lane & 7) * 8, tl = div_g(a, row);
+            if (row < rows && col < p.D)
+              *reinterpret_cast<uint4*>(static_cast<T*>(a.o) + (first + static_cast<int64_t>(tl) * a.Hq + row - tl * a.G) * p.D + col) =
+                  *reinterpret_cast<const uint4*>(out + h * Cfg::OBOX + sw128_off(r, lane & 7));
+          }
+        __syncwarp();
       }
     }
     if (rho == 0) bulk_wait_group0();   // the stores are done before this kernel counts as complete
