@@ -25,15 +25,15 @@
 // even ones and b the odd ones of the same rows, and the output joins the two.
 // Tensor memory columns: S_a 0, S_b 128 (the weights take the first 64 of each), O_a 256, O_b 256 + DP.
 //
-// Bound: a causal prompt of 17984 tokens, 64 heads over 8: 3.11 to 3.21 ms, 1.65 to 1.70 PFLOP/s (cuBLAS:
+// Bound: a causal prompt of 17984 tokens, 64 heads over 8: 3.08 to 3.20 ms, 1.66 to 1.72 PFLOP/s (cuBLAS:
 // 1.89 in bursts, 1.72 kept up under the power limit, where this kernel runs too).  A pair of row tiles takes
 // 2550 to 2750 cycles a key tile, 2048 of them products.  One row tile's own chain is as long: S 512, its
 // arrival 150, the softmax's two halves 1100 and 450, the arrival at the issuer 220, the last products 256.  Two row
 // tiles are what fits tensor memory at head dim 128; at 64, with half the products to the same softmax,
-// the powers bound (16384 tokens, 32 heads over 8: 1090 us, 1.01 PFLOP/s).  A unit costs another 5000 cycles
+// the powers bound (16384 tokens, 32 heads over 8: 1071 us, 1.03 PFLOP/s).  A unit costs another 5000 cycles
 // (queries, the first scores, a masked tile, the output), which bounds many short prompts: ten of 512 tokens
-// 38 us, floor 15.7.  Small calls: the launch 2.5 us, the deal 2.5, loads and one tile 4, code that is
-// fetched as it runs the first time: four questions of up to 64 tokens 13.7 us.
+// 37.4 us, floor 15.7.  Small calls: the launch 2.5 us, the deal 2.5, loads and one tile 4, code that is
+// fetched as it runs the first time: four questions of up to 64 tokens 13.0 us.
 #include <algorithm>
 #include <cmath>
 
