@@ -1119,13 +1119,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         other_f *= inv;
       }
       stored = tiled;
-      if (rows <= quarter * 32) {   // none of this warp's, which still meets the others
+      // None of this warp's.  Tiled stores are made by all four warps together, whose barriers have to be as many, so there it
+      // goes on like the others: what it writes lies behind the box of a whole tile (at 43 to 48 and 65 to 96 score rows a
+      // token), or in sums of a cut one that the join does not read.
+      if (!tiled && rows <= quarter * 32) {
         if (s.split) bar_sync(3 + quarter, 64);
-        if (tiled) {
-          bar_sync(1 + x, 128);
-          if (Cfg::OBOXES == 1)   // cut: a whole tile has no such warp
-            for (int i = 1; i < 2 * (DP / 32) - 1; ++i) bar_sync(1 + x, 128);
-        }
         continue;
       }
 #pragma unroll 1
