@@ -704,7 +704,9 @@ qcf_status qcf_pages_resize(const qcf_page_pool* pool, const int32_t* seqs, cons
 
 /* Moves the pages in use to the lowest ids: with *n_live (device) pages in use, the k-th of those at
  * or above n_live goes to the k-th free one below it, rows, counts and tables alike.  Every
- * holder of a page is a row of the table. */
+ * holder of a page is a row of the table.  A length out of range: nothing has changed, and *n_live is -1.
+ * Where pages move, a row's page that lies outside the cache, or at or above n_live without a count, sets
+ * QCF_DEV_BAD_INDEX and stays in its row. */
 qcf_status qcf_pages_compact(const qcf_page_pool* pool, int32_t* n_live, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus

@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PoolVi
   if (threadIdx.x == 0) {
     if (bad) flag_status(status, QCF_DEV_BAD_INDEX);
     *out.head = PlanHead{!bad, moves, live, 0};
-    *n_live = live;
+    *n_live = bad ? -1 : live;   // nothing moves: no count may say which pages are free
   }
 }
 

@@ -730,7 +730,8 @@ def qcf_pages_resize(pool: PagePool, new_len: torch.Tensor, seqs: Optional[torch
 
 
 def qcf_pages_compact(pool: PagePool, stream=None) -> torch.Tensor:
-    """Moves the pages in use to the lowest ids; returns how many they are (int32 [1] on the device)."""
+    """Moves the pages in use to the lowest ids; returns how many they are (int32 [1] on the device; -1 where a length
+    is out of range, and nothing has changed)."""
     raw = pool._here(stream)
     live = _empty((1,), torch.int32, pool.dev, stream)
     call("qcf_pages_compact", pool.ref, live.data_ptr(), pool._ws_ptr, pool._nb, raw)
