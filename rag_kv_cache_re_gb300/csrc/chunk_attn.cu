@@ -972,6 +972,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             tmem_st16(o_tm + cc * 16, zero);
           }
           tmem_wait_st();
+          tc_fence_before();   // a warp that sees nothing of the first tile hands it on without another
         }
       }
       auto page_bad = [&](const KeyTile& k) {   // the page of this lane's 8 keys of a tile lies outside the cache
@@ -1096,6 +1097,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
           tc_fence_before();
           bar_sync(3 + quarter, 64);
           bar_sync(3 + quarter, 64);   // they have been read
+          tc_fence_after();            // a group's sums are cleared next
           continue;
         }
         bar_sync(3 + quarter, 64);
