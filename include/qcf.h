@@ -646,7 +646,7 @@ qcf_status qcf_packed_causal_attn(const void* q, int64_t q_stride, const void* k
 /* Attention of chunks of new tokens over a paged cache that holds them already
  * (qcf_paged_append): the arguments and the result of qcf_shared_prefix_attn, but for the window,
  * which counts positions (prefix_len + own).  Meant for chunks of prompts, alone or among the single
- * tokens of running sequences (4 of 1024 rows over 5120 keys, 32 heads over 8: 257 us, 623 by that call).  A
+ * tokens of running sequences (4 of 1024 rows over 5120 keys, 32 heads over 8: 254 us, 622 by that call).  A
  * step of single tokens or short questions alone is faster there (64 single tokens over 5120 keys: 37 us, 56
  * here; questions of 33 to 64 rows over 16384: 99 and 106).  Cache rows
  * behind a length (the rest of a last page, pages not named) may hold anything, NaN included.  A page

@@ -25,15 +25,16 @@
 // even ones and b the odd ones of the same rows, and the output joins the two.
 // Tensor memory columns: S_a 0, S_b 128 (the weights take the first 64 of each), O_a 256, O_b 256 + DP.
 //
-// Bound: a causal prompt of 17984 tokens, 64 heads over 8: 3.08 to 3.20 ms, 1.66 to 1.72 PFLOP/s (cuBLAS:
+// Bound: a causal prompt of 17984 tokens, 64 heads over 8: 3.08 to 3.22 ms, 1.64 to 1.72 PFLOP/s (cuBLAS:
 // 1.89 in bursts, 1.72 kept up under the power limit, where this kernel runs too).  A pair of row tiles takes
 // 2550 to 2750 cycles a key tile, 2048 of them products.  One row tile's own chain is as long: S 512, its
 // arrival 150, the softmax's two halves 1100 and 450, the arrival at the issuer 220, the last products 256.  Two row
-// tiles are what fits tensor memory at head dim 128; at 64, with half the products to the same softmax,
-// the powers bound (16384 tokens, 32 heads over 8: 1071 us, 1.03 PFLOP/s).  A unit costs another 5000 cycles
-// (queries, the first scores, a masked tile, the output), which bounds many short prompts: ten of 512 tokens
-// 37.4 us, floor 15.7.  Small calls: the launch 2.5 us, the deal 2.5, loads and one tile 4, code that is
-// fetched as it runs the first time: four questions of up to 64 tokens 13.0 us.
+// tiles are what fits tensor memory at head dim 128.  At 64, with half the products to the same softmax, that
+// chain bounds: 2300 cycles by these figures, and the period is 2260 (16384 tokens, 32 heads over 8: 1071 us, 1.03
+// PFLOP/s), while the tensor pipe, the powers and the issue slots are in use 40, 40 and 43 % of the time (8192 tokens).
+// A unit costs another 5000 cycles (queries, the first scores, a masked tile, the output), which bounds many
+// short prompts: ten of 512 tokens 37.4 us, floor 15.7.  Small calls: the launch 2.5 us, the deal 2.5, loads and one
+// tile 4, code that is fetched as it runs the first time: four questions of up to 64 tokens 13.0 us.
 #include <algorithm>
 #include <cmath>
 
@@ -47,11 +48,13 @@ constexpr int kTileThreads = 384;
 constexpr int kTileRows = 512;        // score rows of a unit
 // The deal is by cost: so many for a unit, for a key tile of a unit with one row tile in use (1680 cycles), with both
 // (2650), and for those of a group, whose own tiles come from pages met nowhere else.  (The mixed step below 273 us, dealt
-// like other tiles 294, at 6 and 8 280; 1024 rows and 100 single tokens of up to 4000 own keys 277, 267, 319.)
+// like other tiles 294, at 6 and 8 280; 1024 rows and 100 single tokens of up to 4000 own keys 277, 267, 319.)  A unit counts
+// for no more than 2650 cycles here and takes 5000, so pairs with many short units get too much: by these cycles the longest
+// pair has 33 us of work at 2048 tokens where the mean is 26, and 30 with a unit at 11.  Other values have not been measured.
 constexpr int kUnitCost = 6, kTileCost1 = 4, kTileCost2 = 6, kGroupCost1 = 5, kGroupCost2 = 7;
 // Tiles at least on each side of a cut through a unit: a cut costs the sums' way out and the join.  2 parts of 512
-// rows: 8 us of the call.  Prompts of 1024 / 2048 / 4096 tokens, 64 rows over 5120 keys, in us: 3 tiles 26.8 / 52.0 / 123.1, 22.6;
-// 4 24.7 / 51.3 / 122.4, 23.8; 6 21.9 / 51.9 / 118.0, 24.4; 8 21.9 / 52.2 / 117.2, 26.0.
+// rows: 8 us of the call.  When this was chosen, prompts of 1024 / 2048 / 4096 tokens, 64 rows over
+// 5120 keys, in us: 3 tiles 26.8 / 52.0 / 123.1, 22.6; 4 24.7 / 51.3 / 122.4, 23.8; 6 21.9 / 51.9 / 118.0, 24.4; 8 21.9 / 52.2 / 117.2, 26.0.
 constexpr int kMinCut = 3;
 constexpr int kMinCost = 18;          // dealt to a pair at least
 constexpr int kSegRing = 4;
@@ -217,8 +220,8 @@ __device__ __forceinline__ uint64_t sdesc_mnmajor_sw64(uint32_t smem_addr) {
 // rows lie side by side in the batch and make one unit, which reads the shared prefix once for all of them and
 // then each one's own tiles, which the rows of the others do not see: their weights are 0, and their sums
 // are left out of the product, for 0 x NaN is NaN and one sequence's values must not spoil another.  (44
-// single tokens of 32 heads over a prefix of 5120 tokens among chunks of 2640: 273 us for the call, 402 with
-// a unit to each.)  It stands in the place of its
+// single tokens of 32 heads over a prefix of 5120 tokens, in five runs beside four chunks of 3172 together: 271 us for the
+// call, 402 with a unit to each at an earlier step.)  It stands in the place of its
 // first sequence; its length is kept as -1 - (32 own tiles + (sequences - 1)).
 struct Span {
   int row0, nq, len;   // nq 0: no rows, or those of a group that began before
